@@ -22,6 +22,7 @@ EXPORTS = ("lp_apply_token_bitmask", "lp_apply_token_bitmask_rows", "lp_apply_pa
            "lp_sample",
            "lp_mask_and_sample", "lp_mask_and_sample_slots", "lp_sample_workspace_bytes",
            "lp_mask_and_sample_noalloc",
+           "lp_beam_select", "lp_beam_select_workspace_bytes",
            "lp_philox4x32_10", "lp_status_string")
 
 
@@ -77,6 +78,12 @@ def declare(lib) -> None:
                                                ctypes.POINTER(SamplingParams), c_vp, c_vp]
     lib.lp_sample_workspace_bytes.restype = c_i64
     lib.lp_sample_workspace_bytes.argtypes = [c_i32, c_i64, c_i64]
+    lib.lp_beam_select_workspace_bytes.restype = c_i64
+    lib.lp_beam_select_workspace_bytes.argtypes = [c_i32, c_i64, c_i64]
+    lib.lp_beam_select.restype = c_i32
+    lib.lp_beam_select.argtypes = [c_vp, c_i32, c_i64, c_i64, c_i64, c_i64, c_vp, c_i64, c_i64,
+                                   c_i64, c_i64, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_vp,
+                                   c_vp, c_vp, c_i64, c_vp]
     lib.lp_philox4x32_10.restype = c_i32
     lib.lp_philox4x32_10.argtypes = [c_vp, c_vp, c_vp, c_i64, c_vp]
     lib.lp_status_string.restype = ctypes.c_char_p

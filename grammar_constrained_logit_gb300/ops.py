@@ -421,6 +421,121 @@ def mask_and_sample_slots(logits: torch.Tensor, bitmask: torch.Tensor | None,
 lp_mask_and_sample_slots = mask_and_sample_slots
 
 
+_beam_workspaces: dict = {}
+
+
+def beam_select_workspace_bytes(dtype: torch.dtype, rows: int, vocab_size: int) -> int:
+    """Bytes of device scratch ``beam_select`` needs for ``rows`` = batch * beams."""
+    n = _lib.load().lp_beam_select_workspace_bytes(_DT[dtype], rows, vocab_size)
+    if n < 0:
+        raise ValueError("invalid dtype or size")
+    return int(n)
+
+
+def _beam_workspace(workspace, lg: torch.Tensor):
+    """The caller's workspace (a uint8 CUDA tensor of any content), or one kept per
+    (device, stream), grown on demand.  When capturing a CUDA graph, pass one that was
+    allocated before the capture.  Returns (pointer, bytes)."""
+    if workspace is not None:
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+                workspace.device != lg.device:
+            raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
+        return workspace.data_ptr(), workspace.numel()
+    need = beam_select_workspace_bytes(lg.dtype, lg.size(0), lg.size(1))
+    key = (lg.device.index, torch.cuda.current_stream(lg.device).cuda_stream)
+    ws = _beam_workspaces.get(key)
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(max(need, 8), dtype=torch.uint8, device=lg.device)
+        _beam_workspaces[key] = ws
+    return ws.data_ptr(), ws.numel()
+
+
+def _row_flags(flags, rows, device, name):
+    if flags is None:
+        return None
+    if flags.device != device:
+        raise ValueError(f"{name} must be on the same device as logits")
+    if flags.numel() != rows:
+        raise ValueError(f"{name} must have {rows} entries")
+    if flags.dtype == torch.bool:
+        flags = flags.view(torch.uint8)
+    elif flags.dtype != torch.uint8:
+        raise TypeError(f"{name} must be uint8 or bool")
+    return flags.contiguous()
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None = None, *,
+                bitmask: torch.Tensor | None = None,
+                row_needs_mask: torch.Tensor | None = None,
+                finished: torch.Tensor | None = None, pad_id: int = 0,
+                vocab_size: int | None = None, out: tuple | None = None,
+                workspace: torch.Tensor | None = None):
+    """One step of beam search: the ``n_select`` best continuations (the number of
+    beams when None) of each batch entry over its beams and the vocabulary.
+
+    ``logits`` [batch, beams, V] (or its [batch * beams, V] view), ``scores`` float32
+    [batch, beams]: the beams' log-probabilities so far, -inf for a beam that does not
+    exist (all but the first at the first step).  Log-probabilities are normalised over
+    the tokens that ``bitmask`` keeps (in the rows that ``row_needs_mask`` flags; all
+    when None).  A beam that ``finished`` (uint8 or bool) flags goes on as one candidate
+    (``pad_id``, its score).
+
+    Returns (scores float32, tokens int64, parents int32), each [batch, n_select],
+    highest score first, ties to the lowest (beam, token); empty places are
+    (-inf, -1, -1).  ``out`` takes the three tensors to write instead."""
+    if scores.dim() != 2:
+        raise ValueError(f"scores must be [batch, beams], got {tuple(scores.shape)}")
+    if scores.dtype != torch.float32:
+        raise TypeError("scores must be float32")
+    batch, beams = scores.shape
+    if logits.dim() == 3:
+        if logits.shape[:2] != scores.shape:
+            raise ValueError("logits [batch, beams, V] must match scores [batch, beams]")
+        logits = logits.flatten(0, 1)
+    lg = _matrix(logits, "logits")
+    rows = lg.size(0)
+    if rows != batch * beams:
+        raise ValueError(f"logits must have {batch * beams} rows, got {rows}")
+    if scores.device != lg.device:
+        raise ValueError("scores must be on the same device as logits")
+    dt = _dtype_code(lg)
+    n = beams if n_select is None else int(n_select)
+    bm = None
+    if bitmask is not None:
+        bm = _bitmask(bitmask.flatten(0, -2) if bitmask.dim() > 2 else bitmask, lg.device)
+    elif row_needs_mask is not None:
+        raise ValueError("row_needs_mask needs a bitmask")
+    flags = _row_flags(row_needs_mask, rows, lg.device, "row_needs_mask")
+    ended = _row_flags(finished, rows, lg.device, "finished")
+    sc = scores.contiguous()
+    if out is None:
+        if n < 0:
+            raise ValueError("n_select must not be negative")
+        out = (torch.empty((batch, n), dtype=torch.float32, device=lg.device),
+               torch.empty((batch, n), dtype=torch.int64, device=lg.device),
+               torch.empty((batch, n), dtype=torch.int32, device=lg.device))
+    else:
+        for t, d in zip(out, (torch.float32, torch.int64, torch.int32), strict=True):
+            if t.dtype != d or t.shape != (batch, n) or not t.is_contiguous() or \
+                    t.device != lg.device:
+                raise ValueError("out must be contiguous float32, int64 and int32 tensors "
+                                 "[batch, n_select] on the logits' device")
+    wp, wn = _beam_workspace(workspace, lg)
+    st = _lib.load().lp_beam_select(
+        lg.data_ptr(), dt, batch, beams, lg.size(1), _stride(lg),
+        None if bm is None else bm.data_ptr(), 0 if bm is None else bm.size(0),
+        0 if bm is None else bm.size(1), 0 if bm is None else _stride(bm),
+        -1 if vocab_size is None else int(vocab_size), None if flags is None else flags.data_ptr(),
+        sc.data_ptr(), None if ended is None else ended.data_ptr(), int(pad_id), n,
+        out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), wp, wn,
+        torch.cuda.current_stream(lg.device).cuda_stream)
+    check("lp_beam_select", st)
+    return out
+
+
+lp_beam_select = beam_select
+
+
 def philox4x32_10(counters: torch.Tensor, keys: torch.Tensor) -> torch.Tensor:
     """Device Philox4x32-10 on n blocks: counters [n, 4], keys [n, 2] (int32 bit
     patterns on the GPU) -> [n, 4] words (int32 bit patterns)."""

@@ -1,6 +1,6 @@
 /*
- * lp.h -- C ABI of liblp.so: grammar-constrained logit masking and fused
- * per-row sampling on one GB300 GPU (sm_103a).
+ * lp.h -- C ABI of liblp.so: grammar-constrained logit masking, fused per-row
+ * sampling and beam search on one GB300 GPU (sm_103a).
  *
  * Operations (each entry point cites the page section that defines it):
  *   lp_apply_token_bitmask   in place, masked logits := -inf
@@ -13,6 +13,8 @@
  *   lp_mask_and_sample       the bitmask applied on the fly, then lp_sample
  *   lp_mask_and_sample_slots the same on [slots, rows_per_slot, V] logits with
  *                            per-slot parameters and optional per-row seeds
+ *   lp_beam_select           beam search: the best candidates over beams x vocabulary,
+ *                            under the bitmask
  *
  * Common conventions
  *   - Logits are a row-major [B, cols] matrix of float32, float16 or bfloat16 with
@@ -311,6 +313,52 @@ lp_status lp_mask_and_sample_noalloc(const void* logits, lp_dtype dt, int64_t B,
                                      const int32_t* indices, int64_t num_indices,
                                      const lp_sampling_params* params, int64_t* out_ids,
                                      cudaStream_t stream);
+
+/*
+ * lp_beam_select -- one step of beam search under a grammar: the n_select best
+ * continuations of each batch entry over its beams and the vocabulary.  The
+ * pages have no counterpart; rows, bitmask and row flags are those of
+ * lp_apply_token_bitmask_rows, and the softmax runs over the kept tokens, as
+ * lp_sample's.
+ *
+ * Row r = b * beams + k is beam k of batch entry b.  With C_r the tokens v <
+ * vocab_size whose bit is set (every token of a row whose row_needs_mask is 0, or
+ * without a bitmask) and whose logit is above -inf, the candidates of entry b are
+ *   - of a beam whose score is above -inf and that is not finished: (k, v) for v in
+ *     C_r with score scores[r] + ((x_rv - max_C x) - log sum_C exp(x - max_C x));
+ *   - of a finished beam with a score above -inf: (k, pad_id) with scores[r];
+ *   - of a beam with score -inf or NaN: none (its logits are not read).
+ * Out come the n_select candidates of highest score, highest first; equal scores
+ * fall to the lowest (beam, token).  Exponentials and the chunks' sums are 32-bit,
+ * their joint sum and the scores that are compared 64-bit; two equal rows get equal
+ * scores to the last bit, whatever their alignment.  NaN logits are no candidates;
+ * tokens of logit +inf share their row's whole mass.  A candidate whose score is
+ * -inf (an overflow) is none.
+ *   logits         device [batch * beams, cols], read only
+ *   bitmask        device int32 [bitmask_rows >= batch * beams, ...], or NULL
+ *   row_needs_mask device uint8 [batch * beams], or NULL: every row is masked
+ *   scores         device float32 [batch * beams]: the beams' log-probabilities so far
+ *   finished       device uint8 [batch * beams], or NULL: no beam is
+ *   out_scores     device float32 [batch, n_select]; -inf in empty places
+ *   out_tokens     device int64 [batch, n_select]; -1 in empty places
+ *   out_parents    device int32 [batch, n_select], the beam k; -1 in empty places
+ *   workspace      device scratch of lp_beam_select_workspace_bytes(dt, batch *
+ *                  beams, vocab_size) bytes, 8-byte aligned, of any content; calls
+ *                  that share it must be ordered (one stream, or events)
+ * Two kernels on the stream.  Invalid: as lp_apply_token_bitmask_rows, beams < 1,
+ * n_select < 0, row_needs_mask without bitmask, a short or misaligned workspace,
+ * logits not aligned to their element.  beams or n_select above 256, more than 2^27
+ * rows, or a vocabulary above 2^31 - 65 return LP_ERR_TOO_LARGE.
+ */
+int64_t lp_beam_select_workspace_bytes(lp_dtype dt, int64_t rows, int64_t vocab_size);
+
+lp_status lp_beam_select(const void* logits, lp_dtype dt, int64_t batch, int64_t beams,
+                         int64_t cols, int64_t logits_stride, const int32_t* bitmask,
+                         int64_t bitmask_rows, int64_t bitmask_words, int64_t bitmask_stride,
+                         int64_t vocab_size, const uint8_t* row_needs_mask, const float* scores,
+                         const uint8_t* finished, int64_t pad_id, int64_t n_select,
+                         float* out_scores, int64_t* out_tokens, int32_t* out_parents,
+                         void* workspace, int64_t workspace_bytes, cudaStream_t stream);
 
 /*
  * lp_philox4x32_10 -- diagnostic: the device's Philox4x32-10 (Salmon et al.,

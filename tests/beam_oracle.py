@@ -1,0 +1,68 @@
+"""Plain 64-bit definitions of the beam-search operators, on the CPU, for their tests."""
+import numpy as np
+
+
+def beam_candidates(x, scores, *, allowed=None, finished=None, pad=0):
+    """Candidates of one batch entry, best first: a list of (score, beam, token).
+    x float64 [beams, V]; scores [beams]; allowed bool [beams, V] or None."""
+    out = []
+    for k in range(x.shape[0]):
+        s = float(scores[k])
+        if not s > -np.inf:
+            continue
+        if finished is not None and finished[k]:
+            out.append((s, k, -1))
+            continue
+        ok = x[k] > -np.inf  # false for NaN
+        if allowed is not None:
+            ok &= allowed[k]
+        v = np.flatnonzero(ok)
+        if v.size == 0:
+            continue
+        m = x[k, v].max()
+        if m == np.inf:
+            v = v[x[k, v] == np.inf]
+            lp = np.full(v.size, -np.log(float(v.size)))
+        else:
+            d = x[k, v] - m
+            lp = d - np.log(np.exp(d).sum())
+        out += [(s + lp[i], k, int(v[i])) for i in np.argsort(-lp, kind="stable")
+                if s + lp[i] > -np.inf]
+    out.sort(key=lambda c: (-c[0], c[1], c[2]))
+    return [(s, k, pad if t < 0 else t) for s, k, t in out]
+
+
+def check_beam(got, x, scores, n, *, allowed=None, finished=None, pad=0, tol=None):
+    """Compares a selection with the definition.  Scores agree within
+
+        2^-24 |score|  (one rounding to 32 bits)  +  4e-6  (the error of log S)
+
+    where log S's bound adds, relative to S: 2^-22 of an exponential by the hardware's
+    approximation, 2^-23 sum_i p_i t_i <= 2^-23 ln V of its argument's two roundings
+    (below 1.5e-6 for V < 2^18), 20 additions of 2^-24 (1.2e-6) and the join's 2^-23.
+    Where neighbours in the true order are further apart than twice that, beam and token
+    are the definition's; nearer ones may trade places, unless they are of one beam."""
+    gs, gt, gp = (np.asarray(a) for a in got)
+    batch, beams = scores.shape
+    for b in range(batch):
+        r = slice(b * beams, (b + 1) * beams)
+        want = beam_candidates(x[r], scores[b], pad=pad,
+                               allowed=None if allowed is None else allowed[r],
+                               finished=None if finished is None else finished[b])
+        true = {(k, t): s for s, k, t in want}
+        m = min(n, len(want))
+        assert (gt[b, m:] == -1).all() and (gp[b, m:] == -1).all()
+        assert np.isneginf(gs[b, m:]).all()
+        picked = [(int(gp[b, i]), int(gt[b, i])) for i in range(m)]
+        assert len(set(picked)) == m, "a candidate twice"
+        for i in range(m):
+            s = want[i][0]
+            off = (2.0 ** -24 * abs(s) + 4e-6) if np.isfinite(s) else 0.0
+            assert picked[i] in true, (b, i, picked[i])
+            assert gs[b, i] == s or abs(float(gs[b, i]) - s) <= off, (b, i, gs[b, i], s)
+            if picked[i] != want[i][1:]:
+                # only a neighbour within the rounding may stand here, and of another beam
+                assert abs(true[picked[i]] - s) <= 2 * off, (b, i, picked[i], want[i])
+        for k in set(p for p, _ in picked):  # one beam's candidates keep their exact order
+            mine = [t for p, t in picked if p == k]
+            assert mine == [t for _, p, t in want if p == k][:len(mine)], (b, k)
