@@ -22,7 +22,7 @@ EXPORTS = ("lp_apply_token_bitmask", "lp_apply_token_bitmask_rows", "lp_apply_pa
            "lp_sample",
            "lp_mask_and_sample", "lp_mask_and_sample_slots", "lp_sample_workspace_bytes",
            "lp_mask_and_sample_noalloc",
-           "lp_beam_select", "lp_beam_select_workspace_bytes",
+           "lp_beam_select", "lp_beam_select_workspace_bytes", "lp_reorder_states",
            "lp_philox4x32_10", "lp_status_string")
 
 
@@ -34,6 +34,13 @@ class SamplingParams(ctypes.Structure):
                 ("top_p", c_vp), ("top_p_scalar", c_f32),
                 ("min_p", c_vp), ("min_p_scalar", c_f32),
                 ("seed", c_u64), ("offset", c_u64)]
+
+
+class State(ctypes.Structure):
+    """lp_state: the bytes of a tensor's rows, strides in bytes."""
+
+    _fields_ = [("data", c_vp), ("row_stride", c_i64), ("run_bytes", c_i64),
+                ("token_bytes", c_i64), ("outer", c_i64 * 3), ("outer_stride", c_i64 * 3)]
 
 
 class LPError(RuntimeError):
@@ -84,6 +91,8 @@ def declare(lib) -> None:
     lib.lp_beam_select.argtypes = [c_vp, c_i32, c_i64, c_i64, c_i64, c_i64, c_vp, c_i64, c_i64,
                                    c_i64, c_i64, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_vp,
                                    c_vp, c_vp, c_i64, c_vp]
+    lib.lp_reorder_states.restype = c_i32
+    lib.lp_reorder_states.argtypes = [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp]
     lib.lp_philox4x32_10.restype = c_i32
     lib.lp_philox4x32_10.argtypes = [c_vp, c_vp, c_vp, c_i64, c_vp]
     lib.lp_status_string.restype = ctypes.c_char_p

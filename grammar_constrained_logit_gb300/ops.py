@@ -536,6 +536,125 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None
 lp_beam_select = beam_select
 
 
+def _state(t: torch.Tensor, row_dim: int, token_dim: int | None) -> _lib.State:
+    """A tensor's rows as lp_state: the longest contiguous run, up to the tokens' axis
+    when one is given, and the axes around it."""
+    if not t.is_cuda:
+        raise ValueError("states must be CUDA tensors")
+    d = t.dim()
+    if not -d <= row_dim < d or (token_dim is not None and not -d <= token_dim < d):
+        raise ValueError(f"axis out of range for a state of shape {tuple(t.shape)}")
+    row_dim %= d
+    if token_dim is not None:
+        token_dim %= d
+        if token_dim == row_dim:
+            raise ValueError("the tokens' axis must not be the rows'")
+    if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+        raise ValueError("a state must not be expanded: its rows would overlap")
+    size = t.element_size()
+    axes = sorted(((st * size, n, i) for i, (n, st) in enumerate(zip(t.shape, t.stride()))
+                   if i != row_dim and (n != 1 or i == token_dim)),
+                  key=lambda a: (a[0], a[1] == 1))
+    run, token, outer, around, closed = size, 0, [], None, False
+    for st, n, i in axes:
+        if i == token_dim:
+            closed = True
+            if not outer and (st == run or n == 1):
+                token, run = run, run * n
+            else:
+                around = (st, n)  # tokens apart from each other: an axis around the runs
+        elif not outer and not closed and st == run:
+            run *= n
+        elif outer and outer[-1][0] * outer[-1][1] == st:
+            outer[-1] = (outer[-1][0], outer[-1][1] * n)
+        else:
+            outer.append((st, n))
+    if around is not None:
+        token = -1
+        outer.append(around)
+    if len(outer) > 3:
+        raise ValueError("a state's other axes must fold to three at most")
+    s = _lib.State()
+    s.data, s.row_stride, s.run_bytes = t.data_ptr(), t.stride(row_dim) * size, run
+    s.token_bytes = token
+    if t.numel() == 0:
+        s.run_bytes = s.token_bytes = 0
+    for d in range(3):
+        st, n = outer[-1 - d] if d < len(outer) else (0, 1)
+        s.outer[d], s.outer_stride[d] = n, st
+    return s
+
+
+class StateReorder:
+    """The states that follow the beams of a search: made once for the tensors that a
+    model keeps, then ``reorder`` after each selection moves all of them in place.
+
+    ``states``: tensors whose first axis is the ``batch * beams`` rows, or tuples
+    (tensor, rows' axis) or (tensor, rows' axis, tokens' axis).  Views are fine (a cache
+    laid out heads first, a slice) as long as rows do not overlap; what is contiguous
+    moves in long runs.  The tensors are held, their memory is read and written at each
+    call."""
+
+    def __init__(self, states, batch: int, beams: int):
+        self.batch, self.beams = int(batch), int(beams)
+        if self.batch < 0 or self.beams < 1:
+            raise ValueError("batch must not be negative and beams at least 1")
+        self.states = []
+        for s in states:
+            t, rows, tokens = ((s, 0, None) if isinstance(s, torch.Tensor) else
+                               (*s, None) if len(s) == 2 else s)
+            self.states.append((t, rows, tokens))
+        self._c = (_lib.State * max(1, len(self.states)))()
+        self.device = None
+        for i, (t, rows, tokens) in enumerate(self.states):
+            self._c[i] = _state(t, rows, tokens)
+            if t.size(rows) != self.batch * self.beams:
+                raise ValueError(f"state {i} must have {self.batch * self.beams} rows, "
+                                 f"got {t.size(rows)}")
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise ValueError("states must be on one device")
+
+    def _check(self, t, name, shape, n):
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on the states' device")
+        if t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {shape}")
+        return t.data_ptr()
+
+    def reorder(self, parents: torch.Tensor, start: torch.Tensor | None = None,
+                stop: torch.Tensor | None = None) -> None:
+        """Row b * beams + k of every state becomes what row b * beams + parents[b, k]
+        was.  ``parents`` int32 [batch, beams], as ``beam_select`` returns them; one
+        outside [0, beams) leaves its row.  ``start`` / ``stop`` int32 [batch]: of the
+        states that have a tokens' axis only tokens [start[b], stop[b]) move (a prompt
+        that all beams share need not)."""
+        if not self.states:
+            return
+        b, k = self.batch, self.beams
+        p = self._check(parents, "parents", "[batch, beams]", b * k)
+        lo = None if start is None else self._check(start, "start", "[batch]", b)
+        hi = None if stop is None else self._check(stop, "stop", "[batch]", b)
+        st = _lib.load().lp_reorder_states(self._c, len(self.states), b, k, p, lo, hi,
+                                           torch.cuda.current_stream(self.device).cuda_stream)
+        check("lp_reorder_states", st)
+
+
+def reorder_states(states, parents: torch.Tensor, start: torch.Tensor | None = None,
+                   stop: torch.Tensor | None = None) -> None:
+    """``StateReorder(states, *parents.shape).reorder(parents, start, stop)``, for a
+    single call."""
+    if parents.dim() != 2:
+        raise ValueError("parents must be [batch, beams]")
+    StateReorder(states, *parents.shape).reorder(parents, start, stop)
+
+
+lp_reorder_states = reorder_states
+
+
 def philox4x32_10(counters: torch.Tensor, keys: torch.Tensor) -> torch.Tensor:
     """Device Philox4x32-10 on n blocks: counters [n, 4], keys [n, 2] (int32 bit
     patterns on the GPU) -> [n, 4] words (int32 bit patterns)."""

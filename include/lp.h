@@ -15,6 +15,7 @@
  *                            per-slot parameters and optional per-row seeds
  *   lp_beam_select           beam search: the best candidates over beams x vocabulary,
  *                            under the bitmask
+ *   lp_reorder_states        beam search: states follow their beams, in place
  *
  * Common conventions
  *   - Logits are a row-major [B, cols] matrix of float32, float16 or bfloat16 with
@@ -359,6 +360,48 @@ lp_status lp_beam_select(const void* logits, lp_dtype dt, int64_t batch, int64_t
                          const uint8_t* finished, int64_t pad_id, int64_t n_select,
                          float* out_scores, int64_t* out_tokens, int32_t* out_parents,
                          void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * lp_reorder_states -- what a model keeps for each row (its cache, the tokens said so
+ * far) follows the beams that lp_beam_select chose.  The pages have no counterpart for
+ * beams; TensorRT-Edge-LLM "Guided Decoder", compactSlots, moves slots the same way
+ * (batch = 1, beams = the slots).
+ *
+ * In every state, row b * beams + k becomes what row b * beams + parents[b, k] was
+ * before the call, for k < beams.  A parent outside [0, beams) leaves its row as it
+ * is.  Everything is in place and needs no scratch; rows that do not change are not
+ * written, and only sources of others are read.
+ *
+ * A state's bytes of row r are, for every (i, j, l) below outer, the run_bytes bytes at
+ *   data + r * row_stride + i * outer_stride[0] + j * outer_stride[1] + l * outer_stride[2]
+ * (strides in bytes; outer[d] = 1 for what is not needed).  They must not overlap, nor
+ * overlap another state's.
+ *   token_bytes  > 0: the run is tokens of that many bytes, and of batch entry b only
+ *                tokens [start[b], stop[b]) take part, both cut to the run; -1: a run is
+ *                one token, the tokens' axis is outer[0], and the same holds; 0: the
+ *                state has no tokens' axis and all of it takes part
+ *   states       HOST array, read during the call; data are device pointers
+ *   parents      device int32 [batch, beams]
+ *   start, stop  device int32 [batch], or NULL: from the first token, to the last
+ * One kernel for each 64 states.  Base and strides that are multiples of 16 bytes move
+ * 16 bytes at a time, others as many as divide them (and the token's or run's bytes).
+ * Invalid: a negative size, token_bytes below -1, run_bytes not a multiple of token_bytes, |row_stride| below
+ * run_bytes, NULL data or parents with work to do, beams < 1.  beams above 256, more
+ * than 2^27 rows, or a state of more than 2^31 runs or 32 KB pieces of runs return
+ * LP_ERR_TOO_LARGE.
+ */
+typedef struct {
+  void* data;
+  int64_t row_stride;
+  int64_t run_bytes;
+  int64_t token_bytes;
+  int64_t outer[3];
+  int64_t outer_stride[3];
+} lp_state;
+
+lp_status lp_reorder_states(const lp_state* states, int64_t n_states, int64_t batch,
+                            int64_t beams, const int32_t* parents, const int32_t* start,
+                            const int32_t* stop, cudaStream_t stream);
 
 /*
  * lp_philox4x32_10 -- diagnostic: the device's Philox4x32-10 (Salmon et al.,

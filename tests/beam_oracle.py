@@ -66,3 +66,18 @@ def check_beam(got, x, scores, n, *, allowed=None, finished=None, pad=0, tol=Non
         for k in set(p for p, _ in picked):  # one beam's candidates keep their exact order
             mine = [t for p, t in picked if p == k]
             assert mine == [t for _, p, t in want if p == k][:len(mine)], (b, k)
+
+
+def reordered(rows, parents, start=None, stop=None):
+    """rows [batch * beams, tokens, ...] after a reorder."""
+    batch, beams = parents.shape
+    out = rows.copy()
+    T = rows.shape[1]
+    for b in range(batch):
+        lo = 0 if start is None else min(max(int(start[b]), 0), T)
+        hi = T if stop is None else min(max(int(stop[b]), 0), T)
+        for k in range(beams):
+            p = int(parents[b, k])
+            if 0 <= p < beams and lo < hi:
+                out[b * beams + k, lo:hi] = rows[b * beams + p, lo:hi]
+    return out

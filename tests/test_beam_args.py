@@ -84,3 +84,105 @@ def test_candidates_by_hand():
     assert beam_candidates(x, np.array([-np.inf, np.nan])) == []
     got = beam_candidates(np.array([[np.inf, 3.0, np.inf]]), np.array([0.0]))
     assert [(k, t) for _, k, t in got] == [(0, 0), (0, 2)] and got[0][0] == -np.log(2.0)
+
+
+# ---------------------------------------------------------------- reorder_states
+
+
+def _state(**kw):
+    s = _lib.State()
+    s.data, s.row_stride, s.run_bytes, s.token_bytes = 0x10000, 64, 64, 0
+    for d in range(3):
+        s.outer[d], s.outer_stride[d] = 1, 0
+    for k, v in kw.items():
+        if k == "outer":
+            for d in range(3):
+                s.outer[d] = v[d]
+        else:
+            setattr(s, k, v)
+    return s
+
+
+def _reorder(lib, *states, n=None, batch=2, beams=4, parents=FAKE, start=None, stop=None):
+    arr = (_lib.State * max(1, len(states)))(*states)
+    return lib.lp_reorder_states(arr if states else None, len(states) if n is None else n, batch,
+                                 beams, parents, start, stop, None)
+
+
+@pytest.mark.parametrize("kw, args, want", [
+    (dict(run_bytes=-1), {}, 1), (dict(token_bytes=-2), {}, 1), (dict(token_bytes=5), {}, 1),
+    (dict(outer=(1, -1, 1)), {}, 1), (dict(data=None), {}, 1), (dict(row_stride=63), {}, 1),
+    (dict(row_stride=0), {}, 1), (dict(row_stride=-63), {}, 1),
+    ({}, dict(batch=-1), 1), ({}, dict(beams=0), 1), ({}, dict(parents=None), 1),
+    ({}, dict(n=-1), 1),
+    ({}, dict(beams=257), 4), ({}, dict(batch=1 << 26), 4),
+    (dict(outer=(1 << 32, 1, 1)), {}, 4), (dict(outer=(1 << 20, 1 << 20, 1)), {}, 4),
+    (dict(run_bytes=1 << 50, row_stride=1 << 50), {}, 4),
+    ({}, dict(batch=0), 0), (dict(run_bytes=0), {}, 0), (dict(outer=(0, 1, 1), data=None), {}, 0),
+])
+def test_reorder_refusals(lib, kw, args, want):
+    assert _reorder(lib, _state(**kw), **args) == want
+
+
+def test_reorder_nothing(lib):
+    assert _reorder(lib) == 0
+    assert _reorder(lib, n=1) == 1  # a count without states
+
+
+def test_state_reorder_binding_refusals():
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.StateReorder([torch.zeros(8, 4)], 2, 4)
+    with pytest.raises(ValueError, match="beams"):
+        ops.StateReorder([], 2, 0)
+    with pytest.raises(ValueError, match="batch, beams"):
+        ops.reorder_states([], torch.zeros(4, dtype=torch.int32))
+    ops.StateReorder([], 2, 4).reorder(torch.zeros(2, 4, dtype=torch.int32))  # nothing to move
+
+
+class _Fake:
+    """A CUDA tensor's geometry without one."""
+
+    def __init__(self, t):
+        self.t, self.is_cuda = t, True
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def _geometry(t, rows, tokens):
+    s = ops._state(_Fake(t), rows, tokens)
+    return (s.row_stride, s.run_bytes, s.token_bytes, tuple(s.outer), tuple(s.outer_stride))
+
+
+def test_state_geometry():
+    """The bytes that a descriptor names, walked on the CPU, are the tensor's own."""
+    base = torch.arange(2 * 6 * 5 * 3 * 4, dtype=torch.int16).view(2, 6, 5, 3, 4)
+    views = [(base, 1, 2), (base, 1, 3), (base, 1, None), (base.transpose(2, 3), 1, 3),
+             (base[:, :, 1:4], 1, 2), (base[0], 0, 1), (base[..., 1:3], 1, 2), (base[:, :, :1], 1, 2),
+             (base.permute(4, 1, 0, 3, 2), 1, 4), (base[1, :, 2], 0, None), (base[0, :, :, 0], 0, 1),
+             (base[0, :, 0, 0, 0], 0, None), (base[:, :, :, :1], 1, 3), (base[:, :, ::2], 1, 2)]
+    flat = base.reshape(-1)
+    for t, rows, tokens in views:
+        row_stride, run, token, outer, strides = _geometry(t, rows, tokens)
+        for r in range(t.size(rows)):
+            want = t.select(rows, r)
+            places = []
+            for i in range(outer[0]):
+                for j in range(outer[1]):
+                    for k in range(outer[2]):
+                        at = t.storage_offset() * 2 + r * row_stride + i * strides[0] + \
+                            j * strides[1] + k * strides[2]
+                        assert at % 2 == 0
+                        places += range(at // 2, (at + run) // 2)
+            assert sorted(flat[places].tolist()) == sorted(want.reshape(-1).tolist())
+        if tokens is not None:
+            T = t.size(tokens)
+            assert token == -1 and outer[0] == T or run // token == T
+    with pytest.raises(ValueError, match="expanded"):
+        _geometry(torch.zeros(1, 4).expand(3, 4), 0, None)
+    with pytest.raises(ValueError, match="rows'"):
+        _geometry(base, 1, 1)
+    with pytest.raises(ValueError, match="out of range"):
+        _geometry(base, 5, None)
+    with pytest.raises(ValueError, match="three"):
+        _geometry(torch.zeros(4, 3, 6, 3, 6, 3, 6, 3)[:, :2, :5, :2, :5, :2, :5, :2], 0, None)
