@@ -23,6 +23,7 @@ EXPORTS = ("lp_apply_token_bitmask", "lp_apply_token_bitmask_rows", "lp_apply_pa
            "lp_mask_and_sample", "lp_mask_and_sample_slots", "lp_sample_workspace_bytes",
            "lp_mask_and_sample_noalloc",
            "lp_beam_select", "lp_beam_select_workspace_bytes", "lp_reorder_states",
+           "lp_cache_write", "lp_cache_read",
            "lp_philox4x32_10", "lp_status_string")
 
 
@@ -41,6 +42,21 @@ class State(ctypes.Structure):
 
     _fields_ = [("data", c_vp), ("row_stride", c_i64), ("run_bytes", c_i64),
                 ("token_bytes", c_i64), ("outer", c_i64 * 3), ("outer_stride", c_i64 * 3)]
+
+
+class CachePart(ctypes.Structure):
+    """lp_cache_part: codes and their scaling, strides in bytes."""
+
+    _fields_ = [("codes", c_vp), ("params", c_vp), ("code_page_stride", c_i64),
+                ("code_slot_stride", c_i64), ("code_head_stride", c_i64),
+                ("param_page_stride", c_i64), ("param_slot_stride", c_i64),
+                ("param_head_stride", c_i64)]
+
+
+class Heads(ctypes.Structure):
+    """lp_heads: [n, heads, dim], strides in elements."""
+
+    _fields_ = [("data", c_vp), ("token_stride", c_i64), ("head_stride", c_i64)]
 
 
 class LPError(RuntimeError):
@@ -93,6 +109,10 @@ def declare(lib) -> None:
                                    c_vp, c_vp, c_i64, c_vp]
     lib.lp_reorder_states.restype = c_i32
     lib.lp_reorder_states.argtypes = [c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp]
+    for f in (lib.lp_cache_write, lib.lp_cache_read):
+        f.restype = c_i32
+        f.argtypes = [c_vp, c_vp, c_i64, c_i32, c_i32, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp,
+                      c_i64, c_vp]
     lib.lp_philox4x32_10.restype = c_i32
     lib.lp_philox4x32_10.argtypes = [c_vp, c_vp, c_vp, c_i64, c_vp]
     lib.lp_status_string.restype = ctypes.c_char_p

@@ -655,6 +655,140 @@ def reorder_states(states, parents: torch.Tensor, start: torch.Tensor | None = N
 lp_reorder_states = reorder_states
 
 
+class QuantCache:
+    """Keys and values (or any number of parts up to 8) held in 8 or 4 bits.
+
+    ``codes`` uint8 [parts, slots, heads, dim * bits / 8] and ``params`` [parts, slots,
+    heads, groups] float32 (8 bits) or [parts, slots, heads, groups, 2] bfloat16 (4
+    bits); or with the slots on pages, [parts, pages, page_size, heads, ...].  Any
+    strides, as long as a head's codes and its params are contiguous: heads-first
+    storage is a permuted view.  ``QuantCache.allocate`` makes both.  A group is dim /
+    groups elements.  The tensors are held; both are states that ``StateReorder`` can
+    move."""
+
+    def __init__(self, codes: torch.Tensor, params: torch.Tensor, *, dim: int, bits: int = 8):
+        if bits not in (4, 8):
+            raise ValueError("bits must be 8 or 4")
+        if codes.dtype != torch.uint8:
+            raise TypeError("codes must be uint8")
+        if params.dtype != (torch.float32 if bits == 8 else torch.bfloat16):
+            raise TypeError("params must be float32 for 8 bits, bfloat16 for 4")
+        if not codes.is_cuda or params.device != codes.device:
+            raise ValueError("codes and params must be CUDA tensors on one device")
+        d = codes.dim()
+        if d not in (4, 5) or params.dim() != d + (bits == 4):
+            raise ValueError("codes must be [parts, slots, heads, bytes] or [parts, pages, "
+                             "page_size, heads, bytes], params alike")
+        if codes.shape[:-1] != params.shape[:d - 1] or (bits == 4 and params.size(-1) != 2):
+            raise ValueError("codes and params must agree in parts, slots and heads")
+        groups = params.size(d - 1)
+        dim = int(dim)
+        if dim < 1 or groups < 1 or dim % groups or (bits == 4 and dim // groups % 2) or \
+                codes.size(-1) * 8 != dim * bits:
+            raise ValueError(f"dim {dim} does not fit {codes.size(-1)} bytes of {bits}-bit codes "
+                             f"in {groups} groups")
+        want = (1,) if bits == 8 else (2, 1)
+        if (codes.size(-1) > 1 and codes.stride(-1) != 1) or any(
+                n > 1 and a != b
+                for n, a, b in zip(params.shape[d - 1:], params.stride()[d - 1:], want)):
+            raise ValueError("a head's codes and params must be contiguous")
+        if codes.size(0) > 8:
+            raise ValueError("a cache has 8 parts at most")
+        self.codes, self.params, self.dim, self.bits = codes, params, dim, bits
+        self.parts, self.heads, self.group = codes.size(0), codes.size(d - 2), dim // groups
+        self.page_size = codes.size(d - 3)
+        self.slots = self.page_size * (codes.size(1) if d == 5 else 1)
+        self.device = codes.device
+        self._parts = (_lib.CachePart * max(1, self.parts))()
+        e = params.element_size()
+        for i in range(self.parts):
+            p = self._parts[i]
+            p.codes, p.params = codes[i].data_ptr(), params[i].data_ptr()
+            p.code_page_stride = codes.stride(1) if d == 5 else 0
+            p.code_slot_stride, p.code_head_stride = codes.stride(d - 3), codes.stride(d - 2)
+            p.param_page_stride = params.stride(1) * e if d == 5 else 0
+            p.param_slot_stride = params.stride(d - 3) * e
+            p.param_head_stride = params.stride(d - 2) * e
+
+    @classmethod
+    def allocate(cls, slots: int, heads: int, dim: int, *, bits: int = 8,
+                 group: int | None = None, parts: int = 2, device=None) -> "QuantCache":
+        """A cache of ``slots`` slots, its memory zero.  ``group``: dim when None in 8
+        bits; in 4 bits 32 where that divides dim, else dim."""
+        if group is None:
+            group = 32 if bits == 4 and dim % 32 == 0 else dim
+        if bits not in (4, 8) or dim < 1 or group < 1 or dim % group or dim * bits % 8:
+            raise ValueError("bits must be 8 or 4, and group divide dim")
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        codes = torch.zeros(parts, slots, heads, dim * bits // 8, dtype=torch.uint8, device=dev)
+        shape = (parts, slots, heads, dim // group)
+        params = (torch.zeros(shape, device=dev) if bits == 8 else
+                  torch.zeros(*shape, 2, dtype=torch.bfloat16, device=dev))
+        return cls(codes, params, dim=dim, bits=bits)
+
+
+def _cache_call(name, cache: QuantCache, xs, slots: torch.Tensor):
+    if slots.dtype != torch.int64:
+        raise TypeError("slots must be int64")
+    if slots.dim() != 1 or not slots.is_contiguous() or slots.device != cache.device:
+        raise ValueError("slots must be contiguous, 1-D and on the cache's device")
+    n, dt = slots.size(0), None
+    if len(xs) != cache.parts:
+        raise ValueError(f"expected {cache.parts} tensors, one for each part, got {len(xs)}")
+    heads = (_lib.Heads * max(1, cache.parts))()
+    for i, x in enumerate(xs):
+        if dt is None:
+            dt = x.dtype
+        if x.dtype != dt:
+            raise TypeError("the parts' tensors must be of one type")
+        if x.device != cache.device:
+            raise ValueError("tensors must be on the cache's device")
+        if tuple(x.shape) != (n, cache.heads, cache.dim):
+            raise ValueError(f"tensors must be [{n}, {cache.heads}, {cache.dim}], "
+                             f"got {tuple(x.shape)}")
+        token, head, inner = x.stride()
+        if cache.dim > 1 and inner != 1:
+            raise ValueError("a head's elements must be contiguous")
+        h = heads[i]
+        h.data, h.token_stride, h.head_stride = x.data_ptr(), token, head
+    if dt is not None and dt not in _DT:
+        raise TypeError(f"tensors must be float32, float16 or bfloat16, not {dt}")
+    st = getattr(_lib.load(), name)(
+        cache._parts, heads, cache.parts, cache.bits, _DT[dt] if dt is not None else 0,
+        cache.slots, max(1, cache.page_size), cache.heads, cache.dim, cache.group,
+        slots.data_ptr(), n, torch.cuda.current_stream(cache.device).cuda_stream)
+    check(name, st)
+
+
+def cache_write(cache: QuantCache, x, slots: torch.Tensor) -> None:
+    """Quantise ``x`` (one [n, heads, dim] tensor for each part of the cache: keys and
+    values; or the tensor itself for a cache of one part) into the cache: token i goes
+    to slot ``slots[i]`` (int64), or nowhere when that is outside the cache."""
+    _cache_call("lp_cache_write", cache, (x,) if isinstance(x, torch.Tensor) else x, slots)
+
+
+lp_cache_write = cache_write
+
+
+def cache_read(cache: QuantCache, slots: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
+               out=None) -> tuple:
+    """The values that slots ``slots`` (int64 [n]) hold, one [n, heads, dim] tensor of
+    ``dtype`` for each part; zeros for a slot outside the cache.  ``out`` takes the
+    tensors to write instead (their type then counts, dim contiguous)."""
+    if out is None:
+        if slots.dim() != 1:
+            raise ValueError("slots must be contiguous, 1-D and on the cache's device")
+        out = torch.empty((cache.parts, slots.size(0), cache.heads, cache.dim), dtype=dtype,
+                          device=cache.device).unbind(0)
+    elif isinstance(out, torch.Tensor):
+        out = (out,)
+    _cache_call("lp_cache_read", cache, out, slots)
+    return tuple(out)
+
+
+lp_cache_read = cache_read
+
+
 def philox4x32_10(counters: torch.Tensor, keys: torch.Tensor) -> torch.Tensor:
     """Device Philox4x32-10 on n blocks: counters [n, 4], keys [n, 2] (int32 bit
     patterns on the GPU) -> [n, 4] words (int32 bit patterns)."""

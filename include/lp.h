@@ -16,6 +16,8 @@
  *   lp_beam_select           beam search: the best candidates over beams x vocabulary,
  *                            under the bitmask
  *   lp_reorder_states        beam search: states follow their beams, in place
+ *   lp_cache_write, lp_cache_read  keys and values quantised to 8 or 4 bits as they are
+ *                            written to a cache, and read back
  *
  * Common conventions
  *   - Logits are a row-major [B, cols] matrix of float32, float16 or bfloat16 with
@@ -402,6 +404,55 @@ typedef struct {
 lp_status lp_reorder_states(const lp_state* states, int64_t n_states, int64_t batch,
                             int64_t beams, const int32_t* parents, const int32_t* start,
                             const int32_t* stop, cudaStream_t stream);
+
+/*
+ * lp_cache_write, lp_cache_read -- a cache of keys and values held in 8 or 4 bits: what
+ * lp_reorder_states moves at each step of a beam search, at a half or a quarter of its
+ * 16-bit size.  The pages have no counterpart.
+ *
+ * A part (the keys; the values) holds, for each slot and head, dim codes in groups of
+ * `group` consecutive elements, and 4 bytes of scaling for each group.  Over a group's
+ * finite elements (|x| <= the largest bf16), in 32-bit arithmetic rounded to nearest:
+ *   bits 8  s = max(max|x| * (1/448), 2^-126), a float32;
+ *           code = e4m3(x * (1/s)), to nearest even, saturating; value = code * s
+ *   bits 4  s = bf16(max((hi/2 - lo/2) * (1/7.5), 2^-126)) and l = bf16(lo), in that order;
+ *           code = rint(min(max((x - l) * (1/s), 0), 15)), element 2i in a byte's low
+ *           half; value = l + code * s
+ * Infinities take the nearest code; NaN stays NaN in 8 bits and takes code 0 in 4.
+ *   parts       HOST array of n_parts <= 8; device pointers, strides in bytes.  Slot i
+ *               lies on page i / page_size at place i % page_size (one page: page_size =
+ *               n_slots).  params and its strides: multiples of 4 bytes
+ *   x, out      HOST array of n_parts: [n, heads, dim] of type dt, dim contiguous,
+ *               strides in elements
+ *   slots       device int64 [n]: token i's slot.  A slot outside [0, n_slots) (padding)
+ *               is not written, and reads as zeros.  Writing one slot twice in a call
+ *               leaves a mix of the two
+ * A read's values are rounded once to 32 bits and then to dt.  One kernel.
+ * Invalid: bits not 4 or 8, a negative size, page_size or group below 1, dim not a
+ * multiple of group, an odd group in 4 bits, more than 8 parts, NULL pointers with work
+ * to do, misaligned params or x.
+ */
+typedef struct {
+  void* codes;
+  void* params;
+  int64_t code_page_stride, code_slot_stride, code_head_stride;
+  int64_t param_page_stride, param_slot_stride, param_head_stride;
+} lp_cache_part;
+
+typedef struct {
+  void* data;
+  int64_t token_stride, head_stride;
+} lp_heads;
+
+lp_status lp_cache_write(const lp_cache_part* parts, const lp_heads* x, int64_t n_parts,
+                         int32_t bits, lp_dtype dt, int64_t n_slots, int64_t page_size,
+                         int64_t heads, int64_t dim, int64_t group, const int64_t* slots,
+                         int64_t n, cudaStream_t stream);
+
+lp_status lp_cache_read(const lp_cache_part* parts, const lp_heads* out, int64_t n_parts,
+                        int32_t bits, lp_dtype dt, int64_t n_slots, int64_t page_size,
+                        int64_t heads, int64_t dim, int64_t group, const int64_t* slots,
+                        int64_t n, cudaStream_t stream);
 
 /*
  * lp_philox4x32_10 -- diagnostic: the device's Philox4x32-10 (Salmon et al.,

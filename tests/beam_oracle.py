@@ -81,3 +81,58 @@ def reordered(rows, parents, start=None, stop=None):
             if 0 <= p < beams and lo < hi:
                 out[b * beams + k, lo:hi] = rows[b * beams + p, lo:hi]
     return out
+
+
+LARGEST, TINY = np.float32(3.3895313892515355e38), np.float32(2.0 ** -126)
+
+
+def to_bf16(x):
+    """float32 -> the nearest bf16, as float32 (finite values)."""
+    u = np.ascontiguousarray(x, np.float32).view(np.uint32).astype(np.uint64)
+    return ((u + 0x7fff + ((u >> 16) & 1)) & 0xffff0000).astype(np.uint32).view(np.float32)
+
+
+def e4m3_values():
+    """What the 256 codes stand for."""
+    c = np.arange(256)
+    e, m = (c >> 3) & 15, (c & 7).astype(np.float64)
+    v = np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10.0))
+    v[(c & 127) == 127] = np.nan
+    return np.where(c & 128, -v, v)
+
+
+def quantised(x, bits, group):
+    """x float32 [..., dim] -> (the value of each code before scaling, scale, low), the
+    definition's 32-bit steps; scale and low [..., groups]."""
+    x = np.asarray(x, np.float32).reshape(*x.shape[:-1], -1, group)
+    fine = np.abs(x) <= LARGEST
+    with np.errstate(all="ignore"):
+        if bits == 8:
+            scale = np.maximum(np.where(fine, np.abs(x), 0).max(-1) * np.float32(1 / 448), TINY)
+            y = x * (np.float32(1) / scale)[..., None]
+            grid = np.sort(e4m3_values()[:127])  # 0 .. 448
+            a = np.minimum(np.abs(y), np.float32(448)).astype(np.float64)
+            i = np.clip(np.searchsorted(grid, a), 1, 126)
+            lo, hi = grid[i - 1], grid[i]
+            up = (a - lo > hi - a) | ((a - lo == hi - a) & (i % 2 == 0))  # ties: an even code
+            code = np.copysign(np.where(up, hi, lo), y)
+            code[np.isnan(y)] = np.nan
+            return code, scale, np.zeros_like(scale)
+        lo = np.where(fine, x, np.inf).min(-1)
+        hi = np.where(fine, x, -np.inf).max(-1)
+        none = ~(lo <= hi)
+        lo, hi = np.where(none, 0, lo).astype(np.float32), np.where(none, 0, hi).astype(np.float32)
+        half = np.float32(0.5)
+        scale = to_bf16(np.maximum((hi * half - lo * half) * np.float32(1 / 7.5), TINY))
+        low = to_bf16(lo)
+        y = (x - low[..., None]) * (np.float32(1) / scale)[..., None]
+        code = np.rint(np.clip(y, 0, 15)).astype(np.float64)
+        code[np.isnan(y)] = 0
+        return code, scale, low
+
+
+def held_values(code, scale, low, bits):
+    """The float32 values that codes stand for, [..., dim]: rounded once."""
+    s, m = scale.astype(np.float64)[..., None], low.astype(np.float64)[..., None]
+    v = (code * s if bits == 8 else m + code * s).astype(np.float32)
+    return v.reshape(*v.shape[:-2], -1)

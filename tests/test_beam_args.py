@@ -186,3 +186,67 @@ def test_state_geometry():
         _geometry(base, 5, None)
     with pytest.raises(ValueError, match="three"):
         _geometry(torch.zeros(4, 3, 6, 3, 6, 3, 6, 3)[:, :2, :5, :2, :5, :2, :5, :2], 0, None)
+
+
+# ------------------------------------------------------------------------- cache
+
+
+@pytest.mark.parametrize("write", [True, False])
+@pytest.mark.parametrize("kw, want", [
+    (dict(dt=3), 2), (dict(bits=5), 1), (dict(bits=16), 1), (dict(n_parts=-1), 1),
+    (dict(n_parts=9), 1), (dict(n_slots=-1), 1), (dict(page=0), 1), (dict(heads=-1), 1),
+    (dict(dim=-1), 1), (dict(group=0), 1), (dict(group=48), 1), (dict(bits=4, dim=9, group=9), 1),
+    (dict(n=-1), 1), (dict(parts=None), 1), (dict(x=None), 1), (dict(slots=None), 1),
+    (dict(part=dict(codes=None)), 1), (dict(part=dict(params=None)), 1),
+    (dict(part=dict(params=0x10002)), 1), (dict(part=dict(param_slot_stride=6)), 1),
+    (dict(x_data=None), 1), (dict(x_data=0x10001), 1),
+    (dict(dim=1 << 40, group=1), 4), (dict(heads=1 << 40), 4),
+    (dict(heads=1 << 30, dim=1 << 30, group=1, n=1 << 10), 4),
+    (dict(n=0), 0), (dict(heads=0), 0), (dict(dim=0), 0), (dict(n_parts=0), 0)])
+def test_cache_refusals(lib, write, kw, want):
+    kw = dict(kw)
+    part = kw.pop("part", None)
+    a = dict(data=kw.pop("x_data")) if "x_data" in kw else None
+    p, h = _lib.CachePart(), _lib.Heads()
+    p.codes = p.params = h.data = 0x10000
+    for k, v in (part or {}).items():
+        setattr(p, k, v)
+    for k, v in (a or {}).items():
+        setattr(h, k, v)
+    args = dict(parts=ctypes.byref(p), x=ctypes.byref(h), n_parts=1, bits=8, dt=2, n_slots=16,
+                page=16, heads=2, dim=64, group=32, slots=FAKE, n=4, stream=None)
+    assert set(kw) <= set(args)
+    args.update(kw)
+    assert (lib.lp_cache_write if write else lib.lp_cache_read)(*args.values()) == want
+
+
+def test_cache_binding_refusals():
+    codes, params = torch.zeros(2, 4, 2, 64, dtype=torch.uint8), torch.zeros(2, 4, 2, 1)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.QuantCache(codes, params, dim=64)
+    with pytest.raises(ValueError, match="bits"):
+        ops.QuantCache(codes, params, dim=64, bits=2)
+    with pytest.raises(TypeError, match="uint8"):
+        ops.QuantCache(codes.char(), params, dim=64)
+    with pytest.raises(TypeError, match="bfloat16"):
+        ops.QuantCache(codes, params, dim=128, bits=4)
+    for kw in (dict(group=5), dict(bits=3), dict(bits=4, group=0)):
+        with pytest.raises(ValueError):
+            ops.QuantCache.allocate(4, 2, 64, device="cpu", **kw)
+
+
+def test_quantised_by_hand():
+    from beam_oracle import e4m3_values, held_values, quantised
+
+    v = e4m3_values()
+    assert v[0x7e] == 448 and v[1] == 2.0 ** -9 and v[0x38] == 1 and v[0xb8] == -1
+    x = np.array([448.0, -1.0, 17.0, 19.0, 0.0, 2.0 ** -10, np.inf, np.nan], np.float32)
+    code, scale, low = quantised(x, 8, 8)
+    assert scale.tolist() == [1.0]
+    # 17 and 19 lie half-way between neighbours: to the even ones; 2^-10 is half a step
+    assert code[0, :7].tolist() == [448, -1, 16, 20, 0, 0, 448] and np.isnan(code[0, 7])
+    x = np.array([-1.0, 14.0, 0.5, 1.5, -np.inf, np.nan], np.float32)
+    code, scale, low = quantised(x, 4, 6)
+    assert scale.tolist() == [1.0] and low.tolist() == [-1.0]
+    assert code[0].tolist() == [0, 15, 2, 2, 0, 0]
+    assert held_values(code, scale, low, 4).tolist() == [-1, 14, 1, 1, -1, -1]
