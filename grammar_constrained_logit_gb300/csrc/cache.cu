@@ -20,8 +20,25 @@ namespace {
 
 constexpr int kMaxParts = 8;
 constexpr int kThreads = 256;
+constexpr int kMaxVecs = 4;     // vectors a lane holds of one group
 constexpr float kLargest = 3.3895313892515355e38f;
 constexpr float kTiny = 1.1754943508222875e-38f;  // 2^-126
+
+// n / d for n < 2^31: with 2^(l-1) < d <= 2^l, m = ceil(2^(31+l) / d) is below 2^32 and
+// n m / 2^(31+l) exceeds n / d by less than n / 2^(31+l) < 1 / d.
+struct Div {
+  uint32_t d, m, shift;
+  void set(uint32_t by) {
+    d = by;
+    uint32_t l = 0;
+    while ((uint64_t(1) << l) < by) ++l;
+    shift = 31 + l;
+    m = uint32_t(((uint64_t(1) << shift) + by - 1) / by);
+  }
+  __device__ __forceinline__ uint32_t quot(uint32_t n) const {
+    return uint32_t((uint64_t(n) * m) >> shift);
+  }
+};
 
 struct CacheArgs {
   lp_cache_part part[kMaxParts];
@@ -29,6 +46,11 @@ struct CacheArgs {
   const int64_t* slots;
   int64_t n, n_slots, page;
   int heads, dim, group;
+  Div per_page;  // where slots are below 2^31
+  // of the vector kernels
+  Div per_token, per_head, per_group;  // groups (write) or units (read); units of a group (read)
+  uint32_t total;                      // groups or units of a part
+  int lanes, reach, segments;          // write: lanes a group, the power of two from there, groups a warp
 };
 
 template <int DT>
@@ -99,14 +121,31 @@ __device__ __forceinline__ Scale scale_of(Range r) {
 
 __device__ __forceinline__ uint32_t code4(float x, const Scale& s) {
   const float y = __fmul_rn(__fsub_rn(x, s.low), s.inv);
-  return __float2uint_rn(fminf(fmaxf(y, 0.0f), 15.0f));  // NaN: 0
+  // NaN: 0.  The sum with 2^23 rounds to an integer, ties to even
+  return __float_as_uint(__fadd_rn(fminf(fmaxf(y, 0.0f), 15.0f), 8388608.0f)) & 15u;
 }
 
 // Where a slot's head lies, from a part's base.
-__device__ __forceinline__ int64_t place(int64_t slot, int64_t page, int64_t page_stride,
+__device__ __forceinline__ int64_t place(const CacheArgs& a, int64_t slot, int64_t page_stride,
                                          int64_t slot_stride, int64_t head, int64_t head_stride) {
-  const int64_t p = slot / page;
-  return p * page_stride + (slot - p * page) * slot_stride + head * head_stride;
+  int64_t at = slot, pages = 0;
+  if (a.page < a.n_slots) {  // more than one page
+    const int64_t p = a.n_slots <= INT32_MAX ? int64_t(a.per_page.quot(uint32_t(slot)))
+                                             : slot / a.page;
+    at = slot - p * a.page;
+    pages = p * page_stride;
+  }
+  return pages + at * slot_stride + head * head_stride;
+}
+
+__device__ __forceinline__ int64_t code_place(const CacheArgs& a, const lp_cache_part& p,
+                                              int64_t slot, int head) {
+  return place(a, slot, p.code_page_stride, p.code_slot_stride, head, p.code_head_stride);
+}
+
+__device__ __forceinline__ int64_t param_place(const CacheArgs& a, const lp_cache_part& p,
+                                               int64_t slot, int head) {
+  return place(a, slot, p.param_page_stride, p.param_slot_stride, head, p.param_head_stride);
 }
 
 // One warp a group.
@@ -135,8 +174,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     }
     const Scale s = scale_of<BITS>(r);
     uint8_t* codes = static_cast<uint8_t*>(part.codes) +
-                     place(slot, a.page, part.code_page_stride, part.code_slot_stride, h,
-                           part.code_head_stride) + int64_t(g) * a.group * BITS / 8;
+                     code_place(a, part, slot, h) + int64_t(g) * a.group * BITS / 8;
     if (BITS == 8) {
       for (int e = lane; e < a.group; e += 32)
         codes[e] = uint8_t(e4m3_pair(__fmul_rn(load_float<DT>(x + e * Bt), s.inv), 0.0f));
@@ -147,8 +185,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     }
     if (lane == 0)
       *reinterpret_cast<uint32_t*>(static_cast<char*>(part.params) +
-                                   place(slot, a.page, part.param_page_stride,
-                                         part.param_slot_stride, h, part.param_head_stride) +
+                                   param_place(a, part, slot, h) +
                                    int64_t(g) * 4) = s.held;
   }
 }
@@ -171,12 +208,10 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
     float v[2] = {0.0f, 0.0f};
     if (slot >= 0 && slot < a.n_slots) {
       const uint32_t code = *(static_cast<const uint8_t*>(part.codes) +
-                              place(slot, a.page, part.code_page_stride, part.code_slot_stride, h,
-                                    part.code_head_stride) + c);
+                              code_place(a, part, slot, h) + c);
       const uint32_t held = *reinterpret_cast<const uint32_t*>(
           static_cast<const char*>(part.params) +
-          place(slot, a.page, part.param_page_stride, part.param_slot_stride, h,
-                part.param_head_stride) + int64_t(c * E / a.group) * 4);
+          param_place(a, part, slot, h) + int64_t(c * E / a.group) * 4);
       if (BITS == 8) {
         v[0] = __fmul_rn(e4m3_value(code), __uint_as_float(held));
       } else {
@@ -190,8 +225,392 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   }
 }
 
+// ---------------------------------------------------------------- vector kernels
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  return uint64_t(__float_as_uint(a)) | uint64_t(__float_as_uint(b)) << 32;
+}
+__device__ __forceinline__ float first(uint64_t v) { return __uint_as_float(uint32_t(v)); }
+__device__ __forceinline__ float second(uint64_t v) { return __uint_as_float(uint32_t(v >> 32)); }
+
+// Two 32-bit operations in one instruction, each rounded to nearest.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Packed maximum and minimum of 16-bit pairs; a NaN gives way to the other operand.
+template <int DT>
+__device__ __forceinline__ uint32_t max16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (DT == LP_BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t min16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (DT == LP_BF16) asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ uint64_t floats16(uint32_t w) {  // the two elements of a word
+  if (DT == LP_BF16) return uint64_t(w << 16) | uint64_t(w & 0xffff0000u) << 32;
+  return pack2(Elt<LP_F16>::half_bits_to_float(w & 0xffffu),
+               Elt<LP_F16>::half_bits_to_float(w >> 16));
+}
+
+// E consecutive elements of an input.  Sixteen are 32 bytes (16-bit types) or twice that,
+// and are loaded 32 bytes at once; eight, 16 bytes at once.
+template <int DT, int E>
+struct Vec {
+  static constexpr int kWords = E * Elt<DT>::kBytes / 4;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void load(const char* p) {
+    if (E == 16) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 8)
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]),
+                       "=r"(w[i + 5]), "=r"(w[i + 6]), "=r"(w[i + 7])
+                     : "l"(p + 4 * i));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p + 4 * i));
+        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ uint64_t pair(int i) const {  // elements 2i and 2i + 1
+    if (DT == LP_F32) return uint64_t(w[2 * i]) | uint64_t(w[2 * i + 1]) << 32;
+    return floats16<DT>(w[i]);
+  }
+  // The finite range, for 8 bits as (-most, most).  Minimum and maximum leave NaN out by
+  // themselves, an infinity shows in the result, and only then the elements are gone
+  // through one by one.
+  template <int BITS>
+  __device__ __forceinline__ Range range() const {
+    Range r;
+    if (DT == LP_F32) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const float x = __uint_as_float(w[i]);
+        if (BITS == 8) r.hi = fmaxf(r.hi, fabsf(x));
+        else r.lo = fminf(r.lo, x), r.hi = fmaxf(r.hi, x);
+      }
+    } else {
+      uint32_t hi = BITS == 8 ? w[0] & 0x7fff7fffu : w[0], lo = w[0];
+#pragma unroll
+      for (int i = 1; i < kWords; ++i) {
+        hi = max16<DT>(hi, BITS == 8 ? w[i] & 0x7fff7fffu : w[i]);
+        if (BITS == 4) lo = min16<DT>(lo, w[i]);
+      }
+      const uint64_t h = floats16<DT>(hi), l = floats16<DT>(lo);
+      r.hi = fmaxf(first(h), second(h));
+      r.lo = fminf(first(l), second(l));
+    }
+    if (BITS == 8) r.lo = -r.hi;
+    if (!(fmaxf(fabsf(r.lo), fabsf(r.hi)) <= kLargest)) {
+      r = Range();
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) r.add(first(pair(i))), r.add(second(pair(i)));
+      if (BITS == 8) r.hi = fmaxf(-r.lo, r.hi), r.lo = -r.hi;
+    }
+    return r;
+  }
+};
+
+// A group on `lanes` neighbouring lanes, R vectors a lane, as many groups side by side in
+// a warp as fit; U turns of that at once.
+template <int DT, int BITS, int E, int R, int U>
+__global__ void __launch_bounds__(kThreads)
+    cache_write_vec_kernel(const __grid_constant__ CacheArgs a) {
+  constexpr int Bt = Elt<DT>::kBytes;
+  const lp_cache_part& part = a.part[blockIdx.y];
+  const lp_heads& xs = a.x[blockIdx.y];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int seg = lane / a.lanes, at = lane - seg * a.lanes;
+  const int units = a.group / E;
+
+  Vec<DT, E> v[U][R];
+  int64_t slot[U];
+  uint32_t g[U];
+  int h[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t id = ((blockIdx.x * U + u) * (kThreads / 32) + warp) * a.segments + seg;
+    slot[u] = -1;
+    if (seg < a.segments && id < a.total) {
+      const uint32_t t = a.per_token.quot(id), rest = id - t * a.per_token.d;
+      h[u] = int(a.per_head.quot(rest));
+      g[u] = rest - uint32_t(h[u]) * a.per_head.d;
+      slot[u] = __ldg(a.slots + t);
+      const char* x = static_cast<const char*>(xs.data) +
+                      (int64_t(t) * xs.token_stride + h[u] * xs.head_stride) * Bt +
+                      int64_t(g[u]) * a.group * Bt;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (R == 1 || r * a.lanes + at < units) v[u][r].load(x + (r * a.lanes + at) * (E * Bt));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const bool live = slot[u] >= 0 && slot[u] < a.n_slots;
+    Range range;
+    if (live) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (R == 1 || r * a.lanes + at < units) {
+          const Range one = v[u][r].template range<BITS>();
+          range.lo = fminf(range.lo, one.lo);
+          range.hi = fmaxf(range.hi, one.hi);
+        }
+    }
+    for (int o = a.reach; o; o >>= 1) {
+      const float hi = __shfl_down_sync(kFullWarp, range.hi, o);
+      if (at + o < a.lanes) range.hi = fmaxf(range.hi, hi);
+      if (BITS == 4) {
+        const float lo = __shfl_down_sync(kFullWarp, range.lo, o);
+        if (at + o < a.lanes) range.lo = fminf(range.lo, lo);
+      }
+    }
+    if (a.lanes > 1) {
+      range.hi = __shfl_sync(kFullWarp, range.hi, lane - at);
+      if (BITS == 4) range.lo = __shfl_sync(kFullWarp, range.lo, lane - at);
+    }
+    if (BITS == 8) range.lo = -range.hi;
+    if (!live) continue;
+    const Scale s = scale_of<BITS>(range);
+    uint8_t* codes = static_cast<uint8_t*>(part.codes) + code_place(a, part, slot[u], h[u]) +
+                     int64_t(g[u]) * a.group * BITS / 8;
+    const uint64_t inv = pack2(s.inv, s.inv), off = pack2(-s.low, -s.low);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (R > 1 && r * a.lanes + at >= units) continue;
+      uint8_t* c = codes + (r * a.lanes + at) * (E * BITS / 8);
+      const Vec<DT, E>& x = v[u][r];
+      uint32_t w[E * BITS / 32];
+      if (BITS == 8) {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+          const uint64_t p = mul2(x.pair(2 * i), inv), q = mul2(x.pair(2 * i + 1), inv);
+          w[i] = e4m3_pair(first(p), second(p)) | e4m3_pair(first(q), second(q)) << 16;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E / 8; ++i) {
+          w[i] = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t y = mul2(add2(x.pair(4 * i + j), off), inv);
+            // NaN: 0.  The sum with 2^23 rounds to an integer, ties to even
+            const uint64_t z =
+                add2(pack2(fminf(fmaxf(first(y), 0.0f), 15.0f), fminf(fmaxf(second(y), 0.0f), 15.0f)),
+                     pack2(8388608.0f, 8388608.0f));
+            w[i] |= (uint32_t(z) & 15u) << (8 * j) | (uint32_t(z >> 32) & 15u) << (8 * j + 4);
+          }
+        }
+      }
+      constexpr int kOut = E * BITS / 32;
+      if (kOut == 4) *reinterpret_cast<uint4*>(c) = make_uint4(w[0], w[1], w[2], w[kOut - 1]);
+      else if (kOut == 2) *reinterpret_cast<uint2*>(c) = make_uint2(w[0], w[kOut - 1]);
+      else *reinterpret_cast<uint32_t*>(c) = w[0];
+    }
+    if (at == 0)
+      *reinterpret_cast<uint32_t*>(static_cast<char*>(part.params) +
+                                   param_place(a, part, slot[u], h[u]) + int64_t(g[u]) * 4) =
+          s.held;
+  }
+}
+
+// E elements a thread, U times at once.
+template <int DT, int BITS, int E, int U>
+__global__ void __launch_bounds__(kThreads)
+    cache_read_vec_kernel(const __grid_constant__ CacheArgs a) {
+  constexpr int Bt = Elt<DT>::kBytes, kIn = E * BITS / 32;
+  const lp_cache_part& part = a.part[blockIdx.y];
+  const lp_heads& xs = a.x[blockIdx.y];
+  uint32_t t[U], c[U];
+  int h[U];
+  int64_t slot[U];
+  uint32_t w[U][kIn], held[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t id = (blockIdx.x * U + u) * kThreads + threadIdx.x;
+    slot[u] = -1;
+    t[u] = id < a.total ? a.per_token.quot(id) : UINT32_MAX;
+    if (id < a.total) {
+      const uint32_t rest = id - t[u] * a.per_token.d;
+      h[u] = int(a.per_head.quot(rest));
+      c[u] = rest - uint32_t(h[u]) * a.per_head.d;
+      slot[u] = __ldg(a.slots + t[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (slot[u] < 0 || slot[u] >= a.n_slots) {
+      slot[u] = -1;
+      continue;
+    }
+    const uint8_t* p = static_cast<const uint8_t*>(part.codes) +
+                       code_place(a, part, slot[u], h[u]) + int64_t(c[u]) * (E * BITS / 8);
+    if (kIn == 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      w[u][0] = v.x, w[u][1] = v.y, w[u][kIn - 2] = v.z, w[u][kIn - 1] = v.w;
+    } else if (kIn == 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      w[u][0] = v.x, w[u][kIn - 1] = v.y;
+    } else {
+      w[u][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    }
+    held[u] = __ldg(reinterpret_cast<const uint32_t*>(
+        static_cast<const char*>(part.params) + param_place(a, part, slot[u], h[u]) +
+        int64_t(a.per_group.quot(c[u])) * 4));
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (t[u] == UINT32_MAX) continue;
+    uint64_t v[E / 2];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) v[i] = 0;
+    if (slot[u] >= 0) {
+      if (BITS == 8) {
+        const float s1 = __uint_as_float(held[u]);
+        const uint64_t s = pack2(s1, s1);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          uint32_t two;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+              : "=r"(two) : "h"(uint16_t(w[u][i / 2] >> (16 * (i & 1)))));
+          v[i] = mul2(floats16<LP_F16>(two), s);
+        }
+      } else {
+        const float s1 = __uint_as_float(held[u] << 16);
+        const float low1 = __uint_as_float(held[u] & 0xffff0000u);
+        const uint64_t s = pack2(s1, s1), low = pack2(low1, low1);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          // A code whose lowest bit is bit b of a word is the last place of a float of
+          // exponent 23 - b: with that float's leading bit it reads 2^(23-b) + code, and
+          // less 2^(23-b) it is the code, exactly.
+          constexpr uint32_t kOne = 127 + 23;
+          const uint32_t x = (i & 3) < 2 ? w[u][i / 4] : w[u][i / 4] >> 16;
+          const int b = 8 * (i & 1);
+          const uint32_t m0 = (kOne - b) << 23, m1 = (kOne - b - 4) << 23;
+          const uint64_t code =
+              add2(uint64_t((x & (15u << b)) | m0) | uint64_t((x & (15u << (b + 4))) | m1) << 32,
+                   pack2(-__uint_as_float(m0), -__uint_as_float(m1)));
+          v[i] = fma2(code, s, low);  // the product is exact: one rounding
+        }
+      }
+    }
+    char* x = static_cast<char*>(xs.data) +
+              (int64_t(t[u]) * xs.token_stride + h[u] * xs.head_stride + int64_t(c[u]) * E) * Bt;
+    constexpr int kOut = E * Bt / 4;
+    uint32_t o[kOut];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      if (DT == LP_F32) {
+        o[(2 * i) % kOut] = uint32_t(v[i]), o[(2 * i + 1) % kOut] = uint32_t(v[i] >> 32);
+      } else if (DT == LP_BF16) {
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(second(v[i])), "f"(first(v[i])));
+      } else {
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(second(v[i])), "f"(first(v[i])));
+      }
+    }
+    if (E == 16) {
+#pragma unroll
+      for (int i = 0; i < kOut; i += 8)
+        asm volatile("st.global.L1::no_allocate.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(o[i]),
+                     "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]),
+                     "r"(o[i + 6]), "r"(o[i + 7]), "l"(x + 4 * i)
+                     : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < kOut; i += 4)
+        __stcs(reinterpret_cast<uint4*>(x + 4 * i), make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+    }
+  }
+}
+
+// Whether vectors of E elements fit the groups, and are aligned wherever they are touched.
 template <int DT, int BITS>
-cudaError_t launch(const CacheArgs& a, bool write, int n_parts, cudaStream_t stream) {
+bool vectors_of(int E, const CacheArgs& a, int n_parts) {
+  if (a.dim % E || a.group % E) return false;
+  uint64_t x = 0, codes = 0;
+  for (int i = 0; i < n_parts; ++i) {
+    x |= reinterpret_cast<uintptr_t>(a.x[i].data) |
+         uint64_t(a.x[i].token_stride) * Elt<DT>::kBytes |
+         uint64_t(a.x[i].head_stride) * Elt<DT>::kBytes;
+    codes |= reinterpret_cast<uintptr_t>(a.part[i].codes) | uint64_t(a.part[i].code_page_stride) |
+             uint64_t(a.part[i].code_slot_stride) | uint64_t(a.part[i].code_head_stride);
+  }
+  return x % (E == 16 ? 32 : 16) == 0 && codes % (E * BITS / 8) == 0;
+}
+
+template <int DT, int BITS, int E, int R, int U>
+cudaError_t write_vec(const CacheArgs& a, int n_parts, cudaStream_t stream) {
+  const uint32_t per_block = uint32_t(kThreads / 32) * U * a.segments;
+  const dim3 grid((a.total + per_block - 1) / per_block, unsigned(n_parts));
+  cache_write_vec_kernel<DT, BITS, E, R, U><<<grid, kThreads, 0, stream>>>(a);
+  return cudaPeekAtLastError();
+}
+
+template <int DT, int BITS, int E, int U>
+cudaError_t read_vec(const CacheArgs& a, int n_parts, cudaStream_t stream) {
+  const dim3 grid((a.total + U * kThreads - 1) / (U * kThreads), unsigned(n_parts));
+  cache_read_vec_kernel<DT, BITS, E, U><<<grid, kThreads, 0, stream>>>(a);
+  return cudaPeekAtLastError();
+}
+
+// Fills in what the vector kernels go by; false where the sizes do not fit them.
+template <int E>
+bool plan_vec(CacheArgs& a, bool write, int* vecs) {
+  const int units = a.group / E;
+  const int64_t per_token = int64_t(a.heads) * (a.dim / (write ? a.group : E));
+  *vecs = (units + 31) / 32;
+  if ((write && *vecs > kMaxVecs) || per_token > INT32_MAX || a.n > INT32_MAX / per_token)
+    return false;
+  a.total = uint32_t(a.n * per_token);
+  a.per_token.set(uint32_t(per_token));
+  a.per_head.set(uint32_t(per_token / a.heads));
+  a.per_group.set(uint32_t(units));
+  a.lanes = (units + *vecs - 1) / *vecs;
+  a.segments = 32 / a.lanes;
+  a.reach = 1;
+  while (a.reach < a.lanes) a.reach *= 2;
+  a.reach /= 2;
+  return true;
+}
+
+template <int DT, int BITS>
+cudaError_t launch_piece(CacheArgs a, bool write, int n_parts, cudaStream_t stream) {
+  int r = 0;
+  if (vectors_of<DT, BITS>(16, a, n_parts) && plan_vec<16>(a, write, &r) && (!write || r <= 2)) {
+    if (!write) return read_vec<DT, BITS, 16, 2>(a, n_parts, stream);
+    if (r == 2) return write_vec<DT, BITS, 16, 2, 1>(a, n_parts, stream);
+    return write_vec<DT, BITS, 16, 1, 2>(a, n_parts, stream);
+  }
+  if (vectors_of<DT, BITS>(8, a, n_parts) && plan_vec<8>(a, write, &r)) {
+    if (!write) return read_vec<DT, BITS, 8, 2>(a, n_parts, stream);
+    if (r > 2) return write_vec<DT, BITS, 8, 4, 1>(a, n_parts, stream);
+    if (r == 2) return write_vec<DT, BITS, 8, 2, 1>(a, n_parts, stream);
+    return write_vec<DT, BITS, 8, 1, 2>(a, n_parts, stream);
+  }
   if (write) {
     const int64_t warps = a.n * a.heads * (a.dim / a.group);
     const dim3 grid(unsigned(std::min<int64_t>((warps + 7) / 8, 152 * 64)), unsigned(n_parts));
@@ -203,6 +622,30 @@ cudaError_t launch(const CacheArgs& a, bool write, int n_parts, cudaStream_t str
     cache_read_kernel<DT, BITS><<<grid, kThreads, 0, stream>>>(a);
   }
   return cudaPeekAtLastError();
+}
+
+template <int DT, int BITS>
+cudaError_t launch(const CacheArgs& a0, bool write, int n_parts, cudaStream_t stream) {
+  CacheArgs a = a0;
+  // heads that follow one another everywhere are one long head
+  bool flat = a.group <= a.dim && int64_t(a.heads) * a.dim <= INT32_MAX;
+  for (int i = 0; i < n_parts; ++i)
+    flat = flat && a.x[i].head_stride == a.dim &&
+           a.part[i].code_head_stride == int64_t(a.dim) * BITS / 8 &&
+           a.part[i].param_head_stride == int64_t(a.dim / a.group) * 4;
+  if (flat) a.dim *= a.heads, a.heads = 1;
+  // as many tokens a launch as 31-bit indices hold
+  const int64_t most = std::max<int64_t>(1, INT32_MAX / (int64_t(a.heads) * a.dim));
+  const int64_t n = a.n;
+  for (int64_t t = 0; t < n; t += most) {
+    a.n = std::min(most, n - t);
+    a.slots = a0.slots + t;
+    for (int i = 0; i < n_parts; ++i)
+      a.x[i].data = static_cast<char*>(a0.x[i].data) + t * a0.x[i].token_stride * Elt<DT>::kBytes;
+    const cudaError_t e = launch_piece<DT, BITS>(a, write, n_parts, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 lp_status run(const lp_cache_part* parts, const lp_heads* x, int64_t n_parts, int bits,
@@ -233,6 +676,7 @@ lp_status run(const lp_cache_part* parts, const lp_heads* x, int64_t n_parts, in
   a.n = n;
   a.n_slots = n_slots;
   a.page = page_size;
+  if (page_size < n_slots && n_slots <= INT32_MAX) a.per_page.set(uint32_t(page_size));
   a.heads = int(heads);
   a.dim = int(dim);
   a.group = int(group);
