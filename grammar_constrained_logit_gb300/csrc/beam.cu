@@ -25,10 +25,11 @@ namespace {
 
 constexpr int kStreamThreads = 256;
 constexpr int kVecs = 4;              // 16-byte groups a lane holds of a chunk
-constexpr int kFinishThreads = 512;
-constexpr int kFinishWarps = kFinishThreads / 32;
+constexpr int kGroups = 512;          // lanes' bests that the bound is taken from
 constexpr int kMaxSelect = 256;       // largest n_select and beams
-constexpr int kBuf = 2048;            // candidates held at once (a power of two)
+constexpr int kBuf = 1024;            // candidates held at once (a power of two)
+constexpr int kList = 2048;           // chunks gone through at once
+constexpr int64_t kMostStaged = 128 * 1024;  // bytes of chunks' maxima held in shared memory
 constexpr int kBufNew = kBuf - kMaxSelect;
 constexpr int kSms = 152;
 
@@ -46,6 +47,8 @@ struct BeamArgs {
   const uint8_t* finished;
   int64_t pad;
   int rows, beams, n, chunks;
+  int staged;      // a batch entry's chunks fit in shared memory
+  int sum_bits;    // S <= V is held in units of 2^-sum_bits, within 63 bits
   float2* part;  // [rows, chunks]: (max, sum of exp(x - max)); rows that are dead or finished: not written
   float* out_scores;
   int64_t* out_tokens;
@@ -53,21 +56,12 @@ struct BeamArgs {
 };
 
 struct Cand {
-  uint64_t key;   // order-preserving bits of the score in 64 bits
+  uint64_t key;   // order-preserving bits of the score
   uint64_t flat;  // beam * 2^31 + token
 };
 
 __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
   return a.key > b.key || (a.key == b.key && a.flat < b.flat);
-}
-
-__device__ __forceinline__ uint64_t dkey(double x) {
-  const uint64_t u = uint64_t(__double_as_longlong(x + 0.0));
-  return (u >> 63) ? ~u : (u | (1ull << 63));
-}
-
-__device__ __forceinline__ double key_double(uint64_t k) {
-  return __longlong_as_double((long long)((k >> 63) ? (k & ~(1ull << 63)) : ~k));
 }
 
 // Bytes sh .. sh+15 of the 32 bytes lo, hi.
@@ -128,23 +122,68 @@ __device__ __forceinline__ uint32_t group_keep(const uint32_t* __restrict__ bm, 
   return k;
 }
 
-// A chunk's groups of this lane, masked tokens as -inf.
-template <int DT>
+// A chunk's groups of this lane, masked tokens as -inf.  EARLY: the logits do not wait
+// for the mask's bits, which costs the bytes that these would have spared.
+template <int DT, bool EARLY>
 __device__ __forceinline__ void load_chunk(uint4 (&v)[kVecs], const char* row, const uint32_t* bm,
                                            int64_t j0, int64_t V, int lane) {
   constexpr int E = Elt<DT>::kPerVec;
+  constexpr uint32_t kAll = (1u << E) - 1u;
   const int sh = int(reinterpret_cast<uintptr_t>(row) & 15);
+  const uint32_t none = neg_inf_word<DT>();
+  if (j0 + kChunk<DT> + (sh ? E : 0) <= V && (sh == 0 || j0 > 0)) {
+    // within the row: nothing to check token by token
+    const char* p = row + (j0 + lane * E) * Elt<DT>::kBytes - sh;
+    auto load = [&](int i) {
+      const uint4* q = reinterpret_cast<const uint4*>(p) + i * 32;
+      return sh == 0 ? __ldg(q) : shifted(__ldg(q), __ldg(q + 1), sh);
+    };
+    if (bm == nullptr) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) v[i] = load(i);
+      return;
+    }
+    const uint8_t* mask = reinterpret_cast<const uint8_t*>(bm) + (j0 + lane * E) / 8;
+    uint32_t keep[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      keep[i] = __ldg(mask + i * (4 * E));
+      if (E == 4) keep[i] = (keep[i] >> (lane & 1) * 4) & kAll;
+    }
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      v[i] = make_uint4(none, none, none, none);
+      if (EARLY || keep[i]) v[i] = load(i);
+    }
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (keep[i] != kAll) v[i] = Elt<DT>::blend(v[i], keep[i], none);
+    return;
+  }
   uint32_t keep[kVecs];
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) keep[i] = group_keep<DT>(bm, j0 + (i * 32 + lane) * E, V);
-  const uint32_t none = neg_inf_word<DT>();
-#pragma unroll
   for (int i = 0; i < kVecs; ++i) {
+    const int64_t j = j0 + (i * 32 + lane) * E;
+    keep[i] = group_keep<DT>(bm, j, V);
     v[i] = make_uint4(none, none, none, none);
-    if (keep[i]) v[i] = load_group<DT>(row, j0 + (i * 32 + lane) * E, V, sh);
+    if (keep[i]) v[i] = load_group<DT>(row, j, V, sh);
   }
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) v[i] = Elt<DT>::blend(v[i], keep[i], none);
+  for (int i = 0; i < kVecs; ++i)
+    if (keep[i] != kAll) v[i] = Elt<DT>::blend(v[i], keep[i], none);
+}
+
+// Element `at` of a chunk's groups, a number known only at run time.
+template <int DT>
+__device__ __forceinline__ float element(const uint4 (&v)[kVecs], unsigned at) {
+  constexpr unsigned E = Elt<DT>::kPerVec;
+  const unsigned g = at / E, e = at % E;
+  const uint4 lo = g & 1 ? v[1] : v[0], hi = g & 1 ? v[3] : v[2];
+  const uint4 w = g & 2 ? hi : lo;
+  if (DT == LP_F32) return __uint_as_float(e & 2 ? (e & 1 ? w.w : w.z) : (e & 1 ? w.y : w.x));
+  const uint32_t pair = e & 4 ? (e & 2 ? w.w : w.z) : (e & 2 ? w.y : w.x);
+  const uint32_t half = e & 1 ? pair >> 16 : pair & 0xffffu;
+  return DT == LP_BF16 ? __uint_as_float(half << 16) : Elt<LP_F16>::half_bits_to_float(half);
 }
 
 __device__ __forceinline__ bool row_live(const BeamArgs& a, int row) {
@@ -157,7 +196,84 @@ __device__ __forceinline__ const uint32_t* row_mask(const BeamArgs& a, int row) 
   return a.bitmask + int64_t(row) * a.bm_stride;
 }
 
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  return uint64_t(__float_as_uint(a)) | uint64_t(__float_as_uint(b)) << 32;
+}
+__device__ __forceinline__ float low_of(uint64_t v) { return __uint_as_float(uint32_t(v)); }
+__device__ __forceinline__ float high_of(uint64_t v) { return __uint_as_float(uint32_t(v >> 32)); }
+
+constexpr float kLog2e = 1.44269504f;
+
+// The differences x - m of two neighbouring tokens, rounded once from the 16-bit value:
+// the mixed-type addition needs no conversion, whose unit the exponentials want.
 template <int DT>
+__device__ __forceinline__ uint64_t differences(const uint4& v, int e, float m) {
+  if (DT == LP_F32) return add2(pack2(Elt<DT>::get(v, e), Elt<DT>::get(v, e + 1)), pack2(-m, -m));
+  const uint32_t w = word_of(v, e >> 1);
+  const uint16_t a = uint16_t(w), b = uint16_t(w >> 16);
+  float x, y;
+  if (DT == LP_BF16) {
+    asm("add.rn.f32.bf16 %0, %1, %2;" : "=f"(x) : "h"(a), "f"(-m));
+    asm("add.rn.f32.bf16 %0, %1, %2;" : "=f"(y) : "h"(b), "f"(-m));
+  } else {
+    asm("add.rn.f32.f16 %0, %1, %2;" : "=f"(x) : "h"(a), "f"(-m));
+    asm("add.rn.f32.f16 %0, %1, %2;" : "=f"(y) : "h"(b), "f"(-m));
+  }
+  return pack2(x, y);
+}
+
+// Sum over a lane's tokens of exp(x - m).  The difference comes first: it is exact near
+// the maximum, where the sum comes from, however far from zero the logits are.  -inf
+// gives 2^-inf = 0; a NaN, or m infinite, gives NaN, and the caller sums again with care.
+template <int DT>
+__device__ __forceinline__ float sum_exp(const uint4 (&v)[kVecs], float m) {
+  const uint64_t scale = pack2(kLog2e, kLog2e);
+  uint64_t s[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+#pragma unroll
+    for (int e = 0; e < Elt<DT>::kPerVec; e += 2) {
+      const uint64_t t = mul2(differences<DT>(v[i], e, m), scale);
+      s[i & 1] = add2(s[i & 1], pack2(ex2(low_of(t)), ex2(high_of(t))));
+    }
+  }
+  const uint64_t both = add2(s[0], s[1]);
+  return low_of(both) + high_of(both);
+}
+
+// The same where there is a NaN, which is no candidate, or a maximum of +inf, whose
+// tokens share all of the mass.
+template <int DT>
+__device__ __forceinline__ float sum_exp_careful(const uint4 (&v)[kVecs], float m) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+    for (int e = 0; e < Elt<DT>::kPerVec; ++e) {
+      const float x = Elt<DT>::get(v[i], e);
+      if (x == m) s += 1.0f;
+      else if (x > -INFINITY && m < INFINITY) s += ex2((x - m) * kLog2e);
+    }
+  return s;
+}
+
+__device__ __forceinline__ float warp_max(float m) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, o));
+  return m;
+}
+
+template <int DT, bool EARLY>
 __global__ void __launch_bounds__(kStreamThreads) beam_stream_kernel(BeamArgs a) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -167,45 +283,39 @@ __global__ void __launch_bounds__(kStreamThreads) beam_stream_kernel(BeamArgs a)
   for (unsigned w = blockIdx.x * (kStreamThreads / 32) + (threadIdx.x >> 5); w < total;
        w += step) {
     const int row = int(w / unsigned(a.chunks)), c = int(w % unsigned(a.chunks));
-    if (!row_live(a, row)) continue;
+    const bool live = row_live(a, row);
+    if (!EARLY && !live) continue;
     uint4 v[kVecs];
-    load_chunk<DT>(v, a.logits + row * a.stride, row_mask(a, row), int64_t(c) * kChunk<DT>, a.V,
-                   lane);
+    load_chunk<DT, EARLY>(v, a.logits + row * a.stride, row_mask(a, row),
+                          int64_t(c) * kChunk<DT>, a.V, lane);
+    if (!live) continue;
     float m = VecMax<DT>::run(v[0], 0xffu);
 #pragma unroll
     for (int i = 1; i < kVecs; ++i) m = fmaxf(m, VecMax<DT>::run(v[i], 0xffu));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, o));
-    m = fmaxf(m, -INFINITY);  // nothing but NaN: no candidate
-    float s[kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      s[i] = 0.0f;
-#pragma unroll
-      for (int e = 0; e < Elt<DT>::kPerVec; ++e) {
-        // the difference first: exact near the maximum, where the sum comes from; the
-        // maximum with -200 turns masked tokens and NaN into 2^-200, which is 0
-        const float x = Elt<DT>::get(v[i], e);
-        const float t = fmaxf((x - m) * 1.44269504f, -200.0f);
-        s[i] += m < INFINITY ? ex2(t) : float(x == m);  // +inf tokens share all of the mass
-      }
-    }
-    float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    m = fmaxf(warp_max(m), -INFINITY);  // nothing but NaN: no candidate
+    float sum = sum_exp<DT>(v, m);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
-    if (lane == 0) a.part[w] = make_float2(m, m > -INFINITY ? sum : 0.0f);
+    if (!(sum < INFINITY)) {
+      sum = 0.0f;
+      if (m > -INFINITY) sum = sum_exp_careful<DT>(v, m);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
+    }
+    if (lane == 0) a.part[w] = make_float2(m, sum);
   }
 }
 
 // Sorts m candidates at c (best first); c has room for the next power of two.
+template <int NT>
 __device__ void sort_best_first(Cand* c, int m) {
   int p = 2;
   while (p < m) p <<= 1;
-  for (int i = m + threadIdx.x; i < p; i += kFinishThreads) c[i] = Cand{0, ~0ull};
+  for (int i = m + threadIdx.x; i < p; i += NT) c[i] = Cand{0, ~0ull};
   __syncthreads();
   for (int k = 2; k <= p; k <<= 1) {
     for (int j = k >> 1; j; j >>= 1) {
-      for (int t = threadIdx.x; t < p / 2; t += kFinishThreads) {
+      for (int t = threadIdx.x; t < p / 2; t += NT) {
         const int lo = 2 * t - (t & (j - 1)), hi = lo + j;
         const Cand x = c[lo], y = c[hi];
         if (better(y, x) == ((lo & k) == 0)) c[lo] = y, c[hi] = x;
@@ -215,231 +325,466 @@ __device__ void sort_best_first(Cand* c, int m) {
   }
 }
 
+// A value held as two floats: hi is the value rounded, lo what that left.  Scores are
+// summed in this form: 64-bit arithmetic is 1/64 of the 32-bit rate here, and
+// the few dozen operations a batch entry needs took 1000 cycles in it.
+struct Two {
+  float hi, lo;
+};
+
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return Two{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+
+__device__ __forceinline__ uint64_t key_of(Two v) {
+  if (!(fabsf(v.hi) < INFINITY)) v.lo = 0.0f;
+  // as 64-bit arithmetic rounds it: lo to a multiple of 2^-52 of hi's leading bit, which
+  // a lo of 2^-29 of that and more is already
+  const uint32_t e = __float_as_uint(v.hi) & 0x7f800000u;
+  if (e > (29u << 23)) {
+    const float b = __uint_as_float(e - (29u << 23));
+    if (fabsf(v.lo) < b) v.lo = __fsub_rn(__fadd_rn(v.lo, 1.5f * b), 1.5f * b);
+  }
+  return uint64_t(fkey(v.hi)) << 32 | fkey(v.lo);
+}
+
+__device__ __forceinline__ float key_score(uint64_t k) { return key_float(uint32_t(k >> 32)); }
+
+constexpr uint64_t kNoScore = 0x007fffffull << 32 | 0xffffffffull;  // keys of -inf: none above
+
+// log of a whole number of units, to 2^-38: the number's leading 7 bits choose
+// c near 1/m, a 10-bit number whose logarithm is tabled (the table-driven scheme of
+// Tang, ACM TOMS 16(4), 1990); t = m c - 1 is below 2^-7 and its series is short.
+struct LogEntry {
+  float c, hi, lo;  // -log c = hi + lo
+};
+struct LogTable {
+  LogEntry at[128];
+};
+
+constexpr double series_log(double x) {  // 2 artanh((x - 1) / (x + 1)), x in [1/2, 1]
+  const double u = (x - 1.0) / (x + 1.0), uu = u * u;
+  double term = u, sum = 0.0;
+  for (int k = 1; k < 80; k += 2) {
+    sum += term / k;
+    term *= uu;
+  }
+  return 2.0 * sum;
+}
+
+constexpr LogTable make_log_table() {
+  LogTable t{};
+  for (int i = 0; i < 128; ++i) {
+    const double c = double(int(1024.0 / (1.0 + (i + 0.5) / 128.0) + 0.5)) / 1024.0;
+    const double v = -series_log(c);
+    t.at[i].c = float(c);
+    t.at[i].hi = float(v);
+    t.at[i].lo = float(v - double(float(v)));
+  }
+  return t;
+}
+
+__device__ const LogTable kLogTable = make_log_table();
+
+// log(S / 2^bits), S > 0
+__device__ __forceinline__ Two log_units(unsigned long long S, int bits, const LogEntry* table) {
+  const int lz = __clzll(S);
+  const unsigned long long f = S << lz;  // m = f / 2^63 in [1, 2)
+  const LogEntry q = table[unsigned(f >> 56) & 127u];
+  const float mh = float(unsigned(f >> 40)) * 0x1p-23f;
+  const float ml = float(unsigned(f >> 16) & 0xffffffu) * 0x1p-47f;
+  const float p = __fmul_rn(mh, q.c);
+  const float th = __fsub_rn(p, 1.0f);  // exact: p is near 1
+  const Two t = two_sum(th, __fmaf_rn(ml, q.c, __fmaf_rn(mh, q.c, -p)));
+  // t - t^2/2 + t^3 (1/3 - t/4 + t^2/5 - t^3/6)
+  const float sq = __fmul_rn(t.hi, t.hi);
+  const float sq_lo = __fmaf_rn(2.0f * t.hi, t.lo, __fmaf_rn(t.hi, t.hi, -sq));
+  const float rest = t.hi * sq *
+      __fmaf_rn(t.hi, __fmaf_rn(t.hi, __fmaf_rn(t.hi, -1.0f / 6, 0.2f), -0.25f), 1.0f / 3);
+  const float e = float(63 - lz - bits);
+  // log 2 = 0x1.62e4p-1 (15 bits, so e times it is exact) + 0x1.7f7d1cp-20
+  Two r = two_sum(e * 0x1.62e4p-1f, q.hi);
+  float lo = __fadd_rn(r.lo, __fmaf_rn(e, 0x1.7f7d1cp-20f, q.lo));
+  r = two_sum(r.hi, t.hi);
+  lo = __fadd_rn(lo, __fadd_rn(r.lo, t.lo));
+  r = two_sum(r.hi, -0.5f * sq);
+  lo = __fadd_rn(lo, __fadd_rn(r.lo, __fmaf_rn(-0.5f, sq_lo, rest)));
+  return two_sum(r.hi, lo);
+}
+
 struct FinishSmem {
   Cand buf[kBuf];             // what is new; the best so far joins behind it to be sorted
   Cand front[kMaxSelect];     // the best so far, sorted
-  double base_s[kMaxSelect];  // score, log S, max of each beam
-  double log_s[kMaxSelect];
-  float top[kMaxSelect];      // -inf: a beam without candidates
-  float least[kMaxSelect];    // tokens below this logit are out
+  Two log_s[kMaxSelect];      // log S
+  float score[kMaxSelect];
+  float top[kMaxSelect];      // M; -inf: a beam without candidates
   uint8_t ended[kMaxSelect];  // finished: one candidate, its own score
-  unsigned list[kFinishThreads];
-  int list_n, count, front_n;
-  Cand bound;                 // candidates worse than this are out
+  uint8_t masked[kMaxSelect];
+  unsigned best[kGroups];
+  LogEntry log_table[128];
+  unsigned list[kList];
+  int list_n, next, count, front_n, exact;
+  float T;
+  Cand bound;                 // exact: candidates worse than this are out
 };
 
-// Smallest float logit of a beam that can still reach the bound.  The slack covers the
-// rounding of the scores' own 64-bit arithmetic.
-__device__ void set_least(FinishSmem& sm, int beams) {
-  const double T = key_double(sm.bound.key);
-  for (int k = threadIdx.x; k < beams; k += kFinishThreads) {
-    const double s = sm.base_s[k], M = sm.top[k], z = sm.log_s[k];
-    float x = -INFINITY;
-    if (T > -INFINITY && s < INFINITY && M < INFINITY) {
-      const double at = ((T - s) + z) + M;
-      const double slack = 0x1p-48 * (fabs(T) + fabs(s) + fabs(z) + fabs(M));
-      x = __double2float_rd(at - slack);
-    }
-    sm.least[k] = x;
-  }
+// s + ((x - M) - log S)
+__device__ __forceinline__ Two score_of(const FinishSmem& sm, int k, float x) {
+  const float M = sm.top[k];
+  if (!(M < INFINITY) && x != M) return Two{-INFINITY, 0.0f};  // +inf tokens share all
+  const Two z = sm.log_s[k];
+  Two d{0.0f, 0.0f};
+  if (x != M) d = two_sum(x, -M);
+  if (!(d.hi > -INFINITY)) return Two{-INFINITY, 0.0f};  // out of the 32-bit range
+  Two e = two_sum(d.hi, -z.hi);
+  e = two_sum(e.hi, __fadd_rn(e.lo, __fsub_rn(d.lo, z.lo)));
+  Two f = two_sum(sm.score[k], e.hi);
+  if (!(fabsf(f.hi) < INFINITY)) return Two{f.hi, 0.0f};
+  return two_sum(f.hi, __fadd_rn(f.lo, e.lo));
+}
+
+// A logit of beam k below this cannot reach a score of T: 32-bit arithmetic, taken low by
+// more than its rounding.
+__device__ __forceinline__ float least_of(const FinishSmem& sm, int k, float T) {
+  const float s = sm.score[k], M = sm.top[k], z = sm.log_s[k].hi;
+  if (!(T > -INFINITY && s < INFINITY && M < INFINITY)) return -INFINITY;
+  const float slack = 0x1p-20f * (fabsf(T) + fabsf(s) + fabsf(z) + fabsf(M)) + 0x1p-20f;
+  const float x = (((T - s) + z) + M) - slack;
+  return x < INFINITY ? x : -INFINITY;  // out of the 32-bit range: no bound
 }
 
 // Joins the first m new candidates with the best so far and makes the n-th best the
 // bound.  keep: the n best become the best so far; else only the bound is taken.
-__device__ void join(FinishSmem& sm, int m, int n, int beams, bool keep) {
+template <int NT>
+__device__ __noinline__ void join(FinishSmem& sm, int m, int n, bool keep) {
   __syncthreads();
   const int front_n = sm.front_n;
-  for (int t = threadIdx.x; t < front_n; t += kFinishThreads) sm.buf[m + t] = sm.front[t];
+  for (int t = threadIdx.x; t < front_n; t += NT) sm.buf[m + t] = sm.front[t];
   __syncthreads();
-  sort_best_first(sm.buf, m + front_n);
+  sort_best_first<NT>(sm.buf, m + front_n);
   const int have = min(m + front_n, n);
   if (keep)
-    for (int t = threadIdx.x; t < have; t += kFinishThreads) sm.front[t] = sm.buf[t];
+    for (int t = threadIdx.x; t < have; t += NT) sm.front[t] = sm.buf[t];
   if (threadIdx.x == 0) {
-    if (have == n) sm.bound = sm.buf[n - 1];
+    if (have == n) sm.bound = sm.buf[n - 1], sm.exact = 1, sm.T = key_score(sm.bound.key);
     if (keep) sm.front_n = have;
     sm.count = 0;
   }
   __syncthreads();
-  set_least(sm, beams);
-  __syncthreads();
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kFinishThreads) beam_finish_kernel(BeamArgs a) {
+// A lower bound of the score that a beam's chunk of maximum m holds.
+__device__ __forceinline__ unsigned low_key(float s, float M, float z, float m) {
+  const float d = m == M ? 0.0f : m - M;
+  const float low = (s + (d - z)) - (0x1p-20f * (fabsf(s) + fabsf(d) + fabsf(z)) + 0x1p-20f);
+  return fkey(low > -INFINITY ? low : s == INFINITY ? s : -INFINITY);
+}
+
+// One beam, by one warp: M and S from its chunks, the chunks' maxima staged.  Returns the
+// lower bound of this lane's best chunk.
+__device__ __forceinline__ unsigned beam_sums(FinishSmem& sm, const BeamArgs& a, int row0, int k,
+                                              float* staged) {
+  constexpr int kHeld = 8;  // chunks a lane keeps in registers; a longer row is read again
+  const int lane = threadIdx.x & 31, C = a.chunks, row = row0 + k;
+  const float2* p = a.part + int64_t(row) * C;
+  // all of these are on their way at once; chunks of a dead row are garbage, not used
+  float2 q[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    q[i] = lane + 32 * i < C ? p[lane + 32 * i] : make_float2(-INFINITY, 0.0f);
+  const float s = __ldg(a.scores + row);
+  const uint8_t fin = a.finished != nullptr ? __ldg(a.finished + row) : 0;
+  const uint8_t need = a.needs != nullptr ? __ldg(a.needs + row) : 1;
+  const bool alive = s > -INFINITY, ended = alive && fin != 0;
+  float M = -INFINITY, mine = -INFINITY;
+  Two z{0.0f, 0.0f};
+  if (alive && !ended) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (staged && lane + 32 * i < C) staged[lane + 32 * i] = q[i].x;
+      mine = fmaxf(mine, q[i].x);
+    }
+    for (int c = lane + 32 * kHeld; c < C; c += 32) {
+      const float m = p[c].x;
+      if (staged) staged[c] = m;
+      mine = fmaxf(mine, m);
+    }
+    M = key_float(__reduce_max_sync(kFullWarp, fkey(mine)));
+    // whole multiples of a unit: their sum is exact, whatever its order.  S is at least 1
+    // and the unit 2^-40 (vocabularies up to 2^23), so what a term loses does not count
+    const float unit = __uint_as_float(unsigned(127 + a.sum_bits) << 23);
+    unsigned long long S = 0;
+    auto term = [&](float2 v) {
+      if (v.x > -INFINITY) S += __float2ull_rn((v.x == M ? v.y : v.y * expf(v.x - M)) * unit);
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (32 * i < C) term(q[i]);
+    for (int c = lane + 32 * kHeld; c < C; c += 32) term(p[c]);
+    // 64-bit lanes in limbs of 22 bits: 32 of them stay within 32 bits
+    const unsigned l0 = __reduce_add_sync(kFullWarp, unsigned(S) & 0x3fffffu);
+    const unsigned l1 = __reduce_add_sync(kFullWarp, unsigned(S >> 22) & 0x3fffffu);
+    const unsigned l2 = __reduce_add_sync(kFullWarp, unsigned(S >> 44));
+    S = l0 + ((unsigned long long)l1 << 22) + ((unsigned long long)l2 << 44);
+    if (M > -INFINITY) z = log_units(S, a.sum_bits, sm.log_table);
+  }
+  if (lane == 0) {
+    sm.score[k] = alive ? s : -INFINITY;
+    sm.ended[k] = ended;
+    sm.masked[k] = a.bitmask != nullptr && need != 0;
+    sm.top[k] = ended ? 0.0f : M;
+    sm.log_s[k] = z;
+  }
+  if (ended) return lane == 0 ? fkey(s) : 0;
+  return mine > -INFINITY ? low_key(s, M, z.hi, mine) : 0;
+}
+
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
+  constexpr int NW = NT / 32;
   extern __shared__ __align__(16) char raw[];
   FinishSmem& sm = *reinterpret_cast<FinishSmem*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x, row0 = b * a.beams, C = a.chunks;
+  float* staged = a.staged ? reinterpret_cast<float*>(raw + sizeof(FinishSmem)) : nullptr;
+  if (tid == 0) sm.count = 0, sm.front_n = 0, sm.list_n = 0, sm.next = 0, sm.exact = 0;
+  for (int i = tid; i < 128; i += NT) sm.log_table[i] = kLogTable.at[i];
+  __syncthreads();
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-  // M and log S of each beam
-  for (int k = warp; k < a.beams; k += kFinishWarps) {
-    const int row = row0 + k;
-    const float s = __ldg(a.scores + row);
-    const bool alive = s > -INFINITY;
-    const bool ended = alive && a.finished != nullptr && __ldg(a.finished + row) != 0;
-    float M = -INFINITY;
-    double z = 0.0;
-    if (alive && !ended) {
-      const float2* p = a.part + int64_t(row) * C;
-      for (int c = lane; c < C; c += 32) M = fmaxf(M, p[c].x);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullWarp, M, o));
-      double S = 0.0;
-      for (int c = lane; c < C; c += 32) {
-        const float2 q = p[c];
-        if (q.x > -INFINITY) S += double(q.x == M ? q.y : q.y * expf(q.x - M));
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(kFullWarp, S, o);
-      z = M > -INFINITY ? log(S) : 0.0;
-    }
-    if (lane == 0) {
-      sm.base_s[k] = double(s);
-      sm.log_s[k] = z;
-      sm.top[k] = ended ? 0.0f : M;
-      sm.ended[k] = ended;
-    }
-  }
-  if (tid == 0) sm.count = 0, sm.front_n = 0, sm.list_n = 0;
-  __syncthreads();
-
-  // A lower bound of the n-th best score: the n-th largest of the threads' best chunks.
-  // Each is a candidate of its own, taken low by the rounding of its 32-bit arithmetic.
-  const unsigned total = unsigned(a.beams) * unsigned(C);
   unsigned best = 0;
-  for (unsigned i = tid; i < total; i += kFinishThreads) {
-    const int k = int(i / unsigned(C)), c = int(i % unsigned(C));
-    const float M = sm.top[k];
-    if (M == -INFINITY) continue;
-    const float s = float(sm.base_s[k]), z = float(sm.log_s[k]);
-    float low;
-    if (sm.ended[k]) {
-      if (c) continue;
-      low = s;
-    } else {
-      const float m = a.part[int64_t(row0 + k) * C + c].x;
-      if (m == -INFINITY) continue;
-      const float d = m == M ? 0.0f : m - M;
-      low = (s + (d - z)) - 0x1p-20f * (fabsf(s) + fabsf(d) + fabsf(z));
-      if (!(low > -INFINITY)) low = s == INFINITY ? s : -INFINITY;
+  for (int k = warp; k < a.beams; k += NW)
+    best = max(best, beam_sums(sm, a, row0, k, staged ? staged + k * C : nullptr));
+
+  // From here a turn takes 32 chunks a warp: of as many beams as there are warps, or of
+  // fewer beams with several warps to each.
+  auto chunk_max = [&](int k, int c) {
+    return staged ? staged[k * C + c] : a.part[int64_t(row0 + k) * C + c].x;
+  };
+  const int per_turn = min(a.beams, NW), share = NW / per_turn;
+  const int my_beam = warp % per_turn, my_share = warp / per_turn;
+  const int c_first = my_share < share ? my_share * 32 + lane : INT32_MAX, c_step = share * 32;
+
+  // A lower bound T of the n-th best score: the n-th largest of these lanes' bests, each a
+  // candidate of its own.  With few lanes to the n, of one chunk a thread instead.
+  const bool few = 32 * per_turn < 4 * a.n;
+  if (few) {
+    __syncthreads();
+    best = 0;
+    for (int k = my_beam; k < a.beams; k += per_turn) {
+      const float M = sm.top[k], s = sm.score[k], z = sm.log_s[k].hi;
+      if (M == -INFINITY) continue;
+      if (sm.ended[k]) {
+        if (c_first == 0) best = max(best, fkey(s));
+        continue;
+      }
+      float mine = -INFINITY;
+      for (int c = c_first; c < C; c += c_step) mine = fmaxf(mine, chunk_max(k, c));
+      if (mine > -INFINITY) best = max(best, low_key(s, M, z, mine));
     }
-    best = max(best, fkey(low));
   }
-  unsigned T = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const int there = __syncthreads_count(best >= (T | (1u << bit)));
-    if (there >= a.n) T |= 1u << bit;
-    if (there == a.n) break;
+  if (NT > kGroups) {
+    best = max(best, __shfl_xor_sync(kFullWarp, best, 16));
+    if (lane < 16) sm.best[warp * 16 + lane] = best;
+  } else {
+    sm.best[tid] = best;
   }
-  if (tid == 0) sm.bound = Cand{T ? dkey(double(key_float(T))) : 0, ~0ull};
   __syncthreads();
-  if (T == 0 && tid == 0) sm.bound.key = dkey(-INFINITY);
-  __syncthreads();
-  set_least(sm, a.beams);
+  if (warp == 0) {
+    // two bits at a time, the upper 16: a bound need not be tight to the last place
+    constexpr int kMine = (NT > kGroups ? kGroups : NT) / 32;
+    unsigned mine[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) mine[i] = sm.best[i * 32 + lane];
+    unsigned T = 0;
+#pragma unroll 1
+    for (int sh = 30; sh >= 16; sh -= 2) {
+      unsigned there[4] = {0, 0, 0, 0};  // three counts of up to 512, ten bits each
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        there[i & 3] += mine[i] >= (T | 1u << sh) ? 1u : 0u;
+        there[i & 3] += mine[i] >= (T | 2u << sh) ? 1u << 10 : 0u;
+        there[i & 3] += mine[i] >= (T | 3u << sh) ? 1u << 20 : 0u;
+      }
+      const unsigned all =
+          __reduce_add_sync(kFullWarp, (there[0] + there[1]) + (there[2] + there[3]));
+      const int c1 = all & 1023u, c2 = all >> 10 & 1023u, c3 = all >> 20;
+      const int q = c3 >= a.n ? 3 : c2 >= a.n ? 2 : c1 >= a.n ? 1 : 0;
+      T |= unsigned(q) << sh;
+      if ((q == 3 ? c3 : q == 2 ? c2 : q == 1 ? c1 : 0) == a.n) break;
+    }
+    // (keys up to 0x007fffff are those of -inf and of what lies below it)
+    if (lane == 0) sm.T = T > 0x007fffffu ? key_float(T) : -INFINITY;
+  }
   __syncthreads();
 
-  for (unsigned i0 = 0; i0 < total; i0 += kFinishThreads) {
-    // the chunks of this stretch whose maximum reaches the bound
-    const unsigned i = i0 + tid;
-    bool in = false;
-    if (i < total) {
-      const int k = int(i / unsigned(C)), c = int(i % unsigned(C));
-      if (sm.top[k] > -INFINITY) {
-        if (sm.ended[k]) {
-          in = c == 0 && dkey(sm.base_s[k]) >= sm.bound.key;
-        } else {
-          const float m = a.part[int64_t(row0 + k) * C + c].x;
-          in = m > -INFINITY && m >= sm.least[k];
-        }
-      }
-    }
-    if (__syncthreads_or(in) == 0) continue;
-    if (in) sm.list[atomicAdd(&sm.list_n, 1)] = i;
-    __syncthreads();
-    const int n_list = sm.list_n;
-    for (int l0 = 0; l0 < n_list;) {
-      const Cand bound = sm.bound;
-      const int before = sm.count;
+  const int turns = (C + c_step - 1) / c_step;
+  for (int k0 = 0, turn = 0; k0 < a.beams;) {
+    // chunks whose maximum reaches the bound, until the list is full or all are seen
+    while (k0 < a.beams) {
+      if (sm.list_n > kList - NT) break;
       __syncthreads();
-      if (l0 + warp < n_list) {
-        const unsigned id = sm.list[l0 + warp];
-        const int k = int(id / unsigned(C)), c = int(id % unsigned(C));
-        const double s = sm.base_s[k];
+      const int k = k0 + my_beam;
+      const int64_t c = int64_t(c_first) + int64_t(turn) * c_step;
+      if (k < a.beams && c < C && sm.top[k] > -INFINITY) {
+        bool in;
+        if (sm.ended[k]) {
+          in = c == 0 && sm.score[k] >= sm.T;
+        } else {
+          const float m = chunk_max(k, int(c));
+          in = m > -INFINITY && m >= least_of(sm, k, sm.T);
+        }
+        if (in) sm.list[atomicAdd(&sm.list_n, 1)] = unsigned(k) << 22 | unsigned(c);
+      }
+      if (++turn == turns) turn = 0, k0 += per_turn;
+      __syncthreads();
+    }
+    const int n_list = sm.list_n;
+    for (;;) {
+      const bool exact = sm.exact;
+      for (;;) {
+        int l = 0;
+        if (lane == 0) l = atomicAdd(&sm.next, 1);
+        l = __shfl_sync(kFullWarp, l, 0);
+        if (l >= n_list) break;
+        const unsigned id = sm.list[l];
+        const int k = int(id >> 22), c = int(id & 0x3fffffu);
         const uint64_t flat0 = uint64_t(k) << 31;
         if (sm.ended[k]) {
-          const Cand y{dkey(s), flat0};
-          if (lane == 0 && !better(bound, y)) {
+          const Cand y{key_of(Two{sm.score[k], 0.0f}), flat0};
+          if (lane == 0 && !(exact && better(sm.bound, y))) {
             const int at = atomicAdd(&sm.count, 1);
             if (at < kBufNew) sm.buf[at] = y;
           }
-        } else {
-          const float M = sm.top[k], least = sm.least[k];
-          const double z = sm.log_s[k];
-          uint4 v[kVecs];
-          load_chunk<DT>(v, a.logits + int64_t(row0 + k) * a.stride, row_mask(a, row0 + k),
-                         int64_t(c) * kChunk<DT>, a.V, lane);
+          continue;
+        }
+        const float least = least_of(sm, k, sm.T);
+        const char* row = a.logits + int64_t(row0 + k) * a.stride;
+        const uint32_t* bm = sm.masked[k] ? a.bitmask + int64_t(row0 + k) * a.bm_stride : nullptr;
+        uint4 v[kVecs];
+        load_chunk<DT, true>(v, row, bm, int64_t(c) * kChunk<DT>, a.V, lane);
+        uint32_t hits = 0;
 #pragma unroll
-          for (int g = 0; g < kVecs; ++g) {
+        for (int g = 0; g < kVecs; ++g)
 #pragma unroll
-            for (int e = 0; e < Elt<DT>::kPerVec; ++e) {
-              const float x = Elt<DT>::get(v[g], e);
-              if (x > -INFINITY && x >= least) {
-                const double score = s + ((x == M ? 0.0 : double(x) - double(M)) - z);
-                const int64_t j =
-                    int64_t(c) * kChunk<DT> + (g * 32 + lane) * Elt<DT>::kPerVec + e;
-                const Cand y{dkey(score), flat0 + uint64_t(j)};
-                if (score > -INFINITY && !better(bound, y)) {
-                  const int at = atomicAdd(&sm.count, 1);
-                  if (at < kBufNew) sm.buf[at] = y;
-                }
-              }
-            }
+          for (int e = 0; e < Elt<DT>::kPerVec; ++e) {
+            const float x = Elt<DT>::get(v[g], e);
+            if (x >= least && x > -INFINITY) hits |= 1u << (g * Elt<DT>::kPerVec + e);
           }
+        for (; hits; hits &= hits - 1) {
+          const unsigned bit = __ffs(hits) - 1;
+          const unsigned j = unsigned(c) * kChunk<DT> + lane * Elt<DT>::kPerVec +
+                             bit / Elt<DT>::kPerVec * (32 * Elt<DT>::kPerVec) +
+                             bit % Elt<DT>::kPerVec;
+          const float x = element<DT>(v, bit);
+          // the score waits until all threads can take one; the logit stands for it
+          Cand y{uint64_t(__float_as_uint(x)), flat0 + j};
+          if (exact) {
+            y.key = key_of(score_of(sm, k, x));
+            if (better(sm.bound, y)) continue;
+          }
+          const int at = atomicAdd(&sm.count, 1);
+          if (at < kBufNew) sm.buf[at] = y;
         }
       }
       __syncthreads();
-      const int count = sm.count;
-      if (count <= kBufNew) {
-        l0 += kFinishWarps;
-        if (count > kBufNew / 2) join(sm, count, a.n, a.beams, true);
-      } else if (before > 0) {
-        // too many: settle what earlier turns left, and read this turn's chunks again
-        join(sm, before, a.n, a.beams, true);
-      } else {
-        // too many from this turn alone: what was seen raises the bound (strictly, as
-        // kBufNew > n and no two candidates are equal), and the turn is done again
-        join(sm, kBufNew, a.n, a.beams, false);
+      const int count = sm.count, got = min(count, kBufNew);
+      if (tid == 0) sm.next = 0;
+      if (!exact) {
+        for (int t = tid; t < got; t += NT) {
+          const Cand y = sm.buf[t];
+          const int k = int(y.flat >> 31);
+          if (!sm.ended[k])
+            sm.buf[t].key = key_of(score_of(sm, k, __uint_as_float(uint32_t(y.key))));
+        }
       }
-      __syncthreads();
+      if (count <= kBufNew) break;
+      // too many: what was seen raises the bound (strictly, as kBufNew > n and no two
+      // candidates are equal), and the list is gone through again
+      join<NT>(sm, kBufNew, a.n, false);
     }
-    if (tid == 0) sm.list_n = 0;
+    if (k0 < a.beams) {
+      if (tid == 0) sm.list_n = 0;
+      join<NT>(sm, sm.count, a.n, true);
+    }
+  }
+  __syncthreads();
+
+  // the new ones and the best so far, in order
+  const int count = sm.count, m = count + sm.front_n;
+  if (sm.front_n > 0) {
+    for (int t = tid; t < sm.front_n; t += NT) sm.buf[count + t] = sm.front[t];
     __syncthreads();
   }
-  join(sm, sm.count, a.n, a.beams, true);
-
-  for (int t = tid; t < a.n; t += kFinishThreads) {
-    float score = -INFINITY;
-    int64_t token = -1;
-    int parent = -1;
-    if (t < sm.front_n) {
-      const Cand y = sm.front[t];
-      parent = int(y.flat >> 31);
-      token = sm.ended[parent] ? a.pad : int64_t(y.flat & 0x7fffffffu);
-      score = float(key_double(y.key));
+  auto put = [&](int at, const Cand& y) {
+    const int64_t to = int64_t(b) * a.n + at;
+    const bool is = y.key > kNoScore;  // a score of -inf, a sum that overflowed, is none
+    const int parent = int(y.flat >> 31);
+    a.out_scores[to] = is ? key_score(y.key) : -INFINITY;
+    a.out_tokens[to] = !is ? -1 : sm.ended[parent] ? a.pad : int64_t(y.flat & 0x7fffffffu);
+    a.out_parents[to] = is ? parent : -1;
+  };
+  if (m <= NT) {
+    // the place of a candidate is the number of better ones, counted by P threads
+    int lg = 0;
+    while (lg < 5 && (m << (lg + 1)) <= NT) ++lg;
+    const int P = 1 << lg, mine = tid >> lg;
+    int rank = 0;
+    Cand y{0, 0};
+    if (mine < m) {
+      y = sm.buf[mine];
+#pragma unroll 4
+      for (int t = tid & (P - 1); t < m; t += P) rank += better(sm.buf[t], y);
     }
-    a.out_scores[int64_t(b) * a.n + t] = score;
-    a.out_tokens[int64_t(b) * a.n + t] = token;
-    a.out_parents[int64_t(b) * a.n + t] = parent;
+    for (int o = P / 2; o; o >>= 1) rank += __shfl_xor_sync(kFullWarp, rank, o);
+    if (mine < m && rank < a.n && (tid & (P - 1)) == 0) put(rank, y);
+  } else {
+    sort_best_first<NT>(sm.buf, m);
+    for (int t = tid; t < min(m, a.n); t += NT) put(t, sm.buf[t]);
   }
+  for (int t = m + tid; t < a.n; t += NT) put(t, Cand{0, 0});
+}
+
+template <typename K>
+int resident_blocks(K kernel) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kStreamThreads, 0) != cudaSuccess)
+    n = 0;
+  return std::max(1, n) * kSms;
+}
+
+template <int DT, int NT>
+cudaError_t finish_with(cudaLaunchConfig_t cfg, BeamArgs a, int64_t batch) {
+  static_assert(sizeof(FinishSmem) <= 48 * 1024, "within the default limit");
+  const int64_t staged = int64_t(a.beams) * a.chunks * 4;
+  a.staged = staged <= kMostStaged;
+  cfg.dynamicSmemBytes = sizeof(FinishSmem) + (a.staged ? size_t(staged) : 0);
+  if (cfg.dynamicSmemBytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(beam_finish_kernel<DT, NT>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(sizeof(FinishSmem) + kMostStaged));
+    if (e != cudaSuccess) return e;
+  }
+  cfg.gridDim = dim3(unsigned(batch));
+  cfg.blockDim = dim3(NT);
+  return cudaLaunchKernelEx(&cfg, beam_finish_kernel<DT, NT>, a);
+}
+
+template <int DT>
+cudaError_t finish(const cudaLaunchConfig_t& cfg, const BeamArgs& a, int64_t batch) {
+  const int64_t total = int64_t(a.beams) * a.chunks;
+#ifdef LP_NT
+  return finish_with<DT, LP_NT>(cfg, a, batch);
+#endif
+  if (total > 1600) return finish_with<DT, 1024>(cfg, a, batch);
+  return finish_with<DT, 512>(cfg, a, batch);
 }
 
 template <int DT>
 cudaError_t launch(const BeamArgs& a0, int64_t batch, cudaStream_t stream) {
   BeamArgs a = a0;
-  static_assert(sizeof(FinishSmem) <= 48 * 1024, "within the default limit");
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -447,15 +792,20 @@ cudaError_t launch(const BeamArgs& a0, int64_t batch, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  const int64_t warps = int64_t(a.rows) * a.chunks;
-  cfg.gridDim = dim3(unsigned(std::min<int64_t>((warps + 7) / 8, kSms * 8)));
+  static const int resident = resident_blocks(beam_stream_kernel<DT, false>);
+  static const int resident_early = resident_blocks(beam_stream_kernel<DT, true>);
+  const int64_t blocks = (int64_t(a.rows) * a.chunks + 7) / 8;
   cfg.blockDim = dim3(kStreamThreads);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, beam_stream_kernel<DT>, a);
+  cudaError_t e;
+  if (blocks <= resident_early) {
+    cfg.gridDim = dim3(unsigned(blocks));
+    e = cudaLaunchKernelEx(&cfg, beam_stream_kernel<DT, true>, a);
+  } else {
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(blocks, resident)));
+    e = cudaLaunchKernelEx(&cfg, beam_stream_kernel<DT, false>, a);
+  }
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(unsigned(batch));
-  cfg.blockDim = dim3(kFinishThreads);
-  cfg.dynamicSmemBytes = sizeof(FinishSmem);
-  return cudaLaunchKernelEx(&cfg, beam_finish_kernel<DT>, a);
+  return finish<DT>(cfg, a, batch);
 }
 
 int64_t chunk_tokens(lp_dtype dt) { return dt == LP_F32 ? kChunk<LP_F32> : kChunk<LP_F16>; }
@@ -528,6 +878,8 @@ extern "C" lp_status lp_beam_select(const void* logits, lp_dtype dt, int64_t bat
   a.beams = int(beams);
   a.n = int(n_select);
   a.chunks = int(chunks);
+  a.sum_bits = 40;
+  while (a.sum_bits > 32 && (V >> (63 - a.sum_bits)) > 0) --a.sum_bits;
   a.part = static_cast<float2*>(workspace);
   a.out_scores = out_scores;
   a.out_tokens = out_tokens;
