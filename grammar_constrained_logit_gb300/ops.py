@@ -10,6 +10,7 @@ and streams.  The names follow the pages: ``apply_token_bitmask_inplace``
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Sequence
 
 import torch
@@ -421,9 +422,14 @@ def mask_and_sample_slots(logits: torch.Tensor, bitmask: torch.Tensor | None,
 lp_mask_and_sample_slots = mask_and_sample_slots
 
 
+# The current stream's handle, without the Stream object that current_stream() makes: a
+# call of these operators is a few microseconds, and that would be two of them.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 _beam_workspaces: dict = {}
 
 
+@functools.lru_cache(maxsize=256)
 def beam_select_workspace_bytes(dtype: torch.dtype, rows: int, vocab_size: int) -> int:
     """Bytes of device scratch ``beam_select`` needs for ``rows`` = batch * beams."""
     n = _lib.load().lp_beam_select_workspace_bytes(_DT[dtype], rows, vocab_size)
@@ -432,27 +438,24 @@ def beam_select_workspace_bytes(dtype: torch.dtype, rows: int, vocab_size: int) 
     return int(n)
 
 
-def _beam_workspace(workspace, lg: torch.Tensor):
+def _beam_workspace(workspace, device, stream: int, need: int):
     """The caller's workspace (a uint8 CUDA tensor of any content), or one kept per
     (device, stream), grown on demand.  When capturing a CUDA graph, pass one that was
-    allocated before the capture.  Returns (pointer, bytes)."""
+    allocated before the capture."""
     if workspace is not None:
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
-                workspace.device != lg.device:
+                workspace.device != device:
             raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
-        return workspace.data_ptr(), workspace.numel()
-    need = beam_select_workspace_bytes(lg.dtype, lg.size(0), lg.size(1))
-    key = (lg.device.index, torch.cuda.current_stream(lg.device).cuda_stream)
+        return workspace
+    key = (device.index, stream)
     ws = _beam_workspaces.get(key)
     if ws is None or ws.numel() < need:
-        ws = torch.empty(max(need, 8), dtype=torch.uint8, device=lg.device)
+        ws = torch.empty(max(need, 8), dtype=torch.uint8, device=device)
         _beam_workspaces[key] = ws
-    return ws.data_ptr(), ws.numel()
+    return ws
 
 
 def _row_flags(flags, rows, device, name):
-    if flags is None:
-        return None
     if flags.device != device:
         raise ValueError(f"{name} must be on the same device as logits")
     if flags.numel() != rows:
@@ -483,52 +486,57 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None
     Returns (scores float32, tokens int64, parents int32), each [batch, n_select],
     highest score first, ties to the lowest (beam, token); empty places are
     (-inf, -1, -1).  ``out`` takes the three tensors to write instead."""
-    if scores.dim() != 2:
-        raise ValueError(f"scores must be [batch, beams], got {tuple(scores.shape)}")
+    shape = scores.shape
+    if len(shape) != 2:
+        raise ValueError(f"scores must be [batch, beams], got {tuple(shape)}")
     if scores.dtype != torch.float32:
         raise TypeError("scores must be float32")
-    batch, beams = scores.shape
+    batch, beams = shape
     if logits.dim() == 3:
-        if logits.shape[:2] != scores.shape:
+        if logits.shape[:2] != shape:
             raise ValueError("logits [batch, beams, V] must match scores [batch, beams]")
         logits = logits.flatten(0, 1)
     lg = _matrix(logits, "logits")
-    rows = lg.size(0)
+    rows, cols = lg.shape
     if rows != batch * beams:
         raise ValueError(f"logits must have {batch * beams} rows, got {rows}")
-    if scores.device != lg.device:
+    device = lg.device
+    if scores.device != device:
         raise ValueError("scores must be on the same device as logits")
     dt = _dtype_code(lg)
     n = beams if n_select is None else int(n_select)
-    bm = None
+    bm = flags = ended = None
     if bitmask is not None:
-        bm = _bitmask(bitmask.flatten(0, -2) if bitmask.dim() > 2 else bitmask, lg.device)
+        bm = _bitmask(bitmask.flatten(0, -2) if bitmask.dim() > 2 else bitmask, device)
+        if row_needs_mask is not None:
+            flags = _row_flags(row_needs_mask, rows, device, "row_needs_mask")
     elif row_needs_mask is not None:
         raise ValueError("row_needs_mask needs a bitmask")
-    flags = _row_flags(row_needs_mask, rows, lg.device, "row_needs_mask")
-    ended = _row_flags(finished, rows, lg.device, "finished")
+    if finished is not None:
+        ended = _row_flags(finished, rows, device, "finished")
     sc = scores.contiguous()
     if out is None:
         if n < 0:
             raise ValueError("n_select must not be negative")
-        out = (torch.empty((batch, n), dtype=torch.float32, device=lg.device),
-               torch.empty((batch, n), dtype=torch.int64, device=lg.device),
-               torch.empty((batch, n), dtype=torch.int32, device=lg.device))
+        out = (torch.empty((batch, n), dtype=torch.float32, device=device),
+               torch.empty((batch, n), dtype=torch.int64, device=device),
+               torch.empty((batch, n), dtype=torch.int32, device=device))
     else:
         for t, d in zip(out, (torch.float32, torch.int64, torch.int32), strict=True):
             if t.dtype != d or t.shape != (batch, n) or not t.is_contiguous() or \
-                    t.device != lg.device:
+                    t.device != device:
                 raise ValueError("out must be contiguous float32, int64 and int32 tensors "
                                  "[batch, n_select] on the logits' device")
-    wp, wn = _beam_workspace(workspace, lg)
+    stream = _raw_stream(device.index)
+    ws = _beam_workspace(workspace, device, stream,
+                         beam_select_workspace_bytes(lg.dtype, rows, cols))
     st = _lib.load().lp_beam_select(
-        lg.data_ptr(), dt, batch, beams, lg.size(1), _stride(lg),
+        lg.data_ptr(), dt, batch, beams, cols, _stride(lg),
         None if bm is None else bm.data_ptr(), 0 if bm is None else bm.size(0),
         0 if bm is None else bm.size(1), 0 if bm is None else _stride(bm),
         -1 if vocab_size is None else int(vocab_size), None if flags is None else flags.data_ptr(),
         sc.data_ptr(), None if ended is None else ended.data_ptr(), int(pad_id), n,
-        out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), wp, wn,
-        torch.cuda.current_stream(lg.device).cuda_stream)
+        out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), ws.numel(), stream)
     check("lp_beam_select", st)
     return out
 
@@ -639,7 +647,7 @@ class StateReorder:
         lo = None if start is None else self._check(start, "start", "[batch]", b)
         hi = None if stop is None else self._check(stop, "stop", "[batch]", b)
         st = _lib.load().lp_reorder_states(self._c, len(self.states), b, k, p, lo, hi,
-                                           torch.cuda.current_stream(self.device).cuda_stream)
+                                           _raw_stream(self.device.index))
         check("lp_reorder_states", st)
 
 
@@ -700,6 +708,7 @@ class QuantCache:
         self.slots = self.page_size * (codes.size(1) if d == 5 else 1)
         self.device = codes.device
         self._parts = (_lib.CachePart * max(1, self.parts))()
+        self._heads_type = _lib.Heads * max(1, self.parts)
         e = params.element_size()
         for i in range(self.parts):
             p = self._parts[i]
@@ -732,31 +741,29 @@ def _cache_call(name, cache: QuantCache, xs, slots: torch.Tensor):
         raise TypeError("slots must be int64")
     if slots.dim() != 1 or not slots.is_contiguous() or slots.device != cache.device:
         raise ValueError("slots must be contiguous, 1-D and on the cache's device")
-    n, dt = slots.size(0), None
+    n = slots.size(0)
     if len(xs) != cache.parts:
         raise ValueError(f"expected {cache.parts} tensors, one for each part, got {len(xs)}")
-    heads = (_lib.Heads * max(1, cache.parts))()
-    for i, x in enumerate(xs):
-        if dt is None:
-            dt = x.dtype
-        if x.dtype != dt:
+    dtype = xs[0].dtype if xs else torch.float32
+    dt = _DT.get(dtype)
+    if dt is None:
+        raise TypeError(f"tensors must be float32, float16 or bfloat16, not {dtype}")
+    shape, device = (n, cache.heads, cache.dim), cache.device
+    heads = cache._heads_type()
+    for h, x in zip(heads, xs):
+        if x.dtype != dtype:
             raise TypeError("the parts' tensors must be of one type")
-        if x.device != cache.device:
+        if x.device != device:
             raise ValueError("tensors must be on the cache's device")
-        if tuple(x.shape) != (n, cache.heads, cache.dim):
-            raise ValueError(f"tensors must be [{n}, {cache.heads}, {cache.dim}], "
-                             f"got {tuple(x.shape)}")
-        token, head, inner = x.stride()
-        if cache.dim > 1 and inner != 1:
+        if x.shape != shape:
+            raise ValueError(f"tensors must be {list(shape)}, got {list(x.shape)}")
+        h.token_stride, h.head_stride, inner = x.stride()
+        if inner != 1 and cache.dim > 1:
             raise ValueError("a head's elements must be contiguous")
-        h = heads[i]
-        h.data, h.token_stride, h.head_stride = x.data_ptr(), token, head
-    if dt is not None and dt not in _DT:
-        raise TypeError(f"tensors must be float32, float16 or bfloat16, not {dt}")
+        h.data = x.data_ptr()
     st = getattr(_lib.load(), name)(
-        cache._parts, heads, cache.parts, cache.bits, _DT[dt] if dt is not None else 0,
-        cache.slots, max(1, cache.page_size), cache.heads, cache.dim, cache.group,
-        slots.data_ptr(), n, torch.cuda.current_stream(cache.device).cuda_stream)
+        cache._parts, heads, cache.parts, cache.bits, dt, cache.slots, max(1, cache.page_size),
+        cache.heads, cache.dim, cache.group, slots.data_ptr(), n, _raw_stream(device.index))
     check(name, st)
 
 
