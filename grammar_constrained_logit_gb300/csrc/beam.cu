@@ -273,6 +273,10 @@ __device__ __forceinline__ float warp_max(float m) {
   return m;
 }
 
+// EARLY: for problems of one chunk a warp, which only wait for memory: the loads wait
+// neither for the row's state nor for its mask.  Loads overlap between warps, not within
+// one: a second chunk in registers (79 of them) took the blocks of an SM from 5 to 3 and
+// 128 x 8 rows of 202048 fp16 from 76 to 88 us.
 template <int DT, bool EARLY>
 __global__ void __launch_bounds__(kStreamThreads) beam_stream_kernel(BeamArgs a) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -353,6 +357,36 @@ __device__ __forceinline__ float key_score(uint64_t k) { return key_float(uint32
 
 constexpr uint64_t kNoScore = 0x007fffffull << 32 | 0xffffffffull;  // keys of -inf: none above
 
+// The same for 32 < m <= NT, one candidate a thread in registers: neighbours up to 16 places
+// apart meet by shuffles, the others through c.  Returns this thread's, in order.
+template <int NT>
+__device__ __forceinline__ Cand sorted_in_threads(Cand* c, int m) {
+  const int t = threadIdx.x;
+  Cand x = t < m ? c[t] : Cand{0, ~0ull};
+  __syncthreads();
+  int p = 2;
+  while (p < m) p <<= 1;
+  for (int k = 2; k <= p; k <<= 1) {
+    for (int j = k >> 1; j; j >>= 1) {
+      Cand y;
+      if (j < 32) {
+        if (t >= p) continue;  // (whole warps: p is at least 32 here)
+        y.key = __shfl_xor_sync(kFullWarp, x.key, j);
+        y.flat = __shfl_xor_sync(kFullWarp, x.flat, j);
+      } else {
+        if (t < p) c[t] = x;
+        __syncthreads();
+        if (t < p) y = c[t ^ j];
+        __syncthreads();
+        if (t >= p) continue;
+      }
+      const bool first = ((t & j) == 0) == ((t & k) == 0);  // the better one belongs here
+      if (better(y, x) == first) x = y;
+    }
+  }
+  return x;
+}
+
 // log of a whole number of units, to 2^-38: the number's leading 7 bits choose
 // c near 1/m, a 10-bit number whose logarithm is tabled (the table-driven scheme of
 // Tang, ACM TOMS 16(4), 1990); t = m c - 1 is below 2^-7 and its series is short.
@@ -423,8 +457,8 @@ struct FinishSmem {
   uint8_t masked[kMaxSelect];
   unsigned best[kGroups];
   LogEntry log_table[128];
-  unsigned list[kList];
-  int list_n, next, count, front_n, exact;
+  unsigned list[kList];       // chunks to go through
+  int list_n, count, front_n, exact, again;
   float T;
   Cand bound;                 // exact: candidates worse than this are out
 };
@@ -540,17 +574,71 @@ __device__ __forceinline__ unsigned beam_sums(FinishSmem& sm, const BeamArgs& a,
   return mine > -INFINITY ? low_key(s, M, z.hi, mine) : 0;
 }
 
-template <int DT, int NT>
+// The n-th largest of the warp's keys, N a lane, taken low: measured from the largest, in
+// steps of 1/64 of the distance (1/1024 at the least), as a bound need not be tight.  -inf
+// when fewer than n are there.
+template <int N>
+__device__ __forceinline__ float nth_largest(const unsigned* keys, int n) {
+  constexpr int kBase = (127 - 4) << 6;  // 2^-4, in steps of 2^-6 of a power of two
+  const int lane = threadIdx.x & 31;
+  unsigned mine[N], most = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) most = max(most, mine[i] = keys[i * 32 + lane]);
+  most = __reduce_max_sync(kFullWarp, most);
+  const float top = key_float(most);
+  int near[N];  // 2047 at the largest, 0 where there is none or it is 2^28 away
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float d = mine[i] == most ? 0.0f : top - key_float(mine[i]);
+    const int q = int(__float_as_uint(d + 0x1p-4f) >> 17) - kBase;
+    near[i] = mine[i] == 0 || !(d < 0x1p27f) ? 0 : max(0, 2047 - q);
+  }
+  int T = 0;
+#pragma unroll
+  for (int sh = 10; sh >= 0; sh -= 2) {
+    unsigned there[4] = {0, 0, 0, 0};  // three counts of up to 512, ten bits each
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      there[i & 3] += near[i] >= (T | 1 << sh) ? 1u : 0u;
+      there[i & 3] += near[i] >= (T | 2 << sh) ? 1u << 10 : 0u;
+      there[i & 3] += near[i] >= (T | 3 << sh) ? 1u << 20 : 0u;
+    }
+    const unsigned all = __reduce_add_sync(kFullWarp, (there[0] + there[1]) + (there[2] + there[3]));
+    const int c1 = all & 1023u, c2 = all >> 10 & 1023u, c3 = all >> 20;
+    T |= (c3 >= n ? 3 : c2 >= n ? 2 : c1 >= n ? 1 : 0) << sh;
+  }
+  if (T == 0) return -INFINITY;
+  if (!(top < INFINITY)) return top;
+  const float d = __uint_as_float(unsigned(2047 - T + 1 + kBase) << 17) - 0x1p-4f;
+  return top - (d + 0x1p-20f * (fabsf(top) + d));
+}
+
+// A cluster's blocks share one batch entry: each goes through its part of the chunks, the
+// first holds what they find.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n"
+               "barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+__device__ __forceinline__ FinishSmem* of_first_block(FinishSmem* p) {
+  uint64_t r;
+  asm("mapa.u64 %0, %1, 0;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)));
+  return reinterpret_cast<FinishSmem*>(r);
+}
+
+template <int DT, int NT, int R>
 __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
   constexpr int NW = NT / 32;
   extern __shared__ __align__(16) char raw[];
   FinishSmem& sm = *reinterpret_cast<FinishSmem*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x, row0 = b * a.beams, C = a.chunks;
+  const int b = blockIdx.x / R, rank = blockIdx.x % R, row0 = b * a.beams, C = a.chunks;
+  FinishSmem& hub = R > 1 ? *of_first_block(&sm) : sm;
   float* staged = a.staged ? reinterpret_cast<float*>(raw + sizeof(FinishSmem)) : nullptr;
-  if (tid == 0) sm.count = 0, sm.front_n = 0, sm.list_n = 0, sm.next = 0, sm.exact = 0;
+  if (tid == 0) sm.count = 0, sm.front_n = 0, sm.list_n = 0, sm.exact = 0;
   for (int i = tid; i < 128; i += NT) sm.log_table[i] = kLogTable.at[i];
-  __syncthreads();
+  if (R > 1) cluster_sync();
+  else __syncthreads();
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
@@ -593,42 +681,24 @@ __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
   }
   __syncthreads();
   if (warp == 0) {
-    // two bits at a time, the upper 16: a bound need not be tight to the last place
     constexpr int kMine = (NT > kGroups ? kGroups : NT) / 32;
-    unsigned mine[kMine];
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) mine[i] = sm.best[i * 32 + lane];
-    unsigned T = 0;
-#pragma unroll 1
-    for (int sh = 30; sh >= 16; sh -= 2) {
-      unsigned there[4] = {0, 0, 0, 0};  // three counts of up to 512, ten bits each
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        there[i & 3] += mine[i] >= (T | 1u << sh) ? 1u : 0u;
-        there[i & 3] += mine[i] >= (T | 2u << sh) ? 1u << 10 : 0u;
-        there[i & 3] += mine[i] >= (T | 3u << sh) ? 1u << 20 : 0u;
-      }
-      const unsigned all =
-          __reduce_add_sync(kFullWarp, (there[0] + there[1]) + (there[2] + there[3]));
-      const int c1 = all & 1023u, c2 = all >> 10 & 1023u, c3 = all >> 20;
-      const int q = c3 >= a.n ? 3 : c2 >= a.n ? 2 : c1 >= a.n ? 1 : 0;
-      T |= unsigned(q) << sh;
-      if ((q == 3 ? c3 : q == 2 ? c2 : q == 1 ? c1 : 0) == a.n) break;
-    }
-    // (keys up to 0x007fffff are those of -inf and of what lies below it)
-    if (lane == 0) sm.T = T > 0x007fffffu ? key_float(T) : -INFINITY;
+    const int beams_of = NT > kGroups ? 2 * kMine : kMine;  // whose lanes fill the groups
+    const float T = !few && a.beams * 4 <= beams_of ? nth_largest<kMine / 4>(sm.best, a.n)
+                                                    : nth_largest<kMine>(sm.best, a.n);
+    if (lane == 0) sm.T = T;
   }
   __syncthreads();
 
   const int turns = (C + c_step - 1) / c_step;
   for (int k0 = 0, turn = 0; k0 < a.beams;) {
-    // chunks whose maximum reaches the bound, until the list is full or all are seen
-    while (k0 < a.beams) {
-      if (sm.list_n > kList - NT) break;
-      __syncthreads();
+    // this block's chunks whose maximum reaches the bound, until the list may be full (of
+    // 32 neighbouring chunks each of R blocks has 32 / R) or all are seen
+    for (int i = 0; k0 < a.beams; ++i) {
+      if (R > 1 ? i == kList * R / NT : sm.list_n > kList - NT) break;
+      if (R == 1) __syncthreads();
       const int k = k0 + my_beam;
       const int64_t c = int64_t(c_first) + int64_t(turn) * c_step;
-      if (k < a.beams && c < C && sm.top[k] > -INFINITY) {
+      if (k < a.beams && c < C && sm.top[k] > -INFINITY && (R == 1 || int(c) % R == rank)) {
         bool in;
         if (sm.ended[k]) {
           in = c == 0 && sm.score[k] >= sm.T;
@@ -639,24 +709,21 @@ __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
         if (in) sm.list[atomicAdd(&sm.list_n, 1)] = unsigned(k) << 22 | unsigned(c);
       }
       if (++turn == turns) turn = 0, k0 += per_turn;
-      __syncthreads();
+      if (R == 1) __syncthreads();
     }
+    if (R > 1) __syncthreads();
     const int n_list = sm.list_n;
     for (;;) {
       const bool exact = sm.exact;
-      for (;;) {
-        int l = 0;
-        if (lane == 0) l = atomicAdd(&sm.next, 1);
-        l = __shfl_sync(kFullWarp, l, 0);
-        if (l >= n_list) break;
+      for (int l = warp; l < n_list; l += NW) {
         const unsigned id = sm.list[l];
         const int k = int(id >> 22), c = int(id & 0x3fffffu);
         const uint64_t flat0 = uint64_t(k) << 31;
         if (sm.ended[k]) {
           const Cand y{key_of(Two{sm.score[k], 0.0f}), flat0};
           if (lane == 0 && !(exact && better(sm.bound, y))) {
-            const int at = atomicAdd(&sm.count, 1);
-            if (at < kBufNew) sm.buf[at] = y;
+            const int at = atomicAdd(&hub.count, 1);
+            if (at < kBufNew) hub.buf[at] = y;
           }
           continue;
         }
@@ -685,32 +752,43 @@ __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
             y.key = key_of(score_of(sm, k, x));
             if (better(sm.bound, y)) continue;
           }
-          const int at = atomicAdd(&sm.count, 1);
-          if (at < kBufNew) sm.buf[at] = y;
+          const int at = atomicAdd(&hub.count, 1);
+          if (at < kBufNew) hub.buf[at] = y;
         }
+      }
+      if (R > 1) cluster_sync();
+      else __syncthreads();
+      // the first block looks at what there is, the others wait for what it says
+      if (R == 1 || rank == 0) {
+        const int count = sm.count, got = min(count, kBufNew);
+        if (!exact) {
+          for (int t = tid; t < got; t += NT) {
+            const Cand y = sm.buf[t];
+            const int k = int(y.flat >> 31);
+            if (!sm.ended[k])
+              sm.buf[t].key = key_of(score_of(sm, k, __uint_as_float(uint32_t(y.key))));
+          }
+        }
+        // too many: what was seen raises the bound (strictly, as kBufNew > n and no two
+        // candidates are equal), and the list is gone through again.  Else, with more of
+        // the chunks to come, the n best are kept.
+        const bool again = count > kBufNew;
+        if (tid == 0) sm.again = again;
+        if (again) join<NT>(sm, kBufNew, a.n, false);
+        else if (k0 < a.beams) join<NT>(sm, count, a.n, true);
+      }
+      if (R > 1) {
+        cluster_sync();
+        if (rank != 0 && tid == 0)
+          sm.again = hub.again, sm.T = hub.T, sm.exact = hub.exact, sm.bound = hub.bound;
       }
       __syncthreads();
-      const int count = sm.count, got = min(count, kBufNew);
-      if (tid == 0) sm.next = 0;
-      if (!exact) {
-        for (int t = tid; t < got; t += NT) {
-          const Cand y = sm.buf[t];
-          const int k = int(y.flat >> 31);
-          if (!sm.ended[k])
-            sm.buf[t].key = key_of(score_of(sm, k, __uint_as_float(uint32_t(y.key))));
-        }
-      }
-      if (count <= kBufNew) break;
-      // too many: what was seen raises the bound (strictly, as kBufNew > n and no two
-      // candidates are equal), and the list is gone through again
-      join<NT>(sm, kBufNew, a.n, false);
+      if (!sm.again) break;
     }
-    if (k0 < a.beams) {
-      if (tid == 0) sm.list_n = 0;
-      join<NT>(sm, sm.count, a.n, true);
-    }
+    if (tid == 0) sm.list_n = 0;
+    __syncthreads();
   }
-  __syncthreads();
+  if (R > 1 && rank != 0) return;
 
   // the new ones and the best so far, in order
   const int count = sm.count, m = count + sm.front_n;
@@ -726,20 +804,17 @@ __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
     a.out_tokens[to] = !is ? -1 : sm.ended[parent] ? a.pad : int64_t(y.flat & 0x7fffffffu);
     a.out_parents[to] = is ? parent : -1;
   };
-  if (m <= NT) {
-    // the place of a candidate is the number of better ones, counted by P threads
-    int lg = 0;
-    while (lg < 5 && (m << (lg + 1)) <= NT) ++lg;
-    const int P = 1 << lg, mine = tid >> lg;
-    int rank = 0;
-    Cand y{0, 0};
-    if (mine < m) {
-      y = sm.buf[mine];
-#pragma unroll 4
-      for (int t = tid & (P - 1); t < m; t += P) rank += better(sm.buf[t], y);
+  if (m <= 32) {
+    // the place of a candidate is the number of better ones
+    const int mine = tid >> 5;  // a warp's worth of threads each
+    for (int t = mine; t < m; t += NW) {
+      const Cand y = sm.buf[t];
+      const int at = __popc(__ballot_sync(kFullWarp, lane < m && better(sm.buf[lane], y)));
+      if (at < a.n && lane == 0) put(at, y);
     }
-    for (int o = P / 2; o; o >>= 1) rank += __shfl_xor_sync(kFullWarp, rank, o);
-    if (mine < m && rank < a.n && (tid & (P - 1)) == 0) put(rank, y);
+  } else if (m <= NT) {
+    const Cand y = sorted_in_threads<NT>(sm.buf, m);
+    if (tid < min(m, a.n)) put(tid, y);
   } else {
     sort_best_first<NT>(sm.buf, m);
     for (int t = tid; t < min(m, a.n); t += NT) put(t, sm.buf[t]);
@@ -755,31 +830,39 @@ int resident_blocks(K kernel) {
   return std::max(1, n) * kSms;
 }
 
-template <int DT, int NT>
+template <int DT, int NT, int R>
 cudaError_t finish_with(cudaLaunchConfig_t cfg, BeamArgs a, int64_t batch) {
   static_assert(sizeof(FinishSmem) <= 48 * 1024, "within the default limit");
   const int64_t staged = int64_t(a.beams) * a.chunks * 4;
   a.staged = staged <= kMostStaged;
   cfg.dynamicSmemBytes = sizeof(FinishSmem) + (a.staged ? size_t(staged) : 0);
   if (cfg.dynamicSmemBytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(beam_finish_kernel<DT, NT>,
+    const cudaError_t e = cudaFuncSetAttribute(beam_finish_kernel<DT, NT, R>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                int(sizeof(FinishSmem) + kMostStaged));
     if (e != cudaSuccess) return e;
   }
-  cfg.gridDim = dim3(unsigned(batch));
+  cudaLaunchAttribute attrs[2];
+  attrs[0] = cfg.attrs[0];
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = R;
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = R > 1 ? 2 : 1;
+  cfg.gridDim = dim3(unsigned(batch * R));
   cfg.blockDim = dim3(NT);
-  return cudaLaunchKernelEx(&cfg, beam_finish_kernel<DT, NT>, a);
+  return cudaLaunchKernelEx(&cfg, beam_finish_kernel<DT, NT, R>, a);
 }
 
 template <int DT>
 cudaError_t finish(const cudaLaunchConfig_t& cfg, const BeamArgs& a, int64_t batch) {
   const int64_t total = int64_t(a.beams) * a.chunks;
 #ifdef LP_NT
-  return finish_with<DT, LP_NT>(cfg, a, batch);
+  return finish_with<DT, LP_NT, LP_R>(cfg, a, batch);
 #endif
-  if (total > 1600) return finish_with<DT, 1024>(cfg, a, batch);
-  return finish_with<DT, 512>(cfg, a, batch);
+  if (a.n > 32 && batch * 8 <= kSms) return finish_with<DT, 1024, 8>(cfg, a, batch);
+  if (total > 1600) return finish_with<DT, 1024, 1>(cfg, a, batch);
+  return finish_with<DT, 512, 1>(cfg, a, batch);
 }
 
 template <int DT>
