@@ -447,6 +447,8 @@ __device__ __forceinline__ Two log_units(unsigned long long S, int bits, const L
   return two_sum(r.hi, lo);
 }
 
+enum { kOn, kAgain, kStretches };
+
 struct FinishSmem {
   Cand buf[kBuf];             // what is new; the best so far joins behind it to be sorted
   Cand front[kMaxSelect];     // the best so far, sorted
@@ -458,7 +460,7 @@ struct FinishSmem {
   unsigned best[kGroups];
   LogEntry log_table[128];
   unsigned list[kList];       // chunks to go through
-  int list_n, count, front_n, exact, again;
+  int list_n, count, front_n, exact, overflow, next;
   float T;
   Cand bound;                 // exact: candidates worse than this are out
 };
@@ -635,7 +637,7 @@ __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
   const int b = blockIdx.x / R, rank = blockIdx.x % R, row0 = b * a.beams, C = a.chunks;
   FinishSmem& hub = R > 1 ? *of_first_block(&sm) : sm;
   float* staged = a.staged ? reinterpret_cast<float*>(raw + sizeof(FinishSmem)) : nullptr;
-  if (tid == 0) sm.count = 0, sm.front_n = 0, sm.list_n = 0, sm.exact = 0;
+  if (tid == 0) sm.count = 0, sm.front_n = 0, sm.list_n = 0, sm.exact = 0, sm.overflow = 0;
   for (int i = tid; i < 128; i += NT) sm.log_table[i] = kLogTable.at[i];
   if (R > 1) cluster_sync();
   else __syncthreads();
@@ -683,48 +685,65 @@ __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
   if (warp == 0) {
     constexpr int kMine = (NT > kGroups ? kGroups : NT) / 32;
     const int beams_of = NT > kGroups ? 2 * kMine : kMine;  // whose lanes fill the groups
-    const float T = !few && a.beams * 4 <= beams_of ? nth_largest<kMine / 4>(sm.best, a.n)
-                                                    : nth_largest<kMine>(sm.best, a.n);
+    const int used = few ? beams_of : a.beams;
+    const float T = used * 4 <= beams_of   ? nth_largest<kMine / 4>(sm.best, a.n)
+                    : used * 2 <= beams_of ? nth_largest<kMine / 2>(sm.best, a.n)
+                                           : nth_largest<kMine>(sm.best, a.n);
     if (lane == 0) sm.T = T;
   }
   __syncthreads();
 
+  // Chunks whose maximum reaches the bound are listed and gone through, all of them at
+  // once; where the list overflows, again from the start in stretches that it holds.
+  bool whole = true;
+  int k0 = 0, turn = 0;
   const int turns = (C + c_step - 1) / c_step;
-  for (int k0 = 0, turn = 0; k0 < a.beams;) {
-    // this block's chunks whose maximum reaches the bound, until the list may be full (of
-    // 32 neighbouring chunks each of R blocks has 32 / R) or all are seen
-    for (int i = 0; k0 < a.beams; ++i) {
-      if (R > 1 ? i == kList * R / NT : sm.list_n > kList - NT) break;
-      if (R == 1) __syncthreads();
-      const int k = k0 + my_beam;
-      const int64_t c = int64_t(c_first) + int64_t(turn) * c_step;
-      if (k < a.beams && c < C && sm.top[k] > -INFINITY && (R == 1 || int(c) % R == rank)) {
-        bool in;
-        if (sm.ended[k]) {
-          in = c == 0 && sm.score[k] >= sm.T;
-        } else {
-          const float m = chunk_max(k, int(c));
-          in = m > -INFINITY && m >= least_of(sm, k, sm.T);
+  for (;;) {
+    if (whole) {
+      for (int k = my_beam; k < a.beams; k += per_turn) {
+        if (sm.top[k] == -INFINITY) continue;
+        const bool ended = sm.ended[k];
+        const float least = ended ? sm.T : least_of(sm, k, sm.T);
+        for (int c = c_first; c < C; c += c_step) {
+          if (R > 1 && c % R != rank) continue;
+          const float m = ended ? (c ? -INFINITY : sm.score[k]) : chunk_max(k, c);
+          if (m > -INFINITY && m >= least) {
+            const int at = atomicAdd(&sm.list_n, 1);
+            if (at < kList) sm.list[at] = unsigned(k) << 22 | unsigned(c);
+            else hub.overflow = 1;
+          }
         }
-        if (in) sm.list[atomicAdd(&sm.list_n, 1)] = unsigned(k) << 22 | unsigned(c);
       }
-      if (++turn == turns) turn = 0, k0 += per_turn;
-      if (R == 1) __syncthreads();
+      k0 = a.beams;
+    } else {
+      // of 32 neighbouring chunks each of R blocks has 32 / R
+      for (int i = 0; i < kList * R / NT && k0 < a.beams; ++i) {
+        const int k = k0 + my_beam;
+        const int64_t c = int64_t(c_first) + int64_t(turn) * c_step;
+        if (k < a.beams && c < C && sm.top[k] > -INFINITY && (R == 1 || int(c) % R == rank)) {
+          const bool ended = sm.ended[k];
+          const float m = ended ? (c ? -INFINITY : sm.score[k]) : chunk_max(k, int(c));
+          if (m > -INFINITY && m >= (ended ? sm.T : least_of(sm, k, sm.T)))
+            sm.list[atomicAdd(&sm.list_n, 1)] = unsigned(k) << 22 | unsigned(c);
+        }
+        if (++turn == turns) turn = 0, k0 += per_turn;
+      }
     }
-    if (R > 1) __syncthreads();
-    const int n_list = sm.list_n;
+    __syncthreads();
+    const int n_list = min(sm.list_n, kList);
     for (;;) {
       const bool exact = sm.exact;
       for (int l = warp; l < n_list; l += NW) {
         const unsigned id = sm.list[l];
         const int k = int(id >> 22), c = int(id & 0x3fffffu);
         const uint64_t flat0 = uint64_t(k) << 31;
+        auto found = [&](const Cand& y) {
+          if (exact && better(sm.bound, y)) return;
+          const int at = atomicAdd(&hub.count, 1);
+          if (at < kBufNew) hub.buf[at] = y;
+        };
         if (sm.ended[k]) {
-          const Cand y{key_of(Two{sm.score[k], 0.0f}), flat0};
-          if (lane == 0 && !(exact && better(sm.bound, y))) {
-            const int at = atomicAdd(&hub.count, 1);
-            if (at < kBufNew) hub.buf[at] = y;
-          }
+          if (lane == 0) found(Cand{key_of(Two{sm.score[k], 0.0f}), flat0});
           continue;
         }
         const float least = least_of(sm, k, sm.T);
@@ -745,46 +764,41 @@ __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
           const unsigned j = unsigned(c) * kChunk<DT> + lane * Elt<DT>::kPerVec +
                              bit / Elt<DT>::kPerVec * (32 * Elt<DT>::kPerVec) +
                              bit % Elt<DT>::kPerVec;
-          const float x = element<DT>(v, bit);
-          // the score waits until all threads can take one; the logit stands for it
-          Cand y{uint64_t(__float_as_uint(x)), flat0 + j};
-          if (exact) {
-            y.key = key_of(score_of(sm, k, x));
-            if (better(sm.bound, y)) continue;
-          }
-          const int at = atomicAdd(&hub.count, 1);
-          if (at < kBufNew) hub.buf[at] = y;
+          found(Cand{key_of(score_of(sm, k, element<DT>(v, bit))), flat0 + j});
         }
       }
       if (R > 1) cluster_sync();
       else __syncthreads();
       // the first block looks at what there is, the others wait for what it says
       if (R == 1 || rank == 0) {
-        const int count = sm.count, got = min(count, kBufNew);
-        if (!exact) {
-          for (int t = tid; t < got; t += NT) {
-            const Cand y = sm.buf[t];
-            const int k = int(y.flat >> 31);
-            if (!sm.ended[k])
-              sm.buf[t].key = key_of(score_of(sm, k, __uint_as_float(uint32_t(y.key))));
-          }
+        const int count = sm.count;
+        int next = kOn;
+        if (sm.overflow) {
+          next = kStretches;
+        } else if (count > kBufNew) {
+          // too many: what was seen raises the bound (strictly, as kBufNew > n and no two
+          // candidates are equal), and the list is gone through again
+          next = kAgain;
+          join<NT>(sm, kBufNew, a.n, false);
+        } else if (k0 < a.beams) {
+          join<NT>(sm, count, a.n, true);  // with chunks to come, the n best are kept
         }
-        // too many: what was seen raises the bound (strictly, as kBufNew > n and no two
-        // candidates are equal), and the list is gone through again.  Else, with more of
-        // the chunks to come, the n best are kept.
-        const bool again = count > kBufNew;
-        if (tid == 0) sm.again = again;
-        if (again) join<NT>(sm, kBufNew, a.n, false);
-        else if (k0 < a.beams) join<NT>(sm, count, a.n, true);
+        if (tid == 0) {
+          sm.next = next;
+          if (next == kStretches) sm.count = 0, sm.overflow = 0;
+        }
       }
       if (R > 1) {
         cluster_sync();
         if (rank != 0 && tid == 0)
-          sm.again = hub.again, sm.T = hub.T, sm.exact = hub.exact, sm.bound = hub.bound;
+          sm.next = hub.next, sm.T = hub.T, sm.exact = hub.exact, sm.bound = hub.bound;
       }
       __syncthreads();
-      if (!sm.again) break;
+      if (sm.next != kAgain) break;
     }
+    if (sm.next == kStretches) whole = false, k0 = 0, turn = 0;
+    if (k0 >= a.beams) break;
+    __syncthreads();
     if (tid == 0) sm.list_n = 0;
     __syncthreads();
   }

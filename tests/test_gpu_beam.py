@@ -257,3 +257,23 @@ def test_logits_are_not_written_and_bad_arguments():
         ops.beam_select(t, sc, 3, out=(sc, sc, sc))
     with pytest.raises(Exception, match="too large"):
         ops.beam_select(t, sc, 257)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("n", [3, 40, 200])
+@pytest.mark.parametrize("batch, beams, V, kept", [(2, 64, 40001, 0), (1, 256, 16000, 5),
+                                                   (2, 5, 1100003, 17)])
+def test_more_chunks_at_the_bound_than_a_list_holds(dtype, n, batch, beams, V, kept):
+    """Every chunk's maximum is the row's: the first tokens of the first beam come out.
+    `kept`: the rows' first tokens are lower, so the winners begin behind them."""
+    t = torch.ones(batch * beams, V, dtype=TYPES[dtype], device="cuda")
+    t[:, :kept] = 0.5
+    t[:, 3 * V // 4:] = 1.0
+    scores = np.full((batch, beams), -1.5, dtype=np.float32)
+    scores[:, 0] = -2.0
+    scores[-1, 1] = -np.inf
+    s, k, p = run(t, scores, n, V)
+    for b in range(batch):
+        first = 1 if b < batch - 1 else 2
+        assert (p[b] == first).all() and k[b].tolist() == list(range(kept, kept + n))
+        assert len(set(s[b])) == 1
