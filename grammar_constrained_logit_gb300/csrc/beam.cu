@@ -24,7 +24,7 @@ namespace lp {
 namespace {
 
 constexpr int kStreamThreads = 256;
-constexpr int kVecs = 4;              // 16-byte groups a lane holds of a chunk
+constexpr int kVecs = 4;              // 16-byte groups a lane holds of a chunk, at most
 constexpr int kGroups = 512;          // lanes' bests that the bound is taken from
 constexpr int kMaxSelect = 256;       // largest n_select and beams
 constexpr int kBuf = 1024;            // candidates held at once (a power of two)
@@ -33,8 +33,10 @@ constexpr int64_t kMostStaged = 128 * 1024;  // bytes of chunks' maxima held in 
 constexpr int kBufNew = kBuf - kMaxSelect;
 constexpr int kSms = 152;
 
-template <int DT>
-constexpr int kChunk = kVecs * 32 * Elt<DT>::kPerVec;  // tokens: 512 f32, 1024 16-bit
+// Tokens of a chunk of N groups a lane: 512 f32 or 1024 of 16 bits with four; a quarter of
+// that with one.
+template <int DT, int N>
+constexpr int kChunk = N * 32 * Elt<DT>::kPerVec;
 
 struct BeamArgs {
   const char* logits;
@@ -47,6 +49,7 @@ struct BeamArgs {
   const uint8_t* finished;
   int64_t pad;
   int rows, beams, n, chunks;
+  int chunk_tokens;
   int staged;      // a batch entry's chunks fit in shared memory
   int sum_bits;    // S <= V is held in units of 2^-sum_bits, within 63 bits
   float2* part;  // [rows, chunks]: (max, sum of exp(x - max)); rows that are dead or finished: not written
@@ -122,55 +125,66 @@ __device__ __forceinline__ uint32_t group_keep(const uint32_t* __restrict__ bm, 
   return k;
 }
 
-// A chunk's groups of this lane, masked tokens as -inf.  EARLY: the logits do not wait
-// for the mask's bits, which costs the bytes that these would have spared.
-template <int DT, bool EARLY>
-__device__ __forceinline__ void load_chunk(uint4 (&v)[kVecs], const char* row, const uint32_t* bm,
-                                           int64_t j0, int64_t V, int lane) {
+// Keep bits of a lane's tokens in a chunk, a group's in E bits; clear from V on.
+template <int DT, int N>
+__device__ __forceinline__ uint32_t chunk_keep(const uint32_t* bm, int64_t j0, int64_t V,
+                                               int lane) {
+  constexpr int E = Elt<DT>::kPerVec;
+  uint32_t keep = 0;
+  if (j0 + kChunk<DT, N> <= V) {
+    if (bm == nullptr) return N * E == 32 ? 0xffffffffu : (1u << (N * E)) - 1u;
+    const uint8_t* mask = reinterpret_cast<const uint8_t*>(bm) + (j0 + lane * E) / 8;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint32_t m = __ldg(mask + i * (4 * E));
+      if (E == 4) m = m >> (lane & 1) * 4 & 15u;
+      keep |= m << (i * E);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      keep |= group_keep<DT>(bm, j0 + (i * 32 + lane) * E, V) << (i * E);
+  }
+  return keep;
+}
+
+// A chunk's groups of this lane, masked tokens as -inf.  ALL: groups that the mask leaves
+// out are loaded too, so that the loads do not wait for its bits.
+template <int DT, int N, bool ALL>
+__device__ __forceinline__ void load_chunk(uint4 (&v)[N], const char* row, uint32_t keep,
+                                           bool masked, int64_t j0, int64_t V, int lane) {
   constexpr int E = Elt<DT>::kPerVec;
   constexpr uint32_t kAll = (1u << E) - 1u;
   const int sh = int(reinterpret_cast<uintptr_t>(row) & 15);
   const uint32_t none = neg_inf_word<DT>();
-  if (j0 + kChunk<DT> + (sh ? E : 0) <= V && (sh == 0 || j0 > 0)) {
+  if (j0 + kChunk<DT, N> + (sh ? E : 0) <= V && (sh == 0 || j0 > 0)) {
     // within the row: nothing to check token by token
-    const char* p = row + (j0 + lane * E) * Elt<DT>::kBytes - sh;
-    auto load = [&](int i) {
-      const uint4* q = reinterpret_cast<const uint4*>(p) + i * 32;
-      return sh == 0 ? __ldg(q) : shifted(__ldg(q), __ldg(q + 1), sh);
-    };
-    if (bm == nullptr) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + (j0 + lane * E) * Elt<DT>::kBytes - sh);
+    if (!masked) {
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) v[i] = load(i);
+      for (int i = 0; i < N; ++i)
+        v[i] = sh == 0 ? __ldg(p + i * 32) : shifted(__ldg(p + i * 32), __ldg(p + i * 32 + 1), sh);
       return;
     }
-    const uint8_t* mask = reinterpret_cast<const uint8_t*>(bm) + (j0 + lane * E) / 8;
-    uint32_t keep[kVecs];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      keep[i] = __ldg(mask + i * (4 * E));
-      if (E == 4) keep[i] = (keep[i] >> (lane & 1) * 4) & kAll;
+    for (int i = 0; i < N; ++i) {
+      if (!ALL) v[i] = make_uint4(none, none, none, none);
+      if (ALL || (keep >> (i * E) & kAll))
+        v[i] = sh == 0 ? __ldg(p + i * 32) : shifted(__ldg(p + i * 32), __ldg(p + i * 32 + 1), sh);
     }
+  } else {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
+    for (int i = 0; i < N; ++i) {
+      const int64_t j = j0 + (i * 32 + lane) * E;
       v[i] = make_uint4(none, none, none, none);
-      if (EARLY || keep[i]) v[i] = load(i);
+      if (ALL ? j < V : (keep >> (i * E) & kAll) != 0) v[i] = load_group<DT>(row, j, V, sh);
     }
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (keep[i] != kAll) v[i] = Elt<DT>::blend(v[i], keep[i], none);
-    return;
-  }
-  uint32_t keep[kVecs];
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int64_t j = j0 + (i * 32 + lane) * E;
-    keep[i] = group_keep<DT>(bm, j, V);
-    v[i] = make_uint4(none, none, none, none);
-    if (keep[i]) v[i] = load_group<DT>(row, j, V, sh);
   }
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-    if (keep[i] != kAll) v[i] = Elt<DT>::blend(v[i], keep[i], none);
+  for (int i = 0; i < N; ++i) {
+    const uint32_t k = keep >> (i * E) & kAll;
+    if (k != kAll) v[i] = Elt<DT>::blend(v[i], k, none);
+  }
 }
 
 // Element `at` of a chunk's groups, a number known only at run time.
@@ -184,16 +198,6 @@ __device__ __forceinline__ float element(const uint4 (&v)[kVecs], unsigned at) {
   const uint32_t pair = e & 4 ? (e & 2 ? w.w : w.z) : (e & 2 ? w.y : w.x);
   const uint32_t half = e & 1 ? pair >> 16 : pair & 0xffffu;
   return DT == LP_BF16 ? __uint_as_float(half << 16) : Elt<LP_F16>::half_bits_to_float(half);
-}
-
-__device__ __forceinline__ bool row_live(const BeamArgs& a, int row) {
-  return __ldg(a.scores + row) > -INFINITY &&
-         (a.finished == nullptr || __ldg(a.finished + row) == 0);
-}
-
-__device__ __forceinline__ const uint32_t* row_mask(const BeamArgs& a, int row) {
-  if (a.bitmask == nullptr || (a.needs != nullptr && __ldg(a.needs + row) == 0)) return nullptr;
-  return a.bitmask + int64_t(row) * a.bm_stride;
 }
 
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -235,12 +239,12 @@ __device__ __forceinline__ uint64_t differences(const uint4& v, int e, float m) 
 // Sum over a lane's tokens of exp(x - m).  The difference comes first: it is exact near
 // the maximum, where the sum comes from, however far from zero the logits are.  -inf
 // gives 2^-inf = 0; a NaN, or m infinite, gives NaN, and the caller sums again with care.
-template <int DT>
-__device__ __forceinline__ float sum_exp(const uint4 (&v)[kVecs], float m) {
+template <int DT, int N>
+__device__ __forceinline__ float sum_exp(const uint4 (&v)[N], float m) {
   const uint64_t scale = pack2(kLog2e, kLog2e);
   uint64_t s[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
+  for (int i = 0; i < N; ++i) {
 #pragma unroll
     for (int e = 0; e < Elt<DT>::kPerVec; e += 2) {
       const uint64_t t = mul2(differences<DT>(v[i], e, m), scale);
@@ -253,11 +257,11 @@ __device__ __forceinline__ float sum_exp(const uint4 (&v)[kVecs], float m) {
 
 // The same where there is a NaN, which is no candidate, or a maximum of +inf, whose
 // tokens share all of the mass.
-template <int DT>
-__device__ __forceinline__ float sum_exp_careful(const uint4 (&v)[kVecs], float m) {
+template <int DT, int N>
+__device__ __forceinline__ float sum_exp_careful(const uint4 (&v)[N], float m) {
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i)
+  for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int e = 0; e < Elt<DT>::kPerVec; ++e) {
       const float x = Elt<DT>::get(v[i], e);
@@ -273,11 +277,42 @@ __device__ __forceinline__ float warp_max(float m) {
   return m;
 }
 
-// EARLY: for problems of one chunk a warp, which only wait for memory: the loads wait
-// neither for the row's state nor for its mask.  Loads overlap between warps, not within
-// one: a second chunk in registers (79 of them) took the blocks of an SM from 5 to 3 and
-// 128 x 8 rows of 202048 fp16 from 76 to 88 us.
-template <int DT, bool EARLY>
+// What a warp knows of a chunk before it reads its tokens.
+template <int DT, int N>
+struct At {
+  int row, c;
+  bool live, masked;
+  uint32_t keep;
+
+  // AT_ONCE: the loads do not wait for one another; the mask is read for nothing where the
+  // row is dead or not masked.
+  template <bool AT_ONCE>
+  __device__ __forceinline__ void find(const BeamArgs& a, int lane) {
+    const float s = __ldg(a.scores + row);
+    const uint8_t fin = a.finished != nullptr ? __ldg(a.finished + row) : 0;
+    const uint8_t need = a.needs != nullptr ? __ldg(a.needs + row) : 1;
+    masked = a.bitmask != nullptr;
+    if (!AT_ONCE) {
+      masked = masked && need != 0;
+      live = s > -INFINITY && fin == 0;
+    }
+    const int64_t j0 = int64_t(c) * kChunk<DT, N>;
+    if (AT_ONCE || live)
+      keep = chunk_keep<DT, N>(masked ? a.bitmask + int64_t(row) * a.bm_stride : nullptr, j0, a.V,
+                               lane);
+    if (AT_ONCE) {
+      if (masked && need == 0) keep = chunk_keep<DT, N>(nullptr, j0, a.V, lane), masked = false;
+      live = s > -INFINITY && fin == 0;
+    }
+  }
+};
+
+// EARLY: for problems of one chunk a warp, which only wait for memory: the tokens' loads
+// wait neither for the row's state nor for its mask.  Loads overlap between warps, not
+// within one.  A second chunk in registers (79 of them) took the blocks of an SM from 5 to
+// 3 and 128 x 8 rows of 202048 fp16 from 76 to 88 us; the next chunk's state and mask
+// asked for ahead took 24 x 5 rows of 65519 from 12.7 to 14.0 us.
+template <int DT, int N, bool EARLY>
 __global__ void __launch_bounds__(kStreamThreads) beam_stream_kernel(BeamArgs a) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -286,23 +321,24 @@ __global__ void __launch_bounds__(kStreamThreads) beam_stream_kernel(BeamArgs a)
   const unsigned step = gridDim.x * (kStreamThreads / 32);
   for (unsigned w = blockIdx.x * (kStreamThreads / 32) + (threadIdx.x >> 5); w < total;
        w += step) {
-    const int row = int(w / unsigned(a.chunks)), c = int(w % unsigned(a.chunks));
-    const bool live = row_live(a, row);
-    if (!EARLY && !live) continue;
-    uint4 v[kVecs];
-    load_chunk<DT, EARLY>(v, a.logits + row * a.stride, row_mask(a, row),
-                          int64_t(c) * kChunk<DT>, a.V, lane);
-    if (!live) continue;
+    At<DT, N> at;
+    at.row = int(w / unsigned(a.chunks)), at.c = int(w % unsigned(a.chunks));
+    at.template find<EARLY>(a, lane);
+    if (!EARLY && !at.live) continue;
+    uint4 v[N];
+    load_chunk<DT, N, EARLY>(v, a.logits + at.row * a.stride, at.keep, at.masked,
+                             int64_t(at.c) * kChunk<DT, N>, a.V, lane);
+    if (!at.live) continue;
     float m = VecMax<DT>::run(v[0], 0xffu);
 #pragma unroll
-    for (int i = 1; i < kVecs; ++i) m = fmaxf(m, VecMax<DT>::run(v[i], 0xffu));
+    for (int i = 1; i < N; ++i) m = fmaxf(m, VecMax<DT>::run(v[i], 0xffu));
     m = fmaxf(warp_max(m), -INFINITY);  // nothing but NaN: no candidate
-    float sum = sum_exp<DT>(v, m);
+    float sum = sum_exp<DT, N>(v, m);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
     if (!(sum < INFINITY)) {
       sum = 0.0f;
-      if (m > -INFINITY) sum = sum_exp_careful<DT>(v, m);
+      if (m > -INFINITY) sum = sum_exp_careful<DT, N>(v, m);
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
     }
@@ -460,7 +496,7 @@ struct FinishSmem {
   unsigned best[kGroups];
   LogEntry log_table[128];
   unsigned list[kList];       // chunks to go through
-  int list_n, count, front_n, exact, overflow, next;
+  int list_n, count, front_n, exact, overflow, next, raised;
   float T;
   Cand bound;                 // exact: candidates worse than this are out
 };
@@ -579,13 +615,16 @@ __device__ __forceinline__ unsigned beam_sums(FinishSmem& sm, const BeamArgs& a,
 // The n-th largest of the warp's keys, N a lane, taken low: measured from the largest, in
 // steps of 1/64 of the distance (1/1024 at the least), as a bound need not be tight.  -inf
 // when fewer than n are there.
-template <int N>
-__device__ __forceinline__ float nth_largest(const unsigned* keys, int n) {
+__device__ __forceinline__ unsigned key_at(const unsigned* keys, int i) { return keys[i]; }
+__device__ __forceinline__ unsigned key_at(const Cand* c, int i) { return unsigned(c[i].key >> 32); }
+
+template <int N, typename K>
+__device__ __forceinline__ float nth_largest(const K* keys, int n) {
   constexpr int kBase = (127 - 4) << 6;  // 2^-4, in steps of 2^-6 of a power of two
   const int lane = threadIdx.x & 31;
   unsigned mine[N], most = 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) most = max(most, mine[i] = keys[i * 32 + lane]);
+  for (int i = 0; i < N; ++i) most = max(most, mine[i] = key_at(keys, i * 32 + lane));
   most = __reduce_max_sync(kFullWarp, most);
   const float top = key_float(most);
   int near[N];  // 2047 at the largest, 0 where there is none or it is 2^28 away
@@ -628,8 +667,8 @@ __device__ __forceinline__ FinishSmem* of_first_block(FinishSmem* p) {
   return reinterpret_cast<FinishSmem*>(r);
 }
 
-template <int DT, int NT, int R>
-__global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
+template <int DT, int NT, int R, int B>
+__global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
   constexpr int NW = NT / 32;
   extern __shared__ __align__(16) char raw[];
   FinishSmem& sm = *reinterpret_cast<FinishSmem*>(raw);
@@ -659,20 +698,21 @@ __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
 
   // A lower bound T of the n-th best score: the n-th largest of these lanes' bests, each a
   // candidate of its own.  With few lanes to the n, of one chunk a thread instead.
-  const bool few = 32 * per_turn < 4 * a.n;
+  const bool few = min(C, 32) * per_turn < 4 * a.n;
   if (few) {
     __syncthreads();
     best = 0;
-    for (int k = my_beam; k < a.beams; k += per_turn) {
-      const float M = sm.top[k], s = sm.score[k], z = sm.log_s[k].hi;
+    const unsigned total = unsigned(a.beams) * unsigned(C);
+    for (unsigned i = tid; i < total; i += NT) {
+      const int k = int(i / unsigned(C)), c = int(i % unsigned(C));
+      const float M = sm.top[k], s = sm.score[k];
       if (M == -INFINITY) continue;
       if (sm.ended[k]) {
-        if (c_first == 0) best = max(best, fkey(s));
+        if (c == 0) best = max(best, fkey(s));
         continue;
       }
-      float mine = -INFINITY;
-      for (int c = c_first; c < C; c += c_step) mine = fmaxf(mine, chunk_max(k, c));
-      if (mine > -INFINITY) best = max(best, low_key(s, M, z, mine));
+      const float m = chunk_max(k, c);
+      if (m > -INFINITY) best = max(best, low_key(s, M, sm.log_s[k].hi, m));
     }
   }
   if (NT > kGroups) {
@@ -749,8 +789,11 @@ __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
         const float least = least_of(sm, k, sm.T);
         const char* row = a.logits + int64_t(row0 + k) * a.stride;
         const uint32_t* bm = sm.masked[k] ? a.bitmask + int64_t(row0 + k) * a.bm_stride : nullptr;
+        // (a small chunk is the beginning of a large one that ends there)
+        const int64_t j0 = int64_t(c) * a.chunk_tokens, end = min(a.V, j0 + a.chunk_tokens);
         uint4 v[kVecs];
-        load_chunk<DT, true>(v, row, bm, int64_t(c) * kChunk<DT>, a.V, lane);
+        load_chunk<DT, kVecs, true>(v, row, chunk_keep<DT, kVecs>(bm, j0, end, lane),
+                                    bm != nullptr, j0, end, lane);
         uint32_t hits = 0;
 #pragma unroll
         for (int g = 0; g < kVecs; ++g)
@@ -761,7 +804,7 @@ __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
           }
         for (; hits; hits &= hits - 1) {
           const unsigned bit = __ffs(hits) - 1;
-          const unsigned j = unsigned(c) * kChunk<DT> + lane * Elt<DT>::kPerVec +
+          const unsigned j = unsigned(j0) + lane * Elt<DT>::kPerVec +
                              bit / Elt<DT>::kPerVec * (32 * Elt<DT>::kPerVec) +
                              bit % Elt<DT>::kPerVec;
           found(Cand{key_of(score_of(sm, k, element<DT>(v, bit))), flat0 + j});
@@ -776,10 +819,19 @@ __global__ void __launch_bounds__(NT, 1) beam_finish_kernel(BeamArgs a) {
         if (sm.overflow) {
           next = kStretches;
         } else if (count > kBufNew) {
-          // too many: what was seen raises the bound (strictly, as kBufNew > n and no two
-          // candidates are equal), and the list is gone through again
+          // too many: what was seen raises the bound, and the list is gone through again.
+          // By its score where that is above the last, else by the whole order (strictly,
+          // as kBufNew > n and no two candidates are equal)
           next = kAgain;
-          join<NT>(sm, kBufNew, a.n, false);
+          if (!exact) {
+            if (warp == 0) {
+              const float T = nth_largest<kGroups / 32>(sm.buf, a.n);
+              if (lane == 0) sm.raised = T > sm.T, sm.T = fmaxf(T, sm.T);
+            }
+            __syncthreads();
+          }
+          if (exact || !sm.raised) join<NT>(sm, kBufNew, a.n, false);
+          else if (tid == 0) sm.count = 0;
         } else if (k0 < a.beams) {
           join<NT>(sm, count, a.n, true);  // with chunks to come, the n best are kept
         }
@@ -844,14 +896,14 @@ int resident_blocks(K kernel) {
   return std::max(1, n) * kSms;
 }
 
-template <int DT, int NT, int R>
+template <int DT, int NT, int R, int B>
 cudaError_t finish_with(cudaLaunchConfig_t cfg, BeamArgs a, int64_t batch) {
   static_assert(sizeof(FinishSmem) <= 48 * 1024, "within the default limit");
   const int64_t staged = int64_t(a.beams) * a.chunks * 4;
   a.staged = staged <= kMostStaged;
   cfg.dynamicSmemBytes = sizeof(FinishSmem) + (a.staged ? size_t(staged) : 0);
   if (cfg.dynamicSmemBytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(beam_finish_kernel<DT, NT, R>,
+    const cudaError_t e = cudaFuncSetAttribute(beam_finish_kernel<DT, NT, R, B>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                int(sizeof(FinishSmem) + kMostStaged));
     if (e != cudaSuccess) return e;
@@ -865,23 +917,39 @@ cudaError_t finish_with(cudaLaunchConfig_t cfg, BeamArgs a, int64_t batch) {
   cfg.numAttrs = R > 1 ? 2 : 1;
   cfg.gridDim = dim3(unsigned(batch * R));
   cfg.blockDim = dim3(NT);
-  return cudaLaunchKernelEx(&cfg, beam_finish_kernel<DT, NT, R>, a);
+  return cudaLaunchKernelEx(&cfg, beam_finish_kernel<DT, NT, R, B>, a);
 }
 
 template <int DT>
 cudaError_t finish(const cudaLaunchConfig_t& cfg, const BeamArgs& a, int64_t batch) {
-  const int64_t total = int64_t(a.beams) * a.chunks;
-#ifdef LP_NT
-  return finish_with<DT, LP_NT, LP_R>(cfg, a, batch);
-#endif
-  if (a.n > 32 && batch * 8 <= kSms) return finish_with<DT, 1024, 8>(cfg, a, batch);
-  if (total > 1600) return finish_with<DT, 1024, 1>(cfg, a, batch);
-  return finish_with<DT, 512, 1>(cfg, a, batch);
+  // Many to find: a cluster of blocks goes through the chunks side by side.  4 x 64 rows of
+  // 32000 bf16, n = 128: 24 us with it, 39 without.  With n up to 32 one block's 16 warps
+  // do in a round or two (53 x 32 rows of 52332 f32, n = 32: 64 us without, 74 with), and
+  // with batches that fill the SMs the cluster only repeats its sums.
+  if (a.n > 32 && batch * 8 <= kSms) return finish_with<DT, 512, 8, 1>(cfg, a, batch);
+  // One block an SM may take 80 registers a thread (8 x 4 rows of 128256 bf16: 9.2 us, with
+  // 64 of them 10.3); with more blocks than SMs two have to fit (161 x 8 rows of 17976:
+  // 26.6 us, else 32.5).
+  if (batch > kSms) return finish_with<DT, 512, 1, 2>(cfg, a, batch);
+  return finish_with<DT, 512, 1, 1>(cfg, a, batch);
+}
+
+template <int DT, int N>
+cudaError_t stream_with(cudaLaunchConfig_t cfg, const BeamArgs& a) {
+  static const int resident = resident_blocks(beam_stream_kernel<DT, N, false>);
+  static const int resident_early = resident_blocks(beam_stream_kernel<DT, N, true>);
+  const int64_t blocks = (int64_t(a.rows) * a.chunks + 7) / 8;
+  cfg.blockDim = dim3(kStreamThreads);
+  if (blocks <= resident_early) {
+    cfg.gridDim = dim3(unsigned(blocks));
+    return cudaLaunchKernelEx(&cfg, beam_stream_kernel<DT, N, true>, a);
+  }
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(blocks, resident)));
+  return cudaLaunchKernelEx(&cfg, beam_stream_kernel<DT, N, false>, a);
 }
 
 template <int DT>
-cudaError_t launch(const BeamArgs& a0, int64_t batch, cudaStream_t stream) {
-  BeamArgs a = a0;
+cudaError_t launch(const BeamArgs& a, int64_t batch, cudaStream_t stream) {
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -889,23 +957,24 @@ cudaError_t launch(const BeamArgs& a0, int64_t batch, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  static const int resident = resident_blocks(beam_stream_kernel<DT, false>);
-  static const int resident_early = resident_blocks(beam_stream_kernel<DT, true>);
-  const int64_t blocks = (int64_t(a.rows) * a.chunks + 7) / 8;
-  cfg.blockDim = dim3(kStreamThreads);
-  cudaError_t e;
-  if (blocks <= resident_early) {
-    cfg.gridDim = dim3(unsigned(blocks));
-    e = cudaLaunchKernelEx(&cfg, beam_stream_kernel<DT, true>, a);
-  } else {
-    cfg.gridDim = dim3(unsigned(std::min<int64_t>(blocks, resident)));
-    e = cudaLaunchKernelEx(&cfg, beam_stream_kernel<DT, false>, a);
-  }
+  const cudaError_t e = a.chunk_tokens == kChunk<DT, kVecs> ? stream_with<DT, kVecs>(cfg, a)
+                                                            : stream_with<DT, 1>(cfg, a);
   if (e != cudaSuccess) return e;
   return finish<DT>(cfg, a, batch);
 }
 
-int64_t chunk_tokens(lp_dtype dt) { return dt == LP_F32 ? kChunk<LP_F32> : kChunk<LP_F16>; }
+// Tokens of the chunks of a call.  The bound is an n-th largest chunk maximum, so with few
+// chunks to the n it admits too much: small ones then.
+int64_t chunk_tokens(lp_dtype dt, int64_t beams, int64_t V, int64_t n) {
+  const int64_t large = dt == LP_F32 ? kChunk<LP_F32, kVecs> : kChunk<LP_F16, kVecs>;
+  return beams * ((V + large - 1) / large) < 8 * n ? large / kVecs : large;
+}
+
+// Rows of a call's workspace hold this many chunks at most, whatever its n.
+int64_t most_chunks(lp_dtype dt, int64_t V) {
+  const int64_t small = (dt == LP_F32 ? kChunk<LP_F32, kVecs> : kChunk<LP_F16, kVecs>) / kVecs;
+  return std::max<int64_t>(1, V / small + (V % small != 0));
+}
 
 bool known(lp_dtype dt) { return dt == LP_F32 || dt == LP_F16 || dt == LP_BF16; }
 
@@ -914,10 +983,8 @@ bool known(lp_dtype dt) { return dt == LP_F32 || dt == LP_F16 || dt == LP_BF16; 
 
 extern "C" int64_t lp_beam_select_workspace_bytes(lp_dtype dt, int64_t rows, int64_t vocab_size) {
   if (!lp::known(dt) || rows < 0 || vocab_size < 0) return -1;
-  const int64_t T = lp::chunk_tokens(dt);
-  const int64_t chunks = std::max<int64_t>(1, vocab_size / T + (vocab_size % T != 0));
-  if (rows > INT64_MAX / 8 / chunks) return -1;
-  return rows * chunks * 8;
+  const int64_t chunks = lp::most_chunks(dt, vocab_size);
+  return rows > INT64_MAX / 8 / chunks ? -1 : rows * chunks * 8;
 }
 
 extern "C" lp_status lp_beam_select(const void* logits, lp_dtype dt, int64_t batch, int64_t beams,
@@ -956,7 +1023,8 @@ extern "C" lp_status lp_beam_select(const void* logits, lp_dtype dt, int64_t bat
       logits_stride > INT64_MAX / eb / rows)
     return LP_ERR_INVALID_ARGUMENT;
   const int64_t need = lp_beam_select_workspace_bytes(dt, rows, V);
-  const int64_t chunks = std::max<int64_t>(1, (V + chunk_tokens(dt) - 1) / chunk_tokens(dt));
+  const int64_t tokens = chunk_tokens(dt, beams, V, n_select);
+  const int64_t chunks = std::max<int64_t>(1, (V + tokens - 1) / tokens);
   if (rows > INT32_MAX / chunks) return LP_ERR_TOO_LARGE;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
                    reinterpret_cast<uintptr_t>(workspace) % 8 != 0))
@@ -975,6 +1043,7 @@ extern "C" lp_status lp_beam_select(const void* logits, lp_dtype dt, int64_t bat
   a.beams = int(beams);
   a.n = int(n_select);
   a.chunks = int(chunks);
+  a.chunk_tokens = int(tokens);
   a.sum_bits = 40;
   while (a.sum_bits > 32 && (V >> (63 - a.sum_bits)) > 0) --a.sum_bits;
   a.part = static_cast<float2*>(workspace);

@@ -53,7 +53,8 @@ def test_beam_select_refusals(lib, kw, want):
 
 def test_beam_workspace_bytes(lib):
     f = lib.lp_beam_select_workspace_bytes
-    assert f(2, 8, 1024) == 64 and f(2, 8, 1025) == 128 and f(0, 8, 1024) == 128
+    # 8 bytes for each 256 16-bit or 128 f32 tokens of a row
+    assert f(2, 8, 1024) == 256 and f(2, 8, 1025) == 320 and f(0, 8, 1024) == 512
     assert f(1, 0, 5) == 0 and f(1, 3, 0) == 24
     assert f(7, 1, 1) == -1 and f(0, -1, 1) == -1 and f(0, 1, -1) == -1
     assert f(0, 1 << 60, 1 << 40) == -1
