@@ -20,7 +20,6 @@ namespace {
 
 constexpr int kMaxParts = 8;
 constexpr int kThreads = 256;
-constexpr int kMaxVecs = 4;     // vectors a lane holds of one group
 constexpr float kLargest = 3.3895313892515355e38f;
 constexpr float kTiny = 1.1754943508222875e-38f;  // 2^-126
 
@@ -47,10 +46,11 @@ struct CacheArgs {
   int64_t n, n_slots, page;
   int heads, dim, group;
   Div per_page;  // where slots are below 2^31
-  // of the vector kernels
-  Div per_token, per_head, per_group;  // groups (write) or units (read); units of a group (read)
-  uint32_t total;                      // groups or units of a part
-  int lanes, reach, segments;          // write: lanes a group, the power of two from there, groups a warp
+  // of the vector kernels: a token has `per_token` items (groups to write, vectors to
+  // read) and a block takes `tokens` tokens at a time, or one of `tiles` parts of a token
+  Div per_token, per_head, tiles, per_group;
+  int items, tokens;                // a block's items at a time; of how many tokens
+  int lanes, reach, segments;       // write: lanes a group, the power of two from there, groups a warp
 };
 
 template <int DT>
@@ -125,27 +125,23 @@ __device__ __forceinline__ uint32_t code4(float x, const Scale& s) {
   return __float_as_uint(__fadd_rn(fminf(fmaxf(y, 0.0f), 15.0f), 8388608.0f)) & 15u;
 }
 
-// Where a slot's head lies, from a part's base.
+// Where a slot lies, from a part's base.
 __device__ __forceinline__ int64_t place(const CacheArgs& a, int64_t slot, int64_t page_stride,
-                                         int64_t slot_stride, int64_t head, int64_t head_stride) {
-  int64_t at = slot, pages = 0;
-  if (a.page < a.n_slots) {  // more than one page
-    const int64_t p = a.n_slots <= INT32_MAX ? int64_t(a.per_page.quot(uint32_t(slot)))
-                                             : slot / a.page;
-    at = slot - p * a.page;
-    pages = p * page_stride;
-  }
-  return pages + at * slot_stride + head * head_stride;
+                                         int64_t slot_stride) {
+  if (a.page >= a.n_slots) return slot * slot_stride;  // one page
+  const int64_t p = a.n_slots <= INT32_MAX ? int64_t(a.per_page.quot(uint32_t(slot)))
+                                           : slot / a.page;
+  return p * page_stride + (slot - p * a.page) * slot_stride;
 }
 
 __device__ __forceinline__ int64_t code_place(const CacheArgs& a, const lp_cache_part& p,
-                                              int64_t slot, int head) {
-  return place(a, slot, p.code_page_stride, p.code_slot_stride, head, p.code_head_stride);
+                                              int64_t slot) {
+  return place(a, slot, p.code_page_stride, p.code_slot_stride);
 }
 
 __device__ __forceinline__ int64_t param_place(const CacheArgs& a, const lp_cache_part& p,
-                                               int64_t slot, int head) {
-  return place(a, slot, p.param_page_stride, p.param_slot_stride, head, p.param_head_stride);
+                                               int64_t slot) {
+  return place(a, slot, p.param_page_stride, p.param_slot_stride);
 }
 
 // One warp a group.
@@ -174,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     }
     const Scale s = scale_of<BITS>(r);
     uint8_t* codes = static_cast<uint8_t*>(part.codes) +
-                     code_place(a, part, slot, h) + int64_t(g) * a.group * BITS / 8;
+                     code_place(a, part, slot) + h * part.code_head_stride + int64_t(g) * a.group * BITS / 8;
     if (BITS == 8) {
       for (int e = lane; e < a.group; e += 32)
         codes[e] = uint8_t(e4m3_pair(__fmul_rn(load_float<DT>(x + e * Bt), s.inv), 0.0f));
@@ -185,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     }
     if (lane == 0)
       *reinterpret_cast<uint32_t*>(static_cast<char*>(part.params) +
-                                   param_place(a, part, slot, h) +
+                                   param_place(a, part, slot) + h * part.param_head_stride +
                                    int64_t(g) * 4) = s.held;
   }
 }
@@ -208,10 +204,10 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
     float v[2] = {0.0f, 0.0f};
     if (slot >= 0 && slot < a.n_slots) {
       const uint32_t code = *(static_cast<const uint8_t*>(part.codes) +
-                              code_place(a, part, slot, h) + c);
+                              code_place(a, part, slot) + h * part.code_head_stride + c);
       const uint32_t held = *reinterpret_cast<const uint32_t*>(
           static_cast<const char*>(part.params) +
-          param_place(a, part, slot, h) + int64_t(c * E / a.group) * 4);
+          param_place(a, part, slot) + h * part.param_head_stride + int64_t(c * E / a.group) * 4);
       if (BITS == 8) {
         v[0] = __fmul_rn(e4m3_value(code), __uint_as_float(held));
       } else {
@@ -250,12 +246,17 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// Packed maximum and minimum of 16-bit pairs; a NaN gives way to the other operand.
+// Packed maximum and minimum of 16-bit pairs; in a maximum a NaN stays.
 template <int DT>
 __device__ __forceinline__ uint32_t max16(uint32_t a, uint32_t b) {
   uint32_t r;
-  if (DT == LP_BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  if (DT == LP_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 template <int DT>
@@ -299,18 +300,18 @@ struct Vec {
     if (DT == LP_F32) return uint64_t(w[2 * i]) | uint64_t(w[2 * i + 1]) << 32;
     return floats16<DT>(w[i]);
   }
-  // The finite range, for 8 bits as (-most, most).  Minimum and maximum leave NaN out by
-  // themselves, an infinity shows in the result, and only then the elements are gone
-  // through one by one.
+  // The finite range, for 8 bits as (-most, most).  An infinity or a NaN shows in the
+  // result, and only then the elements are gone through one by one.  *fine: there is none.
   template <int BITS>
-  __device__ __forceinline__ Range range() const {
+  __device__ __forceinline__ Range range(bool* fine) const {
     Range r;
+    *fine = true;
     if (DT == LP_F32) {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const float x = __uint_as_float(w[i]);
-        if (BITS == 8) r.hi = fmaxf(r.hi, fabsf(x));
-        else r.lo = fminf(r.lo, x), r.hi = fmaxf(r.hi, x);
+        if (BITS == 8) r.hi = max_nan(r.hi, fabsf(x));
+        else r.lo = fminf(r.lo, x), r.hi = max_nan(r.hi, x);
       }
     } else {
       uint32_t hi = BITS == 8 ? w[0] & 0x7fff7fffu : w[0], lo = w[0];
@@ -320,11 +321,12 @@ struct Vec {
         if (BITS == 4) lo = min16<DT>(lo, w[i]);
       }
       const uint64_t h = floats16<DT>(hi), l = floats16<DT>(lo);
-      r.hi = fmaxf(first(h), second(h));
+      r.hi = max_nan(first(h), second(h));
       r.lo = fminf(first(l), second(l));
     }
     if (BITS == 8) r.lo = -r.hi;
-    if (!(fmaxf(fabsf(r.lo), fabsf(r.hi)) <= kLargest)) {
+    if (!(r.hi <= kLargest && r.lo >= -kLargest)) {
+      *fine = false;
       r = Range();
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) r.add(first(pair(i))), r.add(second(pair(i)));
@@ -334,8 +336,39 @@ struct Vec {
   }
 };
 
+// What a thread works on: item `idx` of token `t`, and of every `step`-th after it.
+struct Work {
+  int64_t t, step;
+  int head, idx;
+  bool there;
+};
+
+// item: this thread's among the block's
+template <int U>
+__device__ __forceinline__ Work work_of(const CacheArgs& a, uint32_t item) {
+  Work w;
+  uint32_t block = blockIdx.x, sub = 0, idx = item;
+  if (a.tiles.d > 1) {
+    block = a.tiles.quot(blockIdx.x);
+    idx += (blockIdx.x - block * a.tiles.d) * a.items;
+  } else {
+    sub = a.per_token.quot(item);
+    idx -= sub * a.per_token.d;
+  }
+  w.there = item < uint32_t(a.items) && idx < a.per_token.d;
+  w.t = int64_t(block) * U * a.tokens + sub;
+  w.step = a.tokens;
+  w.head = 0;
+  w.idx = int(idx);
+  if (a.heads > 1) {
+    w.head = int(a.per_head.quot(idx));
+    w.idx -= w.head * int(a.per_head.d);
+  }
+  return w;
+}
+
 // A group on `lanes` neighbouring lanes, R vectors a lane, as many groups side by side in
-// a warp as fit; U turns of that at once.
+// a warp as fit; U tokens of that at once.
 template <int DT, int BITS, int E, int R, int U>
 __global__ void __launch_bounds__(kThreads)
     cache_write_vec_kernel(const __grid_constant__ CacheArgs a) {
@@ -345,39 +378,41 @@ __global__ void __launch_bounds__(kThreads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int seg = lane / a.lanes, at = lane - seg * a.lanes;
   const int units = a.group / E;
+  const Work w = work_of<U>(a, seg < a.segments ? warp * a.segments + seg : UINT32_MAX >> 1);
+  const char* x = static_cast<const char*>(xs.data) +
+                  (w.t * xs.token_stride + w.head * xs.head_stride + int64_t(w.idx) * a.group) * Bt +
+                  at * (E * Bt);
 
   Vec<DT, E> v[U][R];
   int64_t slot[U];
-  uint32_t g[U];
-  int h[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t id = ((blockIdx.x * U + u) * (kThreads / 32) + warp) * a.segments + seg;
     slot[u] = -1;
-    if (seg < a.segments && id < a.total) {
-      const uint32_t t = a.per_token.quot(id), rest = id - t * a.per_token.d;
-      h[u] = int(a.per_head.quot(rest));
-      g[u] = rest - uint32_t(h[u]) * a.per_head.d;
-      slot[u] = __ldg(a.slots + t);
-      const char* x = static_cast<const char*>(xs.data) +
-                      (int64_t(t) * xs.token_stride + h[u] * xs.head_stride) * Bt +
-                      int64_t(g[u]) * a.group * Bt;
+    if (w.there && w.t + u * w.step < a.n) {
+      slot[u] = __ldg(a.slots + w.t + u * w.step);
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if (R == 1 || r * a.lanes + at < units) v[u][r].load(x + (r * a.lanes + at) * (E * Bt));
+        if (R == 1 || r * a.lanes + at < units) v[u][r].load(x + r * a.lanes * (E * Bt));
     }
+    x += w.step * xs.token_stride * Bt;
   }
+  uint8_t* codes0 = static_cast<uint8_t*>(part.codes) + w.head * part.code_head_stride +
+                    int64_t(w.idx) * a.group * BITS / 8 + at * (E * BITS / 8);
+  char* params0 = static_cast<char*>(part.params) + w.head * part.param_head_stride + w.idx * 4;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const bool live = slot[u] >= 0 && slot[u] < a.n_slots;
     Range range;
+    bool fine = true;
     if (live) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
         if (R == 1 || r * a.lanes + at < units) {
-          const Range one = v[u][r].template range<BITS>();
-          range.lo = fminf(range.lo, one.lo);
-          range.hi = fmaxf(range.hi, one.hi);
+          bool f;
+          const Range one = v[u][r].template range<BITS>(&f);
+          range.lo = R == 1 ? one.lo : fminf(range.lo, one.lo);
+          range.hi = R == 1 ? one.hi : fmaxf(range.hi, one.hi);
+          fine = fine && f;
         }
     }
     for (int o = a.reach; o; o >>= 1) {
@@ -395,13 +430,16 @@ __global__ void __launch_bounds__(kThreads)
     if (BITS == 8) range.lo = -range.hi;
     if (!live) continue;
     const Scale s = scale_of<BITS>(range);
-    uint8_t* codes = static_cast<uint8_t*>(part.codes) + code_place(a, part, slot[u], h[u]) +
-                     int64_t(g[u]) * a.group * BITS / 8;
+    uint8_t* codes = codes0 + code_place(a, part, slot[u]);
     const uint64_t inv = pack2(s.inv, s.inv), off = pack2(-s.low, -s.low);
+    // Whether all of the lane's codes round to 0 .. 15 as they are: not where the pair's
+    // rounding moved the range by half a step, nor with infinities and NaN
+    const bool inside = fine && __fmul_rn(__fsub_rn(range.lo, s.low), s.inv) > -0.5f &&
+                        __fmul_rn(__fsub_rn(range.hi, s.low), s.inv) < 15.5f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (R > 1 && r * a.lanes + at >= units) continue;
-      uint8_t* c = codes + (r * a.lanes + at) * (E * BITS / 8);
+      uint8_t* c = codes + r * a.lanes * (E * BITS / 8);
       const Vec<DT, E>& x = v[u][r];
       uint32_t w[E * BITS / 32];
       if (BITS == 8) {
@@ -411,16 +449,22 @@ __global__ void __launch_bounds__(kThreads)
           w[i] = e4m3_pair(first(p), second(p)) | e4m3_pair(first(q), second(q)) << 16;
         }
       } else {
+        uint64_t y[E / 2];
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) y[i] = mul2(add2(x.pair(i), off), inv);
+        if (!inside) {
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i)  // NaN: 0
+            y[i] = pack2(fminf(fmaxf(first(y[i]), 0.0f), 15.0f),
+                         fminf(fmaxf(second(y[i]), 0.0f), 15.0f));
+        }
 #pragma unroll
         for (int i = 0; i < E / 8; ++i) {
           w[i] = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint64_t y = mul2(add2(x.pair(4 * i + j), off), inv);
-            // NaN: 0.  The sum with 2^23 rounds to an integer, ties to even
-            const uint64_t z =
-                add2(pack2(fminf(fmaxf(first(y), 0.0f), 15.0f), fminf(fmaxf(second(y), 0.0f), 15.0f)),
-                     pack2(8388608.0f, 8388608.0f));
+            // the sum with 1.5 * 2^23 rounds to an integer, ties to even
+            const uint64_t z = add2(y[4 * i + j], pack2(12582912.0f, 12582912.0f));
             w[i] |= (uint32_t(z) & 15u) << (8 * j) | (uint32_t(z >> 32) & 15u) << (8 * j + 4);
           }
         }
@@ -431,43 +475,37 @@ __global__ void __launch_bounds__(kThreads)
       else *reinterpret_cast<uint32_t*>(c) = w[0];
     }
     if (at == 0)
-      *reinterpret_cast<uint32_t*>(static_cast<char*>(part.params) +
-                                   param_place(a, part, slot[u], h[u]) + int64_t(g[u]) * 4) =
-          s.held;
+      *reinterpret_cast<uint32_t*>(params0 + param_place(a, part, slot[u])) = s.held;
   }
 }
 
-// E elements a thread, U times at once.
+// E elements a thread, of U tokens at once.
 template <int DT, int BITS, int E, int U>
 __global__ void __launch_bounds__(kThreads)
     cache_read_vec_kernel(const __grid_constant__ CacheArgs a) {
   constexpr int Bt = Elt<DT>::kBytes, kIn = E * BITS / 32;
   const lp_cache_part& part = a.part[blockIdx.y];
   const lp_heads& xs = a.x[blockIdx.y];
-  uint32_t t[U], c[U];
-  int h[U];
+  const Work work = work_of<U>(a, threadIdx.x);
+  if (!work.there) return;
   int64_t slot[U];
   uint32_t w[U][kIn], held[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t id = (blockIdx.x * U + u) * kThreads + threadIdx.x;
     slot[u] = -1;
-    t[u] = id < a.total ? a.per_token.quot(id) : UINT32_MAX;
-    if (id < a.total) {
-      const uint32_t rest = id - t[u] * a.per_token.d;
-      h[u] = int(a.per_head.quot(rest));
-      c[u] = rest - uint32_t(h[u]) * a.per_head.d;
-      slot[u] = __ldg(a.slots + t[u]);
-    }
+    if (work.t + u * work.step < a.n) slot[u] = __ldg(a.slots + work.t + u * work.step);
   }
+  const uint8_t* codes = static_cast<const uint8_t*>(part.codes) +
+                         work.head * part.code_head_stride + int64_t(work.idx) * (E * BITS / 8);
+  const char* params = static_cast<const char*>(part.params) +
+                       work.head * part.param_head_stride + a.per_group.quot(work.idx) * 4;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (slot[u] < 0 || slot[u] >= a.n_slots) {
       slot[u] = -1;
       continue;
     }
-    const uint8_t* p = static_cast<const uint8_t*>(part.codes) +
-                       code_place(a, part, slot[u], h[u]) + int64_t(c[u]) * (E * BITS / 8);
+    const uint8_t* p = codes + code_place(a, part, slot[u]);
     if (kIn == 4) {
       const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
       w[u][0] = v.x, w[u][1] = v.y, w[u][kIn - 2] = v.z, w[u][kIn - 1] = v.w;
@@ -477,13 +515,13 @@ __global__ void __launch_bounds__(kThreads)
     } else {
       w[u][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
     }
-    held[u] = __ldg(reinterpret_cast<const uint32_t*>(
-        static_cast<const char*>(part.params) + param_place(a, part, slot[u], h[u]) +
-        int64_t(a.per_group.quot(c[u])) * 4));
+    held[u] = __ldg(reinterpret_cast<const uint32_t*>(params + param_place(a, part, slot[u])));
   }
+  char* x = static_cast<char*>(xs.data) +
+            (work.t * xs.token_stride + work.head * xs.head_stride + int64_t(work.idx) * E) * Bt;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (t[u] == UINT32_MAX) continue;
+  for (int u = 0; u < U; ++u, x += work.step * xs.token_stride * Bt) {
+    if (work.t + u * work.step >= a.n) return;
     uint64_t v[E / 2];
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) v[i] = 0;
@@ -508,18 +546,16 @@ __global__ void __launch_bounds__(kThreads)
           // exponent 23 - b: with that float's leading bit it reads 2^(23-b) + code, and
           // less 2^(23-b) it is the code, exactly.
           constexpr uint32_t kOne = 127 + 23;
-          const uint32_t x = (i & 3) < 2 ? w[u][i / 4] : w[u][i / 4] >> 16;
+          const uint32_t x4 = (i & 3) < 2 ? w[u][i / 4] : w[u][i / 4] >> 16;
           const int b = 8 * (i & 1);
           const uint32_t m0 = (kOne - b) << 23, m1 = (kOne - b - 4) << 23;
           const uint64_t code =
-              add2(uint64_t((x & (15u << b)) | m0) | uint64_t((x & (15u << (b + 4))) | m1) << 32,
+              add2(uint64_t((x4 & (15u << b)) | m0) | uint64_t((x4 & (15u << (b + 4))) | m1) << 32,
                    pack2(-__uint_as_float(m0), -__uint_as_float(m1)));
           v[i] = fma2(code, s, low);  // the product is exact: one rounding
         }
       }
     }
-    char* x = static_cast<char*>(xs.data) +
-              (int64_t(t[u]) * xs.token_stride + h[u] * xs.head_stride + int64_t(c[u]) * E) * Bt;
     constexpr int kOut = E * Bt / 4;
     uint32_t o[kOut];
 #pragma unroll
@@ -562,53 +598,53 @@ bool vectors_of(int E, const CacheArgs& a, int n_parts) {
   return x % (E == 16 ? 32 : 16) == 0 && codes % (E * BITS / 8) == 0;
 }
 
+// Fills in what the vector kernels go by, for a token of per_token items and blocks of
+// per_block at a time; the grid.
+dim3 plan_work(CacheArgs& a, int64_t per_token, int per_block, int U, int n_parts) {
+  a.per_token.set(uint32_t(per_token));
+  a.per_head.set(uint32_t(per_token / a.heads));
+  const int64_t tiles = per_token > per_block ? (per_token + per_block - 1) / per_block : 1;
+  a.tiles.set(uint32_t(tiles));
+  a.tokens = tiles > 1 ? 1 : int(per_block / per_token);
+  a.items = tiles > 1 ? per_block : a.tokens * int(per_token);
+  const int64_t at_once = int64_t(U) * a.tokens;
+  return dim3(unsigned((a.n + at_once - 1) / at_once * tiles), unsigned(n_parts));
+}
+
 template <int DT, int BITS, int E, int R, int U>
-cudaError_t write_vec(const CacheArgs& a, int n_parts, cudaStream_t stream) {
-  const uint32_t per_block = uint32_t(kThreads / 32) * U * a.segments;
-  const dim3 grid((a.total + per_block - 1) / per_block, unsigned(n_parts));
+cudaError_t write_vec(CacheArgs a, int n_parts, cudaStream_t stream) {
+  const int units = a.group / E;
+  a.lanes = (units + R - 1) / R;
+  a.segments = 32 / a.lanes;
+  a.reach = 1;
+  while (a.reach < a.lanes) a.reach *= 2;
+  a.reach /= 2;
+  const dim3 grid = plan_work(a, int64_t(a.heads) * (a.dim / a.group),
+                              kThreads / 32 * a.segments, U, n_parts);
   cache_write_vec_kernel<DT, BITS, E, R, U><<<grid, kThreads, 0, stream>>>(a);
   return cudaPeekAtLastError();
 }
 
 template <int DT, int BITS, int E, int U>
-cudaError_t read_vec(const CacheArgs& a, int n_parts, cudaStream_t stream) {
-  const dim3 grid((a.total + U * kThreads - 1) / (U * kThreads), unsigned(n_parts));
+cudaError_t read_vec(CacheArgs a, int n_parts, cudaStream_t stream) {
+  a.per_group.set(uint32_t(a.group / E));
+  const dim3 grid = plan_work(a, int64_t(a.heads) * (a.dim / E), kThreads, U, n_parts);
   cache_read_vec_kernel<DT, BITS, E, U><<<grid, kThreads, 0, stream>>>(a);
   return cudaPeekAtLastError();
 }
 
-// Fills in what the vector kernels go by; false where the sizes do not fit them.
-template <int E>
-bool plan_vec(CacheArgs& a, bool write, int* vecs) {
-  const int units = a.group / E;
-  const int64_t per_token = int64_t(a.heads) * (a.dim / (write ? a.group : E));
-  *vecs = (units + 31) / 32;
-  if ((write && *vecs > kMaxVecs) || per_token > INT32_MAX || a.n > INT32_MAX / per_token)
-    return false;
-  a.total = uint32_t(a.n * per_token);
-  a.per_token.set(uint32_t(per_token));
-  a.per_head.set(uint32_t(per_token / a.heads));
-  a.per_group.set(uint32_t(units));
-  a.lanes = (units + *vecs - 1) / *vecs;
-  a.segments = 32 / a.lanes;
-  a.reach = 1;
-  while (a.reach < a.lanes) a.reach *= 2;
-  a.reach /= 2;
-  return true;
-}
-
 template <int DT, int BITS>
-cudaError_t launch_piece(CacheArgs a, bool write, int n_parts, cudaStream_t stream) {
-  int r = 0;
-  if (vectors_of<DT, BITS>(16, a, n_parts) && plan_vec<16>(a, write, &r) && (!write || r <= 2)) {
+cudaError_t launch_piece(const CacheArgs& a, bool write, int n_parts, cudaStream_t stream) {
+  const bool indexed = int64_t(a.heads) * a.dim <= INT32_MAX;
+  if (indexed && vectors_of<DT, BITS>(16, a, n_parts) && !(write && a.group > 2 * 32 * 16)) {
     if (!write) return read_vec<DT, BITS, 16, 2>(a, n_parts, stream);
-    if (r == 2) return write_vec<DT, BITS, 16, 2, 1>(a, n_parts, stream);
+    if (a.group > 32 * 16) return write_vec<DT, BITS, 16, 2, 1>(a, n_parts, stream);
     return write_vec<DT, BITS, 16, 1, 2>(a, n_parts, stream);
   }
-  if (vectors_of<DT, BITS>(8, a, n_parts) && plan_vec<8>(a, write, &r)) {
+  if (indexed && vectors_of<DT, BITS>(8, a, n_parts) && !(write && a.group > 4 * 32 * 8)) {
     if (!write) return read_vec<DT, BITS, 8, 2>(a, n_parts, stream);
-    if (r > 2) return write_vec<DT, BITS, 8, 4, 1>(a, n_parts, stream);
-    if (r == 2) return write_vec<DT, BITS, 8, 2, 1>(a, n_parts, stream);
+    if (a.group > 2 * 32 * 8) return write_vec<DT, BITS, 8, 4, 1>(a, n_parts, stream);
+    if (a.group > 32 * 8) return write_vec<DT, BITS, 8, 2, 1>(a, n_parts, stream);
     return write_vec<DT, BITS, 8, 1, 2>(a, n_parts, stream);
   }
   if (write) {
