@@ -707,6 +707,7 @@ class QuantCache:
         self.page_size = codes.size(d - 3)
         self.slots = self.page_size * (codes.size(1) if d == 5 else 1)
         self.device = codes.device
+        self._sizes = (self.slots, max(1, self.page_size), self.heads, dim, self.group)
         self._parts = (_lib.CachePart * max(1, self.parts))()
         self._heads_type = _lib.Heads * max(1, self.parts)
         e = params.element_size()
@@ -739,31 +740,32 @@ class QuantCache:
 def _cache_call(name, cache: QuantCache, xs, slots: torch.Tensor):
     if slots.dtype != torch.int64:
         raise TypeError("slots must be int64")
-    if slots.dim() != 1 or not slots.is_contiguous() or slots.device != cache.device:
+    device, parts = cache.device, cache.parts
+    if slots.dim() != 1 or not slots.is_contiguous() or slots.device != device:
         raise ValueError("slots must be contiguous, 1-D and on the cache's device")
-    n = slots.size(0)
-    if len(xs) != cache.parts:
-        raise ValueError(f"expected {cache.parts} tensors, one for each part, got {len(xs)}")
+    n = slots.numel()
+    if len(xs) != parts:
+        raise ValueError(f"expected {parts} tensors, one for each part, got {len(xs)}")
     dtype = xs[0].dtype if xs else torch.float32
     dt = _DT.get(dtype)
     if dt is None:
         raise TypeError(f"tensors must be float32, float16 or bfloat16, not {dtype}")
-    shape, device = (n, cache.heads, cache.dim), cache.device
-    heads = cache._heads_type()
-    for h, x in zip(heads, xs):
+    shape = (n, cache.heads, cache.dim)
+    heads = []
+    for x in xs:
         if x.dtype != dtype:
             raise TypeError("the parts' tensors must be of one type")
         if x.device != device:
             raise ValueError("tensors must be on the cache's device")
         if x.shape != shape:
             raise ValueError(f"tensors must be {list(shape)}, got {list(x.shape)}")
-        h.token_stride, h.head_stride, inner = x.stride()
+        token, head, inner = x.stride()
         if inner != 1 and cache.dim > 1:
             raise ValueError("a head's elements must be contiguous")
-        h.data = x.data_ptr()
+        heads.append((x.data_ptr(), token, head))
     st = getattr(_lib.load(), name)(
-        cache._parts, heads, cache.parts, cache.bits, dt, cache.slots, max(1, cache.page_size),
-        cache.heads, cache.dim, cache.group, slots.data_ptr(), n, _raw_stream(device.index))
+        cache._parts, cache._heads_type(*heads), parts, cache.bits, dt, *cache._sizes,
+        slots.data_ptr(), n, _raw_stream(device.index))
     check(name, st)
 
 
@@ -785,12 +787,13 @@ def cache_read(cache: QuantCache, slots: torch.Tensor, *, dtype: torch.dtype = t
     if out is None:
         if slots.dim() != 1:
             raise ValueError("slots must be contiguous, 1-D and on the cache's device")
-        out = torch.empty((cache.parts, slots.size(0), cache.heads, cache.dim), dtype=dtype,
-                          device=cache.device).unbind(0)
-    elif isinstance(out, torch.Tensor):
-        out = (out,)
+        shape = (slots.numel(), cache.heads, cache.dim)
+        out = tuple([torch.empty(shape, dtype=dtype, device=cache.device)
+                     for _ in range(cache.parts)])
+    else:
+        out = (out,) if isinstance(out, torch.Tensor) else tuple(out)
     _cache_call("lp_cache_read", cache, out, slots)
-    return tuple(out)
+    return out
 
 
 lp_cache_read = cache_read
