@@ -272,9 +272,9 @@ __device__ __forceinline__ float sum_exp_careful(const uint4 (&v)[N], float m) {
 }
 
 __device__ __forceinline__ float warp_max(float m) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, o));
-  return m;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
+  return r;
 }
 
 // What a warp knows of a chunk before it reads its tokens.
@@ -311,7 +311,9 @@ struct At {
 // wait neither for the row's state nor for its mask.  Loads overlap between warps, not
 // within one.  A second chunk in registers (79 of them) took the blocks of an SM from 5 to
 // 3 and 128 x 8 rows of 202048 fp16 from 76 to 88 us; the next chunk's state and mask
-// asked for ahead took 24 x 5 rows of 65519 from 12.7 to 14.0 us.
+// asked for ahead took 24 x 5 rows of 65519 from 12.7 to 14.0 us; the next chunk copied
+// into shared memory meanwhile took the former to 83 us, the latter to 13.5.  What bounds
+// a warp is its own instructions, about 7 a token.
 template <int DT, int N, bool EARLY>
 __global__ void __launch_bounds__(kStreamThreads) beam_stream_kernel(BeamArgs a) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -796,12 +798,14 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
                                     bm != nullptr, j0, end, lane);
         uint32_t hits = 0;
 #pragma unroll
-        for (int g = 0; g < kVecs; ++g)
+        for (int g = 0; g < kVecs; ++g) {
+          if (!(VecMax<DT>::run(v[g], 0xffu) >= least)) continue;
 #pragma unroll
           for (int e = 0; e < Elt<DT>::kPerVec; ++e) {
             const float x = Elt<DT>::get(v[g], e);
             if (x >= least && x > -INFINITY) hits |= 1u << (g * Elt<DT>::kPerVec + e);
           }
+        }
         for (; hits; hits &= hits - 1) {
           const unsigned bit = __ffs(hits) - 1;
           const unsigned j = unsigned(j0) + lane * Elt<DT>::kPerVec +
