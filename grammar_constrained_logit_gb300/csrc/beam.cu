@@ -50,6 +50,7 @@ struct BeamArgs {
   int64_t pad;
   int rows, beams, n, chunks;
   int chunk_tokens;
+  int step_rows, step_chunks;  // from a warp's chunk to its next
   int staged;      // a batch entry's chunks fit in shared memory
   int sum_bits;    // S <= V is held in units of 2^-sum_bits, within 63 bits
   float2* part;  // [rows, chunks]: (max, sum of exp(x - max)); rows that are dead or finished: not written
@@ -131,7 +132,7 @@ __device__ __forceinline__ uint32_t chunk_keep(const uint32_t* bm, int64_t j0, i
                                                int lane) {
   constexpr int E = Elt<DT>::kPerVec;
   uint32_t keep = 0;
-  if (j0 + kChunk<DT, N> <= V) {
+  if (unsigned(j0) + kChunk<DT, N> <= unsigned(V)) {
     if (bm == nullptr) return N * E == 32 ? 0xffffffffu : (1u << (N * E)) - 1u;
     const uint8_t* mask = reinterpret_cast<const uint8_t*>(bm) + (j0 + lane * E) / 8;
 #pragma unroll
@@ -157,7 +158,8 @@ __device__ __forceinline__ void load_chunk(uint4 (&v)[N], const char* row, uint3
   constexpr uint32_t kAll = (1u << E) - 1u;
   const int sh = int(reinterpret_cast<uintptr_t>(row) & 15);
   const uint32_t none = neg_inf_word<DT>();
-  if (j0 + kChunk<DT, N> + (sh ? E : 0) <= V && (sh == 0 || j0 > 0)) {
+  // (V is below 2^31: 32-bit comparisons do)
+  if (unsigned(j0) + kChunk<DT, N> + (sh ? E : 0) <= unsigned(V) && (sh == 0 || j0 > 0)) {
     // within the row: nothing to check token by token
     const uint4* p = reinterpret_cast<const uint4*>(row + (j0 + lane * E) * Elt<DT>::kBytes - sh);
     if (!masked) {
@@ -321,15 +323,20 @@ __global__ void __launch_bounds__(kStreamThreads) beam_stream_kernel(BeamArgs a)
   const int lane = threadIdx.x & 31;
   const unsigned total = unsigned(a.rows) * unsigned(a.chunks);
   const unsigned step = gridDim.x * (kStreamThreads / 32);
-  for (unsigned w = blockIdx.x * (kStreamThreads / 32) + (threadIdx.x >> 5); w < total;
-       w += step) {
-    At<DT, N> at;
-    at.row = int(w / unsigned(a.chunks)), at.c = int(w % unsigned(a.chunks));
+  unsigned w = blockIdx.x * (kStreamThreads / 32) + (threadIdx.x >> 5);
+  At<DT, N> at;
+  at.row = int(w / unsigned(a.chunks)), at.c = int(w % unsigned(a.chunks));
+  for (; w < total; w += step) {
+    const int row = at.row, c = at.c;
     at.template find<EARLY>(a, lane);
-    if (!EARLY && !at.live) continue;
     uint4 v[N];
-    load_chunk<DT, N, EARLY>(v, a.logits + at.row * a.stride, at.keep, at.masked,
-                             int64_t(at.c) * kChunk<DT, N>, a.V, lane);
+    if (EARLY || at.live)
+      load_chunk<DT, N, EARLY>(v, a.logits + row * a.stride, at.keep, at.masked,
+                               int64_t(c) * kChunk<DT, N>, a.V, lane);
+    if (!EARLY) {  // (a division is as much as 4 tokens)
+      at.row += a.step_rows, at.c += a.step_chunks;
+      if (at.c >= a.chunks) at.c -= a.chunks, ++at.row;
+    }
     if (!at.live) continue;
     float m = VecMax<DT>::run(v[0], 0xffu);
 #pragma unroll
@@ -939,7 +946,7 @@ cudaError_t finish(const cudaLaunchConfig_t& cfg, const BeamArgs& a, int64_t bat
 }
 
 template <int DT, int N>
-cudaError_t stream_with(cudaLaunchConfig_t cfg, const BeamArgs& a) {
+cudaError_t stream_with(cudaLaunchConfig_t cfg, BeamArgs a) {
   static const int resident = resident_blocks(beam_stream_kernel<DT, N, false>);
   static const int resident_early = resident_blocks(beam_stream_kernel<DT, N, true>);
   const int64_t blocks = (int64_t(a.rows) * a.chunks + 7) / 8;
@@ -948,7 +955,10 @@ cudaError_t stream_with(cudaLaunchConfig_t cfg, const BeamArgs& a) {
     cfg.gridDim = dim3(unsigned(blocks));
     return cudaLaunchKernelEx(&cfg, beam_stream_kernel<DT, N, true>, a);
   }
-  cfg.gridDim = dim3(unsigned(std::min<int64_t>(blocks, resident)));
+  const int64_t grid = std::min<int64_t>(blocks, resident);
+  a.step_rows = int(grid * (kStreamThreads / 32) / a.chunks);
+  a.step_chunks = int(grid * (kStreamThreads / 32) % a.chunks);
+  cfg.gridDim = dim3(unsigned(grid));
   return cudaLaunchKernelEx(&cfg, beam_stream_kernel<DT, N, false>, a);
 }
 
