@@ -644,7 +644,7 @@ __device__ __forceinline__ float nth_largest(const K* keys, int n) {
     near[i] = mine[i] == 0 || !(d < 0x1p27f) ? 0 : max(0, 2047 - q);
   }
   int T = 0;
-#pragma unroll
+#pragma unroll 1  // the kernel runs through its code once: less of it is less to fetch
   for (int sh = 10; sh >= 0; sh -= 2) {
     unsigned there[4] = {0, 0, 0, 0};  // three counts of up to 512, ten bits each
 #pragma unroll
