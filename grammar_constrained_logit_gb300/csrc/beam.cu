@@ -8,14 +8,21 @@
 // A finished row has one candidate, (pad, s_r).  A batch's n best candidates come
 // out highest first, ties to the lowest (beam, token).
 //
-// Two kernels.  The first reads the logits once, a chunk of 2 KB a warp, and leaves
-// (max, sum of exp(x - max)) of each chunk: 8 bytes for 2048, so nothing of the size
-// of the logits is written.  A chunk is a range of token indices, whatever the row's
-// alignment, and its sum has a fixed order: two equal rows get equal scores to the
-// last bit, and ties between them fall by index as stated.  The second kernel, one
-// block a batch, joins the chunks to M_r and S_r, takes the n-th largest chunk
-// maximum's score as a lower bound T of the n-th best candidate, and reads again
-// only the chunks whose maximum reaches T: about n of them, whatever the vocabulary.
+// Two kernels.
+//
+// The first reads the logits once, a chunk of 2 KB a warp (512 bytes where there would be
+// few chunks to the n), and leaves (max, sum of exp(x - max)) of each: 8 bytes, so nothing
+// of the size of the logits is written.  A chunk is a range of token indices, whatever the
+// row's alignment, and its sum has a fixed order: two equal rows get equal scores to the
+// last bit, and ties between them fall by index as stated.  What bounds it is memory, with
+// the warps' own instructions (about 8 a token and lane, one of them the exponential) close
+// behind: 128 x 8 rows of 202048 fp16 take 65 us, 6.3 TB/s, 93% of the measured copy rate.
+//
+// The second, one block (or a cluster of them) a batch entry, joins the chunks to M_r and
+// S_r, takes the n-th largest chunk maximum's score as a lower bound T of the n-th best
+// candidate, and reads again only the chunks whose maximum reaches T: about n of them,
+// whatever the vocabulary.  It waits at each turn for what the last one found, some
+// 10000 cycles in all: 3 to 9 us after the first kernel, hardly more with a full batch.
 #include <algorithm>
 
 #include "common.cuh"
@@ -53,7 +60,7 @@ struct BeamArgs {
   int step_rows, step_chunks;  // from a warp's chunk to its next
   int staged;      // a batch entry's chunks fit in shared memory
   int sum_bits;    // S <= V is held in units of 2^-sum_bits, within 63 bits
-  float2* part;  // [rows, chunks]: (max, sum of exp(x - max)); rows that are dead or finished: not written
+  float2* part;    // [rows, chunks]: (max, sum of exp(x - max)); of live rows only
   float* out_scores;
   int64_t* out_tokens;
   int32_t* out_parents;
@@ -375,8 +382,8 @@ __device__ void sort_best_first(Cand* c, int m) {
 }
 
 // A value held as two floats: hi is the value rounded, lo what that left.  Scores are
-// summed in this form: 64-bit arithmetic is 1/64 of the 32-bit rate here, and
-// the few dozen operations a batch entry needs took 1000 cycles in it.
+// summed in this form, which holds 48 bits and more: 64-bit arithmetic is 1/64 of the
+// 32-bit rate here, and the few dozen operations a batch entry needs took 1000 cycles.
 struct Two {
   float hi, lo;
 };
