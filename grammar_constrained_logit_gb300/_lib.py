@@ -70,7 +70,7 @@ _lock = threading.Lock()
 
 
 def declare(lib) -> None:
-    """Set the argument and result types of every exported entry point."""
+    """Set the argument and result types of the masking and sampling entry points."""
     lib.lp_apply_token_bitmask.restype = c_i32
     lib.lp_apply_token_bitmask.argtypes = [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_i64, c_i64,
                                            c_i64, c_i64, c_vp, c_i64, c_vp]
@@ -101,6 +101,14 @@ def declare(lib) -> None:
                                                ctypes.POINTER(SamplingParams), c_vp, c_vp]
     lib.lp_sample_workspace_bytes.restype = c_i64
     lib.lp_sample_workspace_bytes.argtypes = [c_i32, c_i64, c_i64]
+    lib.lp_philox4x32_10.restype = c_i32
+    lib.lp_philox4x32_10.argtypes = [c_vp, c_vp, c_vp, c_i64, c_vp]
+    lib.lp_status_string.restype = ctypes.c_char_p
+    lib.lp_status_string.argtypes = [c_i32]
+
+
+def declare_beam(lib) -> None:
+    """The same for the beam-search entry points (csrc/beam.cu, reorder.cu, cache.cu)."""
     lib.lp_beam_select_workspace_bytes.restype = c_i64
     lib.lp_beam_select_workspace_bytes.argtypes = [c_i32, c_i64, c_i64]
     lib.lp_beam_select.restype = c_i32
@@ -113,10 +121,6 @@ def declare(lib) -> None:
         f.restype = c_i32
         f.argtypes = [c_vp, c_vp, c_i64, c_i32, c_i32, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp,
                       c_i64, c_vp]
-    lib.lp_philox4x32_10.restype = c_i32
-    lib.lp_philox4x32_10.argtypes = [c_vp, c_vp, c_vp, c_i64, c_vp]
-    lib.lp_status_string.restype = ctypes.c_char_p
-    lib.lp_status_string.argtypes = [c_i32]
 
 
 def load(path: str | None = None):
@@ -131,6 +135,7 @@ def load(path: str | None = None):
                     "(or __graft_entry__.build()) first; there is no fallback path")
             lib = ctypes.CDLL(p)
             declare(lib)
+            declare_beam(lib)
             _lib = lib
     return _lib
 
