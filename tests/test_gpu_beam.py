@@ -277,3 +277,29 @@ def test_more_chunks_at_the_bound_than_a_list_holds(dtype, n, batch, beams, V, k
         first = 1 if b < batch - 1 else 2
         assert (p[b] == first).all() and k[b].tolist() == list(range(kept, kept + n))
         assert len(set(s[b])) == 1
+
+
+@pytest.mark.parametrize("n", [4, 40])
+def test_more_chunks_than_shared_memory_holds(n):
+    """64 beams of 600001 tokens: the chunks' maxima are read from memory."""
+    beams, V = 64, 600001
+    g = torch.Generator("cuda").manual_seed(3)
+    t = torch.rand(beams, V, device="cuda", generator=g).to(torch.bfloat16)
+    at = torch.randperm(beams * V, device="cuda", generator=g)[:60]
+    t.view(-1)[at] = (2.0 + torch.arange(60, device="cuda") / 8).to(torch.bfloat16)
+    scores = torch.zeros(1, beams, device="cuda")
+    s, k, p = ops.beam_select(t, scores, n)
+    lp = t.double().log_softmax(-1).view(-1)
+    best = lp.topk(n)
+    assert torch.equal(p[0].long() * V + k[0], best.indices)
+    assert bool(((s[0].double() - best.values).abs() <= 4e-6 + 2.0 ** -24 * best.values.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("beams, V, n", [(3, 2001, 6), (1, 1025, 1), (7, 300, 14)])
+def test_more_requests_than_multiprocessors(dtype, beams, V, n):
+    rng = np.random.default_rng(V)
+    batch = 170
+    t = placed(rng.standard_normal((batch * beams, V)) * 2.5, dtype, 1, 2)
+    scores = -rng.random((batch, beams), dtype=np.float32) * 10
+    check_beam(run(t, scores, n, V), seen(t, V), scores, n)
