@@ -332,11 +332,11 @@ lp_status lp_mask_and_sample_noalloc(const void* logits, lp_dtype dt, int64_t B,
  *   - of a finished beam with a score above -inf: (k, pad_id) with scores[r];
  *   - of a beam with score -inf or NaN: none (its logits are not read).
  * Out come the n_select candidates of highest score, highest first; equal scores
- * fall to the lowest (beam, token).  Exponentials and the chunks' sums are 32-bit,
- * their joint sum and the scores that are compared 64-bit; two equal rows get equal
- * scores to the last bit, whatever their alignment.  NaN logits are no candidates;
- * tokens of logit +inf share their row's whole mass.  A candidate whose score is
- * -inf (an overflow) is none.
+ * fall to the lowest (beam, token).  Exponentials and the sums of up to 1024 of them
+ * are 32-bit; their joint sum, its logarithm and the scores that are compared hold 38
+ * bits after the point or more.  Two equal rows get equal scores to the last bit,
+ * whatever their alignment.  NaN logits are no candidates; tokens of logit +inf share
+ * their row's whole mass.  A candidate whose score overflows to -inf in 32 bits is none.
  *   logits         device [batch * beams, cols], read only
  *   bitmask        device int32 [bitmask_rows >= batch * beams, ...], or NULL
  *   row_needs_mask device uint8 [batch * beams], or NULL: every row is masked
@@ -346,8 +346,9 @@ lp_status lp_mask_and_sample_noalloc(const void* logits, lp_dtype dt, int64_t B,
  *   out_tokens     device int64 [batch, n_select]; -1 in empty places
  *   out_parents    device int32 [batch, n_select], the beam k; -1 in empty places
  *   workspace      device scratch of lp_beam_select_workspace_bytes(dt, batch *
- *                  beams, vocab_size) bytes, 8-byte aligned, of any content; calls
- *                  that share it must be ordered (one stream, or events)
+ *                  beams, vocab_size) bytes (8 for each 512 bytes of a row), 8-byte
+ *                  aligned, of any content; calls that share it must be ordered (one
+ *                  stream, or events)
  * Two kernels on the stream.  Invalid: as lp_apply_token_bitmask_rows, beams < 1,
  * n_select < 0, row_needs_mask without bitmask, a short or misaligned workspace,
  * logits not aligned to their element.  beams or n_select above 256, more than 2^27
