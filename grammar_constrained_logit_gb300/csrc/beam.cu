@@ -156,11 +156,33 @@ __device__ __forceinline__ uint32_t chunk_keep(const uint32_t* bm, int64_t j0, i
   return keep;
 }
 
+// What a group's words keep, by its keep bits: looked up instead of worked out for each
+// word (5 instructions a group instead of 28 for 8 tokens).
+template <int DT>
+struct KeepTable {
+  uint4 words[1 << Elt<DT>::kPerVec];
+  __device__ __forceinline__ void fill() {  // by a block of at least as many threads
+    const uint32_t k = threadIdx.x;
+    if (k >= (1u << Elt<DT>::kPerVec)) return;
+    words[k] = DT == LP_F32 ? make_uint4(k & 1 ? ~0u : 0u, k & 2 ? ~0u : 0u, k & 4 ? ~0u : 0u,
+                                         k & 8 ? ~0u : 0u)
+                            : make_uint4(keep_mask16(k, 0), keep_mask16(k, 1), keep_mask16(k, 2),
+                                         keep_mask16(k, 3));
+  }
+  __device__ __forceinline__ uint4 kept(const uint4& v, uint32_t k) const {
+    const uint4 m = words[k];
+    const uint32_t none = neg_inf_word<DT>();
+    return make_uint4((v.x & m.x) | (none & ~m.x), (v.y & m.y) | (none & ~m.y),
+                      (v.z & m.z) | (none & ~m.z), (v.w & m.w) | (none & ~m.w));
+  }
+};
+
 // A chunk's groups of this lane, masked tokens as -inf.  ALL: groups that the mask leaves
 // out are loaded too, so that the loads do not wait for its bits.
 template <int DT, int N, bool ALL>
 __device__ __forceinline__ void load_chunk(uint4 (&v)[N], const char* row, uint32_t keep,
-                                           bool masked, int64_t j0, int64_t V, int lane) {
+                                           bool masked, int64_t j0, int64_t V, int lane,
+                                           const KeepTable<DT>* table = nullptr) {
   constexpr int E = Elt<DT>::kPerVec;
   constexpr uint32_t kAll = (1u << E) - 1u;
   const int sh = int(reinterpret_cast<uintptr_t>(row) & 15);
@@ -192,7 +214,8 @@ __device__ __forceinline__ void load_chunk(uint4 (&v)[N], const char* row, uint3
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const uint32_t k = keep >> (i * E) & kAll;
-    if (k != kAll) v[i] = Elt<DT>::blend(v[i], k, none);
+    if (table) v[i] = table->kept(v[i], k);
+    else if (k != kAll) v[i] = Elt<DT>::blend(v[i], k, none);
   }
 }
 
@@ -325,6 +348,9 @@ struct At {
 // a warp is its own instructions, about 7 a token.
 template <int DT, int N, bool EARLY>
 __global__ void __launch_bounds__(kStreamThreads) beam_stream_kernel(BeamArgs a) {
+  __shared__ KeepTable<DT> table;
+  table.fill();
+  __syncthreads();
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -339,7 +365,7 @@ __global__ void __launch_bounds__(kStreamThreads) beam_stream_kernel(BeamArgs a)
     uint4 v[N];
     if (EARLY || at.live)
       load_chunk<DT, N, EARLY>(v, a.logits + row * a.stride, at.keep, at.masked,
-                               int64_t(c) * kChunk<DT, N>, a.V, lane);
+                               int64_t(c) * kChunk<DT, N>, a.V, lane, &table);
     if (!EARLY) {  // (a division is as much as 4 tokens)
       at.row += a.step_rows, at.c += a.step_chunks;
       if (at.c >= a.chunks) at.c -= a.chunks, ++at.row;
