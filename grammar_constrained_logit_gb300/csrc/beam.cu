@@ -347,7 +347,7 @@ struct At {
 // into shared memory meanwhile took the former to 83 us, the latter to 13.5.  What bounds
 // a warp is its own instructions, about 7 a token.
 template <int DT, int N, bool EARLY>
-__global__ void __launch_bounds__(kStreamThreads) beam_stream_kernel(BeamArgs a) {
+__global__ void __launch_bounds__(kStreamThreads, EARLY ? 5 : 6) beam_stream_kernel(BeamArgs a) {
   __shared__ KeepTable<DT> table;
   table.fill();
   __syncthreads();
@@ -940,6 +940,27 @@ int resident_blocks(K kernel) {
   return std::max(1, n) * kSms;
 }
 
+// Clusters of R blocks that run at once (a cluster lies within one group of SMs).
+template <int DT, int NT, int R, int B>
+int resident_clusters() {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = R;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(R);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = sizeof(FinishSmem);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, beam_finish_kernel<DT, NT, R, B>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  return n;
+}
+
 template <int DT, int NT, int R, int B>
 cudaError_t finish_with(cudaLaunchConfig_t cfg, BeamArgs a, int64_t batch) {
   static_assert(sizeof(FinishSmem) <= 48 * 1024, "within the default limit");
@@ -966,11 +987,12 @@ cudaError_t finish_with(cudaLaunchConfig_t cfg, BeamArgs a, int64_t batch) {
 
 template <int DT>
 cudaError_t finish(const cudaLaunchConfig_t& cfg, const BeamArgs& a, int64_t batch) {
-  // Many to find: a cluster of blocks goes through the chunks side by side.  4 x 64 rows of
-  // 32000 bf16, n = 128: 24 us with it, 39 without.  With n up to 32 one block's 16 warps
-  // do in a round or two (53 x 32 rows of 52332 f32, n = 32: 64 us without, 74 with), and
-  // with batches that fill the SMs the cluster only repeats its sums.
-  if (a.n > 32 && batch * 8 <= kSms) return finish_with<DT, 512, 8, 1>(cfg, a, batch);
+  // Many to find: a cluster of blocks goes through the chunks side by side, as long as all
+  // clusters run at once.  4 x 64 rows of 32000 bf16, n = 128: 24 us with it, 39 without;
+  // 4 x 16 rows of 4175, n = 32: 11.8 and 13.5; but 17 x 16 rows of 19473, n = 32, where 16
+  // clusters run: 24 and 20.  With n up to 16 one block's 16 warps do.
+  static const int clusters = resident_clusters<DT, 512, 8, 1>();
+  if (a.n > 16 && batch <= clusters) return finish_with<DT, 512, 8, 1>(cfg, a, batch);
   // One block an SM may take 80 registers a thread (8 x 4 rows of 128256 bf16: 9.2 us, with
   // 64 of them 10.3); with more blocks than SMs two have to fit (161 x 8 rows of 17976:
   // 26.6 us, else 32.5).
