@@ -499,8 +499,10 @@ constexpr LogTable make_log_table() {
 
 __device__ const LogTable kLogTable = make_log_table();
 
-// log(S / 2^bits), S > 0
+// log(S / 2^bits), S > 0.  Exactly 0 for a row of one token, which then scores as a
+// finished beam would.
 __device__ __forceinline__ Two log_units(unsigned long long S, int bits, const LogEntry* table) {
+  if (S == 1ull << bits) return Two{0.0f, 0.0f};
   const int lz = __clzll(S);
   const unsigned long long f = S << lz;  // m = f / 2^63 in [1, 2)
   const LogEntry q = table[unsigned(f >> 56) & 127u];

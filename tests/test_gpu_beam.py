@@ -303,3 +303,19 @@ def test_more_requests_than_multiprocessors(dtype, beams, V, n):
     t = placed(rng.standard_normal((batch * beams, V)) * 2.5, dtype, 1, 2)
     scores = -rng.random((batch, beams), dtype=np.float32) * 10
     check_beam(run(t, scores, n, V), seen(t, V), scores, n)
+
+
+def test_a_single_token_scores_as_its_beam():
+    """One kept token has probability 1: its score is the beam's, to the last bit, and ties
+    with finished beams fall by beam."""
+    V = 2100
+    t = torch.randn(6, V, device="cuda").half()
+    allowed = np.zeros((6, V), dtype=bool)
+    allowed[np.arange(6), [5, 0, 2099, 1024, 77, 3]] = True
+    scores = np.array([[-0.3, -0.3, -0.3, -1e-6, -0.3, -7.7]], dtype=np.float32)
+    fin = torch.tensor([[0, 1, 0, 0, 1, 0]], dtype=torch.uint8, device="cuda")
+    s, k, p = run(t, scores, 8, V, bitmask=torch.from_numpy(syn.pack_bits(allowed)).cuda(),
+                  finished=fin, pad_id=9)
+    assert p[0].tolist() == [3, 0, 1, 2, 4, 5, -1, -1]
+    assert k[0].tolist() == [1024, 5, 9, 2099, 9, 3, -1, -1]
+    assert np.array_equal(s[0, :6], scores[0, [3, 0, 1, 2, 4, 5]])
