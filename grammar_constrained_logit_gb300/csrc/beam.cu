@@ -705,9 +705,12 @@ __device__ __forceinline__ void cluster_sync() {
                "barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
-__device__ __forceinline__ FinishSmem* of_first_block(FinishSmem* p) {
+// Only while that block is sure to run: the first one is left last, and nobody reads it
+// behind the barrier that may be its last; what it has to say it writes to the others
+// before that.
+__device__ __forceinline__ FinishSmem* of_block(FinishSmem* p, int rank) {
   uint64_t r;
-  asm("mapa.u64 %0, %1, 0;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)));
+  asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
   return reinterpret_cast<FinishSmem*>(r);
 }
 
@@ -718,7 +721,7 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
   FinishSmem& sm = *reinterpret_cast<FinishSmem*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / R, rank = blockIdx.x % R, row0 = b * a.beams, C = a.chunks;
-  FinishSmem& hub = R > 1 ? *of_first_block(&sm) : sm;
+  FinishSmem& hub = R > 1 ? *of_block(&sm, 0) : sm;
   float* staged = a.staged ? reinterpret_cast<float*>(raw + sizeof(FinishSmem)) : nullptr;
   if (tid == 0) sm.count = 0, sm.front_n = 0, sm.list_n = 0, sm.exact = 0, sm.overflow = 0;
   for (int i = tid; i < 128; i += NT) sm.log_table[i] = kLogTable.at[i];
@@ -864,6 +867,7 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
         int next = kOn;
         if (sm.overflow) {
           next = kStretches;
+          __syncthreads();  // everyone has seen it before it is taken back
         } else if (count > kBufNew) {
           // too many: what was seen raises the bound, and the list is gone through again.
           // By its score where that is above the last, else by the whole order (strictly,
@@ -887,9 +891,14 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
         }
       }
       if (R > 1) {
+        if (rank == 0) {
+          __syncthreads();
+          if (tid > 0 && tid < R) {
+            FinishSmem& other = *of_block(&sm, tid);
+            other.next = sm.next, other.T = sm.T, other.exact = sm.exact, other.bound = sm.bound;
+          }
+        }
         cluster_sync();
-        if (rank != 0 && tid == 0)
-          sm.next = hub.next, sm.T = hub.T, sm.exact = hub.exact, sm.bound = hub.bound;
       }
       __syncthreads();
       if (sm.next != kAgain) break;
