@@ -126,6 +126,8 @@ def declare_beam(lib) -> None:
 def load(path: str | None = None):
     """Open liblp.so once per process; raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB
