@@ -16,7 +16,7 @@
 // place within the token and steps over tokens, so its addresses are worked out once;
 // extrema are taken of 16-bit pairs; arithmetic goes two 32-bit values at a time; codes
 // are rounded by adding 1.5 * 2^23 and read by placing them in a float's last bits.
-// 32768 tokens of 2 x 8 x 128 bf16 written to 8 bits: 33.4 us, 88% of the measured copy
+// 32768 tokens of 2 x 8 x 128 bf16 written to 8 bits: 31.1 us, 95% of the measured copy
 // rate; 131072 read back from 4 bits: 111 us, 94%.
 #include <algorithm>
 
@@ -657,14 +657,23 @@ cudaError_t launch_piece(const CacheArgs& a, bool write, int n_parts, cudaStream
     if (!write)
       return few ? read_vec<DT, BITS, 16, 1>(a, n_parts, stream)
                  : read_vec<DT, BITS, 16, U>(a, n_parts, stream);
-    if (a.group > 32 * 16) return write_vec<DT, BITS, 16, 2, 1>(a, n_parts, stream);
+    // Groups of more than one vector have two on a lane, of half the lanes: fewer steps to
+    // their range, and its parameters are made by fewer threads.  32768 x 2 x 8 x 128 bf16:
+    // 31.3 us written to 4 bits in groups of 32 and 31.1 to 8 in groups of 128, with one
+    // vector a lane 35.6 and 33.4.  Two tokens at once for 4 bits (with one 33.3), one for 8
+    // (31.9 in groups of 32, with two 32.7).  32-bit values are four loads as they are: 25.5
+    // and 27.0 with two vectors (16384, 4 bits, groups of 32), 26.3 and 26.1 (8, of 128).
+    constexpr int pair_tokens = BITS == 4 && DT != LP_F32 ? 2 : 1;
+    if (a.group > 32 * 16 || (DT != LP_F32 && a.group > 16 && !few))
+      return write_vec<DT, BITS, 16, 2, pair_tokens>(a, n_parts, stream);
     return few ? write_vec<DT, BITS, 16, 1, 1>(a, n_parts, stream)
                : write_vec<DT, BITS, 16, 1, U>(a, n_parts, stream);
   }
   if (indexed && vectors_of<DT, BITS>(8, a, n_parts) && !(write && a.group > 4 * 32 * 8)) {
     if (!write) return read_vec<DT, BITS, 8, 4>(a, n_parts, stream);
-    if (a.group > 2 * 32 * 8) return write_vec<DT, BITS, 8, 4, 1>(a, n_parts, stream);
-    if (a.group > 32 * 8) return write_vec<DT, BITS, 8, 2, 2>(a, n_parts, stream);
+    // The same, four on a lane: 32768 x 2 x 8 x 72 fp16, one group a head, written to 8 bits
+    // 23.3 us and in groups of 24 to 4 bits 26.6, with one vector a lane 33.8 and 40.4.
+    if (a.group > 16) return write_vec<DT, BITS, 8, 4, 1>(a, n_parts, stream);
     return write_vec<DT, BITS, 8, 1, 4>(a, n_parts, stream);
   }
   if (write) {
