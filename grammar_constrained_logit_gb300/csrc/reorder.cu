@@ -58,6 +58,12 @@ struct Plan {                   // of one batch entry
   int sources;
 };
 
+struct Shared {                 // beside the slots that a launch asks for
+  Plan plan;
+  uint32_t taken[kMaxBeams / 32];
+  uint8_t parent[kMaxBeams];    // itself: the row stays
+};
+
 // Bytes [lo, hi) of the rows at p, W at a time; room: one 16-byte slot a thread and source.
 template <int W>
 __device__ void move_columns(char* p, int64_t row_stride, int64_t lo, int64_t hi, const Plan& plan,
@@ -123,9 +129,10 @@ __device__ __forceinline__ void move_few(int sources, char* p, int64_t row_strid
 __global__ void reorder_kernel(const __grid_constant__ ReorderArgs a) {
   extern __shared__ __align__(16) char raw[];
   uint4* room = reinterpret_cast<uint4*>(raw);
-  __shared__ Plan plan;
-  __shared__ uint32_t taken[kMaxBeams / 32];
-  __shared__ uint8_t parent[kMaxBeams];  // itself: the row stays
+  __shared__ Shared sh;
+  Plan& plan = sh.plan;
+  uint32_t* taken = sh.taken;
+  uint8_t* parent = sh.parent;
 
   int s = 0;  // the last state that begins at this block or before
   for (int half = kLaunchStates / 2; half; half >>= 1)
@@ -312,7 +319,9 @@ extern "C" lp_status lp_reorder_states(const lp_state* states, int64_t n_states,
   const int threads =
       int(std::max<int64_t>(32, std::min<int64_t>(kThreads, (98304 / 16 / beams) & ~31)));
   const size_t smem = size_t(threads) * 16 * size_t(beams);
-  if (smem > 48 * 1024 &&
+  // A block's 48 KB without leave are for the kernel's own arrays too: with 12 beams the
+  // slots alone are all of them (16 bytes: the alignment between the two)
+  if (smem + sizeof(Shared) + 16 > 48 * 1024 &&
       cudaFuncSetAttribute(reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kMaxBeams * 32 * 16) != cudaSuccess)
     return LP_ERR_CUDA;
