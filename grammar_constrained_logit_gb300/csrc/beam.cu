@@ -946,8 +946,10 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
 template <typename K>
 int resident_blocks(K kernel) {
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kStreamThreads, 0) != cudaSuccess)
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kStreamThreads, 0) != cudaSuccess) {
+    (void)cudaGetLastError();
     n = 0;
+  }
   return std::max(1, n) * kSms;
 }
 
@@ -966,7 +968,7 @@ int resident_clusters() {
   cfg.numAttrs = 1;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, beam_finish_kernel<DT, NT, R, B>, &cfg) != cudaSuccess) {
-    cudaGetLastError();
+    (void)cudaGetLastError();
     n = 0;
   }
   return n;
@@ -1133,5 +1135,5 @@ extern "C" lp_status lp_beam_select(const void* logits, lp_dtype dt, int64_t bat
   const cudaError_t e = dt == LP_F32   ? launch<LP_F32>(a, batch, stream)
                         : dt == LP_F16 ? launch<LP_F16>(a, batch, stream)
                                        : launch<LP_BF16>(a, batch, stream);
-  return e == cudaSuccess ? LP_OK : LP_ERR_CUDA;
+  return status_of(e);
 }

@@ -631,16 +631,14 @@ cudaError_t write_vec(CacheArgs a, int n_parts, cudaStream_t stream) {
   a.reach /= 2;
   const dim3 grid = plan_work(a, int64_t(a.heads) * (a.dim / a.group),
                               kThreads / 32 * a.segments, U, n_parts);
-  cache_write_vec_kernel<DT, BITS, E, R, U><<<grid, kThreads, 0, stream>>>(a);
-  return cudaPeekAtLastError();
+  return launch_kernel(cache_write_vec_kernel<DT, BITS, E, R, U>, grid, kThreads, 0, stream, a);
 }
 
 template <int DT, int BITS, int E, int U>
 cudaError_t read_vec(CacheArgs a, int n_parts, cudaStream_t stream) {
   a.per_group.set(uint32_t(a.group / E));
   const dim3 grid = plan_work(a, int64_t(a.heads) * (a.dim / E), kThreads, U, n_parts);
-  cache_read_vec_kernel<DT, BITS, E, U><<<grid, kThreads, 0, stream>>>(a);
-  return cudaPeekAtLastError();
+  return launch_kernel(cache_read_vec_kernel<DT, BITS, E, U>, grid, kThreads, 0, stream, a);
 }
 
 template <int DT, int BITS>
@@ -679,14 +677,12 @@ cudaError_t launch_piece(const CacheArgs& a, bool write, int n_parts, cudaStream
   if (write) {
     const int64_t warps = a.n * a.heads * (a.dim / a.group);
     const dim3 grid(unsigned(std::min<int64_t>((warps + 7) / 8, 152 * 64)), unsigned(n_parts));
-    cache_write_kernel<DT, BITS><<<grid, kThreads, 0, stream>>>(a);
-  } else {
-    const int64_t threads = a.n * a.heads * (int64_t(a.dim) * BITS / 8);
-    const dim3 grid(unsigned(std::min<int64_t>((threads + kThreads - 1) / kThreads, 152 * 64)),
-                    unsigned(n_parts));
-    cache_read_kernel<DT, BITS><<<grid, kThreads, 0, stream>>>(a);
+    return launch_kernel(cache_write_kernel<DT, BITS>, grid, kThreads, 0, stream, a);
   }
-  return cudaPeekAtLastError();
+  const int64_t threads = a.n * a.heads * (int64_t(a.dim) * BITS / 8);
+  const dim3 grid(unsigned(std::min<int64_t>((threads + kThreads - 1) / kThreads, 152 * 64)),
+                  unsigned(n_parts));
+  return launch_kernel(cache_read_kernel<DT, BITS>, grid, kThreads, 0, stream, a);
 }
 
 template <int DT, int BITS>
@@ -755,7 +751,7 @@ lp_status run(const lp_cache_part* parts, const lp_heads* x, int64_t n_parts, in
     e = dt == LP_F32   ? launch<LP_F32, 4>(a, write, np, stream)
         : dt == LP_F16 ? launch<LP_F16, 4>(a, write, np, stream)
                        : launch<LP_BF16, 4>(a, write, np, stream);
-  return e == cudaSuccess ? LP_OK : LP_ERR_CUDA;
+  return status_of(e);
 }
 
 }  // namespace

@@ -1,4 +1,4 @@
-// common.cuh -- device helpers shared by the apply and sample kernels of liblp.so:
+// common.cuh -- helpers shared by the kernels of liblp.so: launches and their status,
 // element-type traits for 16-byte vectors, the bitmask bit window of a vector, an
 // order-preserving integer key for float logits, Philox4x32-10 and Gumbel noise.
 #pragma once
@@ -11,6 +11,26 @@
 namespace lp {
 
 constexpr uint32_t kFullWarp = 0xffffffffu;
+
+// An entry point's status. The runtime keeps a failed call's error for whoever asks next:
+// it is taken back here, so that one failure is not reported again by a later call.
+inline lp_status status_of(cudaError_t e) {
+  if (e == cudaSuccess) return LP_OK;
+  (void)cudaGetLastError();
+  return LP_ERR_CUDA;
+}
+
+// A launch's own error, whatever error an earlier call may have left behind.
+template <typename... K, typename... A>
+cudaError_t launch_kernel(void (*kernel)(K...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // ------------------------------------------------------------------ elements
 

@@ -321,10 +321,11 @@ extern "C" lp_status lp_reorder_states(const lp_state* states, int64_t n_states,
   const size_t smem = size_t(threads) * 16 * size_t(beams);
   // A block's 48 KB without leave are for the kernel's own arrays too: with 12 beams the
   // slots alone are all of them (16 bytes: the alignment between the two)
-  if (smem + sizeof(Shared) + 16 > 48 * 1024 &&
-      cudaFuncSetAttribute(reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kMaxBeams * 32 * 16) != cudaSuccess)
-    return LP_ERR_CUDA;
+  if (smem + sizeof(Shared) + 16 > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBeams * 32 * 16);
+    if (e != cudaSuccess) return status_of(e);
+  }
   ReorderArgs a = {};
   a.batch = batch;
   a.seg = seg;
@@ -357,8 +358,8 @@ extern "C" lp_status lp_reorder_states(const lp_state* states, int64_t n_states,
       ++a.n;
     }
     if (a.n == 0) break;
-    reorder_kernel<<<a.first[a.n], threads, smem, stream>>>(a);
-    if (cudaPeekAtLastError() != cudaSuccess) return LP_ERR_CUDA;
+    const cudaError_t e = launch_kernel(reorder_kernel, a.first[a.n], threads, smem, stream, a);
+    if (e != cudaSuccess) return status_of(e);
   }
   return LP_OK;
 }

@@ -1,5 +1,6 @@
 """Calls of the operators around their kernels: what a launch needs, what a failed one leaves
 behind, whose scratch it uses."""
+import ctypes
 import os
 import subprocess
 import sys
@@ -8,7 +9,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from grammar_constrained_logit_gb300 import _lib  # noqa: E402
+from grammar_constrained_logit_gb300 import _lib, ops  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +43,61 @@ def test_every_number_of_beams(counts):
     r = subprocess.run([sys.executable, "-c", EVERY_COUNT, *map(str, counts)], cwd=ROOT,
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+class _FailingStream:
+    """A stream on which every launch fails on the host: its capture was made invalid."""
+
+    def __enter__(self):
+        with open("/proc/self/maps") as f:
+            path = next(p for p in (line.split()[-1] for line in f) if "libcudart.so" in p)
+        self.rt, self.h = ctypes.CDLL(path), ctypes.c_void_p()
+        assert self.rt.cudaStreamCreateWithFlags(ctypes.byref(self.h), 1) == 0  # non-blocking
+        assert self.rt.cudaStreamBeginCapture(self.h, 2) == 0  # relaxed
+        assert self.rt.cudaStreamSynchronize(self.h) != 0  # not while capturing
+        self.rt.cudaGetLastError()
+        return torch.cuda.ExternalStream(self.h.value)
+
+    def __exit__(self, *_):
+        graph = ctypes.c_void_p()
+        assert self.rt.cudaStreamEndCapture(self.h, ctypes.byref(graph)) != 0
+        assert self.rt.cudaStreamDestroy(self.h) == 0
+        self.rt.cudaGetLastError()
+
+
+@pytest.mark.parametrize("failing", ["select", "reorder", "write", "read"])
+def test_a_failed_launch_is_reported_once(failing):
+    t = torch.randn(8, 900, device="cuda")
+    scores = torch.zeros(2, 4, device="cuda")
+    n = 5
+    out = tuple(torch.empty(2, n, dtype=d, device="cuda")
+                for d in (torch.float32, torch.int64, torch.int32))
+    ws = torch.empty(ops.beam_select_workspace_bytes(t.dtype, 8, 900), dtype=torch.uint8,
+                     device="cuda")
+    rows = torch.arange(8, device="cuda").float().view(8, 1).repeat(1, 64)
+    mover = ops.StateReorder([rows], 2, 4)
+    parents = torch.tensor([[1, 2, 3, 0], [0, 0, 2, 2]], dtype=torch.int32, device="cuda")
+    cache = ops.QuantCache.allocate(6, 2, 64)
+    x = [torch.randn(6, 2, 64, device="cuda") for _ in range(2)]
+    back = [torch.zeros_like(v) for v in x]
+    slots = torch.arange(6, device="cuda")
+    calls = {"select": lambda: ops.beam_select(t, scores, n, out=out, workspace=ws),
+             "reorder": lambda: mover.reorder(parents),
+             "write": lambda: ops.cache_write(cache, x, slots),
+             "read": lambda: ops.cache_read(cache, slots, out=back)}
+    for call in calls.values():  # whatever a first call sets up is set up
+        call()
+    torch.cuda.synchronize()
+    before = rows.clone()
+    with _FailingStream() as s, torch.cuda.stream(s):
+        with pytest.raises(_lib.LPError) as e:
+            calls[failing]()
+    assert e.value.status == _lib.LP_ERR_CUDA
+    torch.cuda.synchronize()
+    assert torch.equal(rows, before)
+    for name in ("reorder", "write", "read", "select"):  # none of them hears of it again
+        calls[name]()
+    torch.cuda.synchronize()
+    at = [(parents[b, k] + 4 * b).item() for b in range(2) for k in range(4)]
+    assert torch.equal(rows, before[at])
+    assert all(float((a - b).abs().max()) < 0.5 for a, b in zip(back, x))
