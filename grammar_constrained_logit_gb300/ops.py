@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import threading
 from typing import Sequence
 
 import torch
@@ -426,7 +427,30 @@ lp_mask_and_sample_slots = mask_and_sample_slots
 # call of these operators is a few microseconds, and that would be two of them.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
-_beam_workspaces: dict = {}
+
+class _Kept(threading.local):
+    """Scratch kept between calls, a tensor for each (device, stream), apart for each thread:
+    a call is several launches that hand on what they found, and two threads' launches on
+    one stream can alternate."""
+
+    def __init__(self):
+        self.tensors: dict = {}
+
+
+_beam_scratch = _Kept()
+
+
+def _scratch(kept: _Kept, device, stream: int, need: int, make) -> torch.Tensor:
+    """At least ``need`` bytes: the kept tensor, grown on demand.  A capture gets a new one,
+    from the graph's memory: a kept one could be replaced while the graph lives, or be
+    another graph's.  (Asking costs 0.3 us; a new tensor at every call took 3.)"""
+    if torch.cuda.is_current_stream_capturing():
+        return make(max(need, 8), dtype=torch.uint8, device=device)
+    key = (device.index, stream)
+    ws = kept.tensors.get(key)
+    if ws is None or ws.numel() < need:
+        ws = kept.tensors[key] = make(max(need, 8), dtype=torch.uint8, device=device)
+    return ws
 
 
 @functools.lru_cache(maxsize=256)
@@ -436,23 +460,6 @@ def beam_select_workspace_bytes(dtype: torch.dtype, rows: int, vocab_size: int) 
     if n < 0:
         raise ValueError("invalid dtype or size")
     return int(n)
-
-
-def _beam_workspace(workspace, device, stream: int, need: int):
-    """The caller's workspace (a uint8 CUDA tensor of any content), or one kept per
-    (device, stream), grown on demand.  When capturing a CUDA graph, pass one that was
-    allocated before the capture."""
-    if workspace is not None:
-        if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
-                workspace.device != device:
-            raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
-        return workspace
-    key = (device.index, stream)
-    ws = _beam_workspaces.get(key)
-    if ws is None or ws.numel() < need:
-        ws = torch.empty(max(need, 8), dtype=torch.uint8, device=device)
-        _beam_workspaces[key] = ws
-    return ws
 
 
 def _row_flags(flags, rows, device, name):
@@ -485,7 +492,10 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None
 
     Returns (scores float32, tokens int64, parents int32), each [batch, n_select],
     highest score first, ties to the lowest (beam, token); empty places are
-    (-inf, -1, -1).  ``out`` takes the three tensors to write instead."""
+    (-inf, -1, -1).  ``out`` takes the three tensors to write instead.  ``workspace``
+    (uint8, ``beam_select_workspace_bytes``, any content) is scratch to use instead of
+    what is kept for the thread and stream, or in a capture a part of the graph's memory;
+    two threads, or graphs that replay side by side, must not share one."""
     shape = scores.shape
     if len(shape) != 2:
         raise ValueError(f"scores must be [batch, beams], got {tuple(shape)}")
@@ -518,9 +528,9 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None
     if out is None:
         if n < 0:
             raise ValueError("n_select must not be negative")
-        out = (torch.empty((batch, n), dtype=torch.float32, device=device),
-               torch.empty((batch, n), dtype=torch.int64, device=device),
-               torch.empty((batch, n), dtype=torch.int32, device=device))
+        out = (torch.empty(batch, n, dtype=torch.float32, device=device),
+               torch.empty(batch, n, dtype=torch.int64, device=device),
+               torch.empty(batch, n, dtype=torch.int32, device=device))
     else:
         for t, d in zip(out, (torch.float32, torch.int64, torch.int32), strict=True):
             if t.dtype != d or t.shape != (batch, n) or not t.is_contiguous() or \
@@ -528,8 +538,12 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None
                 raise ValueError("out must be contiguous float32, int64 and int32 tensors "
                                  "[batch, n_select] on the logits' device")
     stream = _raw_stream(device.index)
-    ws = _beam_workspace(workspace, device, stream,
-                         beam_select_workspace_bytes(lg.dtype, rows, cols))
+    ws = workspace
+    if ws is None:
+        ws = _scratch(_beam_scratch, device, stream,
+                      beam_select_workspace_bytes(lg.dtype, rows, cols), torch.empty)
+    elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
     st = _lib.load().lp_beam_select(
         lg.data_ptr(), dt, batch, beams, cols, _stride(lg),
         None if bm is None else bm.data_ptr(), 0 if bm is None else bm.size(0),

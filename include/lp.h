@@ -347,8 +347,10 @@ lp_status lp_mask_and_sample_noalloc(const void* logits, lp_dtype dt, int64_t B,
  *   out_parents    device int32 [batch, n_select], the beam k; -1 in empty places
  *   workspace      device scratch of lp_beam_select_workspace_bytes(dt, batch *
  *                  beams, vocab_size) bytes (8 for each 512 bytes of a row), 8-byte
- *                  aligned, of any content; calls that share it must be ordered (one
- *                  stream, or events)
+ *                  aligned, of any content.  A call is two kernels that hand on
+ *                  partial sums in it: calls that share it must be ordered (one stream,
+ *                  or events) and must not be made by two host threads at once, whose
+ *                  launches could alternate; graphs that hold it must not replay at once
  * Two kernels on the stream.  Invalid: as lp_apply_token_bitmask_rows, beams < 1,
  * n_select < 0, row_needs_mask without bitmask, a short or misaligned workspace,
  * logits not aligned to their element.  beams or n_select above 256, more than 2^27

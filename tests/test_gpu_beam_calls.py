@@ -4,6 +4,7 @@ import ctypes
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 
@@ -101,3 +102,111 @@ def test_a_failed_launch_is_reported_once(failing):
     at = [(parents[b, k] + 4 * b).item() for b in range(2) for k in range(4)]
     assert torch.equal(rows, before[at])
     assert all(float((a - b).abs().max()) < 0.5 for a, b in zip(back, x))
+
+
+class _Watched:
+    """The library, which notes the scratch that a call of one entry point is given."""
+
+    def __init__(self, lib, name, instead=None):
+        self._lib, self._name, self._instead, self.seen = lib, name, instead, []
+
+    def __getattr__(self, name):
+        fn = getattr(self._lib, name)
+        if name != self._name:
+            return fn
+
+        def call(*args):
+            self.seen.append(getattr(args[-3], "value", args[-3]))
+            return self._instead() if self._instead else fn(*args)
+
+        return call
+
+
+def _search_step(seed, batch=2, beams=4, V=5000):
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = torch.randn(batch * beams, V, device="cuda", generator=g) * 2
+    return x, -torch.rand(batch, beams, device="cuda", generator=g) * 5
+
+
+def _same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def _two_threads(work):
+    failed = []
+
+    def run(i):
+        try:
+            work(i)
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if failed:
+        raise failed[0]
+
+
+def test_two_threads_on_one_stream_have_their_own_scratch(monkeypatch):
+    """A selection is two launches that hand on partial sums: with both threads between
+    the call and its return, neither's scratch may be the other's."""
+    steps = [_search_step(i) for i in range(2)]
+    torch.cuda.synchronize()
+    inside = threading.Barrier(2)
+    lib = _Watched(_lib.load(), "lp_beam_select", lambda: inside.wait(30) and 0)
+    monkeypatch.setattr(_lib, "load", lambda: lib)
+    _two_threads(lambda i: ops.beam_select(*steps[i]))
+    assert len(lib.seen) == 2 and lib.seen[0] != lib.seen[1]
+
+
+def test_two_threads_on_one_stream_select_as_one():
+    steps = [_search_step(i, 2 + i, 4, 20000 + 999 * i) for i in range(2)]
+    want = [ops.beam_select(*s) for s in steps]
+    torch.cuda.synchronize()
+
+    def work(i):
+        got = [ops.beam_select(*steps[i]) for _ in range(300)]
+        torch.cuda.synchronize()
+        assert all(_same(g, want[i]) for g in got)
+
+    _two_threads(work)
+
+
+def test_captured_without_a_workspace(monkeypatch):
+    """A graph's scratch is its own: neither that of the calls before it on its stream, nor
+    freed by a larger one after it, nor another graph's."""
+    small, large = _search_step(1), _search_step(2, 16, 8, 60000)
+    want = ops.beam_select(*small)
+    torch.cuda.synchronize()
+    lib = _Watched(_lib.load(), "lp_beam_select")
+    monkeypatch.setattr(_lib, "load", lambda: lib)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ops.beam_select(*small)
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(ops.beam_select(*small))
+        graphs.append(g)
+    with torch.cuda.stream(side):
+        ops.beam_select(*large)
+    torch.cuda.synchronize()
+    before, one, two, after = lib.seen
+    assert len({before, one, two}) == 3 and after not in (one, two)
+    # what the large call made the allocator give up is someone else's now
+    torch.cuda.empty_cache()
+    others = [torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(_same(o, want) for o in outs)
+    assert all(bool((o == 7).all()) for o in others)
