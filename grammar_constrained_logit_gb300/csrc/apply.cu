@@ -347,10 +347,9 @@ extern "C" lp_status lp_apply_token_bitmask_rows(void* logits, lp_dtype dt, int6
   if (B == 0) return LP_OK;
   if (g.vocab > 0 && (logits == nullptr || bitmask == nullptr)) return LP_ERR_INVALID_ARGUMENT;
   if (g.vocab == 0) {  // no row keeps a token, and there is nothing to mask
-    if (row_has_token != nullptr &&
-        cudaMemsetAsync(row_has_token, 0, size_t(B) * sizeof(int32_t), stream) != cudaSuccess)
-      return LP_ERR_CUDA;
-    return LP_OK;
+    return row_has_token == nullptr
+               ? LP_OK
+               : status_of(cudaMemsetAsync(row_has_token, 0, size_t(B) * sizeof(int32_t), stream));
   }
   const int64_t eb = elt_bytes(dt);
   ApplyArgs a{};

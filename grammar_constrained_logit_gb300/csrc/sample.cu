@@ -2253,7 +2253,7 @@ lp_status run_sample(const void* logits, lp_dtype dt, int64_t B, int64_t vocab,
     case LP_F16: e = launch_sample<LP_F16>(a, plan, B, ws, stream); break;
     default: e = launch_sample<LP_BF16>(a, plan, B, ws, stream); break;
   }
-  return e == cudaSuccess ? LP_OK : LP_ERR_CUDA;
+  return status_of(e);
 }
 
 }  // namespace
@@ -2354,6 +2354,7 @@ void* noalloc_scratch(lp_status& st) {
   static void* addr[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    (void)cudaGetLastError();
     st = LP_ERR_CUDA;
     return nullptr;
   }
@@ -2406,7 +2407,7 @@ extern "C" lp_status lp_philox4x32_10(const uint32_t* counters, const uint32_t* 
   if (!counters || !keys || !out) return LP_ERR_INVALID_ARGUMENT;
   const int64_t blocks = std::min<int64_t>((n + 255) / 256, 4096);
   philox_kernel<<<unsigned(blocks), 256, 0, stream>>>(counters, keys, out, n);
-  return cudaGetLastError() == cudaSuccess ? LP_OK : LP_ERR_CUDA;
+  return status_of(cudaGetLastError());
 }
 
 extern "C" const char* lp_status_string(lp_status status) {

@@ -9,7 +9,7 @@
 // enqueued on a copy stream and an event is recorded after them, so the compute
 // stream waits on the event rather than the host on the copy.  No kernel runs
 // here.
-#include "lp.h"
+#include "common.cuh"
 
 extern "C" lp_status lp_upload_bitmask(int32_t* device_bitmask, int64_t device_stride,
                                        const int32_t* host_bitmask, int64_t host_stride,
@@ -22,16 +22,14 @@ extern "C" lp_status lp_upload_bitmask(int32_t* device_bitmask, int64_t device_s
   const bool mask_work = rows > 0 && words > 0;
   if (mask_work && (device_bitmask == nullptr || host_bitmask == nullptr))
     return LP_ERR_INVALID_ARGUMENT;
-  if (mask_work &&
-      cudaMemcpy2DAsync(device_bitmask, size_t(device_stride) * 4, host_bitmask,
-                        size_t(host_stride) * 4, size_t(words) * 4, size_t(rows),
-                        cudaMemcpyHostToDevice, copy_stream) != cudaSuccess)
-    return LP_ERR_CUDA;
-  if (rows > 0 && device_flags != nullptr &&
-      cudaMemcpyAsync(device_flags, host_flags, size_t(rows), cudaMemcpyHostToDevice,
-                      copy_stream) != cudaSuccess)
-    return LP_ERR_CUDA;
-  if (uploaded != nullptr && cudaEventRecord(uploaded, copy_stream) != cudaSuccess)
-    return LP_ERR_CUDA;
-  return LP_OK;
+  cudaError_t e = cudaSuccess;
+  if (mask_work)
+    e = cudaMemcpy2DAsync(device_bitmask, size_t(device_stride) * 4, host_bitmask,
+                          size_t(host_stride) * 4, size_t(words) * 4, size_t(rows),
+                          cudaMemcpyHostToDevice, copy_stream);
+  if (e == cudaSuccess && rows > 0 && device_flags != nullptr)
+    e = cudaMemcpyAsync(device_flags, host_flags, size_t(rows), cudaMemcpyHostToDevice,
+                        copy_stream);
+  if (e == cudaSuccess && uploaded != nullptr) e = cudaEventRecord(uploaded, copy_stream);
+  return lp::status_of(e);
 }

@@ -44,7 +44,7 @@
  *   - Errors: arguments are checked on the host before any launch.  An invalid
  *     argument returns LP_ERR_INVALID_ARGUMENT and launches nothing.  A zero-size
  *     problem returns LP_OK and launches nothing.  A launch failure returns
- *     LP_ERR_CUDA (the CUDA error is left for cudaGetLastError to report).
+ *     LP_ERR_CUDA; the CUDA error is taken back, so no later call reports it again.
  */
 #ifndef LP_H_
 #define LP_H_

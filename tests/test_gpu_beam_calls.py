@@ -210,3 +210,41 @@ def test_captured_without_a_workspace(monkeypatch):
     torch.cuda.synchronize()
     assert all(_same(o, want) for o in outs)
     assert all(bool((o == 7).all()) for o in others)
+
+
+@pytest.mark.parametrize("failing", ["sample", "upload", "rows", "apply"])
+def test_a_failed_masking_or_sampling_call_is_reported_once(failing):
+    x, bm = torch.randn(4, 900, device="cuda"), torch.full((4, 29), -1, dtype=torch.int32,
+                                                           device="cuda")
+    ws = torch.zeros(ops.sample_workspace_bytes(x.dtype, 4, 900), dtype=torch.uint8, device="cuda")
+    ids = torch.empty(4, dtype=torch.int64, device="cuda")
+    host = torch.zeros(4, 29, dtype=torch.int32).pin_memory()
+    mask = torch.zeros_like(bm)
+    has = torch.empty(4, dtype=torch.int32, device="cuda")
+    lib = _lib.load()
+
+    def rows():  # the entry point itself: the binding would allocate
+        st = lib.lp_apply_token_bitmask_rows(
+            x.data_ptr(), _lib.LP_F32, 4, 900, 900, bm.data_ptr(), 4, 29, 29, -1, None,
+            has.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        _lib.check("lp_apply_token_bitmask_rows", st)
+
+    def upload():
+        st = lib.lp_upload_bitmask(mask.data_ptr(), 29, host.data_ptr(), 29, 4, 29, None, None,
+                                   torch.cuda.current_stream().cuda_stream, None)
+        _lib.check("lp_upload_bitmask", st)
+
+    calls = {"sample": lambda: ops.sample(x, temperature=0.0, out=ids, workspace=ws),
+             "upload": upload, "rows": rows,
+             "apply": lambda: ops.apply_token_bitmask_inplace(x, bm)}
+    for call in calls.values():
+        call()
+    torch.cuda.synchronize()
+    with _FailingStream() as s, torch.cuda.stream(s):
+        with pytest.raises(_lib.LPError) as e:
+            calls[failing]()
+    assert e.value.status == _lib.LP_ERR_CUDA
+    for name in ("apply", "rows", "sample", "upload"):
+        calls[name]()
+    torch.cuda.synchronize()
+    assert torch.equal(ids, x.argmax(1)) and torch.equal(mask.cpu(), host)
