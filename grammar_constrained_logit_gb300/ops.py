@@ -289,7 +289,34 @@ def _ids_out(out, B, device):
     return out
 
 
-_workspaces: dict = {}
+# The current stream's handle, without the Stream object that current_stream() makes: a
+# call of the beam-search operators is a few microseconds, and that would be two of them.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+class _Kept(threading.local):
+    """Scratch kept between calls, a tensor for each (device, stream), apart for each thread:
+    a call is several launches that hand on what they found, and two threads' launches on
+    one stream can alternate."""
+
+    def __init__(self):
+        self.tensors: dict = {}
+
+
+_sample_scratch, _beam_scratch = _Kept(), _Kept()
+
+
+def _scratch(kept: _Kept, device, stream: int, need: int, make) -> torch.Tensor:
+    """At least ``need`` bytes: the kept tensor, grown on demand.  A capture gets a new one,
+    from the graph's memory: a kept one could be replaced while the graph lives, or be
+    another graph's.  (Asking costs 0.3 us; a new tensor at every call took 3.)"""
+    if torch.cuda.is_current_stream_capturing():
+        return make(max(need, 8), dtype=torch.uint8, device=device)
+    key = (device.index, stream)
+    ws = kept.tensors.get(key)
+    if ws is None or ws.numel() < need:
+        ws = kept.tensors[key] = make(max(need, 8), dtype=torch.uint8, device=device)
+    return ws
 
 
 def sample_workspace_bytes(dtype: torch.dtype, batch_size: int, vocab_size: int) -> int:
@@ -300,25 +327,20 @@ def sample_workspace_bytes(dtype: torch.dtype, batch_size: int, vocab_size: int)
     return int(n)
 
 
-def _workspace(workspace, lg: torch.Tensor, B: int, vocab: int):
+def _workspace(workspace, lg: torch.Tensor, B: int, vocab: int) -> torch.Tensor:
     """The caller's workspace (a uint8 CUDA tensor, zero-filled before its first
-    use), or one kept per (device, stream), grown on demand; the library keeps its
-    counters valid across calls.  When capturing a CUDA graph, pass an explicit
-    workspace allocated before the capture: the capture stream would otherwise get
-    a workspace of its own allocated (and zero-filled) inside the graph.
-    Returns (pointer, bytes)."""
+    use), or the thread's own for (device, stream); the library keeps its counters
+    valid across calls.  A capture without one gets its own in the graph, zero-filled
+    at each replay: pass one that was allocated before the capture to save that.
+    Two threads, or graphs that replay side by side, must not share a workspace."""
     need = sample_workspace_bytes(lg.dtype, B, max(vocab, 0))
     if workspace is not None:
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
                 workspace.device != lg.device:
             raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
-        return ctypes.c_void_p(workspace.data_ptr()), workspace.numel()
-    key = (lg.device.index, torch.cuda.current_stream(lg.device).cuda_stream)
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < need:
-        ws = torch.zeros(max(need, 1), dtype=torch.uint8, device=lg.device)
-        _workspaces[key] = ws
-    return ctypes.c_void_p(ws.data_ptr()), ws.numel()
+        return workspace
+    stream = torch.cuda.current_stream(lg.device).cuda_stream
+    return _scratch(_sample_scratch, lg.device, stream, need, torch.zeros)
 
 
 def sample(logits: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, seed: int = 0,
@@ -333,10 +355,10 @@ def sample(logits: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
     keep: list = []
     p = _params(B, lg.device, temperature, top_k, top_p, min_p, seed, offset, keep)
     ids = _ids_out(out, B, lg.device)
-    wp, wn = _workspace(workspace, lg, B, V)
+    ws = _workspace(workspace, lg, B, V)
     lib = _lib.load()
     st = lib.lp_sample(_ptr(lg), _dtype_code(lg), B, V, _stride(lg),
-                       ctypes.byref(p), _ptr(ids), wp, wn, _stream(lg))
+                       ctypes.byref(p), _ptr(ids), _ptr(ws), ws.numel(), _stream(lg))
     check("lp_sample", st)
     return ids
 
@@ -361,14 +383,14 @@ def mask_and_sample(logits: torch.Tensor, bitmask: torch.Tensor | None, temperat
     p = _params(B, lg.device, temperature, top_k, top_p, min_p, seed, offset, keep)
     ids = _ids_out(out, B, lg.device)
     # the workspace is sized by the widest vocabulary the call can use
-    wp, wn = _workspace(workspace, lg, B, lg.size(1))
+    ws = _workspace(workspace, lg, B, lg.size(1))
     lib = _lib.load()
     st = lib.lp_mask_and_sample(
         _ptr(lg), _dtype_code(lg), B, lg.size(1), _stride(lg), _ptr(bm),
         0 if bm is None else bm.size(0), 0 if bm is None else bm.size(1),
         0 if bm is None else _stride(bm), -1 if vocab_size is None else int(vocab_size),
-        _ptr(idx), 0 if idx is None else idx.numel(), ctypes.byref(p), _ptr(ids), wp, wn,
-        _stream(lg))
+        _ptr(idx), 0 if idx is None else idx.numel(), ctypes.byref(p), _ptr(ids), _ptr(ws),
+        ws.numel(), _stream(lg))
     check("lp_mask_and_sample", st)
     return ids
 
@@ -408,49 +430,19 @@ def mask_and_sample_slots(logits: torch.Tensor, bitmask: torch.Tensor | None,
         if sd.numel() != B:
             raise ValueError(f"seeds must have {B} entries")
     ids = _ids_out(out, B, lg.device)
-    wp, wn = _workspace(workspace, lg, B, lg.size(1))
+    ws = _workspace(workspace, lg, B, lg.size(1))
     lib = _lib.load()
     st = lib.lp_mask_and_sample_slots(
         _ptr(lg), _dtype_code(lg), B, lg.size(1), _stride(lg), _ptr(bm),
         0 if bm is None else bm.size(0), 0 if bm is None else bm.size(1),
         0 if bm is None else _stride(bm), -1 if vocab_size is None else int(vocab_size),
         _ptr(idx), 0 if idx is None else idx.numel(), ctypes.byref(p), R, _ptr(sd), _ptr(ids),
-        wp, wn, _stream(lg))
+        _ptr(ws), ws.numel(), _stream(lg))
     check("lp_mask_and_sample_slots", st)
     return ids
 
 
 lp_mask_and_sample_slots = mask_and_sample_slots
-
-
-# The current stream's handle, without the Stream object that current_stream() makes: a
-# call of these operators is a few microseconds, and that would be two of them.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-class _Kept(threading.local):
-    """Scratch kept between calls, a tensor for each (device, stream), apart for each thread:
-    a call is several launches that hand on what they found, and two threads' launches on
-    one stream can alternate."""
-
-    def __init__(self):
-        self.tensors: dict = {}
-
-
-_beam_scratch = _Kept()
-
-
-def _scratch(kept: _Kept, device, stream: int, need: int, make) -> torch.Tensor:
-    """At least ``need`` bytes: the kept tensor, grown on demand.  A capture gets a new one,
-    from the graph's memory: a kept one could be replaced while the graph lives, or be
-    another graph's.  (Asking costs 0.3 us; a new tensor at every call took 3.)"""
-    if torch.cuda.is_current_stream_capturing():
-        return make(max(need, 8), dtype=torch.uint8, device=device)
-    key = (device.index, stream)
-    ws = kept.tensors.get(key)
-    if ws is None or ws.numel() < need:
-        ws = kept.tensors[key] = make(max(need, 8), dtype=torch.uint8, device=device)
-    return ws
 
 
 @functools.lru_cache(maxsize=256)

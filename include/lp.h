@@ -217,8 +217,10 @@ lp_status lp_apply_packed_bitmask(void* out, int64_t out_stride, const void* log
  *                  resets the counters of the rows it samples.  To restore full
  *                  speed at once, zero those first 256 + 4 * 16384 bytes again
  *                  (or the whole workspace).  Calls that share a workspace must
- *                  be ordered (one stream, or events).  A NULL, misaligned or
- *                  short workspace is LP_ERR_INVALID_ARGUMENT.
+ *                  be ordered (one stream, or events) and not be made by two host
+ *                  threads at once, whose launches could alternate; graphs that
+ *                  hold it must not replay at once.  A NULL, misaligned or short
+ *                  workspace is LP_ERR_INVALID_ARGUMENT.
  * Each call is two kernels on the stream: a streaming pass over the logits and
  * a per-row finish, the second launched as a programmatic dependent of the
  * first.  An id of -2 means a wait inside the streaming kernel gave up (a copy
@@ -306,7 +308,8 @@ lp_status lp_mask_and_sample_slots(const void* logits, lp_dtype dt, int64_t B, i
  *   - Sharing: every call uses the same array and leaves its counters zero for
  *     the next.  Calls that overlap on the GPU (in flight at once on different
  *     streams, or from several host threads without ordering) race on it and
- *     give undefined ids; order them (one stream, or events).
+ *     give undefined ids; order them (one stream, or events, and never two host
+ *     threads in the call at once).
  * Arguments, results and other errors as lp_mask_and_sample.
  */
 lp_status lp_mask_and_sample_noalloc(const void* logits, lp_dtype dt, int64_t B, int64_t cols,

@@ -248,3 +248,74 @@ def test_a_failed_masking_or_sampling_call_is_reported_once(failing):
         calls[name]()
     torch.cuda.synchronize()
     assert torch.equal(ids, x.argmax(1)) and torch.equal(mask.cpu(), host)
+
+
+def test_sampler_two_threads_on_one_stream_have_their_own_scratch(monkeypatch):
+    x = torch.randn(4, 3000, device="cuda")
+    torch.cuda.synchronize()
+    inside = threading.Barrier(2)
+    lib = _Watched(_lib.load(), "lp_sample", lambda: inside.wait(30) and 0)
+    monkeypatch.setattr(_lib, "load", lambda: lib)
+
+    def work(i):
+        for _ in range(2):
+            ops.sample(x)
+
+    _two_threads(work)
+    one, two, three, four = lib.seen  # the calls went in pairs, one of each thread
+    assert one != two and {one, two} == {three, four}  # kept between calls
+
+
+def test_sampler_two_threads_on_one_stream_draw_as_one():
+    xs = [torch.randn(64, 20000 + 1000 * i, device="cuda") for i in range(2)]
+    want = [[ops.sample(x, 0.8, 40, 0.9, seed=j) for j in range(100)] for x in xs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        got = [ops.sample(xs[i], 0.8, 40, 0.9, seed=j) for j in range(100)]
+        torch.cuda.synchronize()
+        assert _same(got, want[i])
+
+    _two_threads(work)
+
+
+@pytest.mark.parametrize("entry", ["lp_sample", "lp_mask_and_sample", "lp_mask_and_sample_slots"])
+def test_sampler_captured_without_a_workspace(monkeypatch, entry):
+    def call(x):
+        if entry == "lp_sample":
+            return ops.sample(x, 0.8, 40, 0.9, seed=5)
+        if entry == "lp_mask_and_sample":
+            return ops.mask_and_sample(x, None, 0.8, 40, 0.9, seed=5)
+        return ops.mask_and_sample_slots(x, None, 2, 0.8, 40, 0.9, seed=5)
+
+    small, large = (torch.randn(r, v, device="cuda") for r, v in ((8, 5000), (512, 90000)))
+    want = call(small)
+    torch.cuda.synchronize()
+    lib = _Watched(_lib.load(), entry)
+    monkeypatch.setattr(_lib, "load", lambda: lib)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(small)
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(call(small))
+        graphs.append(g)
+    with torch.cuda.stream(side):
+        call(large)
+    torch.cuda.synchronize()
+    before, one, two, after = lib.seen
+    assert len({before, one, two}) == 3 and after not in (one, two)
+    torch.cuda.empty_cache()
+    others = [torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    assert all(bool((o == 7).all()) for o in others)
