@@ -291,7 +291,8 @@ def _ids_out(out, B, device):
 
 # The current stream's handle, without the Stream object that current_stream() makes: a
 # call of the beam-search operators is a few microseconds, and that would be two of them.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (A torch built for the CPU alone has none; importing this module needs none.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class _Kept(threading.local):
