@@ -47,8 +47,26 @@ def _matrix_host(t: torch.Tensor) -> torch.Tensor:
     return t
 
 
+# The current stream's handle and the current device, without the objects and checks around
+# them: a call of these operators is a few microseconds, and a Stream would be two of them.
+# (A torch built for the CPU alone has neither; importing this module needs none.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _call(name: str, device, *args) -> None:
+    """The entry point ``name`` with ``device`` current: its kernels run there, and the default
+    stream's handle, which is the same on every device, means that device's."""
+    if _current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(name, device, *args)
+    st = getattr(_lib.load(), name)(*args)
+    if st != _lib.LP_OK:
+        check(name, st)
+
+
 def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    return ctypes.c_void_p(_raw_stream(t.device.index))
 
 
 def _bitmask(bitmask: torch.Tensor, device) -> torch.Tensor:
@@ -100,12 +118,10 @@ def apply_token_bitmask_inplace(logits: torch.Tensor, bitmask: torch.Tensor, *,
     lg = _matrix(logits, "logits")
     bm = _bitmask(bitmask, lg.device)
     idx = _indices(indices, lg.device)
-    lib = _lib.load()
-    st = lib.lp_apply_token_bitmask(
-        _ptr(lg), _dtype_code(lg), lg.size(0), lg.size(1), _stride(lg), _ptr(bm), bm.size(0),
-        bm.size(1), _stride(bm), -1 if vocab_size is None else int(vocab_size), _ptr(idx),
-        0 if idx is None else idx.numel(), _stream(lg))
-    check("lp_apply_token_bitmask", st)
+    _call("lp_apply_token_bitmask", lg.device, _ptr(lg), _dtype_code(lg), lg.size(0), lg.size(1),
+          _stride(lg), _ptr(bm), bm.size(0), bm.size(1), _stride(bm),
+          -1 if vocab_size is None else int(vocab_size), _ptr(idx),
+          0 if idx is None else idx.numel(), _stream(lg))
 
 
 lp_apply_token_bitmask = apply_token_bitmask_inplace
@@ -130,12 +146,9 @@ def apply_token_bitmask_rows(logits: torch.Tensor, bitmask: torch.Tensor,
         if flags.numel() != B:
             raise ValueError(f"row_needs_mask must have {B} entries")
     has = torch.empty(B, dtype=torch.int32, device=lg.device) if report else None
-    lib = _lib.load()
-    st = lib.lp_apply_token_bitmask_rows(
-        _ptr(lg), _dtype_code(lg), B, lg.size(1), _stride(lg), _ptr(bm), bm.size(0), bm.size(1),
-        _stride(bm), -1 if vocab_size is None else int(vocab_size), _ptr(flags), _ptr(has),
-        _stream(lg))
-    check("lp_apply_token_bitmask_rows", st)
+    _call("lp_apply_token_bitmask_rows", lg.device, _ptr(lg), _dtype_code(lg), B, lg.size(1),
+          _stride(lg), _ptr(bm), bm.size(0), bm.size(1), _stride(bm),
+          -1 if vocab_size is None else int(vocab_size), _ptr(flags), _ptr(has), _stream(lg))
     return has
 
 
@@ -169,13 +182,10 @@ def upload_bitmask(device_bitmask: torch.Tensor, host_bitmask: torch.Tensor, *,
         raise ValueError("row flags must be uint8 with at least one entry per row")
     stream = copy_stream if copy_stream is not None else torch.cuda.current_stream(db.device)
     ev = event if event is not None else torch.cuda.Event()
-    lib = _lib.load()
     # PyTorch creates an event's CUDA handle at its first record, so the event is
     # recorded here, on the copy stream right after the enqueued copies
-    st = lib.lp_upload_bitmask(_ptr(db), _stride(db), _ptr(hb), _stride(hb), rows, words,
-                               _ptr(device_flags), _ptr(host_flags),
-                               ctypes.c_void_p(stream.cuda_stream), None)
-    check("lp_upload_bitmask", st)
+    _call("lp_upload_bitmask", db.device, _ptr(db), _stride(db), _ptr(hb), _stride(hb), rows, words,
+          _ptr(device_flags), _ptr(host_flags), ctypes.c_void_p(stream.cuda_stream), None)
     ev.record(stream)
     return ev
 
@@ -245,13 +255,10 @@ def apply_packed_bitmask(logits: torch.Tensor, bitmask: torch.Tensor,
     if o.dtype != lg.dtype or o.shape != lg.shape:
         raise ValueError("out must match logits in dtype and shape")
     idx = _indices(indices, lg.device)
-    lib = _lib.load()
-    st = lib.lp_apply_packed_bitmask(
-        _ptr(o), _stride(o), _ptr(lg), _dtype_code(lg), lg.size(0), lg.size(1), _stride(lg),
-        _ptr(bm), bm.size(0), bm.size(1), _stride(bm), float(fill_value),
-        -1 if vocab_size is None else int(vocab_size), _ptr(idx),
-        0 if idx is None else idx.numel(), _stream(lg))
-    check("lp_apply_packed_bitmask", st)
+    _call("lp_apply_packed_bitmask", lg.device, _ptr(o), _stride(o), _ptr(lg), _dtype_code(lg),
+          lg.size(0), lg.size(1), _stride(lg), _ptr(bm), bm.size(0), bm.size(1), _stride(bm),
+          float(fill_value), -1 if vocab_size is None else int(vocab_size), _ptr(idx),
+          0 if idx is None else idx.numel(), _stream(lg))
     return out
 
 
@@ -287,12 +294,6 @@ def _ids_out(out, B, device):
     if out.dtype != torch.int64 or out.numel() != B or not out.is_contiguous():
         raise ValueError("out must be a contiguous int64 tensor of B elements")
     return out
-
-
-# The current stream's handle, without the Stream object that current_stream() makes: a
-# call of the beam-search operators is a few microseconds, and that would be two of them.
-# (A torch built for the CPU alone has none; importing this module needs none.)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class _Kept(threading.local):
@@ -340,8 +341,8 @@ def _workspace(workspace, lg: torch.Tensor, B: int, vocab: int) -> torch.Tensor:
                 workspace.device != lg.device:
             raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
         return workspace
-    stream = torch.cuda.current_stream(lg.device).cuda_stream
-    return _scratch(_sample_scratch, lg.device, stream, need, torch.zeros)
+    device = lg.device
+    return _scratch(_sample_scratch, device, _raw_stream(device.index), need, torch.zeros)
 
 
 def sample(logits: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, seed: int = 0,
@@ -357,10 +358,8 @@ def sample(logits: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
     p = _params(B, lg.device, temperature, top_k, top_p, min_p, seed, offset, keep)
     ids = _ids_out(out, B, lg.device)
     ws = _workspace(workspace, lg, B, V)
-    lib = _lib.load()
-    st = lib.lp_sample(_ptr(lg), _dtype_code(lg), B, V, _stride(lg),
-                       ctypes.byref(p), _ptr(ids), _ptr(ws), ws.numel(), _stream(lg))
-    check("lp_sample", st)
+    _call("lp_sample", lg.device, _ptr(lg), _dtype_code(lg), B, V, _stride(lg), ctypes.byref(p),
+          _ptr(ids), _ptr(ws), ws.numel(), _stream(lg))
     return ids
 
 
@@ -385,14 +384,11 @@ def mask_and_sample(logits: torch.Tensor, bitmask: torch.Tensor | None, temperat
     ids = _ids_out(out, B, lg.device)
     # the workspace is sized by the widest vocabulary the call can use
     ws = _workspace(workspace, lg, B, lg.size(1))
-    lib = _lib.load()
-    st = lib.lp_mask_and_sample(
-        _ptr(lg), _dtype_code(lg), B, lg.size(1), _stride(lg), _ptr(bm),
-        0 if bm is None else bm.size(0), 0 if bm is None else bm.size(1),
-        0 if bm is None else _stride(bm), -1 if vocab_size is None else int(vocab_size),
-        _ptr(idx), 0 if idx is None else idx.numel(), ctypes.byref(p), _ptr(ids), _ptr(ws),
-        ws.numel(), _stream(lg))
-    check("lp_mask_and_sample", st)
+    _call("lp_mask_and_sample", lg.device, _ptr(lg), _dtype_code(lg), B, lg.size(1), _stride(lg),
+          _ptr(bm), 0 if bm is None else bm.size(0), 0 if bm is None else bm.size(1),
+          0 if bm is None else _stride(bm), -1 if vocab_size is None else int(vocab_size),
+          _ptr(idx), 0 if idx is None else idx.numel(), ctypes.byref(p), _ptr(ids), _ptr(ws),
+          ws.numel(), _stream(lg))
     return ids
 
 
@@ -432,14 +428,11 @@ def mask_and_sample_slots(logits: torch.Tensor, bitmask: torch.Tensor | None,
             raise ValueError(f"seeds must have {B} entries")
     ids = _ids_out(out, B, lg.device)
     ws = _workspace(workspace, lg, B, lg.size(1))
-    lib = _lib.load()
-    st = lib.lp_mask_and_sample_slots(
-        _ptr(lg), _dtype_code(lg), B, lg.size(1), _stride(lg), _ptr(bm),
-        0 if bm is None else bm.size(0), 0 if bm is None else bm.size(1),
-        0 if bm is None else _stride(bm), -1 if vocab_size is None else int(vocab_size),
-        _ptr(idx), 0 if idx is None else idx.numel(), ctypes.byref(p), R, _ptr(sd), _ptr(ids),
-        _ptr(ws), ws.numel(), _stream(lg))
-    check("lp_mask_and_sample_slots", st)
+    _call("lp_mask_and_sample_slots", lg.device, _ptr(lg), _dtype_code(lg), B, lg.size(1),
+          _stride(lg), _ptr(bm), 0 if bm is None else bm.size(0), 0 if bm is None else bm.size(1),
+          0 if bm is None else _stride(bm), -1 if vocab_size is None else int(vocab_size),
+          _ptr(idx), 0 if idx is None else idx.numel(), ctypes.byref(p), R, _ptr(sd), _ptr(ids),
+          _ptr(ws), ws.numel(), _stream(lg))
     return ids
 
 
@@ -521,9 +514,9 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None
     if out is None:
         if n < 0:
             raise ValueError("n_select must not be negative")
-        out = (torch.empty(batch, n, dtype=torch.float32, device=device),
-               torch.empty(batch, n, dtype=torch.int64, device=device),
-               torch.empty(batch, n, dtype=torch.int32, device=device))
+        out = (torch.empty((batch, n), dtype=torch.float32, device=device),
+               torch.empty((batch, n), dtype=torch.int64, device=device),
+               torch.empty((batch, n), dtype=torch.int32, device=device))
     else:
         for t, d in zip(out, (torch.float32, torch.int64, torch.int32), strict=True):
             if t.dtype != d or t.shape != (batch, n) or not t.is_contiguous() or \
@@ -537,14 +530,14 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None
                       beam_select_workspace_bytes(lg.dtype, rows, cols), torch.empty)
     elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
         raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
-    st = _lib.load().lp_beam_select(
-        lg.data_ptr(), dt, batch, beams, cols, _stride(lg),
-        None if bm is None else bm.data_ptr(), 0 if bm is None else bm.size(0),
-        0 if bm is None else bm.size(1), 0 if bm is None else _stride(bm),
-        -1 if vocab_size is None else int(vocab_size), None if flags is None else flags.data_ptr(),
-        sc.data_ptr(), None if ended is None else ended.data_ptr(), int(pad_id), n,
-        out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), ws.numel(), stream)
-    check("lp_beam_select", st)
+    _call("lp_beam_select", device, lg.data_ptr(), dt, batch, beams, cols,
+          lg.stride(0) if rows > 1 else max(lg.stride(0), cols),
+          None if bm is None else bm.data_ptr(), 0 if bm is None else bm.size(0),
+          0 if bm is None else bm.size(1), 0 if bm is None else _stride(bm),
+          -1 if vocab_size is None else int(vocab_size),
+          None if flags is None else flags.data_ptr(), sc.data_ptr(),
+          None if ended is None else ended.data_ptr(), int(pad_id), n, out[0].data_ptr(),
+          out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), ws.numel(), stream)
     return out
 
 
@@ -653,9 +646,8 @@ class StateReorder:
         p = self._check(parents, "parents", "[batch, beams]", b * k)
         lo = None if start is None else self._check(start, "start", "[batch]", b)
         hi = None if stop is None else self._check(stop, "stop", "[batch]", b)
-        st = _lib.load().lp_reorder_states(self._c, len(self.states), b, k, p, lo, hi,
-                                           _raw_stream(self.device.index))
-        check("lp_reorder_states", st)
+        _call("lp_reorder_states", self.device, self._c, len(self.states), b, k, p, lo, hi,
+              _raw_stream(self.device.index))
 
 
 def reorder_states(states, parents: torch.Tensor, start: torch.Tensor | None = None,
@@ -770,10 +762,8 @@ def _cache_call(name, cache: QuantCache, xs, slots: torch.Tensor):
         if inner != 1 and cache.dim > 1:
             raise ValueError("a head's elements must be contiguous")
         heads.append((x.data_ptr(), token, head))
-    st = getattr(_lib.load(), name)(
-        cache._parts, cache._heads_type(*heads), parts, cache.bits, dt, *cache._sizes,
-        slots.data_ptr(), n, _raw_stream(device.index))
-    check(name, st)
+    _call(name, device, cache._parts, cache._heads_type(*heads), parts, cache.bits, dt,
+          *cache._sizes, slots.data_ptr(), n, _raw_stream(device.index))
 
 
 def cache_write(cache: QuantCache, x, slots: torch.Tensor) -> None:
@@ -814,9 +804,7 @@ def philox4x32_10(counters: torch.Tensor, keys: torch.Tensor) -> torch.Tensor:
     if c.dim() != 2 or c.size(1) != 4 or k.shape != (c.size(0), 2) or not c.is_cuda:
         raise ValueError("counters must be [n, 4] and keys [n, 2], on the GPU")
     out = torch.empty_like(c)
-    lib = _lib.load()
-    check("lp_philox4x32_10",
-          lib.lp_philox4x32_10(_ptr(c), _ptr(k), _ptr(out), c.size(0), _stream(c)))
+    _call("lp_philox4x32_10", c.device, _ptr(c), _ptr(k), _ptr(out), c.size(0), _stream(c))
     return out
 
 
