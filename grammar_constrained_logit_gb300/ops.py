@@ -544,6 +544,11 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None
 lp_beam_select = beam_select
 
 
+def _expanded(t: torch.Tensor) -> bool:
+    """Whether elements of ``t`` share their memory by a stride of zero."""
+    return any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride()))
+
+
 def _state(t: torch.Tensor, row_dim: int, token_dim: int | None) -> _lib.State:
     """A tensor's rows as lp_state: the longest contiguous run, up to the tokens' axis
     when one is given, and the axes around it."""
@@ -557,7 +562,7 @@ def _state(t: torch.Tensor, row_dim: int, token_dim: int | None) -> _lib.State:
         token_dim %= d
         if token_dim == row_dim:
             raise ValueError("the tokens' axis must not be the rows'")
-    if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+    if _expanded(t):
         raise ValueError("a state must not be expanded: its rows would overlap")
     size = t.element_size()
     axes = sorted(((st * size, n, i) for i, (n, st) in enumerate(zip(t.shape, t.stride()))
@@ -699,6 +704,8 @@ class QuantCache:
                 n > 1 and a != b
                 for n, a, b in zip(params.shape[d - 1:], params.stride()[d - 1:], want)):
             raise ValueError("a head's codes and params must be contiguous")
+        if _expanded(codes) or _expanded(params):
+            raise ValueError("codes and params must not be expanded: slots would overlap")
         if codes.size(0) > 8:
             raise ValueError("a cache has 8 parts at most")
         self.codes, self.params, self.dim, self.bits = codes, params, dim, bits
@@ -789,6 +796,8 @@ def cache_read(cache: QuantCache, slots: torch.Tensor, *, dtype: torch.dtype = t
                      for _ in range(cache.parts)])
     else:
         out = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if any(_expanded(t) for t in out):
+            raise ValueError("out must not be expanded: tokens would overlap")
     _cache_call("lp_cache_read", cache, out, slots)
     return out
 

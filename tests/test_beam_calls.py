@@ -112,3 +112,25 @@ def test_launches_are_on_the_tensors_device(recorded, monkeypatch, index):
     assert len(recorded.calls) == 11
     assert {device for _, device in recorded.calls} == {index}
     assert recorded.current == [0]
+
+
+def test_what_is_written_must_not_be_expanded(recorded):
+    codes, params = torch.zeros(2, 6, 2, 8, dtype=torch.uint8), torch.zeros(2, 6, 2, 1)
+    for c, p in ((codes[:, :1].expand(2, 6, 2, 8), params),
+                 (codes, params[:, :, :1].expand(2, 6, 2, 1)),
+                 (codes[:1].expand(2, 6, 2, 8), params)):
+        with pytest.raises(ValueError, match="expanded"):
+            ops.QuantCache(OnGpu(c), OnGpu(p), dim=8)
+    one = torch.zeros(1, 1, 1, 8, dtype=torch.uint8).as_strided((1, 1, 1, 8), (0, 0, 0, 1))
+    ops.QuantCache(OnGpu(one), OnGpu(torch.zeros(1, 1, 1, 1)), dim=8)  # nothing overlaps
+
+    cache = ops.QuantCache(OnGpu(codes), OnGpu(params), dim=8)
+    slots = OnGpu(torch.arange(3))
+    full = OnGpu(torch.zeros(3, 2, 8))
+    for wide in (torch.zeros(1, 2, 8).expand(3, 2, 8), torch.zeros(3, 1, 8).expand(3, 2, 8)):
+        with pytest.raises(ValueError, match="expanded"):
+            ops.cache_read(cache, slots, out=(full, OnGpu(wide)))
+        assert not recorded.calls
+    ops.cache_write(cache, (full, OnGpu(torch.zeros(1, 2, 8).expand(3, 2, 8))), slots)  # reads
+    ops.cache_read(cache, slots, out=(full, OnGpu(torch.zeros(3, 2, 8))))
+    assert [name for name, _ in recorded.calls] == ["lp_cache_write", "lp_cache_read"]
