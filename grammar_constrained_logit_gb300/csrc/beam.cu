@@ -32,7 +32,8 @@ namespace {
 
 constexpr int kStreamThreads = 256;
 constexpr int kVecs = 4;              // 16-byte groups a lane holds of a chunk, at most
-constexpr int kGroups = 512;          // lanes' bests that the bound is taken from
+constexpr int kFinishThreads = 512;   // of a block of the second kernel
+constexpr int kFinishWarps = kFinishThreads / 32;
 constexpr int kMaxSelect = 256;       // largest n_select and beams
 constexpr int kBuf = 1024;            // candidates held at once (a power of two)
 constexpr int kList = 2048;           // chunks gone through at once
@@ -389,15 +390,14 @@ __global__ void __launch_bounds__(kStreamThreads, EARLY ? 5 : 6) beam_stream_ker
 }
 
 // Sorts m candidates at c (best first); c has room for the next power of two.
-template <int NT>
 __device__ void sort_best_first(Cand* c, int m) {
   int p = 2;
   while (p < m) p <<= 1;
-  for (int i = m + threadIdx.x; i < p; i += NT) c[i] = Cand{0, ~0ull};
+  for (int i = m + threadIdx.x; i < p; i += kFinishThreads) c[i] = Cand{0, ~0ull};
   __syncthreads();
   for (int k = 2; k <= p; k <<= 1) {
     for (int j = k >> 1; j; j >>= 1) {
-      for (int t = threadIdx.x; t < p / 2; t += NT) {
+      for (int t = threadIdx.x; t < p / 2; t += kFinishThreads) {
         const int lo = 2 * t - (t & (j - 1)), hi = lo + j;
         const Cand x = c[lo], y = c[hi];
         if (better(y, x) == ((lo & k) == 0)) c[lo] = y, c[hi] = x;
@@ -435,9 +435,8 @@ __device__ __forceinline__ float key_score(uint64_t k) { return key_float(uint32
 
 constexpr uint64_t kNoScore = 0x007fffffull << 32 | 0xffffffffull;  // keys of -inf: none above
 
-// The same for 32 < m <= NT, one candidate a thread in registers: neighbours up to 16 places
-// apart meet by shuffles, the others through c.  Returns this thread's, in order.
-template <int NT>
+// The same for 32 < m <= kFinishThreads, one candidate a thread in registers: neighbours up
+// to 16 places apart meet by shuffles, the others through c.  Returns this thread's, in order.
 __device__ __forceinline__ Cand sorted_in_threads(Cand* c, int m) {
   const int t = threadIdx.x;
   Cand x = t < m ? c[t] : Cand{0, ~0ull};
@@ -537,7 +536,7 @@ struct FinishSmem {
   float top[kMaxSelect];      // M; -inf: a beam without candidates
   uint8_t ended[kMaxSelect];  // finished: one candidate, its own score
   uint8_t masked[kMaxSelect];
-  unsigned best[kGroups];
+  unsigned best[kFinishThreads];  // each thread's, which the bound is taken from
   LogEntry log_table[128];
   unsigned list[kList];       // chunks to go through
   int list_n, count, front_n, exact, overflow, next, raised;
@@ -572,16 +571,15 @@ __device__ __forceinline__ float least_of(const FinishSmem& sm, int k, float T) 
 
 // Joins the first m new candidates with the best so far and makes the n-th best the
 // bound.  keep: the n best become the best so far; else only the bound is taken.
-template <int NT>
 __device__ __noinline__ void join(FinishSmem& sm, int m, int n, bool keep) {
   __syncthreads();
   const int front_n = sm.front_n;
-  for (int t = threadIdx.x; t < front_n; t += NT) sm.buf[m + t] = sm.front[t];
+  for (int t = threadIdx.x; t < front_n; t += kFinishThreads) sm.buf[m + t] = sm.front[t];
   __syncthreads();
-  sort_best_first<NT>(sm.buf, m + front_n);
+  sort_best_first(sm.buf, m + front_n);
   const int have = min(m + front_n, n);
   if (keep)
-    for (int t = threadIdx.x; t < have; t += NT) sm.front[t] = sm.buf[t];
+    for (int t = threadIdx.x; t < have; t += kFinishThreads) sm.front[t] = sm.buf[t];
   if (threadIdx.x == 0) {
     if (have == n) sm.bound = sm.buf[n - 1], sm.exact = 1, sm.T = key_score(sm.bound.key);
     if (keep) sm.front_n = have;
@@ -714,9 +712,8 @@ __device__ __forceinline__ FinishSmem* of_block(FinishSmem* p, int rank) {
   return reinterpret_cast<FinishSmem*>(r);
 }
 
-template <int DT, int NT, int R, int B>
-__global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
-  constexpr int NW = NT / 32;
+template <int DT, int R, int B>
+__global__ void __launch_bounds__(kFinishThreads, B) beam_finish_kernel(BeamArgs a) {
   extern __shared__ __align__(16) char raw[];
   FinishSmem& sm = *reinterpret_cast<FinishSmem*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -724,14 +721,14 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
   FinishSmem& hub = R > 1 ? *of_block(&sm, 0) : sm;
   float* staged = a.staged ? reinterpret_cast<float*>(raw + sizeof(FinishSmem)) : nullptr;
   if (tid == 0) sm.count = 0, sm.front_n = 0, sm.list_n = 0, sm.exact = 0, sm.overflow = 0;
-  for (int i = tid; i < 128; i += NT) sm.log_table[i] = kLogTable.at[i];
+  for (int i = tid; i < 128; i += kFinishThreads) sm.log_table[i] = kLogTable.at[i];
   if (R > 1) cluster_sync();
   else __syncthreads();
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
   unsigned best = 0;
-  for (int k = warp; k < a.beams; k += NW)
+  for (int k = warp; k < a.beams; k += kFinishWarps)
     best = max(best, beam_sums(sm, a, row0, k, staged ? staged + k * C : nullptr));
 
   // From here a turn takes 32 chunks a warp: of as many beams as there are warps, or of
@@ -739,7 +736,7 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
   auto chunk_max = [&](int k, int c) {
     return staged ? staged[k * C + c] : a.part[int64_t(row0 + k) * C + c].x;
   };
-  const int per_turn = min(a.beams, NW), share = NW / per_turn;
+  const int per_turn = min(a.beams, kFinishWarps), share = kFinishWarps / per_turn;
   const int my_beam = warp % per_turn, my_share = warp / per_turn;
   const int c_first = my_share < share ? my_share * 32 + lane : INT32_MAX, c_step = share * 32;
 
@@ -750,7 +747,7 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
     __syncthreads();
     best = 0;
     const unsigned total = unsigned(a.beams) * unsigned(C);
-    for (unsigned i = tid; i < total; i += NT) {
+    for (unsigned i = tid; i < total; i += kFinishThreads) {
       const int k = int(i / unsigned(C)), c = int(i % unsigned(C));
       const float M = sm.top[k], s = sm.score[k];
       if (M == -INFINITY) continue;
@@ -762,20 +759,14 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
       if (m > -INFINITY) best = max(best, low_key(s, M, sm.log_s[k].hi, m));
     }
   }
-  if (NT > kGroups) {
-    best = max(best, __shfl_xor_sync(kFullWarp, best, 16));
-    if (lane < 16) sm.best[warp * 16 + lane] = best;
-  } else {
-    sm.best[tid] = best;
-  }
+  sm.best[tid] = best;
   __syncthreads();
   if (warp == 0) {
-    constexpr int kMine = (NT > kGroups ? kGroups : NT) / 32;
-    const int beams_of = NT > kGroups ? 2 * kMine : kMine;  // whose lanes fill the groups
-    const int used = few ? beams_of : a.beams;
-    const float T = used * 4 <= beams_of   ? nth_largest<kMine / 4>(sm.best, a.n)
-                    : used * 2 <= beams_of ? nth_largest<kMine / 2>(sm.best, a.n)
-                                           : nth_largest<kMine>(sm.best, a.n);
+    constexpr int W = kFinishWarps;
+    const int used = few ? W : a.beams;  // warps whose lanes have found something
+    const float T = used * 4 <= W   ? nth_largest<W / 4>(sm.best, a.n)
+                    : used * 2 <= W ? nth_largest<W / 2>(sm.best, a.n)
+                                    : nth_largest<W>(sm.best, a.n);
     if (lane == 0) sm.T = T;
   }
   __syncthreads();
@@ -804,7 +795,7 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
       k0 = a.beams;
     } else {
       // of 32 neighbouring chunks each of R blocks has 32 / R
-      for (int i = 0; i < kList * R / NT && k0 < a.beams; ++i) {
+      for (int i = 0; i < kList * R / kFinishThreads && k0 < a.beams; ++i) {
         const int k = k0 + my_beam;
         const int64_t c = int64_t(c_first) + int64_t(turn) * c_step;
         if (k < a.beams && c < C && sm.top[k] > -INFINITY && (R == 1 || int(c) % R == rank)) {
@@ -820,7 +811,7 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
     const int n_list = min(sm.list_n, kList);
     for (;;) {
       const bool exact = sm.exact;
-      for (int l = warp; l < n_list; l += NW) {
+      for (int l = warp; l < n_list; l += kFinishWarps) {
         const unsigned id = sm.list[l];
         const int k = int(id >> 22), c = int(id & 0x3fffffu);
         const uint64_t flat0 = uint64_t(k) << 31;
@@ -875,15 +866,15 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
           next = kAgain;
           if (!exact) {
             if (warp == 0) {
-              const float T = nth_largest<kGroups / 32>(sm.buf, a.n);
+              const float T = nth_largest<kFinishWarps>(sm.buf, a.n);
               if (lane == 0) sm.raised = T > sm.T, sm.T = fmaxf(T, sm.T);
             }
             __syncthreads();
           }
-          if (exact || !sm.raised) join<NT>(sm, kBufNew, a.n, false);
+          if (exact || !sm.raised) join(sm, kBufNew, a.n, false);
           else if (tid == 0) sm.count = 0;
         } else if (k0 < a.beams) {
-          join<NT>(sm, count, a.n, true);  // with chunks to come, the n best are kept
+          join(sm, count, a.n, true);  // with chunks to come, the n best are kept
         }
         if (tid == 0) {
           sm.next = next;
@@ -914,7 +905,7 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
   // the new ones and the best so far, in order
   const int count = sm.count, m = count + sm.front_n;
   if (sm.front_n > 0) {
-    for (int t = tid; t < sm.front_n; t += NT) sm.buf[count + t] = sm.front[t];
+    for (int t = tid; t < sm.front_n; t += kFinishThreads) sm.buf[count + t] = sm.front[t];
     __syncthreads();
   }
   auto put = [&](int at, const Cand& y) {
@@ -928,19 +919,19 @@ __global__ void __launch_bounds__(NT, B) beam_finish_kernel(BeamArgs a) {
   if (m <= 32) {
     // the place of a candidate is the number of better ones
     const int mine = tid >> 5;  // a warp's worth of threads each
-    for (int t = mine; t < m; t += NW) {
+    for (int t = mine; t < m; t += kFinishWarps) {
       const Cand y = sm.buf[t];
       const int at = __popc(__ballot_sync(kFullWarp, lane < m && better(sm.buf[lane], y)));
       if (at < a.n && lane == 0) put(at, y);
     }
-  } else if (m <= NT) {
-    const Cand y = sorted_in_threads<NT>(sm.buf, m);
+  } else if (m <= kFinishThreads) {
+    const Cand y = sorted_in_threads(sm.buf, m);
     if (tid < min(m, a.n)) put(tid, y);
   } else {
-    sort_best_first<NT>(sm.buf, m);
-    for (int t = tid; t < min(m, a.n); t += NT) put(t, sm.buf[t]);
+    sort_best_first(sm.buf, m);
+    for (int t = tid; t < min(m, a.n); t += kFinishThreads) put(t, sm.buf[t]);
   }
-  for (int t = m + tid; t < a.n; t += NT) put(t, Cand{0, 0});
+  for (int t = m + tid; t < a.n; t += kFinishThreads) put(t, Cand{0, 0});
 }
 
 template <typename K>
@@ -954,7 +945,7 @@ int resident_blocks(K kernel) {
 }
 
 // Clusters of R blocks that run at once (a cluster lies within one group of SMs).
-template <int DT, int NT, int R, int B>
+template <int DT, int R, int B>
 int resident_clusters() {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -962,26 +953,26 @@ int resident_clusters() {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(R);
-  cfg.blockDim = dim3(NT);
+  cfg.blockDim = dim3(kFinishThreads);
   cfg.dynamicSmemBytes = sizeof(FinishSmem);
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, beam_finish_kernel<DT, NT, R, B>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, beam_finish_kernel<DT, R, B>, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();
     n = 0;
   }
   return n;
 }
 
-template <int DT, int NT, int R, int B>
+template <int DT, int R, int B>
 cudaError_t finish_with(cudaLaunchConfig_t cfg, BeamArgs a, int64_t batch) {
   static_assert(sizeof(FinishSmem) <= 48 * 1024, "within the default limit");
   const int64_t staged = int64_t(a.beams) * a.chunks * 4;
   a.staged = staged <= kMostStaged;
   cfg.dynamicSmemBytes = sizeof(FinishSmem) + (a.staged ? size_t(staged) : 0);
   if (cfg.dynamicSmemBytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(beam_finish_kernel<DT, NT, R, B>,
+    const cudaError_t e = cudaFuncSetAttribute(beam_finish_kernel<DT, R, B>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                int(sizeof(FinishSmem) + kMostStaged));
     if (e != cudaSuccess) return e;
@@ -994,8 +985,8 @@ cudaError_t finish_with(cudaLaunchConfig_t cfg, BeamArgs a, int64_t batch) {
   cfg.attrs = attrs;
   cfg.numAttrs = R > 1 ? 2 : 1;
   cfg.gridDim = dim3(unsigned(batch * R));
-  cfg.blockDim = dim3(NT);
-  return cudaLaunchKernelEx(&cfg, beam_finish_kernel<DT, NT, R, B>, a);
+  cfg.blockDim = dim3(kFinishThreads);
+  return cudaLaunchKernelEx(&cfg, beam_finish_kernel<DT, R, B>, a);
 }
 
 template <int DT>
@@ -1004,13 +995,13 @@ cudaError_t finish(const cudaLaunchConfig_t& cfg, const BeamArgs& a, int64_t bat
   // clusters run at once.  4 x 64 rows of 32000 bf16, n = 128: 24 us with it, 39 without;
   // 4 x 16 rows of 4175, n = 32: 11.8 and 13.5; but 17 x 16 rows of 19473, n = 32, where 16
   // clusters run: 24 and 20.  With n up to 16 one block's 16 warps do.
-  static const int clusters = resident_clusters<DT, 512, 8, 1>();
-  if (a.n > 16 && batch <= clusters) return finish_with<DT, 512, 8, 1>(cfg, a, batch);
+  static const int clusters = resident_clusters<DT, 8, 1>();
+  if (a.n > 16 && batch <= clusters) return finish_with<DT, 8, 1>(cfg, a, batch);
   // One block an SM may take 80 registers a thread (8 x 4 rows of 128256 bf16: 9.2 us, with
   // 64 of them 10.3); with more blocks than SMs two have to fit (161 x 8 rows of 17976:
   // 26.6 us, else 32.5).
-  if (batch > kSms) return finish_with<DT, 512, 1, 2>(cfg, a, batch);
-  return finish_with<DT, 512, 1, 1>(cfg, a, batch);
+  if (batch > kSms) return finish_with<DT, 1, 2>(cfg, a, batch);
+  return finish_with<DT, 1, 1>(cfg, a, batch);
 }
 
 template <int DT, int N>
