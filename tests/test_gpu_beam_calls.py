@@ -1,6 +1,7 @@
 """Calls of the operators around their kernels: what a launch needs, what a failed one leaves
 behind, whose scratch it uses."""
 import ctypes
+import math
 import os
 import subprocess
 import sys
@@ -319,3 +320,24 @@ def test_sampler_captured_without_a_workspace(monkeypatch, entry):
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
     assert all(bool((o == 7).all()) for o in others)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kept", [0, 9])
+def test_more_chunks_at_the_bound_than_a_clusters_lists_hold(dtype, kept):
+    """More than 16 to find in few requests: eight blocks go through the chunks side by
+    side, each with a list of 2048.  Every chunk's maximum is the row's, and there are more
+    than 8 x 2048: the first tokens of the first beam of the best score come out.  Scores are
+    near -14: a rounding to 32 bits, and 4e-6 for the logarithm of the row's sum."""
+    beams, V, n = 64, 300001 if dtype == torch.bfloat16 else 150001, 40
+    assert beams * -(-V // (2048 // dtype.itemsize)) > 8 * 2048
+    t = torch.ones(2 * beams, V, dtype=dtype, device="cuda")
+    t[:, :kept] = 0.5
+    scores = torch.full((2, beams), -1.5, device="cuda")
+    scores[:, 0] = -2.0
+    scores[1, 1] = float("-inf")
+    s, k, p = ops.beam_select(t, scores, n)
+    for b in range(2):
+        assert p[b].tolist() == [1 + b] * n and k[b].tolist() == list(range(kept, kept + n))
+        z = math.log((V - kept) + kept * math.exp(-0.5))
+        assert s[b].unique().numel() == 1 and abs(float(s[b, 0]) + 1.5 + z) <= 4e-6 + 2.0 ** -24 * 16
