@@ -18,7 +18,7 @@ namespace lp {
 namespace {
 
 constexpr int kMaxBeams = 256;
-constexpr int kLaunchStates = 64;  // states of one launch (its parameters: 5 KB)
+constexpr int kLaunchStates = 64;  // states of one launch (its parameters: 6 KB)
 constexpr int kThreads = 256;
 constexpr int kHeld = 8;           // sources whose columns fit in registers
 constexpr int64_t kMostSeg = 32768, kLeastSeg = 8192;  // bytes of a row, a block
@@ -27,6 +27,7 @@ constexpr int64_t kEnoughBlocks = 152 * 16;
 struct State {
   char* data;
   int64_t row_stride, run, token;   // bytes; token: 0: none, -1: outer[0] is the tokens' axis
+  int64_t tokens;                   // of a run, where token is a size
   int64_t outer_stride[3];          // bytes
   int outer[3];
   int width;                        // bytes of an access: the alignment of base and strides
@@ -161,8 +162,10 @@ __global__ void reorder_kernel(const __grid_constant__ ReorderArgs a) {
   // the bytes of this block: its segment within the batch entry's range
   int64_t lo = 0, hi = st.run;
   if (st.token > 0) {
-    lo = max(start, 0) * st.token;
-    hi = min(hi, max(stop, 0) * st.token);
+    // cut to the run's tokens before they are bytes: an end far behind them, as where none is
+    // given, times a token of 4 GB would pass 63 bits
+    lo = min(int64_t(max(start, 0)), st.tokens) * st.token;
+    hi = min(int64_t(max(stop, 0)), st.tokens) * st.token;
   } else if (st.token < 0) {
     if (at0 < start || at0 >= stop) return;
   }
@@ -345,6 +348,7 @@ extern "C" lp_status lp_reorder_states(const lp_state* states, int64_t n_states,
       t.row_stride = s.row_stride;
       t.run = s.run_bytes;
       t.token = s.token_bytes;
+      t.tokens = s.token_bytes > 0 ? s.run_bytes / s.token_bytes : 0;
       uint64_t bits = reinterpret_cast<uint64_t>(s.data) | uint64_t(s.row_stride) | 16;
       for (int d = 0; d < 3; ++d) {
         t.outer[d] = int(s.outer[d]);

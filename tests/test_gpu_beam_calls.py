@@ -341,3 +341,19 @@ def test_more_chunks_at_the_bound_than_a_clusters_lists_hold(dtype, kept):
         assert p[b].tolist() == [1 + b] * n and k[b].tolist() == list(range(kept, kept + n))
         z = math.log((V - kept) + kept * math.exp(-0.5))
         assert s[b].unique().numel() == 1 and abs(float(s[b, 0]) + 1.5 + z) <= 4e-6 + 2.0 ** -24 * 16
+
+
+def test_tokens_of_more_than_4_gb():
+    """A token of 2^32 bytes and more: the range up to the last token, or to one far beyond
+    it, ends at the row's end."""
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB")
+    t = torch.empty(2, 1, (1 << 32) + 16, dtype=torch.uint8, device="cuda")
+    p = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda")
+    for i, stop in enumerate((None, 1, 2, (1 << 31) - 1)):
+        t[0].fill_(10 + i)
+        t[1].fill_(20 + i)
+        end = None if stop is None else torch.tensor([stop], dtype=torch.int32, device="cuda")
+        ops.reorder_states([(t, 0, 1)], p, stop=end)
+        for row, value in ((0, 20 + i), (1, 10 + i)):
+            assert int(t[row].amin()) == value == int(t[row].amax()), (stop, row)
