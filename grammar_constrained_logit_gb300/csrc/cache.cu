@@ -717,7 +717,8 @@ lp_status run(const lp_cache_part* parts, const lp_heads* x, int64_t n_parts, in
       page_size < 1 || heads < 0 || dim < 0 || group < 1 || dim % group != 0 ||
       (bits == 4 && group % 2 != 0) || n < 0)
     return LP_ERR_INVALID_ARGUMENT;
-  if (heads > INT32_MAX || dim > INT32_MAX) return LP_ERR_TOO_LARGE;
+  // (a group's bytes are counted in 31 bits)
+  if (heads > INT32_MAX || dim > INT32_MAX || group > (1 << 29)) return LP_ERR_TOO_LARGE;
   if (n_parts == 0 || n == 0 || heads == 0 || dim == 0) return LP_OK;
   if (heads > INT64_MAX / 4 / dim || n > INT64_MAX / 4 / (heads * dim)) return LP_ERR_TOO_LARGE;
   if (parts == nullptr || x == nullptr || slots == nullptr) return LP_ERR_INVALID_ARGUMENT;

@@ -436,7 +436,8 @@ lp_status lp_reorder_states(const lp_state* states, int64_t n_states, int64_t ba
  * A read's values are rounded once to 32 bits and then to dt.  One kernel.
  * Invalid: bits not 4 or 8, a negative size, page_size or group below 1, dim not a
  * multiple of group, an odd group in 4 bits, more than 8 parts, NULL pointers with work
- * to do, misaligned params or x.
+ * to do, misaligned params or x.  heads or dim of 2^31 and more, a group of more than
+ * 2^29, or n * heads * dim above 2^61 return LP_ERR_TOO_LARGE.
  */
 typedef struct {
   void* codes;

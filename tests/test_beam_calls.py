@@ -1,5 +1,6 @@
 """Calls of the operators whose checks and launches are followed on the host: nothing here
 reaches a GPU."""
+import ctypes
 import os
 import subprocess
 import sys
@@ -134,3 +135,19 @@ def test_what_is_written_must_not_be_expanded(recorded):
     ops.cache_write(cache, (full, OnGpu(torch.zeros(1, 2, 8).expand(3, 2, 8))), slots)  # reads
     ops.cache_read(cache, slots, out=(full, OnGpu(torch.zeros(3, 2, 8))))
     assert [name for name, _ in recorded.calls] == ["lp_cache_write", "lp_cache_read"]
+
+
+@pytest.mark.parametrize("write", [True, False])
+@pytest.mark.parametrize("bits, dt, group", [(8, 0, (1 << 29) + 1), (4, 2, 1 << 30),
+                                             (8, 1, (1 << 31) - 1)])
+def test_groups_whose_bytes_pass_31_bits_are_refused(write, bits, dt, group):
+    """A thread's place within a group is a 32-bit number of bytes."""
+    from grammar_constrained_logit_gb300 import build
+
+    build.build()
+    p, h = _lib.CachePart(), _lib.Heads()
+    p.codes = p.params = h.data = 0x10000  # never dereferenced: the calls are refused
+    lib = _lib.load()
+    st = (lib.lp_cache_write if write else lib.lp_cache_read)(
+        ctypes.byref(p), ctypes.byref(h), 1, bits, dt, 4, 4, 1, group, group, 0x10000, 1, None)
+    assert st == _lib.LP_ERR_TOO_LARGE
