@@ -32,11 +32,11 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _matrix(t: torch.Tensor, name: str) -> torch.Tensor:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() == 1:
-        t = t.unsqueeze(0)
     if t.dim() != 2:
-        raise ValueError(f"{name} must be 1-D or 2-D, got {tuple(t.shape)}")
-    if t.size(1) > 1 and t.stride(1) != 1:
+        if t.dim() != 1:
+            raise ValueError(f"{name} must be 1-D or 2-D, got {tuple(t.shape)}")
+        t = t.unsqueeze(0)
+    if t.stride(1) != 1 and t.size(1) > 1:
         raise ValueError(f"{name} rows must be contiguous (stride(1) == 1)")
     return t
 
@@ -54,12 +54,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _call(name: str, device, *args) -> None:
+def _call(name: str, device, args: tuple) -> None:
     """The entry point ``name`` with ``device`` current: its kernels run there, and the default
     stream's handle, which is the same on every device, means that device's."""
     if _current_device() != device.index:
         with torch.cuda.device(device):
-            return _call(name, device, *args)
+            return _call(name, device, args)
     st = getattr(_lib.load(), name)(*args)
     if st != _lib.LP_OK:
         check(name, st)
@@ -118,10 +118,10 @@ def apply_token_bitmask_inplace(logits: torch.Tensor, bitmask: torch.Tensor, *,
     lg = _matrix(logits, "logits")
     bm = _bitmask(bitmask, lg.device)
     idx = _indices(indices, lg.device)
-    _call("lp_apply_token_bitmask", lg.device, _ptr(lg), _dtype_code(lg), lg.size(0), lg.size(1),
-          _stride(lg), _ptr(bm), bm.size(0), bm.size(1), _stride(bm),
-          -1 if vocab_size is None else int(vocab_size), _ptr(idx),
-          0 if idx is None else idx.numel(), _stream(lg))
+    _call("lp_apply_token_bitmask", lg.device, (
+        _ptr(lg), _dtype_code(lg), lg.size(0), lg.size(1), _stride(lg), _ptr(bm), bm.size(0),
+        bm.size(1), _stride(bm), -1 if vocab_size is None else int(vocab_size), _ptr(idx),
+        0 if idx is None else idx.numel(), _stream(lg)))
 
 
 lp_apply_token_bitmask = apply_token_bitmask_inplace
@@ -146,9 +146,10 @@ def apply_token_bitmask_rows(logits: torch.Tensor, bitmask: torch.Tensor,
         if flags.numel() != B:
             raise ValueError(f"row_needs_mask must have {B} entries")
     has = torch.empty(B, dtype=torch.int32, device=lg.device) if report else None
-    _call("lp_apply_token_bitmask_rows", lg.device, _ptr(lg), _dtype_code(lg), B, lg.size(1),
-          _stride(lg), _ptr(bm), bm.size(0), bm.size(1), _stride(bm),
-          -1 if vocab_size is None else int(vocab_size), _ptr(flags), _ptr(has), _stream(lg))
+    _call("lp_apply_token_bitmask_rows", lg.device, (
+        _ptr(lg), _dtype_code(lg), B, lg.size(1), _stride(lg), _ptr(bm), bm.size(0), bm.size(1),
+        _stride(bm), -1 if vocab_size is None else int(vocab_size), _ptr(flags), _ptr(has),
+        _stream(lg)))
     return has
 
 
@@ -184,8 +185,9 @@ def upload_bitmask(device_bitmask: torch.Tensor, host_bitmask: torch.Tensor, *,
     ev = event if event is not None else torch.cuda.Event()
     # PyTorch creates an event's CUDA handle at its first record, so the event is
     # recorded here, on the copy stream right after the enqueued copies
-    _call("lp_upload_bitmask", db.device, _ptr(db), _stride(db), _ptr(hb), _stride(hb), rows, words,
-          _ptr(device_flags), _ptr(host_flags), ctypes.c_void_p(stream.cuda_stream), None)
+    _call("lp_upload_bitmask", db.device, (
+        _ptr(db), _stride(db), _ptr(hb), _stride(hb), rows, words, _ptr(device_flags),
+        _ptr(host_flags), ctypes.c_void_p(stream.cuda_stream), None))
     ev.record(stream)
     return ev
 
@@ -255,10 +257,11 @@ def apply_packed_bitmask(logits: torch.Tensor, bitmask: torch.Tensor,
     if o.dtype != lg.dtype or o.shape != lg.shape:
         raise ValueError("out must match logits in dtype and shape")
     idx = _indices(indices, lg.device)
-    _call("lp_apply_packed_bitmask", lg.device, _ptr(o), _stride(o), _ptr(lg), _dtype_code(lg),
-          lg.size(0), lg.size(1), _stride(lg), _ptr(bm), bm.size(0), bm.size(1), _stride(bm),
-          float(fill_value), -1 if vocab_size is None else int(vocab_size), _ptr(idx),
-          0 if idx is None else idx.numel(), _stream(lg))
+    _call("lp_apply_packed_bitmask", lg.device, (
+        _ptr(o), _stride(o), _ptr(lg), _dtype_code(lg), lg.size(0), lg.size(1), _stride(lg),
+        _ptr(bm), bm.size(0), bm.size(1), _stride(bm), float(fill_value),
+        -1 if vocab_size is None else int(vocab_size), _ptr(idx), 0 if idx is None else idx.numel(),
+        _stream(lg)))
     return out
 
 
@@ -358,8 +361,9 @@ def sample(logits: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
     p = _params(B, lg.device, temperature, top_k, top_p, min_p, seed, offset, keep)
     ids = _ids_out(out, B, lg.device)
     ws = _workspace(workspace, lg, B, V)
-    _call("lp_sample", lg.device, _ptr(lg), _dtype_code(lg), B, V, _stride(lg), ctypes.byref(p),
-          _ptr(ids), _ptr(ws), ws.numel(), _stream(lg))
+    _call("lp_sample", lg.device, (
+        _ptr(lg), _dtype_code(lg), B, V, _stride(lg), ctypes.byref(p), _ptr(ids), _ptr(ws),
+        ws.numel(), _stream(lg)))
     return ids
 
 
@@ -384,11 +388,12 @@ def mask_and_sample(logits: torch.Tensor, bitmask: torch.Tensor | None, temperat
     ids = _ids_out(out, B, lg.device)
     # the workspace is sized by the widest vocabulary the call can use
     ws = _workspace(workspace, lg, B, lg.size(1))
-    _call("lp_mask_and_sample", lg.device, _ptr(lg), _dtype_code(lg), B, lg.size(1), _stride(lg),
-          _ptr(bm), 0 if bm is None else bm.size(0), 0 if bm is None else bm.size(1),
-          0 if bm is None else _stride(bm), -1 if vocab_size is None else int(vocab_size),
-          _ptr(idx), 0 if idx is None else idx.numel(), ctypes.byref(p), _ptr(ids), _ptr(ws),
-          ws.numel(), _stream(lg))
+    _call("lp_mask_and_sample", lg.device, (
+        _ptr(lg), _dtype_code(lg), B, lg.size(1), _stride(lg), _ptr(bm),
+        0 if bm is None else bm.size(0), 0 if bm is None else bm.size(1),
+        0 if bm is None else _stride(bm), -1 if vocab_size is None else int(vocab_size), _ptr(idx),
+        0 if idx is None else idx.numel(), ctypes.byref(p), _ptr(ids), _ptr(ws), ws.numel(),
+        _stream(lg)))
     return ids
 
 
@@ -428,11 +433,12 @@ def mask_and_sample_slots(logits: torch.Tensor, bitmask: torch.Tensor | None,
             raise ValueError(f"seeds must have {B} entries")
     ids = _ids_out(out, B, lg.device)
     ws = _workspace(workspace, lg, B, lg.size(1))
-    _call("lp_mask_and_sample_slots", lg.device, _ptr(lg), _dtype_code(lg), B, lg.size(1),
-          _stride(lg), _ptr(bm), 0 if bm is None else bm.size(0), 0 if bm is None else bm.size(1),
-          0 if bm is None else _stride(bm), -1 if vocab_size is None else int(vocab_size),
-          _ptr(idx), 0 if idx is None else idx.numel(), ctypes.byref(p), R, _ptr(sd), _ptr(ids),
-          _ptr(ws), ws.numel(), _stream(lg))
+    _call("lp_mask_and_sample_slots", lg.device, (
+        _ptr(lg), _dtype_code(lg), B, lg.size(1), _stride(lg), _ptr(bm),
+        0 if bm is None else bm.size(0), 0 if bm is None else bm.size(1),
+        0 if bm is None else _stride(bm), -1 if vocab_size is None else int(vocab_size), _ptr(idx),
+        0 if idx is None else idx.numel(), ctypes.byref(p), R, _ptr(sd), _ptr(ids), _ptr(ws),
+        ws.numel(), _stream(lg)))
     return ids
 
 
@@ -493,13 +499,14 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None
             raise ValueError("logits [batch, beams, V] must match scores [batch, beams]")
         logits = logits.flatten(0, 1)
     lg = _matrix(logits, "logits")
+    dtype = lg.dtype
     rows, cols = lg.shape
     if rows != batch * beams:
         raise ValueError(f"logits must have {batch * beams} rows, got {rows}")
     device = lg.device
     if scores.device != device:
         raise ValueError("scores must be on the same device as logits")
-    dt = _dtype_code(lg)
+    dt = _DT[dtype] if dtype in _DT else _dtype_code(lg)
     n = beams if n_select is None else int(n_select)
     bm = flags = ended = None
     if bitmask is not None:
@@ -510,7 +517,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None
         raise ValueError("row_needs_mask needs a bitmask")
     if finished is not None:
         ended = _row_flags(finished, rows, device, "finished")
-    sc = scores.contiguous()
+    sc = scores if scores.is_contiguous() else scores.contiguous()
     if out is None:
         if n < 0:
             raise ValueError("n_select must not be negative")
@@ -527,17 +534,17 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_select: int | None
     ws = workspace
     if ws is None:
         ws = _scratch(_beam_scratch, device, stream,
-                      beam_select_workspace_bytes(lg.dtype, rows, cols), torch.empty)
+                      beam_select_workspace_bytes(dtype, rows, cols), torch.empty)
     elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
         raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
-    _call("lp_beam_select", device, lg.data_ptr(), dt, batch, beams, cols,
-          lg.stride(0) if rows > 1 else max(lg.stride(0), cols),
-          None if bm is None else bm.data_ptr(), 0 if bm is None else bm.size(0),
-          0 if bm is None else bm.size(1), 0 if bm is None else _stride(bm),
-          -1 if vocab_size is None else int(vocab_size),
-          None if flags is None else flags.data_ptr(), sc.data_ptr(),
-          None if ended is None else ended.data_ptr(), int(pad_id), n, out[0].data_ptr(),
-          out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), ws.numel(), stream)
+    _call("lp_beam_select", device, (
+        lg.data_ptr(), dt, batch, beams, cols,
+        lg.stride(0) if rows > 1 else max(lg.stride(0), cols),
+        None if bm is None else bm.data_ptr(), 0 if bm is None else bm.size(0),
+        0 if bm is None else bm.size(1), 0 if bm is None else _stride(bm),
+        -1 if vocab_size is None else int(vocab_size), None if flags is None else flags.data_ptr(),
+        sc.data_ptr(), None if ended is None else ended.data_ptr(), int(pad_id), n,
+        out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), ws.numel(), stream))
     return out
 
 
@@ -651,8 +658,8 @@ class StateReorder:
         p = self._check(parents, "parents", "[batch, beams]", b * k)
         lo = None if start is None else self._check(start, "start", "[batch]", b)
         hi = None if stop is None else self._check(stop, "stop", "[batch]", b)
-        _call("lp_reorder_states", self.device, self._c, len(self.states), b, k, p, lo, hi,
-              _raw_stream(self.device.index))
+        _call("lp_reorder_states", self.device, (
+            self._c, len(self.states), b, k, p, lo, hi, _raw_stream(self.device.index)))
 
 
 def reorder_states(states, parents: torch.Tensor, start: torch.Tensor | None = None,
@@ -769,8 +776,9 @@ def _cache_call(name, cache: QuantCache, xs, slots: torch.Tensor):
         if inner != 1 and cache.dim > 1:
             raise ValueError("a head's elements must be contiguous")
         heads.append((x.data_ptr(), token, head))
-    _call(name, device, cache._parts, cache._heads_type(*heads), parts, cache.bits, dt,
-          *cache._sizes, slots.data_ptr(), n, _raw_stream(device.index))
+    _call(name, device, (
+        cache._parts, cache._heads_type(*heads), parts, cache.bits, dt, *cache._sizes,
+        slots.data_ptr(), n, _raw_stream(device.index)))
 
 
 def cache_write(cache: QuantCache, x, slots: torch.Tensor) -> None:
@@ -813,7 +821,8 @@ def philox4x32_10(counters: torch.Tensor, keys: torch.Tensor) -> torch.Tensor:
     if c.dim() != 2 or c.size(1) != 4 or k.shape != (c.size(0), 2) or not c.is_cuda:
         raise ValueError("counters must be [n, 4] and keys [n, 2], on the GPU")
     out = torch.empty_like(c)
-    _call("lp_philox4x32_10", c.device, _ptr(c), _ptr(k), _ptr(out), c.size(0), _stream(c))
+    _call("lp_philox4x32_10", c.device, (
+        _ptr(c), _ptr(k), _ptr(out), c.size(0), _stream(c)))
     return out
 
 
