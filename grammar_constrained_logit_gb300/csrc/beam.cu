@@ -15,14 +15,17 @@
 // of the size of the logits is written.  A chunk is a range of token indices, whatever the
 // row's alignment, and its sum has a fixed order: two equal rows get equal scores to the
 // last bit, and ties between them fall by index as stated.  What bounds it is memory, with
-// the warps' own instructions (about 8 a token and lane, one of them the exponential) close
+// the warps' own instructions (7.7 a token and lane, one of them the exponential) close
 // behind: 128 x 8 rows of 202048 fp16 take 65 us, 6.3 TB/s, 93% of the measured copy rate.
 //
 // The second, one block (or a cluster of them) a batch entry, joins the chunks to M_r and
 // S_r, takes the n-th largest chunk maximum's score as a lower bound T of the n-th best
 // candidate, and reads again only the chunks whose maximum reaches T: about n of them,
 // whatever the vocabulary.  It waits at each turn for what the last one found, some
-// 10000 cycles in all: 3 to 9 us after the first kernel, hardly more with a full batch.
+// 10000 cycles in all: 5 us after the first kernel for a few rows, 8 with a full batch, 12
+// with 4 x 64 beams to join.  Far more where the bound admits too much: 1 x 64 rows of
+// 18000 bf16, n = 128, take 21 us, but 48 with one beam alive, whose 18 chunks are fewer
+// than n and bound nothing.
 #include <algorithm>
 
 #include "common.cuh"
@@ -346,7 +349,7 @@ struct At {
 // 3 and 128 x 8 rows of 202048 fp16 from 76 to 88 us; the next chunk's state and mask
 // asked for ahead took 24 x 5 rows of 65519 from 12.7 to 14.0 us; the next chunk copied
 // into shared memory meanwhile took the former to 83 us, the latter to 13.5.  What bounds
-// a warp is its own instructions, about 7 a token.
+// a warp is its own instructions, 7.7 a token.  None of these cases has a mask.
 template <int DT, int N, bool EARLY>
 __global__ void __launch_bounds__(kStreamThreads, EARLY ? 5 : 6) beam_stream_kernel(BeamArgs a) {
   __shared__ KeepTable<DT> table;
@@ -994,7 +997,12 @@ cudaError_t finish(const cudaLaunchConfig_t& cfg, const BeamArgs& a, int64_t bat
   // Many to find: a cluster of blocks goes through the chunks side by side, as long as all
   // clusters run at once.  4 x 64 rows of 32000 bf16, n = 128: 24 us with it, 39 without;
   // 4 x 16 rows of 4175, n = 32: 11.8 and 13.5; but 17 x 16 rows of 19473, n = 32, where 16
-  // clusters run: 24 and 20.  With n up to 16 one block's 16 warps do.
+  // clusters run: 24 and 20.  With n up to 16 one block's 16 warps do; n stands for the
+  // chunks that are read again, of which the first look at all of an entry's chunks is
+  // apart: 15 x 16 rows of 155059 bf16 take 25.7 us in 15 blocks with n = 16, and 28.3 in
+  // clusters with n = 32.  (72 registers a thread leave one block to an SM, whether or not
+  // the chunks' maxima take up to 128 KB of its shared memory, so what is asked without
+  // them holds with them.)
   static const int clusters = resident_clusters<DT, 8, 1>();
   if (a.n > 16 && batch <= clusters) return finish_with<DT, 8, 1>(cfg, a, batch);
   // One block an SM may take 80 registers a thread (8 x 4 rows of 128256 bf16: 9.2 us, with

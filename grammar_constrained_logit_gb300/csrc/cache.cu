@@ -670,10 +670,16 @@ cudaError_t launch_piece(const CacheArgs& a, bool write, int n_parts, cudaStream
   if (indexed && vectors_of<DT, BITS>(8, a, n_parts) && !(write && a.group > 4 * 32 * 8)) {
     if (!write) return read_vec<DT, BITS, 8, 4>(a, n_parts, stream);
     // The same, four on a lane: 32768 x 2 x 8 x 72 fp16, one group a head, written to 8 bits
-    // 23.3 us and in groups of 24 to 4 bits 26.6, with one vector a lane 33.8 and 40.4.
+    // 23.3 us and in groups of 24 to 4 bits 26.6, with one vector a lane 33.8 and 40.4 (their
+    // bytes take 17.1 and 14.9).  A group's parameters are made by its lanes: with a group a
+    // lane, 128 in groups of 8 to 4 bits, 55 us for 29.8.
     if (a.group > 16) return write_vec<DT, BITS, 8, 4, 1>(a, n_parts, stream);
     return write_vec<DT, BITS, 8, 1, 4>(a, n_parts, stream);
   }
+  // What no vector fits: odd widths, strides off their boundaries, groups of more than 1024.
+  // Right for all of it and no more: an element or a byte a thread, places by division.
+  // 32768 x 2 x 8 x 34 bf16 to 8 bits take 156 us (their bytes 8.2), 4096 x 2 x 4 x 2048 in
+  // groups of 2048 82 (29.7); 131072 x 2 x 8 x 34 read from 4 bits 195 (27.7).
   if (write) {
     const int64_t warps = a.n * a.heads * (a.dim / a.group);
     const dim3 grid(unsigned(std::min<int64_t>((warps + 7) / 8, 152 * 64)), unsigned(n_parts));

@@ -10,6 +10,12 @@
 // rows that change) x the row's bytes.  32 x 4 rows of an 8-bit cache of 8 layers, 2.05 GB
 // read and written, take 303 us: 6.8 TB/s, the measured copy rate; copies through a second
 // buffer of the same rows would move half as much again.
+//
+// More than 8 distinct sources, or more than 32 beams, go through shared memory, a word at a
+// time: rows of 512 tokens of 2 layers of 8 x 128 bf16 run at 82% of that rate with 8 x 32 of
+// them (and with 16 x 16, where requests are of both kinds), at 56% with 4 x 64.  Tokens that
+// lie apart are a block each, which finds out what moves again: 512 tokens of 64 rows in runs
+// of 2 KB take 88 us, their bytes 25.
 #include <algorithm>
 
 #include "common.cuh"

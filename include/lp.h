@@ -333,12 +333,16 @@ lp_status lp_mask_and_sample_noalloc(const void* logits, lp_dtype dt, int64_t B,
  *   - of a beam whose score is above -inf and that is not finished: (k, v) for v in
  *     C_r with score scores[r] + ((x_rv - max_C x) - log sum_C exp(x - max_C x));
  *   - of a finished beam with a score above -inf: (k, pad_id) with scores[r];
- *   - of a beam with score -inf or NaN: none (its logits are not read).
+ *   - of a beam with score -inf or NaN: none.  Its logits, and a finished beam's, do not
+ *     count, but must be readable: those of a small problem are read before it is known.
  * Out come the n_select candidates of highest score, highest first; equal scores
  * fall to the lowest (beam, token).  Exponentials and the sums of up to 1024 of them
- * are 32-bit; their joint sum, its logarithm and the scores that are compared hold 38
- * bits after the point or more.  Two equal rows get equal scores to the last bit,
- * whatever their alignment.  NaN logits are no candidates; tokens of logit +inf share
+ * are 32-bit, so a row's log sum is within 4e-6 of the exact one and the order of two
+ * beams' candidates that are closer may not be the exact scores'.  The joint sum, its
+ * logarithm and the scores that are compared are held to 38 bits after the point or
+ * more: a beam's own candidates come in the order of their logits as far as those tell
+ * them apart, and two equal rows get equal scores to the last bit, whatever their
+ * alignment.  NaN logits are no candidates; tokens of logit +inf share
  * their row's whole mass.  A candidate whose score overflows to -inf in 32 bits is none.
  *   logits         device [batch * beams, cols], read only
  *   bitmask        device int32 [bitmask_rows >= batch * beams, ...], or NULL
