@@ -24,6 +24,9 @@ EXPORTS = ("lp_apply_token_bitmask", "lp_apply_token_bitmask_rows", "lp_apply_pa
            "lp_mask_and_sample_noalloc",
            "lp_beam_select", "lp_beam_select_workspace_bytes", "lp_reorder_states",
            "lp_cache_write", "lp_cache_read",
+           "lp_cache_attend", "lp_cache_attend_workspace_bytes",
+           "lp_cache_evict", "lp_cache_evict_workspace_bytes",
+           "lp_verify_drafts", "lp_verify_drafts_workspace_bytes",
            "lp_philox4x32_10", "lp_status_string")
 
 
@@ -57,6 +60,13 @@ class Heads(ctypes.Structure):
     """lp_heads: [n, heads, dim], strides in elements."""
 
     _fields_ = [("data", c_vp), ("token_stride", c_i64), ("head_stride", c_i64)]
+
+
+class Rows(ctypes.Structure):
+    """lp_rows: [batch, rows, heads, dim], strides in elements."""
+
+    _fields_ = [("data", c_vp), ("batch_stride", c_i64), ("row_stride", c_i64),
+                ("head_stride", c_i64)]
 
 
 class LPError(RuntimeError):
@@ -123,6 +133,28 @@ def declare_beam(lib) -> None:
                       c_i64, c_vp]
 
 
+def declare_attend(lib) -> None:
+    """The same for csrc/attend.cu, evict.cu and verify.cu."""
+    lib.lp_cache_attend_workspace_bytes.restype = c_i64
+    lib.lp_cache_attend_workspace_bytes.argtypes = [c_i64] * 5
+    lib.lp_cache_attend.restype = c_i32
+    lib.lp_cache_attend.argtypes = [c_vp, c_i32, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp,
+                                    c_i32, c_i64, c_i64, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp,
+                                    c_vp, c_f32, c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp]
+    lib.lp_cache_evict_workspace_bytes.restype = c_i64
+    lib.lp_cache_evict_workspace_bytes.argtypes = [c_i64] * 3
+    lib.lp_cache_evict.restype = c_i32
+    lib.lp_cache_evict.argtypes = [c_vp, c_i64, c_i32, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp,
+                                   c_i64, c_i64, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_i64,
+                                   c_i64, c_i64, c_vp, c_vp, c_i64, c_vp]
+    lib.lp_verify_drafts_workspace_bytes.restype = c_i64
+    lib.lp_verify_drafts_workspace_bytes.argtypes = [c_i32, c_i64, c_i64]
+    lib.lp_verify_drafts.restype = c_i32
+    lib.lp_verify_drafts.argtypes = [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_i64, c_i64, c_i64,
+                                     c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_vp, c_vp,
+                                     c_f32, c_u64, c_u64, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]
+
+
 def load(path: str | None = None):
     """Open liblp.so once per process; raise if it is missing."""
     global _lib
@@ -138,6 +170,7 @@ def load(path: str | None = None):
             lib = ctypes.CDLL(p)
             declare(lib)
             declare_beam(lib)
+            declare_attend(lib)
             _lib = lib
     return _lib
 

@@ -1,0 +1,224 @@
+// attend.cu -- attention over the quantised cache: the entry point, and the kernels for
+// what the tensor-core ones do not take.
+//
+//   x_rt = scale q_r . k_t,   p = softmax over the tokens that row r sees,   out = sum p_t v_t
+//   k, v = code * s  (8 bits),   l + code * s  (4 bits)
+//
+// One pass over the tokens: with M the largest score so far, sums of 2^(x - M) and of
+// 2^(x - M) v are kept, and scaled by 2^(M - M') when M grows to M'.
+#include <algorithm>
+#include <cmath>
+
+#include "attend.cuh"
+
+namespace lp {
+namespace {
+
+constexpr int kWarps = 4;       // of a block of the general kernels
+constexpr int kMostDim = 1024;
+
+// The value of element d of a head's codes.
+__device__ __forceinline__ float value_at(const AttendArgs& a, const uint8_t* codes,
+                                          const char* params, int d) {
+  const uint32_t held = *reinterpret_cast<const uint32_t*>(params + int64_t(d / a.group) * 4);
+  if (a.bits == 8) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(codes[d])));
+    return __fmul_rn(Elt<LP_F16>::half_bits_to_float(h & 0xffffu), __uint_as_float(held));
+  }
+  const uint32_t code = (codes[d >> 1] >> (4 * (d & 1))) & 15u;
+  return __fmaf_rn(float(code), __uint_as_float(held << 16), __uint_as_float(held & 0xffff0000u));
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kFullWarp, x, o);
+  return x;
+}
+
+struct Head {  // of one part, at one slot
+  const uint8_t* codes;
+  const char* params;
+};
+
+__device__ __forceinline__ Head head_at(const AttendArgs& a, int part, int64_t slot, int h) {
+  const lp_cache_part& p = a.part[part];
+  Head r;
+  r.codes = static_cast<const uint8_t*>(p.codes) +
+            slot_place(a, slot, p.code_page_stride, p.code_slot_stride) + h * p.code_head_stride;
+  r.params = static_cast<const char*>(p.params) +
+             slot_place(a, slot, p.param_page_stride, p.param_slot_stride) +
+             h * p.param_head_stride;
+  return r;
+}
+
+// Any width, group, stride and alignment: a warp a query, its lanes across the head.
+__global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(const __grid_constant__ AttendArgs a) {
+  extern __shared__ float shared_floats[];
+  const int lane = threadIdx.x & 31;
+  float* q = shared_floats + (threadIdx.x >> 5) * 2 * a.dim;
+  float* sum = q + a.dim;
+  const int q_heads = a.heads * a.shared;
+  const int64_t total = int64_t(a.batch) * a.rows * q_heads;
+  for (int64_t i = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < total;
+       i += int64_t(gridDim.x) * kWarps) {
+    const int j = int(i % q_heads), r = int(i / q_heads % a.rows), b = int(i / q_heads / a.rows);
+    const int h = j / a.shared;
+    const Sequence s = sequence(a, b);
+    const Seen v = seen(a, s, r);
+    const char* from = static_cast<const char*>(a.q.data) + b * a.q.batch_stride +
+                       r * a.q.row_stride + j * a.q.head_stride;
+    char* to = static_cast<char*>(a.out.data) + b * a.out.batch_stride + r * a.out.row_stride +
+               j * a.out.head_stride;
+    for (int d = lane; d < a.dim; d += 32) q[d] = load_as_float(from, d, a.dt), sum[d] = 0.0f;
+    float top = -INFINITY, mass = 0.0f;
+    for (int t = v.lo; t < v.end; ++t) {
+      const int64_t slot = slot_of(a, b, t);
+      if (slot < 0) continue;
+      const Head key = head_at(a, 0, slot, h);
+      float x = 0.0f;
+      for (int d = lane; d < a.dim; d += 32) x += q[d] * value_at(a, key.codes, key.params, d);
+      x = warp_sum(x) * a.scale;
+      const float now = fmaxf(top, x);
+      const float ref = now == -INFINITY ? 0.0f : now;
+      const float keep = exp2f(top - ref), e = exp2f(x - ref);
+      top = now;
+      mass = mass * keep + e;
+      const Head value = head_at(a, 1, slot, h);
+      for (int d = lane; d < a.dim; d += 32)
+        sum[d] = sum[d] * keep + e * value_at(a, value.codes, value.params, d);
+    }
+    const float inv = mass == 0.0f ? 0.0f : 1.0f / mass;
+    for (int d = lane; d < a.dim; d += 32)
+      store_float(to, d, mass == 0.0f ? 0.0f : sum[d] * inv, a.dt);
+    if (a.lse != nullptr && lane == 0)
+      a.lse[i] = mass == 0.0f ? -INFINITY : top + log2f(mass);
+  }
+}
+
+// weights[b, h, t] += the sum of 2^(x - lse) over the rows and query heads of h: a warp a
+// token and head, its rows one after another.
+__global__ void __launch_bounds__(kWarps * 32) weights_any_kernel(const __grid_constant__ AttendArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int q_heads = a.heads * a.shared;
+  const int64_t total = int64_t(a.batch) * a.heads * a.most;
+  for (int64_t i = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < total;
+       i += int64_t(gridDim.x) * kWarps) {
+    const int t = int(i % a.most), h = int(i / a.most % a.heads), b = int(i / a.most / a.heads);
+    const Sequence s = sequence(a, b);
+    if (t >= s.tokens) continue;
+    const int64_t slot = slot_of(a, b, t);
+    if (slot < 0) continue;
+    const Head key = head_at(a, 0, slot, h);
+    float sum = 0.0f;
+    for (int r = 0; r < s.rows; ++r) {
+      const Seen v = seen(a, s, r);
+      if (t < v.lo || t >= v.end) continue;
+      for (int j = h * a.shared; j < (h + 1) * a.shared; ++j) {
+        const char* q = static_cast<const char*>(a.q.data) + b * a.q.batch_stride +
+                        r * a.q.row_stride + j * a.q.head_stride;
+        float x = 0.0f;
+        for (int d = lane; d < a.dim; d += 32)
+          x += load_as_float(q, d, a.dt) * value_at(a, key.codes, key.params, d);
+        x = warp_sum(x) * a.scale;
+        const float lse = a.lse[(int64_t(b) * a.rows + r) * q_heads + j];
+        if (lse != -INFINITY) sum += exp2f(x - lse);
+      }
+    }
+    if (lane == 0) {
+      float* w = a.weights + b * a.weights_batch + h * a.weights_head + t;
+      *w += sum;
+    }
+  }
+}
+
+cudaError_t attend_any(const AttendArgs& a, cudaStream_t stream) {
+  const int64_t warps = int64_t(a.batch) * a.rows * a.heads * a.shared;
+  const dim3 grid(unsigned(std::min<int64_t>((warps + kWarps - 1) / kWarps, 152 * 64)));
+  cudaError_t e = launch_kernel(attend_any_kernel, grid, dim3(kWarps * 32),
+                                size_t(kWarps) * 2 * a.dim * 4, stream, a);
+  if (e != cudaSuccess || a.weights == nullptr || a.most == 0) return e;
+  const int64_t tokens = int64_t(a.batch) * a.heads * a.most;
+  const dim3 all(unsigned(std::min<int64_t>((tokens + kWarps - 1) / kWarps, 152 * 64)));
+  return launch_kernel(weights_any_kernel, all, dim3(kWarps * 32), 0, stream, a);
+}
+
+bool fits(int64_t a, int64_t b, int64_t most) { return b == 0 || a <= most / b; }
+
+}  // namespace
+}  // namespace lp
+
+extern "C" int64_t lp_cache_attend_workspace_bytes(int64_t batch, int64_t rows, int64_t q_heads,
+                                                   int64_t heads, int64_t dim) {
+  using namespace lp;
+  if (batch < 0 || rows < 0 || q_heads < 0 || heads < 0 || dim < 0 || dim > kMostDim ||
+      !fits(rows, q_heads, 1 << 24) || !fits(batch, rows * q_heads, INT32_MAX))
+    return -1;
+  return (batch * rows * q_heads * 4 + 15) / 16 * 16;
+}
+
+extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, int64_t n_slots,
+                                     int64_t page_size, int64_t heads, int64_t dim, int64_t group,
+                                     const lp_rows* q, const lp_rows* out, lp_dtype dt,
+                                     int64_t batch, int64_t rows, int64_t q_heads,
+                                     const int32_t* blocks, int64_t blocks_stride,
+                                     int64_t max_blocks, int64_t block_size,
+                                     const int32_t* lengths, const int32_t* n_rows, float scale,
+                                     int64_t window, float* weights, int64_t weights_batch_stride,
+                                     int64_t weights_head_stride, void* workspace,
+                                     int64_t workspace_bytes, cudaStream_t stream) {
+  using namespace lp;
+  if (dt != LP_F32 && dt != LP_F16 && dt != LP_BF16) return LP_ERR_UNSUPPORTED_DTYPE;
+  if ((bits != 8 && bits != 4) || n_slots < 0 || page_size < 1 || heads < 0 || dim < 0 ||
+      group < 1 || dim % group != 0 || (bits == 4 && group % 2 != 0) || batch < 0 || rows < 0 ||
+      q_heads < 0 || (heads == 0 ? q_heads != 0 : q_heads % heads != 0) || max_blocks < 0 ||
+      block_size < 1 || blocks_stride < max_blocks || window < 0 || !std::isfinite(scale))
+    return LP_ERR_INVALID_ARGUMENT;
+  if (dim > kMostDim || !fits(block_size, max_blocks, INT32_MAX) ||
+      !fits(rows, q_heads, 1 << 24) || !fits(batch, rows * q_heads, INT32_MAX) ||
+      batch > INT32_MAX)
+    return LP_ERR_TOO_LARGE;
+  if (batch == 0 || rows == 0 || q_heads == 0 || dim == 0) return LP_OK;
+  const int eb = dt == LP_F32 ? 4 : 2;
+  if (parts == nullptr || q == nullptr || out == nullptr || q->data == nullptr ||
+      out->data == nullptr || lengths == nullptr || (max_blocks > 0 && blocks == nullptr) ||
+      (reinterpret_cast<uintptr_t>(q->data) | reinterpret_cast<uintptr_t>(out->data)) % eb != 0 ||
+      (reinterpret_cast<uintptr_t>(blocks) | reinterpret_cast<uintptr_t>(lengths) |
+       reinterpret_cast<uintptr_t>(n_rows) | reinterpret_cast<uintptr_t>(weights)) % 4 != 0)
+    return LP_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < 2; ++i) {
+    const lp_cache_part& p = parts[i];
+    if (n_slots > 0 && (p.codes == nullptr || p.params == nullptr)) return LP_ERR_INVALID_ARGUMENT;
+    if ((reinterpret_cast<uintptr_t>(p.params) | uint64_t(p.param_page_stride) |
+         uint64_t(p.param_slot_stride) | uint64_t(p.param_head_stride)) % 4 != 0)
+      return LP_ERR_INVALID_ARGUMENT;
+  }
+  const int64_t need = lp_cache_attend_workspace_bytes(batch, rows, q_heads, heads, dim);
+  if (workspace == nullptr || workspace_bytes < need ||
+      reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
+    return LP_ERR_INVALID_ARGUMENT;
+  AttendArgs a = {};
+  a.part[0] = parts[0], a.part[1] = parts[1];
+  a.n_slots = n_slots;
+  a.page = page_size;
+  if (page_size < n_slots && n_slots <= INT32_MAX) a.per_page.set(uint32_t(page_size));
+  a.heads = int(heads), a.dim = int(dim), a.group = int(group), a.bits = bits;
+  a.q = *q, a.out = *out;
+  for (lp_rows* r : {&a.q, &a.out}) r->batch_stride *= eb, r->row_stride *= eb, r->head_stride *= eb;
+  a.dt = dt;
+  a.batch = int(batch), a.rows = int(rows), a.shared = int(q_heads / heads);
+  a.blocks = blocks;
+  a.blocks_stride = blocks_stride;
+  a.block = block_size;
+  a.most = int(max_blocks * block_size);
+  a.per_block.set(uint32_t(std::min<int64_t>(block_size, INT32_MAX)));
+  a.lengths = lengths;
+  a.n_rows = n_rows;
+  a.scale = float(double(scale) * 1.4426950408889634);
+  a.window = window;
+  a.weights = weights;
+  a.weights_batch = weights_batch_stride;
+  a.weights_head = weights_head_stride;
+  a.lse = weights != nullptr ? static_cast<float*>(workspace) : nullptr;
+  return status_of(attend_any(a, stream));
+}

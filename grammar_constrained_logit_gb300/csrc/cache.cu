@@ -30,22 +30,6 @@ constexpr int kThreads = 256;
 constexpr float kLargest = 3.3895313892515355e38f;
 constexpr float kTiny = 1.1754943508222875e-38f;  // 2^-126
 
-// n / d for n < 2^31: with 2^(l-1) < d <= 2^l, m = ceil(2^(31+l) / d) is below 2^32 and
-// n m / 2^(31+l) exceeds n / d by less than n / 2^(31+l) < 1 / d.
-struct Div {
-  uint32_t d, m, shift;
-  void set(uint32_t by) {
-    d = by;
-    uint32_t l = 0;
-    while ((uint64_t(1) << l) < by) ++l;
-    shift = 31 + l;
-    m = uint32_t(((uint64_t(1) << shift) + by - 1) / by);
-  }
-  __device__ __forceinline__ uint32_t quot(uint32_t n) const {
-    return uint32_t((uint64_t(n) * m) >> shift);
-  }
-};
-
 struct CacheArgs {
   lp_cache_part part[kMaxParts];
   lp_heads x[kMaxParts];

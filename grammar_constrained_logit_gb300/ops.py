@@ -309,6 +309,7 @@ class _Kept(threading.local):
 
 
 _sample_scratch, _beam_scratch = _Kept(), _Kept()
+_attend_scratch, _evict_scratch, _verify_scratch = _Kept(), _Kept(), _Kept()
 
 
 def _scratch(kept: _Kept, device, stream: int, need: int, make) -> torch.Tensor:
@@ -811,6 +812,312 @@ def cache_read(cache: QuantCache, slots: torch.Tensor, *, dtype: torch.dtype = t
 
 
 lp_cache_read = cache_read
+
+
+def _given_workspace(workspace: torch.Tensor, device, what: str) -> torch.Tensor:
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+            workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on the {what} device")
+    return workspace
+
+
+def _per_sequence(t: torch.Tensor, name: str, batch: int, device) -> int:
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.device != device:
+        raise ValueError(f"{name} must be on the cache's device")
+    if t.shape != (batch,) or (batch > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous [{batch}], got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _blocks(blocks: torch.Tensor, block_size, cache: QuantCache) -> tuple:
+    """(pointer, stride, blocks a sequence, their size) of a block table."""
+    if blocks.dtype != torch.int32:
+        raise TypeError("blocks must be int32")
+    if blocks.device != cache.device:
+        raise ValueError("blocks must be on the cache's device")
+    if blocks.dim() != 2 or (blocks.size(1) > 1 and blocks.stride(1) != 1):
+        raise ValueError("blocks must be [batch, n] with contiguous rows")
+    size = max(1, cache.page_size) if block_size is None else int(block_size)
+    if size < 1:
+        raise ValueError("block_size must be at least 1")
+    n = blocks.size(1)
+    return blocks.data_ptr(), max(blocks.stride(0), n), n, size
+
+
+def _weights(weights: torch.Tensor, batch: int, heads: int, tokens: int, device) -> tuple:
+    """(pointer, strides) of a tensor of weights for each sequence, head and token."""
+    if weights.dtype != torch.float32:
+        raise TypeError("weights must be float32")
+    if weights.device != device:
+        raise ValueError("weights must be on the cache's device")
+    if weights.dim() != 3 or weights.size(0) != batch or weights.size(1) != heads or \
+            weights.size(2) < tokens:
+        raise ValueError(f"weights must be [{batch}, {heads}, {tokens} or more], "
+                         f"got {list(weights.shape)}")
+    if (weights.size(2) > 1 and weights.stride(2) != 1) or _expanded(weights):
+        raise ValueError("a head's weights must be contiguous, and weights not expanded")
+    return weights.data_ptr(), weights.stride(0), weights.stride(1)
+
+
+@functools.lru_cache(maxsize=256)
+def cache_attend_workspace_bytes(batch: int, rows: int, q_heads: int, heads: int,
+                                 dim: int) -> int:
+    """Bytes of device scratch ``cache_attend`` needs."""
+    n = _lib.load().lp_cache_attend_workspace_bytes(batch, rows, q_heads, heads, dim)
+    if n < 0:
+        raise ValueError("invalid size")
+    return int(n)
+
+
+def _rows(t: torch.Tensor, dim: int) -> tuple:
+    b, r, h, inner = t.stride()
+    if inner != 1 and dim > 1:
+        raise ValueError("a head's elements must be contiguous")
+    return t.data_ptr(), b, r, h
+
+
+def cache_attend(cache: QuantCache, q: torch.Tensor, blocks: torch.Tensor, lengths: torch.Tensor,
+                 *, block_size: int | None = None, n_rows: torch.Tensor | None = None,
+                 scale: float | None = None, window: int | None = None,
+                 weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of ``q`` [batch, rows, q_heads, dim] (or [batch, q_heads, dim], a token a
+    sequence) over a cache of keys and values, from its codes.
+
+    Sequence b has ``lengths[b]`` tokens (int32); token t lies in slot ``blocks[b, t //
+    block_size] * block_size + t % block_size`` (``blocks`` int32 [batch, n]; ``block_size``:
+    the cache's page size when None), and takes no part where that is outside the cache.  Its
+    queries are its last tokens: row r of n sees tokens below lengths[b] - (n - 1 - r), of
+    those the last ``window`` where one is given.  n is the number of rows, or ``n_rows[b]``
+    (int32); rows behind it, and rows that see nothing, give zeros.  ``scale``: dim ** -0.5
+    when None.  q_heads is a multiple of the cache's heads; neighbours share a head.
+
+    ``weights`` float32 [batch, heads, at least n * block_size] takes up, added, each token's
+    attention weight over the rows and the query heads of its head: what ``cache_evict`` goes
+    by.  Returns what ``q`` is like, or ``out``.  ``workspace`` (uint8,
+    ``cache_attend_workspace_bytes``, any content) is scratch to use instead of what is kept
+    for the thread and stream, or in a capture a part of the graph's memory; two threads, or
+    graphs that replay side by side, must not share one."""
+    device, heads, dim = cache.device, cache.heads, cache.dim
+    if cache.parts != 2:
+        raise ValueError("the cache must have two parts, keys and values")
+    dt = _DT.get(q.dtype)
+    if dt is None:
+        raise TypeError(f"q must be float32, float16 or bfloat16, not {q.dtype}")
+    if q.device != device:
+        raise ValueError("q must be on the cache's device")
+    if q.dim() not in (3, 4) or q.size(-1) != dim:
+        raise ValueError(f"q must be [batch, rows, q_heads, {dim}], got {list(q.shape)}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=device)
+    elif out.dtype != q.dtype or out.shape != q.shape or out.device != device or _expanded(out):
+        raise ValueError("out must be like q, and not expanded")
+    q4, out4 = (q, out) if q.dim() == 4 else (q.unsqueeze(1), out.unsqueeze(1))
+    batch, rows, q_heads, _ = q4.shape
+    if heads == 0 or q_heads % heads:
+        raise ValueError(f"q_heads must be a multiple of the cache's {heads} heads, got {q_heads}")
+    table = _blocks(blocks, block_size, cache)
+    if blocks.size(0) != batch:
+        raise ValueError(f"blocks must have {batch} rows, got {blocks.size(0)}")
+    lens = _per_sequence(lengths, "lengths", batch, device)
+    taken = None if n_rows is None else _per_sequence(n_rows, "n_rows", batch, device)
+    if window is not None and window < 1:
+        raise ValueError("window must be at least 1")
+    held = (None, 0, 0) if weights is None else \
+        _weights(weights, batch, heads, table[2] * table[3], device)
+    stream = _raw_stream(device.index)
+    if workspace is None:
+        workspace = _scratch(_attend_scratch, device, stream,
+                             cache_attend_workspace_bytes(batch, rows, q_heads, heads, dim),
+                             torch.empty)
+    else:
+        _given_workspace(workspace, device, "cache's")
+    _call("lp_cache_attend", device, (
+        cache._parts, cache.bits, *cache._sizes, ctypes.byref(_lib.Rows(*_rows(q4, dim))),
+        ctypes.byref(_lib.Rows(*_rows(out4, dim))), dt, batch, rows, q_heads, *table, lens, taken,
+        dim ** -0.5 if scale is None else float(scale), 0 if window is None else int(window),
+        *held, workspace.data_ptr(), workspace.numel(), stream))
+    return out
+
+
+lp_cache_attend = cache_attend
+
+
+@functools.lru_cache(maxsize=256)
+def cache_evict_workspace_bytes(batch: int, heads: int, keep: int) -> int:
+    """Bytes of device scratch ``cache_evict`` needs."""
+    n = _lib.load().lp_cache_evict_workspace_bytes(batch, heads, keep)
+    if n < 0:
+        raise ValueError("invalid size")
+    return int(n)
+
+
+def cache_evict(cache: QuantCache, weights: torch.Tensor, blocks: torch.Tensor,
+                lengths: torch.Tensor, keep: int, *, first: int = 0, recent: int = 0,
+                block_size: int | None = None, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Cut every sequence of more than ``keep`` tokens to ``keep``, in place: each head keeps
+    the first ``first`` and the last ``recent`` ones, and of those between the heaviest by
+    ``weights`` (float32 [batch, heads, tokens], as ``cache_attend`` adds them up; ties to the
+    earliest, NaN as the least).  What a head keeps moves to the sequence's first places, in
+    its order, weights too; the weights of the places behind become 0.
+
+    ``blocks``, ``block_size`` and ``lengths`` as ``cache_attend``'s; sequences must not share
+    blocks.  Returns the new lengths, int32 [batch] (or ``out``, apart from ``lengths``); their
+    next token goes to place new_length.  ``workspace``: as ``cache_attend``'s, of
+    ``cache_evict_workspace_bytes``."""
+    device, heads = cache.device, cache.heads
+    keep, first, recent = int(keep), int(first), int(recent)
+    if min(keep, first, recent) < 0 or first + recent > keep:
+        raise ValueError("first and recent must not be negative, nor more than keep together")
+    table = _blocks(blocks, block_size, cache)
+    batch = blocks.size(0)
+    lens = _per_sequence(lengths, "lengths", batch, device)
+    held = _weights(weights, batch, heads, table[2] * table[3], device)
+    if out is None:
+        out = torch.empty(batch, dtype=torch.int32, device=device)
+    else:
+        _per_sequence(out, "out", batch, device)
+    keep = min(keep, max(table[2] * table[3], first + recent))  # no sequence is longer
+    stream = _raw_stream(device.index)
+    if workspace is None:
+        workspace = _scratch(_evict_scratch, device, stream,
+                             cache_evict_workspace_bytes(batch, heads, keep), torch.empty)
+    else:
+        _given_workspace(workspace, device, "cache's")
+    _call("lp_cache_evict", device, (
+        cache._parts, cache.parts, cache.bits, *cache._sizes, *held, batch, *table, lens, keep,
+        first, recent, out.data_ptr(), workspace.data_ptr(), workspace.numel(), stream))
+    return out
+
+
+lp_cache_evict = cache_evict
+
+
+@functools.lru_cache(maxsize=256)
+def verify_drafts_workspace_bytes(dtype: torch.dtype, rows: int, vocab_size: int) -> int:
+    """Bytes of device scratch ``verify_drafts`` needs for ``rows`` = slots * rows_per_slot."""
+    n = _lib.load().lp_verify_drafts_workspace_bytes(_DT[dtype], rows, vocab_size)
+    if n < 0:
+        raise ValueError("invalid dtype or size")
+    return int(n)
+
+
+def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, uniforms: torch.Tensor, *,
+                  draft_probs: torch.Tensor | None = None, bitmask: torch.Tensor | None = None,
+                  row_needs_mask: torch.Tensor | None = None, temperature=1.0, seed: int = 0,
+                  offset: int = 0, seeds: torch.Tensor | None = None,
+                  vocab_size: int | None = None, out: tuple | None = None,
+                  workspace: torch.Tensor | None = None):
+    """Accept or refuse drafted tokens so that what is said follows the target's
+    distribution, under the bitmask.
+
+    ``logits`` [slots, rows, V] (or its [slots * rows, V] view): row i is the target after the
+    slot's first i ``drafts`` (int64 [slots, rows - 1]; a token outside the vocabulary ends a
+    slot's drafts).  Draft i is accepted while ``uniforms`` [slots, rows - 1] (float32, in
+    [0, 1)) * q(draft) < p(draft): p the softmax of logits / ``temperature`` (a scalar or one
+    value per slot; <= 0 is greedy) over the tokens that the row's bitmask keeps, q the
+    ``draft_probs`` [slots, rows - 1, V] (float32) that the drafts were drawn from, or 1 where
+    they are None.  The row after the accepted drafts says one token more: drawn from max(p -
+    q, 0) where a draft was refused, else from p, with ``sample``'s noise keyed by (``seed`` or
+    the row's ``seeds`` (int64 bit patterns, one per row), row, ``offset``).  ``bitmask`` and
+    ``row_needs_mask`` as ``beam_select``'s.
+
+    Returns (tokens int64 [slots, rows], accepted int32 [slots]): a slot's accepted drafts, the
+    token after them (-1 where its mask admits none), then -1.  ``out`` takes the two tensors
+    to write instead.  ``workspace``: as ``beam_select``'s, of
+    ``verify_drafts_workspace_bytes``."""
+    if drafts.dim() != 2:
+        raise ValueError(f"drafts must be [slots, rows - 1], got {tuple(drafts.shape)}")
+    if drafts.dtype != torch.int64:
+        raise TypeError("drafts must be int64")
+    slots, per_slot = drafts.size(0), drafts.size(1) + 1
+    if logits.dim() == 3:
+        if logits.size(0) != slots or logits.size(1) != per_slot:
+            raise ValueError("logits [slots, rows, V] must match drafts [slots, rows - 1]")
+        logits = logits.flatten(0, 1)
+    lg = _matrix(logits, "logits")
+    dtype = lg.dtype
+    rows, cols = lg.shape
+    if rows != slots * per_slot:
+        raise ValueError(f"logits must have {slots * per_slot} rows, got {rows}")
+    device = lg.device
+    dt = _DT[dtype] if dtype in _DT else _dtype_code(lg)
+    if uniforms.dtype != torch.float32:
+        raise TypeError("uniforms must be float32")
+    if uniforms.shape != drafts.shape:
+        raise ValueError("uniforms must be like drafts")
+    if drafts.device != device or uniforms.device != device:
+        raise ValueError("drafts and uniforms must be on the same device as logits")
+    bm = flags = None
+    if bitmask is not None:
+        bm = _bitmask(bitmask.flatten(0, -2) if bitmask.dim() > 2 else bitmask, device)
+        if row_needs_mask is not None:
+            flags = _row_flags(row_needs_mask, rows, device, "row_needs_mask")
+    elif row_needs_mask is not None:
+        raise ValueError("row_needs_mask needs a bitmask")
+    vocab = -1 if vocab_size is None else int(vocab_size)
+    if draft_probs is not None:
+        if draft_probs.dtype != torch.float32:
+            raise TypeError("draft_probs must be float32")
+        if draft_probs.device != device:
+            raise ValueError("draft_probs must be on the same device as logits")
+        used = vocab if vocab >= 0 else cols if bm is None else min(cols, bm.size(1) * 32)
+        if draft_probs.dim() != 3 or draft_probs.shape[:2] != drafts.shape or \
+                draft_probs.size(2) < used:
+            raise ValueError(f"draft_probs must be [{slots}, {per_slot - 1}, {used} or more], "
+                             f"got {list(draft_probs.shape)}")
+        if draft_probs.numel() == 0:
+            draft_probs = None
+        elif draft_probs.size(2) > 1 and draft_probs.stride(2) != 1:
+            raise ValueError("a row of draft_probs must be contiguous")
+    sd = None
+    if seeds is not None:
+        if seeds.dtype != torch.int64 or seeds.device != device or seeds.numel() != rows:
+            raise ValueError(f"seeds must be {rows} int64 values on the logits' device")
+        sd = seeds.contiguous()
+    heat = 0.0
+    if isinstance(temperature, torch.Tensor) and temperature.numel() != 1:
+        if temperature.numel() != slots:
+            raise ValueError(f"temperature must have {slots} values, got {temperature.numel()}")
+        temperature = temperature.to(device=device, dtype=torch.float32).contiguous()
+    elif isinstance(temperature, torch.Tensor) and temperature.is_cuda:
+        temperature = temperature.to(device=device, dtype=torch.float32).expand(slots).contiguous()
+    else:
+        heat, temperature = float(temperature), None
+    if out is None:
+        out = (torch.empty((slots, per_slot), dtype=torch.int64, device=device),
+               torch.empty(slots, dtype=torch.int32, device=device))
+    else:
+        for t, d, shape in zip(out, (torch.int64, torch.int32), ((slots, per_slot), (slots,)),
+                               strict=True):
+            if t.dtype != d or t.shape != shape or not t.is_contiguous() or t.device != device:
+                raise ValueError("out must be contiguous int64 [slots, rows] and int32 [slots] "
+                                 "tensors on the logits' device")
+    dr, un = drafts.contiguous(), uniforms.contiguous()
+    stream = _raw_stream(device.index)
+    if workspace is None:
+        workspace = _scratch(_verify_scratch, device, stream,
+                             verify_drafts_workspace_bytes(dtype, rows, cols), torch.empty)
+    else:
+        _given_workspace(workspace, device, "logits'")
+    _call("lp_verify_drafts", device, (
+        lg.data_ptr(), dt, rows, cols, lg.stride(0) if rows > 1 else max(lg.stride(0), cols),
+        None if bm is None else bm.data_ptr(), 0 if bm is None else bm.size(0),
+        0 if bm is None else bm.size(1), 0 if bm is None else _stride(bm), vocab,
+        None if flags is None else flags.data_ptr(), per_slot, dr.data_ptr(),
+        None if draft_probs is None else draft_probs.data_ptr(),
+        0 if draft_probs is None else draft_probs.stride(0),
+        0 if draft_probs is None else draft_probs.stride(1), un.data_ptr(),
+        None if temperature is None else temperature.data_ptr(), heat,
+        int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), None if sd is None else sd.data_ptr(),
+        out[0].data_ptr(), out[1].data_ptr(), workspace.data_ptr(), workspace.numel(), stream))
+    return out
+
+
+lp_verify_drafts = verify_drafts
 
 
 def philox4x32_10(counters: torch.Tensor, keys: torch.Tensor) -> torch.Tensor:

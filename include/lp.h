@@ -18,6 +18,10 @@
  *   lp_reorder_states        beam search: states follow their beams, in place
  *   lp_cache_write, lp_cache_read  keys and values quantised to 8 or 4 bits as they are
  *                            written to a cache, and read back
+ *   lp_cache_attend          attention over such a cache, from its codes
+ *   lp_cache_evict           a cache cut to its tokens of most attention weight, in place
+ *   lp_verify_drafts         drafted tokens against the target's probabilities, under the
+ *                            bitmask
  *
  * Common conventions
  *   - Logits are a row-major [B, cols] matrix of float32, float16 or bfloat16 with
@@ -464,6 +468,139 @@ lp_status lp_cache_read(const lp_cache_part* parts, const lp_heads* out, int64_t
                         int32_t bits, lp_dtype dt, int64_t n_slots, int64_t page_size,
                         int64_t heads, int64_t dim, int64_t group, const int64_t* slots,
                         int64_t n, cudaStream_t stream);
+
+/*
+ * lp_cache_attend -- attention over the cache of lp_cache_write, from its codes: nothing of
+ * the cache's size is written.  The pages have no counterpart.
+ *
+ * Sequence b has lengths[b] tokens in the cache (cut to [0, max_blocks * block_size]); token
+ * t's slot is blocks[b, t / block_size] * block_size + t % block_size.  A token whose slot is
+ * outside [0, n_slots) takes no part.  Part 0 holds keys, part 1 values; head j of q goes
+ * with the cache's head j / (q_heads / heads).  Of the sequence's `rows` queries the first
+ * n = n_rows[b] (cut to [0, rows]) take part: they are its last n tokens, and row r sees
+ *   t < end_r = lengths[b] - (n - 1 - r), and t >= end_r - window where window > 0:
+ *   out[b, r, j] = sum_t p_t value_t,  p = softmax over those t of (scale * q[b, r, j] . key_t).
+ * Rows from n on, and rows that see nothing, are zeros.  What a row does not see does not
+ * count, whatever it holds.
+ *   weights  device float32 [batch, heads, max_blocks * block_size], or NULL; a head's
+ *            tokens are contiguous.  weights[b, h, t] += the sum of p_t over the rows and the
+ *            query heads of h
+ * Codes are taken as the whole numbers or e4m3 values that they are, and scaled in 32 bits.
+ * Queries of 16 bits are taken as they are, those of 32 bits rounded to 22 bits or more.
+ * A weight p_t is rounded to 11 bits for bf16 and to 22 for the other types (1.5 * 2^-39 of
+ * the row's largest product of weight and value's scale where it is small).  Sums are 32-bit.
+ *   q, out       [batch, rows, q_heads, dim] of type dt, dim contiguous, strides in elements
+ *   blocks       device int32 [batch, max_blocks], blocks_stride elements from row to row
+ *   lengths      device int32 [batch];  n_rows: device int32 [batch], or NULL: all
+ *   workspace    device scratch of lp_cache_attend_workspace_bytes, 16-byte aligned, of any
+ *                content.  A call is two kernels, or three with weights, that hand on sums in
+ *                it: calls that share it must be ordered, as lp_beam_select's
+ * Equal calls give equal results to the last bit.  Invalid: what lp_cache_write refuses of a
+ * cache; q_heads not a multiple of heads; a negative size; block_size < 1; blocks_stride <
+ * max_blocks; NULL or misaligned pointers with work to do; a scale that is not finite.  dim
+ * above 1024, more than 2^31 - 1 tokens (max_blocks * block_size), rows * q_heads above 2^24, or more than
+ * 2^31 - 1 rows of heads in all return LP_ERR_TOO_LARGE.
+ */
+typedef struct {
+  void* data;
+  int64_t batch_stride, row_stride, head_stride;
+} lp_rows;
+
+int64_t lp_cache_attend_workspace_bytes(int64_t batch, int64_t rows, int64_t q_heads,
+                                        int64_t heads, int64_t dim);
+
+lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, int64_t n_slots,
+                          int64_t page_size, int64_t heads, int64_t dim, int64_t group,
+                          const lp_rows* q, const lp_rows* out, lp_dtype dt, int64_t batch,
+                          int64_t rows, int64_t q_heads, const int32_t* blocks,
+                          int64_t blocks_stride, int64_t max_blocks, int64_t block_size,
+                          const int32_t* lengths, const int32_t* n_rows, float scale,
+                          int64_t window, float* weights, int64_t weights_batch_stride,
+                          int64_t weights_head_stride, void* workspace, int64_t workspace_bytes,
+                          cudaStream_t stream);
+
+/*
+ * lp_cache_evict -- each sequence of a cache cut to `keep` tokens, each head by its own
+ * weights (as lp_cache_attend adds them up), in place.  The pages have no counterpart.
+ *
+ * A sequence of n = lengths[b] tokens (cut as lp_cache_attend's) keeps all of them if n <=
+ * keep.  Otherwise every head h keeps the tokens t < first and t >= n - recent, and of the
+ * others the keep - first - recent of largest weights[b, h, t]; equal weights go to the
+ * lowest t, and NaN counts as less than every number.  Its kept tokens move, in their order,
+ * to the sequence's first `keep` places: codes and params of every part, and weights, whose
+ * places from keep to n become 0.  new_lengths[b] = min(n, keep).
+ *   parts        HOST array of n_parts <= 8, as lp_cache_write's
+ *   weights      as lp_cache_attend's, not NULL with work to do
+ *   new_lengths  device int32 [batch], apart from lengths
+ *   workspace    device scratch of lp_cache_evict_workspace_bytes, 16-byte aligned, of any
+ *                content; calls that share it must be ordered
+ * Sequences must not share blocks, nor name one twice.  What would move from or to a slot
+ * outside the cache does not.  Codes of what moved away stay where they were.  Invalid: what
+ * lp_cache_write refuses of a cache, a negative size, first + recent > keep, block_size < 1,
+ * blocks_stride < max_blocks, new_lengths that overlaps lengths, NULL or misaligned pointers
+ * with work to do.  dim above 2^29, more than 2^31 - 1 tokens
+ * (max_blocks * block_size) or 2^31 - 1 heads of sequences return LP_ERR_TOO_LARGE.
+ */
+int64_t lp_cache_evict_workspace_bytes(int64_t batch, int64_t heads, int64_t keep);
+
+lp_status lp_cache_evict(const lp_cache_part* parts, int64_t n_parts, int32_t bits,
+                         int64_t n_slots, int64_t page_size, int64_t heads, int64_t dim,
+                         int64_t group, float* weights, int64_t weights_batch_stride,
+                         int64_t weights_head_stride, int64_t batch, const int32_t* blocks,
+                         int64_t blocks_stride, int64_t max_blocks, int64_t block_size,
+                         const int32_t* lengths, int64_t keep, int64_t first, int64_t recent,
+                         int32_t* new_lengths, void* workspace, int64_t workspace_bytes,
+                         cudaStream_t stream);
+
+/*
+ * lp_verify_drafts -- drafted tokens accepted or refused so that what is said follows the
+ * target's distribution (speculative sampling), on the [slots, rows_per_slot, V] layout of
+ * lp_mask_and_sample_slots.
+ *
+ * Row i of a slot is the target's logits after the slot's first i drafts.  p_i: softmax of
+ * logit / temperature over the row's candidates, which are lp_mask_and_sample's (bit set, or
+ * the row not masked; logit above -inf); with temperature <= 0 or NaN all of p_i lies on the
+ * lowest-index largest logit.  q_i: draft_probs[slot, i], or all of it on the draft where
+ * draft_probs is NULL.  Draft i = drafts[slot, i] is there if it and all before it are in
+ * [0, vocab_size), and accepted if, besides, uniforms[slot, i] * q_i(draft) < p_i(draft) and
+ * all before it were accepted (a NaN accepts nothing).  With n drafts accepted, row n says
+ * one more token:
+ *   - draft n was there, and refused: argmax over v of log r_v + g_v, r = max(p_n - q_n, 0),
+ *     or r = p_n where that is 0 everywhere (NaN counts as 0);
+ *   - else argmax over v of logit_v / temperature + g_v, or the largest logit with
+ *     temperature <= 0,
+ * over the row's candidates, ties to the lowest; -1 if it has none.  g is lp_sample's noise,
+ * of row b = slot * rows_per_slot + n keyed by (seeds[b], b, offset), or (seed, b, offset)
+ * where seeds is NULL.  rows_per_slot = 1 is lp_mask_and_sample_slots without filters.
+ *   logits       device, B = slots * rows_per_slot rows of cols elements
+ *   bitmask, row_needs_mask  as lp_apply_token_bitmask_rows's, or NULL
+ *   drafts       device int64 [slots, rows_per_slot - 1]
+ *   draft_probs  device float32 [slots, rows_per_slot - 1, cols of its own >= vocab_size],
+ *                strides in elements, or NULL
+ *   uniforms     device float32 [slots, rows_per_slot - 1], in [0, 1)
+ *   temperature  device float32 [slots], or NULL: temperature_scalar
+ *   out_tokens   device int64 [slots, rows_per_slot]: the accepted drafts, the token that the
+ *                row after them says, then -1
+ *   out_accepted device int32 [slots]
+ *   workspace    device scratch of lp_verify_drafts_workspace_bytes, 16-byte aligned, of any
+ *                content; calls that share it must be ordered, as lp_beam_select's
+ * Invalid: as lp_apply_token_bitmask_rows, rows_per_slot < 1, B not a multiple of it,
+ * row_needs_mask without bitmask, logits not aligned to their element, NULL or misaligned
+ * pointers with work to do.  rows_per_slot above 256, more than 2^27 rows, or a vocabulary
+ * above 2^31 - 65 return LP_ERR_TOO_LARGE.
+ */
+int64_t lp_verify_drafts_workspace_bytes(lp_dtype dt, int64_t rows, int64_t vocab_size);
+
+lp_status lp_verify_drafts(const void* logits, lp_dtype dt, int64_t B, int64_t cols,
+                           int64_t logits_stride, const int32_t* bitmask, int64_t bitmask_rows,
+                           int64_t bitmask_words, int64_t bitmask_stride, int64_t vocab_size,
+                           const uint8_t* row_needs_mask, int64_t rows_per_slot,
+                           const int64_t* drafts, const float* draft_probs,
+                           int64_t probs_slot_stride, int64_t probs_row_stride,
+                           const float* uniforms, const float* temperature,
+                           float temperature_scalar, uint64_t seed, uint64_t offset,
+                           const uint64_t* seeds, int64_t* out_tokens, int32_t* out_accepted,
+                           void* workspace, int64_t workspace_bytes, cudaStream_t stream);
 
 /*
  * lp_philox4x32_10 -- diagnostic: the device's Philox4x32-10 (Salmon et al.,
