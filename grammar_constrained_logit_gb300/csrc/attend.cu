@@ -12,6 +12,16 @@
 #include "attend.cuh"
 
 namespace lp {
+
+cudaError_t attend_8n1(const AttendArgs& a, int block, cudaStream_t stream);
+cudaError_t attend_8n2(const AttendArgs& a, int block, cudaStream_t stream);
+cudaError_t attend_8w1(const AttendArgs& a, int block, cudaStream_t stream);
+cudaError_t attend_8w2(const AttendArgs& a, int block, cudaStream_t stream);
+cudaError_t attend_4n1(const AttendArgs& a, int block, cudaStream_t stream);
+cudaError_t attend_4n2(const AttendArgs& a, int block, cudaStream_t stream);
+cudaError_t attend_4w1(const AttendArgs& a, int block, cudaStream_t stream);
+cudaError_t attend_4w2(const AttendArgs& a, int block, cudaStream_t stream);
+
 namespace {
 
 constexpr int kWarps = 4;       // of a block of the general kernels
@@ -143,6 +153,30 @@ cudaError_t attend_any(const AttendArgs& a, cudaStream_t stream) {
   return launch_kernel(weights_any_kernel, all, dim3(kWarps * 32), 0, stream, a);
 }
 
+// The tensor-core kernels: of the cache's bits, with queries and weights in one piece or two.
+using Launch = cudaError_t (*)(const AttendArgs&, int, cudaStream_t);
+
+// The blocks that groups are made of, for the widths that there are kernels for; 0: none.
+int block_of(int dim, int group) {
+  for (int most : {dim == 128 || dim == 256 ? 128 : dim == 64 || dim == 192 ? 64 : 32, 32, 16}) {
+    if (dim != 64 && dim != 80 && dim != 96 && dim != 128 && dim != 192 && dim != 256) return 0;
+    if (dim % most == 0 && group % most == 0) return most;
+  }
+  return 0;
+}
+
+bool aligned(const AttendArgs& a, int unit, bool params) {
+  uint64_t x = 0;
+  for (const lp_cache_part& p : a.part)
+    x |= params ? reinterpret_cast<uintptr_t>(p.params) | uint64_t(p.param_page_stride) |
+                      uint64_t(p.param_slot_stride) | uint64_t(p.param_head_stride)
+                : reinterpret_cast<uintptr_t>(p.codes) | uint64_t(p.code_page_stride) |
+                      uint64_t(p.code_slot_stride) | uint64_t(p.code_head_stride);
+  return x % unit == 0;
+}
+
+int rows_at_once(int64_t rows) { return rows <= 8 ? 8 : 16; }
+
 bool fits(int64_t a, int64_t b, int64_t most) { return b == 0 || a <= most / b; }
 
 }  // namespace
@@ -154,7 +188,10 @@ extern "C" int64_t lp_cache_attend_workspace_bytes(int64_t batch, int64_t rows, 
   if (batch < 0 || rows < 0 || q_heads < 0 || heads < 0 || dim < 0 || dim > kMostDim ||
       !fits(rows, q_heads, 1 << 24) || !fits(batch, rows * q_heads, INT32_MAX))
     return -1;
-  return (batch * rows * q_heads * 4 + 15) / 16 * 16;
+  // of each row its sum; and what the workers leave of the units that they share
+  const int64_t left = heads == 0 ? 0 : int64_t(kSms) * kMostWarps * 2 *
+                                            rows_at_once(rows * (q_heads / heads)) * (dim * 4 + 8);
+  return (batch * rows * q_heads * 4 + 15) / 16 * 16 + (left + 15) / 16 * 16;
 }
 
 extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, int64_t n_slots,
@@ -174,7 +211,7 @@ extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, i
       q_heads < 0 || (heads == 0 ? q_heads != 0 : q_heads % heads != 0) || max_blocks < 0 ||
       block_size < 1 || blocks_stride < max_blocks || window < 0 || !std::isfinite(scale))
     return LP_ERR_INVALID_ARGUMENT;
-  if (dim > kMostDim || !fits(block_size, max_blocks, INT32_MAX) ||
+  if (dim > kMostDim || !fits(block_size, max_blocks, 1 << 30) ||
       !fits(rows, q_heads, 1 << 24) || !fits(batch, rows * q_heads, INT32_MAX) ||
       batch > INT32_MAX)
     return LP_ERR_TOO_LARGE;
@@ -220,5 +257,21 @@ extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, i
   a.weights_batch = weights_batch_stride;
   a.weights_head = weights_head_stride;
   a.lse = weights != nullptr ? static_cast<float*>(workspace) : nullptr;
-  return status_of(attend_any(a, stream));
+  const int block = block_of(a.dim, a.group);
+  const int row = a.dim * bits / 8;
+  if (block == 0 || n_slots == 0 || !aligned(a, row % 16 == 0 ? 16 : 8, false))
+    return status_of(attend_any(a, stream));
+  a.wide_params = a.dim / a.group % 4 == 0 && aligned(a, 16, true);
+  a.team = 5;
+  while (a.heads % a.team != 0) --a.team;
+  a.head_groups = a.heads / a.team;
+  a.min_tiles = 4;
+  const int at_once = rows_at_once(int64_t(a.rows) * a.shared);
+  char* left = static_cast<char*>(workspace) + (batch * rows * q_heads * 4 + 15) / 16 * 16;
+  const int64_t held = int64_t(kSms) * kMostWarps * 2 * at_once;
+  a.sums = reinterpret_cast<float*>(left);
+  a.tops = reinterpret_cast<float2*>(left + held * a.dim * 4);
+  static const Launch launches[2][2][2] = {{{attend_8n1, attend_8n2}, {attend_8w1, attend_8w2}},
+                                           {{attend_4n1, attend_4n2}, {attend_4w1, attend_4w2}}};
+  return status_of(launches[bits == 4][dt != LP_BF16][at_once == 16](a, block, stream));
 }

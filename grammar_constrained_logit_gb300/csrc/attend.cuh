@@ -6,6 +6,9 @@
 
 namespace lp {
 
+constexpr int kSms = 152;
+constexpr int kMostWarps = 16;  // resident on an SM, at most
+
 struct AttendArgs {
   lp_cache_part part[2];  // keys, values
   int64_t n_slots, page;
@@ -25,6 +28,13 @@ struct AttendArgs {
   float* weights;
   int64_t weights_batch, weights_head;
   float* lse;      // [batch, rows, q_heads]: log2 of a row's sum; only with weights
+  // of the tensor-core kernels: the work is cut into tiles of tokens, in the order
+  // (sequence, group of `team` heads, tile of rows, tile of tokens), and each of `workers`
+  // teams of warps, a warp a head, takes a range of them
+  int team, head_groups, row_tiles, workers, min_tiles;
+  bool wide_params, wide_out;  // 16-byte copies of params; 8-byte stores of results
+  float* sums;     // [workers, 2, team, tile's rows, dim]: of what a worker has of a unit
+  float2* tops;    // [workers, 2, team, tile's rows]: (largest exponent, mass)
 };
 
 // What a sequence has: its tokens, and the queries that take part.

@@ -233,7 +233,7 @@ extern "C" lp_status lp_cache_evict(const lp_cache_part* parts, int64_t n_parts,
       blocks_stride < max_blocks || keep < 0 || first < 0 || recent < 0 || first > keep ||
       recent > keep - first)
     return LP_ERR_INVALID_ARGUMENT;
-  if (heads > INT32_MAX || dim > (1 << 29) || !fits(block_size, max_blocks, INT32_MAX) ||
+  if (heads > INT32_MAX || dim > (1 << 29) || !fits(block_size, max_blocks, 1 << 30) ||
       !fits(batch, heads, INT32_MAX) || batch > INT32_MAX)
     return LP_ERR_TOO_LARGE;
   if (batch == 0) return LP_OK;

@@ -498,8 +498,8 @@ lp_status lp_cache_read(const lp_cache_part* parts, const lp_heads* out, int64_t
  * Equal calls give equal results to the last bit.  Invalid: what lp_cache_write refuses of a
  * cache; q_heads not a multiple of heads; a negative size; block_size < 1; blocks_stride <
  * max_blocks; NULL or misaligned pointers with work to do; a scale that is not finite.  dim
- * above 1024, more than 2^31 - 1 tokens (max_blocks * block_size), rows * q_heads above 2^24, or more than
- * 2^31 - 1 rows of heads in all return LP_ERR_TOO_LARGE.
+ * above 1024, more than 2^30 tokens (max_blocks * block_size), rows * q_heads above 2^24, or
+ * more than 2^31 - 1 rows of heads in all return LP_ERR_TOO_LARGE.
  */
 typedef struct {
   void* data;
@@ -538,8 +538,8 @@ lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, int64_t n_sl
  * outside the cache does not.  Codes of what moved away stay where they were.  Invalid: what
  * lp_cache_write refuses of a cache, a negative size, first + recent > keep, block_size < 1,
  * blocks_stride < max_blocks, new_lengths that overlaps lengths, NULL or misaligned pointers
- * with work to do.  dim above 2^29, more than 2^31 - 1 tokens
- * (max_blocks * block_size) or 2^31 - 1 heads of sequences return LP_ERR_TOO_LARGE.
+ * with work to do.  dim above 2^29, more than 2^30 tokens (max_blocks *
+ * block_size) or 2^31 - 1 heads of sequences return LP_ERR_TOO_LARGE.
  */
 int64_t lp_cache_evict_workspace_bytes(int64_t batch, int64_t heads, int64_t keep);
 

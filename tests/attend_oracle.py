@@ -30,6 +30,19 @@ def held(cache):
     return values(codes.cpu().numpy(), params.float().cpu().numpy(), cache.bits, cache.group)
 
 
+def reach(cache):
+    """What a weight's rounding is multiplied by, at most: |code * scale| of the values.  In 4
+    bits that is the value less its group's low, which comes to it unrounded: the weight of a
+    token is rounded where it meets the code, p s c, so it is off by its rounding times s c,
+    however near the value l + s c is to zero."""
+    v = held(cache)[1]
+    if cache.bits == 8:
+        return np.abs(v)
+    p = cache.params if cache.codes.dim() == 4 else cache.params.flatten(1, 2)
+    low = p[1, ..., 1].double().cpu().numpy()
+    return np.abs(v - np.repeat(low, cache.group, -1))
+
+
 def slots_of(blocks, b, n, size, total):
     """Slots of a sequence's n tokens; -1 outside the cache."""
     t = np.arange(n)
@@ -37,12 +50,14 @@ def slots_of(blocks, b, n, size, total):
     return np.where((s >= 0) & (s < total), s, -1)
 
 
-def attended(kv, q, blocks, lengths, size, *, n_rows=None, scale=None, window=None, dtype="f32"):
+def attended(kv, q, blocks, lengths, size, *, n_rows=None, scale=None, window=None, dtype="f32",
+             reach=None):
     """(out, how far it may be off, weights [batch, heads, tokens], how far those may be).
 
     An element of the output is sum_t p_t v_t.  With d the error of a score, a weight's
-    relative error is below 2 d (its own and the sum's) plus its rounding; the sums over n
-    tokens add n roundings of 2^-24; and the result is rounded once.  A score is a sum of dim
+    relative error is below 2 d (its own and the sum's); it is rounded where it meets the
+    value's code (`reach`); the sums over n tokens, of codes' parts and of lows' parts, add n
+    roundings of 2^-24; and the result is rounded once.  A score is a sum of dim
     products in 32 bits, of which tensor cores cut off bits (2^-23 a step, at most), a product
     with the scale and one with its group's params; an exponential is off by 2^-21.  A
     weight that is small beside the row's largest product of weight and scale is rounded to
@@ -76,9 +91,11 @@ def attended(kv, q, blocks, lengths, size, *, n_rows=None, scale=None, window=No
                 d = (dim + 8) * 2.0 ** -23 * most_x.max() + 2.0 ** -21
                 out[b, r, j] = p @ v
                 mass = p @ np.abs(v)
+                far = mass if reach is None else p @ reach[at[t], h]
                 small = t.size * 448 * 2.0 ** -38 * np.nanmax(p[:, None] * np.abs(v))
-                rel = 2 * d + WEIGHT[dtype] + (t.size + 64) * 2.0 ** -24
-                off[b, r, j] = rel * mass + small + HALF_STEP[dtype] * np.abs(out[b, r, j])
+                rel = 2 * d + (t.size + 64) * 2.0 ** -24
+                off[b, r, j] = rel * (mass + far) + WEIGHT[dtype] * far + small + \
+                    HALF_STEP[dtype] * np.abs(out[b, r, j])
                 weights[b, h, t] += p
                 woff[b, h, t] += p * (2 * d + (t.size + 64) * 2.0 ** -24) + 2.0 ** -149
     return out, off, weights, woff

@@ -4,7 +4,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from attend_oracle import attended, held  # noqa: E402
+from attend_oracle import attended, held, reach  # noqa: E402
 from grammar_constrained_logit_gb300 import ops  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -66,7 +66,7 @@ def check(cache, q, blocks, lengths, size, dtype, *, weights=False, **kw):
                            torch.tensor(lengths, dtype=torch.int32, device="cuda"),
                            block_size=size, n_rows=nr, weights=w, **kw)
     want, off, ww, woff = attended(held(cache), qd.double().cpu().numpy(), blocks, lengths, size,
-                                   n_rows=n_rows, dtype=dtype, **kw)
+                                   n_rows=n_rows, dtype=dtype, reach=reach(cache), **kw)
     d = np.abs(got.double().cpu().numpy() - want)
     assert got.dtype == qd.dtype and got.shape == qd.shape
     assert (d <= off).all(), (d.max(), (d / np.maximum(off, 1e-300)).max())
@@ -227,7 +227,7 @@ def test_strides(bits, group, dtype):
                            out=out)
     assert got is out
     want, off, _, _ = attended(held(cache), q.double().cpu().numpy(), blocks, lengths, size,
-                               dtype=dtype)
+                               dtype=dtype, reach=reach(cache))
     assert (np.abs(out.double().cpu().numpy() - want) <= off).all()
     out.fill_(7.0)
     assert (room == 7.0).all()
