@@ -1,11 +1,14 @@
 // evict.cu -- a cache's sequences cut to their tokens of most attention weight, in place.
 //
 // Of a head's n > keep tokens stay the first ones, the last ones and the K = keep - first -
-// recent heaviest of those between.  The K-th largest weight is found digit by digit, eight
+// recent heaviest of those between.  The K-th largest weight is found digit by digit, eleven
 // bits of an order-preserving key at a time; what is above it stays, and of what equals it
-// the lowest ones.  The j-th kept token, at s(j) >= j, moves to place j.  s(j) > j' for every
-// j' < j: places written for earlier tokens hold no source of later ones, so a block that
-// goes through them in order, and reads a batch before it writes it, needs no second copy.
+// the lowest ones.  The j-th kept token, at s(j) >= j, moves to place j.
+//
+// s(j') > j for every j < j': what is written for a token is never the source of a later one,
+// so loads may run ahead of stores as far as they like, and a store has to wait only for the
+// loads of its own round and those before it.  A round is what the blocks of a cluster hold
+// in registers; they meet at one barrier a round, with the next round's loads under way.
 #include <algorithm>
 
 #include "common.cuh"
@@ -15,8 +18,13 @@ namespace {
 
 constexpr int kMaxParts = 8;
 constexpr int kThreads = 1024;
-constexpr int kMoveThreads = 512;
-constexpr int kAtOnce = 4;  // pieces a thread holds
+constexpr int kMoveThreads = 256;
+constexpr int kAtOnce = 4;       // pieces a thread holds of a round
+constexpr int kRoundTokens = 256;
+constexpr int kMostCluster = 8;
+constexpr int kSms = 152;
+constexpr int kBins = 2048;
+constexpr int kHeldTokens = 40 * 1024;  // weights that a block holds in shared memory
 
 struct EvictArgs {
   lp_cache_part part[kMaxParts];
@@ -37,7 +45,33 @@ struct EvictArgs {
   int keep, first, recent;
   int32_t* new_lengths;
   int32_t* source;  // [batch, heads, keep]: s(j)
+  int slice;        // tokens of a sequence to a block of the selection
+  int round_tokens;
+  Div per_token;    // pieces
 };
+
+__device__ __forceinline__ int cluster_size() {
+  uint32_t n;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return int(n);
+}
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t n;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(n));
+  return int(n);
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of another block's shared memory, at the place of `p` in this one's.
+__device__ __forceinline__ int remote(const int* p, int rank) {
+  uint32_t at, v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(at) : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(uint32_t(rank)));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return int(v);
+}
 
 __device__ __forceinline__ int64_t place(const EvictArgs& a, int64_t slot, int64_t page_stride,
                                          int64_t slot_stride) {
@@ -78,7 +112,114 @@ __device__ __forceinline__ int scan(int x, int* warps, int* all) {
   return before + incl - x;
 }
 
-// Which tokens stay: a block a sequence and head.  Moves the weights.
+// Which tokens stay, and where the weights go: a cluster of blocks a sequence and head, each
+// with a slice of the weights in shared memory.
+__global__ void __launch_bounds__(kThreads) evict_slices_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ float held[];
+  __shared__ int bins[3][kBins], warps[2][kThreads / 32], found[2], counts[2];
+  const int blocks = cluster_size(), rank = cluster_rank(), tid = threadIdx.x;
+  const int lane = tid & 31, warp = tid >> 5;
+  const int unit = blockIdx.x / blocks, b = unit / a.heads, h = unit - b * a.heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int n = min(max(__ldg(a.lengths + b), 0), a.most);
+  const int left = min(n, a.keep);
+  if (n <= a.keep || a.weights == nullptr) {  // for all of the cluster
+    if (h == 0 && rank == 0 && tid == 0) a.new_lengths[b] = left;
+    return;
+  }
+  float* w = a.weights + b * a.weights_batch + h * a.weights_head;
+  int32_t* source = a.source + (int64_t(b) * a.heads + h) * a.keep;
+  const int lo = a.first, hi = n - a.recent;
+  const int t0 = min(n, rank * a.slice), t1 = min(n, t0 + a.slice);  // this block's
+  for (int i = tid; i < 3 * kBins; i += kThreads) bins[0][i] = 0;
+  for (int i = tid; i < t1 - t0; i += kThreads) held[i] = w[t0 + i];
+  __syncthreads();
+  int want = a.keep - a.first - a.recent;  // of [lo, hi)
+  const bool none = want == 0;
+  uint32_t key = 0;  // of the want-th largest, as far as it is known
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    if (none) break;
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, digits = pass < 2 ? kBins : 1024;
+    for (int i = tid; i < t1 - t0; i += kThreads) {
+      const int t = t0 + i;
+      if (t < lo || t >= hi) continue;
+      const uint32_t k = weight_key(held[i]);
+      if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == (key >> (pass == 1 ? 21 : 10)))
+        atomicAdd(&bins[pass][(k >> shift) & (digits - 1)], 1);
+    }
+    cluster_sync();
+    // this thread's two digits, the highest first, over all blocks
+    const int top = digits - 1 - 2 * tid;
+    int c0 = 0, c1 = 0;
+    if (top > 0)
+      for (int r = 0; r < blocks; ++r)
+        c0 += remote(&bins[pass][top], r), c1 += remote(&bins[pass][top - 1], r);
+    int incl = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFullWarp, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warps[0][warp] = incl;
+    __syncthreads();
+    int before = incl - c0 - c1;
+    for (int i = 0; i < warp; ++i) before += warps[0][i];
+    if (top > 0) {
+      if (before < want && want <= before + c0) found[0] = top, found[1] = before;
+      else if (before + c0 < want && want <= before + c0 + c1) found[0] = top - 1, found[1] = before + c0;
+    }
+    __syncthreads();
+    key |= uint32_t(found[0]) << shift;
+    want -= found[1];
+  }
+  // A thread's run of tokens, in order: what stays for sure, and what equals the key
+  const int run = (t1 - t0 + kThreads - 1) / kThreads;
+  const int i0 = min(t1 - t0, tid * run), i1 = min(t1 - t0, i0 + run);
+  int sure = 0, equal = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int t = t0 + i;
+    if (t < lo || t >= hi) {
+      ++sure;
+    } else if (!none) {
+      const uint32_t k = weight_key(held[i]);
+      sure += k > key, equal += k == key;
+    }
+  }
+  int in_sure = sure, in_equal = equal;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFullWarp, in_sure, o), z = __shfl_up_sync(kFullWarp, in_equal, o);
+    if (lane >= o) in_sure += y, in_equal += z;
+  }
+  __syncthreads();
+  if (lane == 31) warps[0][warp] = in_sure, warps[1][warp] = in_equal;
+  __syncthreads();
+  int at_sure = in_sure - sure, at_equal = in_equal - equal;
+  for (int i = 0; i < warp; ++i) at_sure += warps[0][i], at_equal += warps[1][i];
+  if (tid == kThreads - 1) counts[0] = at_sure + sure, counts[1] = at_equal + equal;
+  cluster_sync();
+  for (int r = 0; r < rank; ++r) at_sure += remote(&counts[0], r), at_equal += remote(&counts[1], r);
+  // every block has read its weights: they may be written
+  int j = at_sure + min(at_equal, want);
+  for (int i = i0; i < i1; ++i) {
+    const int t = t0 + i;
+    bool stays = t < lo || t >= hi;
+    if (!stays && !none) {
+      const uint32_t k = weight_key(held[i]);
+      stays = k > key || (k == key && at_equal < want);
+      at_equal += k == key;
+    }
+    if (stays) source[j] = t, w[j] = held[i], ++j;
+  }
+  for (int t = max(t0, left) + tid; t < t1; t += kThreads) w[t] = 0.0f;
+  if (h == 0 && rank == 0 && tid == 0) a.new_lengths[b] = left;
+  cluster_sync();  // counts are read by others
+}
+
+// The same for sequences longer than a cluster's shared memory holds: a block each, going
+// through the weights in order.
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ int counts[256], warps[kThreads / 32], digit, above;
   const int b = blockIdx.x / a.heads, h = blockIdx.x - b * a.heads, tid = threadIdx.x;
@@ -154,48 +295,192 @@ __device__ __forceinline__ void store_piece(const Piece& p, char* to, int unit) 
   else *reinterpret_cast<uint8_t*>(to) = uint8_t(p.w[0]);
 }
 
-// Moves codes and params: a block a sequence and head.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
+// Moves codes and params: a cluster of blocks a sequence and head, in rounds.
+__global__ void __launch_bounds__(kMoveThreads, 3)
+    evict_move_kernel(const __grid_constant__ EvictArgs a) {
+  __shared__ int64_t from_slots[2][kRoundTokens], to_slots[2][kRoundTokens];
+  const int blocks = cluster_size(), rank = cluster_rank();
+  const int owner = blockIdx.x / blocks, b = owner / a.heads, h = owner - b * a.heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int n = min(max(__ldg(a.lengths + b), 0), a.most);
+  if (n <= a.keep) return;  // for all of the cluster
+  const int32_t* source = a.source + (int64_t(b) * a.heads + h) * a.keep;
+  const int codes = a.code_bytes / a.code_unit;
+  const int per_part = codes + a.param_bytes / a.param_unit;
+  const int rounds = (a.keep + a.round_tokens * blocks - 1) / (a.round_tokens * blocks);
+
+  const auto look = [&](int round) {  // the slots of a round's tokens
+    if (threadIdx.x < a.round_tokens && round < rounds) {
+      const int64_t j = (int64_t(round) * blocks + rank) * a.round_tokens + threadIdx.x;
+      int64_t from = -1, to = -1;
+      if (j < a.keep) {
+        const int s = source[j];
+        if (s != j) from = slot_of(a, b, s), to = slot_of(a, b, int(j));
+      }
+      if (from < 0 || to < 0) from = to = -1;
+      from_slots[round & 1][threadIdx.x] = from;
+      to_slots[round & 1][threadIdx.x] = to;
+    }
+  };
+  struct Round {
+    Piece held[kAtOnce];
+    char* to[kAtOnce];
+    int unit[kAtOnce];
+  };
+  const auto load = [&](int round, Round& x) {
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      x.to[u] = nullptr;
+      x.unit[u] = 0;
+      if (round >= rounds) continue;
+      const int i = u * kMoveThreads + threadIdx.x;
+      const int token = int(a.per_token.quot(uint32_t(i)));
+      if (token >= a.round_tokens) continue;
+      const int64_t from = from_slots[round & 1][token], to = to_slots[round & 1][token];
+      if (from < 0) continue;
+      int piece = i - token * int(a.per_token.d), part = 0;
+      while (piece >= per_part) piece -= per_part, ++part;
+      const lp_cache_part& p = a.part[part];
+      const bool is_code = piece < codes;
+      const int64_t page_stride = is_code ? p.code_page_stride : p.param_page_stride;
+      const int64_t slot_stride = is_code ? p.code_slot_stride : p.param_slot_stride;
+      char* base = static_cast<char*>(is_code ? p.codes : p.params) +
+                   h * (is_code ? p.code_head_stride : p.param_head_stride) +
+                   (is_code ? piece * a.code_unit : (piece - codes) * a.param_unit);
+      x.unit[u] = is_code ? a.code_unit : a.param_unit;
+      x.to[u] = base + place(a, to, page_stride, slot_stride);
+      load_piece(x.held[u], base + place(a, from, page_stride, slot_stride), x.unit[u]);
+    }
+  };
+  const auto store = [&](const Round& x) {
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      if (x.to[u] != nullptr) store_piece(x.held[u], x.to[u], x.unit[u]);
+  };
+  const auto landed = [&](Round& x) {  // the loads' values are here
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      asm volatile("" : "+r"(x.held[u].w[0]), "+r"(x.held[u].w[1]), "+r"(x.held[u].w[2]),
+                        "+r"(x.held[u].w[3]) :: "memory");
+  };
+
+  Round x, y;
+#pragma unroll
+  for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x.held[u].w[e] = y.held[u].w[e] = 0;
+  look(0);
+  __syncthreads();
+  load(0, x);
+  look(1);
+  for (int round = 0; round < rounds; round += 2) {
+    __syncthreads();
+    load(round + 1, y);
+    landed(x);
+    cluster_sync();
+    look(round + 2);
+    store(x);
+    if (round + 1 >= rounds) break;
+    __syncthreads();
+    load(round + 2, x);
+    landed(y);
+    cluster_sync();
+    look(round + 3);
+    store(y);
+  }
+}
+
+// The same for tokens of more pieces than a round: a block a sequence and head.
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_move_wide_kernel(const __grid_constant__ EvictArgs a) {
   const int b = blockIdx.x / a.heads, h = blockIdx.x - b * a.heads;
   const int n = min(max(__ldg(a.lengths + b), 0), a.most);
   if (n <= a.keep) return;
   const int32_t* source = a.source + (int64_t(b) * a.heads + h) * a.keep;
   const int codes = a.code_bytes / a.code_unit, params = a.param_bytes / a.param_unit;
-  const int per_part = codes + params, per_token = a.n_parts * per_part;
+  const int per_part = codes + params;
+  const int64_t per_token = int64_t(a.n_parts) * per_part;
   const int64_t total = int64_t(a.keep) * per_token;
-  for (int64_t i0 = 0; i0 < total; i0 += kMoveThreads * kAtOnce) {
-    Piece held[kAtOnce];
-    char* to[kAtOnce];
-    int unit[kAtOnce];
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      to[u] = nullptr;
-      unit[u] = 0;
-      const int64_t i = i0 + u * kMoveThreads + threadIdx.x;
-      if (i >= total) continue;
-      const int j = int(i / per_token), piece = int(i - int64_t(j) * per_token);
+  for (int64_t i0 = 0; i0 < total; i0 += kMoveThreads) {
+    Piece held;
+    char* to = nullptr;
+    int unit = 0;
+    const int64_t i = i0 + threadIdx.x;
+    if (i < total) {
+      const int j = int(i / per_token);
+      const int64_t piece = i - j * per_token;
       const int s = source[j];
-      if (s == j) continue;
       const int64_t from_slot = slot_of(a, b, s), to_slot = slot_of(a, b, j);
-      if (from_slot < 0 || to_slot < 0) continue;
-      const lp_cache_part& p = a.part[piece / per_part];
-      const int e = piece % per_part;
-      const bool is_code = e < codes;
-      const int64_t page_stride = is_code ? p.code_page_stride : p.param_page_stride;
-      const int64_t slot_stride = is_code ? p.code_slot_stride : p.param_slot_stride;
-      char* base = static_cast<char*>(is_code ? p.codes : p.params) +
-                   h * (is_code ? p.code_head_stride : p.param_head_stride) +
-                   (is_code ? e * a.code_unit : (e - codes) * a.param_unit);
-      unit[u] = is_code ? a.code_unit : a.param_unit;
-      to[u] = base + place(a, to_slot, page_stride, slot_stride);
-      load_piece(held[u], base + place(a, from_slot, page_stride, slot_stride), unit[u]);
+      if (s != j && from_slot >= 0 && to_slot >= 0) {
+        const lp_cache_part& p = a.part[piece / per_part];
+        const int e = int(piece % per_part);
+        const bool is_code = e < codes;
+        const int64_t page_stride = is_code ? p.code_page_stride : p.param_page_stride;
+        const int64_t slot_stride = is_code ? p.code_slot_stride : p.param_slot_stride;
+        char* base = static_cast<char*>(is_code ? p.codes : p.params) +
+                     h * (is_code ? p.code_head_stride : p.param_head_stride) +
+                     (is_code ? int64_t(e) * a.code_unit : int64_t(e - codes) * a.param_unit);
+        unit = is_code ? a.code_unit : a.param_unit;
+        to = base + place(a, to_slot, page_stride, slot_stride);
+        load_piece(held, base + place(a, from_slot, page_stride, slot_stride), unit);
+      }
     }
     __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u)
-      if (to[u] != nullptr) store_piece(held[u], to[u], unit[u]);
+    if (to != nullptr) store_piece(held, to, unit);
     __syncthreads();
   }
+}
+
+cudaError_t launch_cluster(void (*kernel)(EvictArgs), int64_t units, int blocks, int threads,
+                           size_t smem, cudaStream_t stream, const EvictArgs& a) {
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = unsigned(blocks);
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(units * blocks));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+cudaError_t launch(EvictArgs a, cudaStream_t stream) {
+  const int64_t units = int64_t(a.batch) * a.heads;
+  cudaError_t e;
+  if (a.most <= kMostCluster * kHeldTokens && units <= INT32_MAX / kMostCluster) {
+    // as many blocks as there is room for on all SMs, and as have 2048 tokens each
+    int blocks = (a.most + kHeldTokens - 1) / kHeldTokens;
+    blocks = blocks > 4 ? 8 : blocks > 2 ? 4 : blocks > 1 ? 2 : 1;
+    while (blocks < kMostCluster && units * blocks * 2 <= 2 * kSms && a.most > 2048 * blocks)
+      blocks *= 2;
+    a.slice = (a.most + blocks - 1) / blocks;
+    const int smem = std::max(1, a.slice) * 4;
+    e = cudaFuncSetAttribute(evict_slices_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+      e = launch_cluster(evict_slices_kernel, units, blocks, kThreads, smem, stream, a);
+  } else {
+    e = launch_kernel(evict_select_kernel, dim3(unsigned(units)), dim3(kThreads), 0, stream, a);
+  }
+  if (e != cudaSuccess || a.n_parts == 0 || a.weights == nullptr || a.n_slots == 0 || a.keep == 0)
+    return e;
+  const int64_t pieces = int64_t(a.n_parts) *
+                         (a.code_bytes / a.code_unit + a.param_bytes / a.param_unit);
+  if (pieces > kMoveThreads * kAtOnce || units > INT32_MAX / kMostCluster)
+    return launch_kernel(evict_move_wide_kernel, dim3(unsigned(units)), dim3(kMoveThreads), 0,
+                         stream, a);
+  a.per_token.set(uint32_t(pieces));
+  a.round_tokens = int(std::min<int64_t>(kRoundTokens, kMoveThreads * kAtOnce / pieces));
+  int blocks = 1;
+  while (blocks < kMostCluster && units * blocks * 2 <= 3 * kSms &&
+         a.keep > a.round_tokens * blocks)
+    blocks *= 2;
+  return launch_cluster(evict_move_kernel, units, blocks, kMoveThreads, 0, stream, a);
 }
 
 bool fits(int64_t a, int64_t b, int64_t most) { return b == 0 || a <= most / b; }
@@ -284,9 +569,5 @@ extern "C" lp_status lp_cache_evict(const lp_cache_part* parts, int64_t n_parts,
   a.keep = int(keep), a.first = int(first), a.recent = int(recent);
   a.new_lengths = new_lengths;
   a.source = static_cast<int32_t*>(workspace);
-  const dim3 grid(unsigned(batch * a.heads));
-  cudaError_t e = launch_kernel(evict_select_kernel, grid, dim3(kThreads), 0, stream, a);
-  if (e == cudaSuccess && a.n_parts > 0 && heads > 0 && n_slots > 0)
-    e = launch_kernel(evict_move_kernel, grid, dim3(kMoveThreads), 0, stream, a);
-  return status_of(e);
+  return status_of(launch(a, stream));
 }

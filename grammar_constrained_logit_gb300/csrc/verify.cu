@@ -5,8 +5,13 @@
 //   argmax_v log r_v + g_v says one token more, r = max(p_n - q_n, 0) after a refusal and
 //   r = p_n else: with Gumbel noise g that is a draw from r / sum r.
 //
-// The first kernel reads every row once for (M, S) and its largest token; the second decides
-// a slot's acceptances from them and goes through the one row that says a token.
+// The first kernel reads every row once and leaves (largest, sum of exp((x - largest) / T)) of
+// each chunk of 2 KB; the second, a cluster of blocks a slot, joins those to (M, S), decides the
+// slot's acceptances, and goes through the one row that says a token.
+//
+// There a token that cannot win is told by its noise word alone: log r + g > best means
+// -log u < r exp(-best), and 1 - u <= -log u, so where 1 - u is not below that (with a margin
+// for its roundings) neither logarithm is taken.
 #include <algorithm>
 
 #include "common.cuh"
@@ -14,14 +19,15 @@
 namespace lp {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kMostRows = 256;  // of a slot
-
-struct RowStats {
-  float top, sum;  // over the candidates; -inf and 0 where there is none
-  int first;       // the lowest-index largest
-  int pad;
-};
+constexpr int kStreamThreads = 256;
+constexpr int kVecs = 4;                    // 16-byte vectors a lane has of a chunk
+constexpr int kChunkVecs = kVecs * 32;
+constexpr int kThreads = 512;               // of a block of the second kernel
+constexpr int kWarps = kThreads / 32;
+constexpr int kMostRows = 256;              // of a slot
+constexpr int kMostCluster = 8;
+constexpr int kSms = 152;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct VerifyArgs {
   const char* logits;
@@ -41,7 +47,8 @@ struct VerifyArgs {
   const uint64_t* seeds;
   int64_t* out_tokens;
   int32_t* out_accepted;
-  RowStats* stats;
+  float2* part;  // [rows, chunks]
+  int chunks;
 };
 
 __device__ __forceinline__ float heat_of(const VerifyArgs& a, int slot) {
@@ -61,78 +68,200 @@ __device__ __forceinline__ bool kept(const uint32_t* mask, int v) {
 // x / T of a candidate relative to the row's largest; candidates at +inf share the mass.
 __device__ __forceinline__ float relative(float x, float top) { return x == top ? 0.0f : x - top; }
 
-// Whether (x, v) goes before (y, w): larger, or as large and lower.
-__device__ __forceinline__ bool before(float x, int v, float y, int w) {
-  return x > y || (x == y && v < w);
+// What a candidate's distance to the largest is multiplied by, as a power of two.
+__device__ __forceinline__ float rate_of(float heat) {
+  return fminf(kLog2e / heat, 3e38f);
 }
 
 __device__ __forceinline__ void best_of(float& x, int& v, float y, int w) {
-  if (before(y, w, x, v)) x = y, v = w;
+  if (y > x || (y == x && w < v)) x = y, v = w;
 }
 
-// The block's best, in every thread; two barriers.
-__device__ __forceinline__ void block_best(float& x, int& v, float* xs, int* vs) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float y = __shfl_xor_sync(kFullWarp, x, o);
-    const int w = __shfl_xor_sync(kFullWarp, v, o);
-    best_of(x, v, y, w);
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) xs[threadIdx.x >> 5] = x, vs[threadIdx.x >> 5] = v;
-  __syncthreads();
-  x = xs[0], v = vs[0];
-  for (int i = 1; i < kThreads / 32; ++i) best_of(x, v, xs[i], vs[i]);
-}
-
-// A block a row.
+// A row's 16-byte vectors: aligned ones, of which the first and the last may hold tokens
+// that are not the row's.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) verify_stats_kernel(const __grid_constant__ VerifyArgs a) {
-  __shared__ float xs[kThreads / 32];
-  __shared__ int vs[kThreads / 32];
-  const int64_t row = blockIdx.x;
-  const char* x = a.logits + row * a.stride;
-  const uint32_t* mask = mask_of(a, row);
-  const float heat = heat_of(a, int(row / a.per_slot));
-  float top = -INFINITY;
-  int first = INT32_MAX;
-  for (int v = threadIdx.x; v < a.V; v += kThreads)
-    if (kept(mask, v)) {
-      const float y = Elt<DT>::load1(x + int64_t(v) * Elt<DT>::kBytes);
-      if (y > top) top = y, first = v;
-    }
-  block_best(top, first, xs, vs);
-  float sum = 0.0f;
-  if (top > -INFINITY && heat > 0.0f)
-    for (int v = threadIdx.x; v < a.V; v += kThreads)
-      if (kept(mask, v)) {
-        const float y = Elt<DT>::load1(x + int64_t(v) * Elt<DT>::kBytes);
-        if (y > -INFINITY) sum += expf(__fdiv_rn(relative(y, top), heat));
-      }
+struct RowVecs {
+  static constexpr int kPer = Elt<DT>::kPerVec;
+  const char* at;
+  const uint32_t* mask;
+  int before, V;  // tokens of the first vector before the row
+
+  __device__ __forceinline__ RowVecs(const VerifyArgs& a, int64_t row) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.logits) + row * a.stride;
+    before = int(p & 15) / Elt<DT>::kBytes;
+    at = reinterpret_cast<const char*>(p & ~uintptr_t(15));
+    mask = mask_of(a, row);
+    V = a.V;
+  }
+  __device__ __forceinline__ int64_t count() const {
+    return (int64_t(before) + V + kPer - 1) / kPer;
+  }
+  __device__ __forceinline__ int first_token(int64_t q) const { return int(q * kPer - before); }
+  // Bits of the vector's tokens that are candidates, as far as the mask goes.
+  __device__ __forceinline__ uint32_t bits(int64_t q) const {
+    const int j = first_token(q), lo = max(0, -j), n = min(kPer, V - j);
+    uint32_t keep = ((1u << n) - 1u) & ~((1u << lo) - 1u);
+    if (mask != nullptr) keep &= mask_bits(mask, j + lo, kPer - lo, V) << lo;
+    return keep;
+  }
+};
+
+// A warp a chunk.
+template <int DT>
+__global__ void __launch_bounds__(kStreamThreads)
+    verify_stream_kernel(const __grid_constant__ VerifyArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t total = int64_t(a.rows) * a.chunks;
+  for (int64_t i = int64_t(blockIdx.x) * (kStreamThreads / 32) + (threadIdx.x >> 5); i < total;
+       i += int64_t(gridDim.x) * (kStreamThreads / 32)) {
+    const int64_t row = i / a.chunks;
+    const int chunk = int(i - row * a.chunks);
+    const RowVecs<DT> x(a, row);
+    const int64_t vecs = x.count();
+    uint4 raw[kVecs];
+    uint32_t keep[kVecs];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) xs[threadIdx.x >> 5] = sum;
+    for (int u = 0; u < kVecs; ++u) {
+      const int64_t q = int64_t(chunk) * kChunkVecs + u * 32 + lane;
+      keep[u] = 0;
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (q < vecs) {
+        raw[u] = __ldg(reinterpret_cast<const uint4*>(x.at) + q);
+        keep[u] = x.bits(q);
+      }
+    }
+    const float rate = rate_of(heat_of(a, int(row / a.per_slot)));
+    float top = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) top = fmaxf(top, VecMax<DT>::run(raw[u], keep[u]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullWarp, top, o));
+    float sum = 0.0f;
+    if (top > -INFINITY) {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+        for (int e = 0; e < RowVecs<DT>::kPer; ++e) {
+          const float y = Elt<DT>::get(raw[u], e);
+          const float t = (top == INFINITY ? relative(y, top) : y - top) * rate;
+          // NaN is no candidate: a maximum takes the other side
+          sum += ex2((keep[u] >> e) & 1u ? fmaxf(t, -200.0f) : -200.0f);
+        }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
+    }
+    if (lane == 0) a.part[i] = make_float2(top, sum);
+  }
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t n;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+struct Found {
+  float score;
+  int token;
+};
+
+// The best of all the cluster's threads, in every thread.
+__device__ __forceinline__ Found cluster_best(Found f, Found* warps, Found* mine) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    best_of(f.score, f.token, __shfl_xor_sync(kFullWarp, f.score, o),
+            __shfl_xor_sync(kFullWarp, f.token, o));
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = f;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < kThreads / 32; ++i) sum += xs[i];
-    RowStats s;
-    s.top = top, s.sum = sum, s.first = first, s.pad = 0;
-    a.stats[row] = s;
+    for (int i = 1; i < kWarps; ++i) best_of(f.score, f.token, warps[i].score, warps[i].token);
+    *mine = f;
   }
+  cluster_sync();
+  const uint32_t at = uint32_t(__cvta_generic_to_shared(mine));
+  f.score = -INFINITY, f.token = INT32_MAX;
+  for (uint32_t r = 0; r < cluster_size(); ++r) {
+    uint32_t remote, s, t;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(r));
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(s), "=r"(t) : "r"(remote) : "memory");
+    best_of(f.score, f.token, __uint_as_float(s), int(t));
+  }
+  cluster_sync();  // nobody leaves, or writes the next one, before all have read
+  return f;
 }
 
-// A block a slot.
+template <int DT>
+__device__ __forceinline__ float logit_at(const char* x, int v) {
+  return Elt<DT>::load1(x + int64_t(v) * Elt<DT>::kBytes);
+}
+
+// A cluster of blocks a slot.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) verify_say_kernel(const __grid_constant__ VerifyArgs a) {
-  __shared__ float xs[kThreads / 32];
-  __shared__ int vs[kThreads / 32];
+  __shared__ float tops[kMostRows], sums[kMostRows];
+  __shared__ int firsts[kMostRows];  // greedy: the lowest-index largest
+  __shared__ Found warps[kWarps];
+  __shared__ alignas(8) Found mine;
   __shared__ int count, there;
-  const int slot = blockIdx.x, R = a.per_slot, tid = threadIdx.x;
+  const int blocks = int(cluster_size()), rank = int(cluster_rank());
+  const int slot = blockIdx.x / blocks, R = a.per_slot, tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) count = there = R - 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const float heat = heat_of(a, slot);
   const bool greedy = !(heat > 0.0f);
+  const float rate = rate_of(heat);
   const int64_t* drafts = a.drafts + int64_t(slot) * (R - 1);
-  if (tid == 0) count = there = R - 1;
+  for (int i = tid >> 5; i < R; i += kWarps) {
+    const int64_t row = int64_t(slot) * R + i;
+    const float2* part = a.part + row * a.chunks;
+    float top = -INFINITY, sum = 0.0f;
+    for (int c = lane; c < a.chunks; c += 32) {
+      const float2 p = part[c];
+      const float now = fmaxf(top, p.x);
+      if (now > -INFINITY)
+        sum = sum * ex2(relative(top, now) * rate) + p.y * ex2(relative(p.x, now) * rate);
+      top = now;
+    }
+    float all = top;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) all = fmaxf(all, __shfl_xor_sync(kFullWarp, all, o));
+    sum = top > -INFINITY ? sum * ex2(relative(top, all) * rate) : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
+    int first = INT32_MAX;
+    if (greedy && all > -INFINITY) {  // in the first chunk that has it
+      int chunk = INT32_MAX;
+      for (int c = lane; c < a.chunks; c += 32)
+        if (chunk == INT32_MAX && part[c].x == all) chunk = c;
+      chunk = __reduce_min_sync(kFullWarp, chunk);
+      const RowVecs<DT> x(a, row);
+      const int64_t vecs = x.count();
+      for (int u = 0; u < kVecs; ++u) {
+        const int64_t q = int64_t(chunk) * kChunkVecs + u * 32 + lane;
+        if (q >= vecs) continue;
+        const uint4 raw = __ldg(reinterpret_cast<const uint4*>(x.at) + q);
+        const uint32_t keep = x.bits(q);
+#pragma unroll
+        for (int e = RowVecs<DT>::kPer - 1; e >= 0; --e)
+          if (((keep >> e) & 1u) && Elt<DT>::get(raw, e) == all)
+            first = min(first, x.first_token(q) + e);
+      }
+      first = __reduce_min_sync(kFullWarp, first);
+    }
+    if (lane == 0) tops[i] = all, sums[i] = sum, firsts[i] = first;
+  }
   __syncthreads();
   for (int i = tid; i < R - 1; i += kThreads) {
     const int64_t v = drafts[i];
@@ -141,13 +270,12 @@ __global__ void __launch_bounds__(kThreads) verify_say_kernel(const __grid_const
       atomicMin(&there, i);
     } else {
       const int64_t row = int64_t(slot) * R + i;
-      const RowStats s = a.stats[row];
       double p = 0.0;
       if (greedy) {
-        p = v == s.first ? 1.0 : 0.0;
+        p = v == firsts[i] ? 1.0 : 0.0;
       } else if (kept(mask_of(a, row), int(v))) {
-        const float x = Elt<DT>::load1(a.logits + row * a.stride + v * Elt<DT>::kBytes);
-        if (x > -INFINITY) p = exp(double(relative(x, s.top)) / double(heat)) / double(s.sum);
+        const float x = logit_at<DT>(a.logits + row * a.stride, int(v));
+        if (x > -INFINITY) p = exp(double(relative(x, tops[i])) / double(heat)) / double(sums[i]);
       }
       const double q = a.probs != nullptr
                            ? double(a.probs[slot * a.probs_slot + i * a.probs_row + v]) : 1.0;
@@ -158,10 +286,10 @@ __global__ void __launch_bounds__(kThreads) verify_say_kernel(const __grid_const
   __syncthreads();
   const int n = count;
   const int64_t row = int64_t(slot) * R + n;
-  const RowStats s = a.stats[row];
+  const float top = tops[n], sum = sums[n];
   const bool refused = n < there;
-  int token = s.first;
-  if (!greedy && s.top > -INFINITY) {
+  int token = firsts[n];
+  if (!greedy && top > -INFINITY) {
     const uint32_t* mask = mask_of(a, row);
     const char* x = a.logits + row * a.stride;
     const float* q = refused && a.probs != nullptr
@@ -169,33 +297,77 @@ __global__ void __launch_bounds__(kThreads) verify_say_kernel(const __grid_const
     const int64_t draft = refused ? drafts[n] : -1;
     const uint64_t seed = a.seeds != nullptr ? a.seeds[row] : a.seed;
     const uint2 key = make_uint2(uint32_t(seed), uint32_t(seed >> 32));
+    const bool whole = (reinterpret_cast<uintptr_t>(x) % (4 * Elt<DT>::kBytes)) == 0;
+    const bool whole_q = q != nullptr && reinterpret_cast<uintptr_t>(q) % 16 == 0;
+    const float inv = 1.0f / sum;
+    const float shift = __fdiv_rn(top, heat);
     for (int rest = refused; rest >= 0; --rest) {  // the second time where nothing was left
-      float best = -INFINITY;
-      token = INT32_MAX;
-      for (int v4 = tid * 4; v4 < a.V; v4 += kThreads * 4) {
-        const uint4 w = philox4x32_10(make_uint4(uint32_t(v4) >> 2, uint32_t(row),
-                                                 uint32_t(a.offset), uint32_t(a.offset >> 32)), key);
-        for (int e = 0; e < 4 && v4 + e < a.V; ++e) {
-          const int v = v4 + e;
-          if (!kept(mask, v)) continue;
-          const float y = Elt<DT>::load1(x + int64_t(v) * Elt<DT>::kBytes);
-          if (!(y > -INFINITY)) continue;
-          float score;
-          if (rest) {
-            const float p = expf(__fdiv_rn(relative(y, s.top), heat)) / s.sum;
-            const float r = p - (q != nullptr ? q[v] : v == draft ? 1.0f : 0.0f);
-            if (!(r > 0.0f)) continue;
-            score = logf(r);
+      Found f = {-INFINITY, INT32_MAX};
+      float bound = 3e38f;  // exp(-best), of what r is measured in
+      const int step = blocks * kThreads * 4;
+      for (int v4 = (rank * kThreads + tid) * 4; v4 < a.V; v4 += step) {
+        const int m = min(4, a.V - v4);
+        uint32_t keep = (1u << m) - 1u;
+        if (mask != nullptr) keep &= __ldg(mask + (v4 >> 5)) >> (v4 & 31);
+        if (keep != 0) {
+          float y[4], d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (whole && m == 4) {
+            if (DT == LP_F32) {
+              const float4 w = __ldg(reinterpret_cast<const float4*>(x) + v4 / 4);
+              y[0] = w.x, y[1] = w.y, y[2] = w.z, y[3] = w.w;
+            } else {
+              const uint2 w = __ldg(reinterpret_cast<const uint2*>(x) + v4 / 4);
+              const uint4 w4 = make_uint4(w.x, w.y, 0, 0);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] = Elt<DT>::get(w4, e);
+            }
           } else {
-            score = __fdiv_rn(y, heat);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = e < m ? logit_at<DT>(x, v4 + e) : -INFINITY;
           }
-          best_of(best, token, score + gumbel_from_word(word_of(w, e)), v);
+          if (rest && q != nullptr) {
+            if (whole_q && m == 4) {
+              const float4 w = __ldg(reinterpret_cast<const float4*>(q) + v4 / 4);
+              d[0] = w.x, d[1] = w.y, d[2] = w.z, d[3] = w.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) d[e] = e < m ? __ldg(q + v4 + e) : 0.0f;
+            }
+          } else if (rest) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[e] = v4 + e == draft ? 1.0f : 0.0f;
+          }
+          const uint4 w = philox4x32_10(make_uint4(uint32_t(v4) >> 2, uint32_t(row),
+                                                   uint32_t(a.offset), uint32_t(a.offset >> 32)), key);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!((keep >> e) & 1u) || !(y[e] > -INFINITY)) continue;
+            const uint32_t word = word_of(w, e);
+            const float p = ex2(relative(y[e], top) * rate) * (rest ? inv : 1.0f);
+            const float missing = (float(~word >> 9) + 0.5f) * 1.1920928955078125e-07f;  // 1 - u
+            // p is within 1e-5 of itself, whatever is left of p - d
+            if (!(missing < fmaf(p, 1.00002f, -d[e]) * bound * 1.001f)) continue;
+            float score;
+            if (rest) {
+              const float r = expf(__fdiv_rn(relative(y[e], top), heat)) / sum - d[e];
+              if (!(r > 0.0f)) continue;
+              score = logf(r);
+            } else {
+              score = __fdiv_rn(y[e], heat);
+            }
+            best_of(f.score, f.token, score + gumbel_from_word(word), v4 + e);
+            if (fabsf(shift) < 1024.0f) bound = fminf(expf((rest ? 0.0f : shift) - f.score), 3e38f);
+          }
         }
+        // what the warp has found holds for all of its lanes
+        bound = __uint_as_float(__reduce_min_sync(__activemask(), __float_as_uint(bound)));
       }
-      block_best(best, token, xs, vs);
+      f = cluster_best(f, warps, &mine);
+      token = f.token;
       if (token != INT32_MAX) break;
     }
   }
+  if (rank != 0) return;
   if (token == INT32_MAX) token = -1;
   for (int i = tid; i < R; i += kThreads)
     a.out_tokens[int64_t(slot) * R + i] = i < n ? drafts[i] : i == n ? token : -1;
@@ -203,12 +375,36 @@ __global__ void __launch_bounds__(kThreads) verify_say_kernel(const __grid_const
 }
 
 template <int DT>
-cudaError_t launch(const VerifyArgs& a, cudaStream_t stream) {
-  cudaError_t e = launch_kernel(verify_stats_kernel<DT>, dim3(unsigned(a.rows)), dim3(kThreads), 0,
-                                stream, a);
+cudaError_t launch(VerifyArgs a, cudaStream_t stream) {
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(kStreamThreads);
+  const int64_t warps = int64_t(a.rows) * a.chunks;
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>((warps + 7) / 8, kSms * 64)));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_stream_kernel<DT>, a);
   if (e != cudaSuccess) return e;
-  return launch_kernel(verify_say_kernel<DT>, dim3(unsigned(a.rows / a.per_slot)), dim3(kThreads),
-                       0, stream, a);
+  const int64_t slots = a.rows / a.per_slot;
+  // blocks to a slot: as many as have a round of tokens, and as all slots have room for
+  int blocks = kMostCluster;
+  while (blocks > 1 && (slots * blocks > kSms * 4 || blocks * kThreads * 4 >= 2 * a.V)) blocks /= 2;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = unsigned(blocks);
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(unsigned(slots * blocks));
+  return cudaLaunchKernelEx(&cfg, verify_say_kernel<DT>, a);
+}
+
+// Chunks of a row, wherever it starts.
+int64_t chunks_of(lp_dtype dt, int64_t V) {
+  const int64_t per = dt == LP_F32 ? 4 : 8;
+  return std::max<int64_t>(1, (V + per - 1 + per * kChunkVecs - 1) / (per * kChunkVecs));
 }
 
 }  // namespace
@@ -219,7 +415,7 @@ extern "C" int64_t lp_verify_drafts_workspace_bytes(lp_dtype dt, int64_t rows,
   if ((dt != LP_F32 && dt != LP_F16 && dt != LP_BF16) || rows < 0 || vocab_size < 0 ||
       rows > (int64_t(1) << 27) || vocab_size > INT32_MAX - 64)
     return -1;
-  return rows * int64_t(sizeof(lp::RowStats));
+  return (rows * lp::chunks_of(dt, vocab_size) * 8 + 15) / 16 * 16;
 }
 
 extern "C" lp_status lp_verify_drafts(const void* logits, lp_dtype dt, int64_t B, int64_t cols,
@@ -288,7 +484,8 @@ extern "C" lp_status lp_verify_drafts(const void* logits, lp_dtype dt, int64_t B
   a.seeds = seeds;
   a.out_tokens = out_tokens;
   a.out_accepted = out_accepted;
-  a.stats = static_cast<RowStats*>(workspace);
+  a.part = static_cast<float2*>(workspace);
+  a.chunks = int(chunks_of(dt, V));
   const cudaError_t e = dt == LP_F32   ? launch<LP_F32>(a, stream)
                         : dt == LP_F16 ? launch<LP_F16>(a, stream)
                                        : launch<LP_BF16>(a, stream);

@@ -566,7 +566,7 @@ lp_status lp_cache_evict(const lp_cache_part* parts, int64_t n_parts, int32_t bi
  * all before it were accepted (a NaN accepts nothing).  With n drafts accepted, row n says
  * one more token:
  *   - draft n was there, and refused: argmax over v of log r_v + g_v, r = max(p_n - q_n, 0),
- *     or r = p_n where that is 0 everywhere (NaN counts as 0);
+ *     or r = p_n where that is 0 everywhere (NaN counts as 0, and so does p below 2^-120);
  *   - else argmax over v of logit_v / temperature + g_v, or the largest logit with
  *     temperature <= 0,
  * over the row's candidates, ties to the lowest; -1 if it has none.  g is lp_sample's noise,
