@@ -262,10 +262,24 @@ extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, i
   if (block == 0 || n_slots == 0 || !aligned(a, row % 16 == 0 ? 16 : 8, false))
     return status_of(attend_any(a, stream));
   a.wide_params = a.dim / a.group % 4 == 0 && aligned(a, 16, true);
-  a.team = 5;
+  {
+    const lp_cache_part &k = parts[0], &v = parts[1];
+    const bool one_page = page_size >= n_slots;
+    const int64_t unit = row % 16 == 0 ? 16 : 8;
+    const auto alike = [&](int64_t s, int64_t t, int64_t sp, int64_t tp, int64_t size) {
+      return s == t && s > 0 && (one_page || (sp == tp && sp == s * page_size)) &&
+             s / size <= INT64_MAX / n_slots && s / size * n_slots <= UINT32_MAX;
+    };
+    if (alike(k.code_slot_stride, v.code_slot_stride, k.code_page_stride, v.code_page_stride, unit) &&
+        alike(k.param_slot_stride, v.param_slot_stride, k.param_page_stride, v.param_page_stride, 4)) {
+      a.code_step = uint32_t(k.code_slot_stride / unit);
+      a.param_step = uint32_t(k.param_slot_stride / 4);
+    }
+  }
+  a.team = 4;
   while (a.heads % a.team != 0) --a.team;
   a.head_groups = a.heads / a.team;
-  a.min_tiles = 4;
+  a.min_tiles = 2;
   const int at_once = rows_at_once(int64_t(a.rows) * a.shared);
   char* left = static_cast<char*>(workspace) + (batch * rows * q_heads * 4 + 15) / 16 * 16;
   const int64_t held = int64_t(kSms) * kMostWarps * 2 * at_once;

@@ -32,7 +32,10 @@ struct AttendArgs {
   // (sequence, group of `team` heads, tile of rows, tile of tokens), and each of `workers`
   // teams of warps, a warp a head, takes a range of them
   int team, head_groups, row_tiles, workers, min_tiles;
-  bool wide_params, wide_out;  // 16-byte copies of params; 8-byte stores of results
+  bool wide_params;   // 16-byte copies of params
+  // a slot's place is slot * stride in both parts, and counted in copied units (codes) and
+  // words (params) it is below 2^32: then these are the strides
+  uint32_t code_step, param_step;
   float* sums;     // [workers, 2, team, tile's rows, dim]: of what a worker has of a unit
   float2* tops;    // [workers, 2, team, tile's rows]: (largest exponent, mass)
 };

@@ -45,6 +45,8 @@ struct Shape {
   static constexpr int kStage = 2 * (kCodes + kParams);
   static constexpr int kStages = 2;
   static constexpr int kRows = 8 * NR;
+  // blocks of four warps on an SM: 168 registers a thread where that holds the sums, else 255
+  static constexpr int kResident = NR == 1 && DIM <= 128 ? 3 : 2;
 };
 
 // Which 16 bytes of a row lie where: rows that are read together lie in different banks.
@@ -129,6 +131,13 @@ __device__ __forceinline__ void copy_async(uint32_t to, const char* from, int un
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes)
                  : "memory");
+}
+
+__device__ __forceinline__ void copy_all(uint32_t to, const char* from, int unit) {
+  if (unit == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
 }
 
 __device__ __forceinline__ float power_of_two(int e) {  // e in [-126, 127]
@@ -305,6 +314,47 @@ struct Loader {
                ? __ldg(a.blocks + int64_t(b) * a.blocks_stride + a.per_block.quot(uint32_t(t)))
                : -1;
   }
+  // Keys and values lie alike: one place for both.  ALL: every token is there.
+  template <int PARTS, bool ALL>
+  __device__ __forceinline__ void copies(uint32_t base, uint32_t mine, uint32_t held) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < (T::kTile * T::kChunks + 31) / 32; ++k) {
+      const int idx = k * 32 + lane;
+      const int token = 32 % T::kChunks == 0 ? k * (32 / T::kChunks) + lane / T::kChunks
+                                             : idx / T::kChunks;
+      const int piece = 32 % T::kChunks == 0 ? lane % T::kChunks : idx - token * T::kChunks;
+      const uint32_t row = __shfl_sync(kFullWarp, mine, token);
+      if (T::kTile * T::kChunks % 32 != 0 && token >= T::kTile) continue;
+      const int64_t at = int64_t(uint64_t(row) * T::kUnit) + piece * T::kUnit;
+      const uint32_t to = base + token * T::kRow +
+                          swizzled<T::kRow>(piece * T::kUnit, swizzle<T::kRow>(token));
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        if (ALL) copy_all(to + p * T::kCodes, codes[p] + at, T::kUnit);
+        else copy_async(to + p * T::kCodes, codes[p] + at, T::kUnit,
+                        (held >> token) & 1u ? T::kUnit : 0);
+      }
+    }
+  }
+  template <int PARTS>
+  __device__ __forceinline__ void param_copy(const AttendArgs& a, uint32_t base, int p,
+                                             const char* from, bool there) {
+    const int lane = threadIdx.x & 31;
+    if (T::kTile == 32 || (lane >> 4) == p || (PARTS == 1 && lane < 16)) {
+      const uint32_t at = base + 2 * T::kCodes + p * T::kParams +
+                          (lane & (T::kTile - 1)) * T::kBlocks * 4;
+      if (T::kBlocks % 4 == 0 && a.wide_params) {
+#pragma unroll
+        for (int k = 0; k < T::kBlocks; k += 4)
+          if (k < groups) copy_async(at + 4 * k, from + 4 * k, 16, there ? 16 : 0);
+      } else {
+#pragma unroll
+        for (int k = 0; k < T::kBlocks; ++k)
+          if (k < groups) copy_async(at + 4 * k, from + 4 * k, 4, there ? 4 : 0);
+      }
+    }
+  }
   // Starts the copies of a tile whose blocks are looked up; which of its tokens are there.
   // PARTS: 2, or 1 for the keys alone.
   template <int PARTS>
@@ -317,37 +367,36 @@ struct Loader {
     if (!there) slot = 0;
     const uint32_t held = __ballot_sync(kFullWarp, there);
     const uint32_t base = uint32_t(__cvta_generic_to_shared(smem)) + stage * T::kStage;
-#pragma unroll
-    for (int p = 0; p < PARTS; ++p) {
-      const lp_cache_part& part = a.part[p];
-      const uint64_t mine = reinterpret_cast<uint64_t>(
-          codes[p] + slot_place(a, slot, part.code_page_stride, part.code_slot_stride));
-      const uint32_t to = base + p * T::kCodes;
-#pragma unroll
-      for (int k = 0; k < (T::kTile * T::kChunks + 31) / 32; ++k) {
-        const int idx = k * 32 + lane;
-        const int token = idx / T::kChunks, piece = idx - token * T::kChunks;
-        const uint64_t row = __shfl_sync(kFullWarp, mine, token);
-        if (T::kTile * T::kChunks % 32 == 0 || token < T::kTile)
-          copy_async(to + token * T::kRow +
-                         swizzled<T::kRow>(piece * T::kUnit, swizzle<T::kRow>(token)),
-                     reinterpret_cast<const char*>(row) + piece * T::kUnit, T::kUnit,
-                     (held >> token) & 1u ? T::kUnit : 0);
+    if (a.code_step != 0) {
+      const uint32_t mine = uint32_t(slot) * a.code_step;
+      if (held == kFullWarp) {
+        copies<PARTS, true>(base, mine, held);
+      } else {
+        copies<PARTS, false>(base, mine, held);
       }
-      if (T::kTile == 32 || (lane >> 4) == p || (PARTS == 1 && lane < 16)) {
-        const char* from = params[p] + slot_place(a, slot, part.param_page_stride,
-                                                  part.param_slot_stride);
-        const uint32_t at = base + 2 * T::kCodes + p * T::kParams +
-                            (lane & (T::kTile - 1)) * T::kBlocks * 4;
-        if (T::kBlocks % 4 == 0 && a.wide_params) {
+      const int64_t at = int64_t(uint64_t(uint32_t(slot) * a.param_step) * 4);
 #pragma unroll
-          for (int k = 0; k < T::kBlocks; k += 4)
-            if (k < groups) copy_async(at + 4 * k, from + 4 * k, 16, there ? 16 : 0);
-        } else {
+      for (int p = 0; p < PARTS; ++p) param_copy<PARTS>(a, base, p, params[p] + at, there);
+    } else {
 #pragma unroll
-          for (int k = 0; k < T::kBlocks; ++k)
-            if (k < groups) copy_async(at + 4 * k, from + 4 * k, 4, there ? 4 : 0);
+      for (int p = 0; p < PARTS; ++p) {
+        const lp_cache_part& part = a.part[p];
+        const uint64_t mine = reinterpret_cast<uint64_t>(
+            codes[p] + slot_place(a, slot, part.code_page_stride, part.code_slot_stride));
+        const uint32_t to = base + p * T::kCodes;
+#pragma unroll 1
+        for (int idx = lane; idx < (T::kTile * T::kChunks + 31) / 32 * 32; idx += 32) {
+          const int token = idx / T::kChunks, piece = idx - token * T::kChunks;
+          const uint64_t row = __shfl_sync(kFullWarp, mine, token);
+          if (token < T::kTile)
+            copy_async(to + token * T::kRow +
+                           swizzled<T::kRow>(piece * T::kUnit, swizzle<T::kRow>(token)),
+                       reinterpret_cast<const char*>(row) + piece * T::kUnit, T::kUnit,
+                       (held >> token) & 1u ? T::kUnit : 0);
         }
+        param_copy<PARTS>(a, base, p,
+                          params[p] + slot_place(a, slot, part.param_page_stride,
+                                                 part.param_slot_stride), there);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -666,11 +715,11 @@ __device__ __forceinline__ void Sums<T>::split_nan(const Queries<T>& q, char* va
 
 // ------------------------------------------------------------------ kernels
 
-constexpr int kMostTeamWarps = 5;
+constexpr int kMostTeamWarps = 4;
 
 // One worker's range of tiles, unit by unit.
 template <class T>
-__global__ void __launch_bounds__(kMostTeamWarps * 32)
+__global__ void __launch_bounds__(kMostTeamWarps * 32, T::kResident)
     attend_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ __align__(128) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
@@ -719,8 +768,6 @@ __global__ void __launch_bounds__(kMostTeamWarps * 32)
     const int tile = int(at - base - int64_t(unit) * tiles.count);
     const int count = int(min(int64_t(tiles.count - tile), stop - at));
     const int rt = unit % a.row_tiles, h = unit / a.row_tiles * a.team + in_team;
-    Queries<T> q;
-    q.load(a, b, h, rt, s);
     // tiles that a row of this tile of rows sees
     const int r0 = rt * T::kRows / a.shared;
     const int r1 = min(rt * T::kRows + T::kRows - 1, a.rows * a.shared - 1) / a.shared;
@@ -730,8 +777,6 @@ __global__ void __launch_bounds__(kMostTeamWarps * 32)
     // tokens that all of them see
     const int from = highest.lo, until = r1 < s.rows ? lowest.end : 0;
 
-    Sums<T> sums;
-    sums.clear();
     Loader<T> load;
     load.init(a, smem + warp * (T::kStages * T::kStage), b, h);
     uint32_t held = 0;
@@ -740,6 +785,10 @@ __global__ void __launch_bounds__(kMostTeamWarps * 32)
       held = load.template start<2>(a, first, highest.end, 0);
       if (first + 1 < last) load.look(a, first + 1);
     }
+    Queries<T> q;
+    q.load(a, b, h, rt, s);
+    Sums<T> sums;
+    sums.clear();
     for (int i = first; i < last; ++i) {
       uint32_t held_next = 0;
       const int stage = (i - first) & 1;
@@ -805,10 +854,14 @@ __global__ void __launch_bounds__(kMostTeamWarps * 32)
 
 // Joins what several workers have of a unit: a block a row of a head.  Rows of sequences
 // without tiles become zeros.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinHeld = kSms * kMostWarps;  // workers, at most
+
 template <int TILE, int ROWS>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendArgs a) {
-  __shared__ float acc[4][256];
-  __shared__ float masses[4];
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    attend_join_kernel(const __grid_constant__ AttendArgs a) {
+  __shared__ float acc[kJoinWarps][256], factors[kJoinHeld];
+  __shared__ float most[kJoinWarps], masses[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_head = a.rows * a.shared;
   const int row = blockIdx.x % per_head;
@@ -822,48 +875,65 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
              j * a.out.head_stride;
   float* lse = a.lse != nullptr ? a.lse + (int64_t(b) * a.rows + r) * (a.heads * a.shared) + j
                                 : nullptr;
+  const int64_t begin = base + (int64_t(h / a.team) * a.row_tiles + rt) * tiles;
+  const int w0 = tiles > 0 ? d.owner(begin) : 0, w1 = tiles > 0 ? d.owner(begin + tiles - 1) : 0;
+  // a worker's first unit is its part 0, its last one part 1
+  const bool inside = tiles > 0 && d.start(w0) != begin;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tiles == 0) {
-    for (int i = threadIdx.x; i < a.dim; i += 128) store_float(to, i, 0.0f, a.dt);
+    for (int i = threadIdx.x; i < a.dim; i += blockDim.x) store_float(to, i, 0.0f, a.dt);
     if (lse != nullptr && threadIdx.x == 0) *lse = -INFINITY;
     return;
   }
-  const int64_t begin = base + (int64_t(h / a.team) * a.row_tiles + rt) * tiles;
-  const int w0 = d.owner(begin), w1 = d.owner(begin + tiles - 1);
   if (w0 == w1) return;  // written whole
-  const auto slot = [&](int w) {
-    const int part = w == w0 && d.start(w) != begin ? 1 : 0;
-    return ((int64_t(w) * 2 + part) * a.team + h % a.team) * ROWS + row % ROWS;
+  const int n = w1 - w0 + 1;
+  const auto slot = [&](int i) {
+    return ((int64_t(w0 + i) * 2 + (i == 0 && inside)) * a.team + h % a.team) * ROWS + row % ROWS;
   };
   float top = -INFINITY;
-  for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, a.tops[slot(w)].x);
+  for (int i = threadIdx.x; i < n; i += blockDim.x) top = fmaxf(top, a.tops[slot(i)].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullWarp, top, o));
+  if (lane == 0) most[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, most[i]);
   const float from = top == -INFINITY ? 0.0f : top;
-  float sum[8] = {};  // elements lane * 2 + 64 i and the next
   float mass = 0.0f;
-#pragma unroll 4
-  for (int w = w0 + warp; w <= w1; w += 4) {
-    const int64_t p = slot(w);
-    const float2 t = a.tops[p];
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const float2 t = a.tops[slot(i)];
     const float f = ex2(t.x - from);
+    factors[i] = f;
     mass = fmaf(f, t.y, mass);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mass += __shfl_xor_sync(kFullWarp, mass, o);
+  if (lane == 0) masses[warp] = mass;
+  __syncthreads();
+  float sum[8] = {};  // elements lane * 2 + 64 i and the next
+#pragma unroll 8
+  for (int k = warp; k < n; k += kJoinWarps) {
+    const float* p = a.sums + slot(k) * a.dim + lane * 2;
+    const float f = factors[k];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (lane * 2 + 64 * i < a.dim) {
-        const float2 x = *reinterpret_cast<const float2*>(a.sums + p * a.dim + lane * 2 + 64 * i);
+      if (64 * i + lane * 2 < a.dim) {
+        const float2 x = *reinterpret_cast<const float2*>(p + 64 * i);
         sum[2 * i] = fmaf(f, x.x, sum[2 * i]), sum[2 * i + 1] = fmaf(f, x.y, sum[2 * i + 1]);
       }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     acc[warp][lane * 2 + 64 * i] = sum[2 * i], acc[warp][lane * 2 + 64 * i + 1] = sum[2 * i + 1];
-  if (lane == 0) masses[warp] = mass;
   __syncthreads();
-  mass = (masses[0] + masses[1]) + (masses[2] + masses[3]);
-  for (int i = threadIdx.x; i < a.dim; i += 128) {
-    const float x = (acc[0][i] + acc[1][i]) + (acc[2][i] + acc[3][i]);
+  mass = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) mass += masses[i];
+  for (int i = threadIdx.x; i < a.dim; i += blockDim.x) {
+    float x = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) x += acc[k][i];
     store_float(to, i, mass == 0.0f ? 0.0f : x / mass, a.dt);
   }
   if (lse != nullptr && threadIdx.x == 0)
@@ -873,7 +943,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 // weights[b, h, t] += the sum over a head's rows of 2^(x - lse): the scores once more, from
 // the keys alone.  A tile belongs to one warp, whatever the rows: no sum has two writers.
 template <class T>
-__global__ void __launch_bounds__(kMostTeamWarps * 32)
+__global__ void __launch_bounds__(kMostTeamWarps * 32, T::kResident)
     weights_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ __align__(128) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
@@ -1012,7 +1082,8 @@ cudaError_t attend_with(AttendArgs a, cudaStream_t stream) {
                    size_t(warps) * T::kStages * T::kStage, stream, a);
   if (e != cudaSuccess) return e;
   const int64_t rows = int64_t(a.batch) * a.heads * a.rows * a.shared;
-  e = launch_after(attend_join_kernel<T::kTile, T::kRows>, dim3(unsigned(rows)), dim3(128), 0,
+  e = launch_after(attend_join_kernel<T::kTile, T::kRows>, dim3(unsigned(rows)),
+                   dim3(kJoinWarps * 32), 0,
                    stream, a);
   if (e != cudaSuccess || a.weights == nullptr) return e;
   e = prepare_kernel<T>(weights_kernel<T>, warps, &blocks);

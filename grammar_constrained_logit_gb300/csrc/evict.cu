@@ -1,14 +1,14 @@
 // evict.cu -- a cache's sequences cut to their tokens of most attention weight, in place.
 //
 // Of a head's n > keep tokens stay the first ones, the last ones and the K = keep - first -
-// recent heaviest of those between.  The K-th largest weight is found digit by digit, eleven
+// recent heaviest of those between.  The K-th largest weight is found digit by digit, eight
 // bits of an order-preserving key at a time; what is above it stays, and of what equals it
 // the lowest ones.  The j-th kept token, at s(j) >= j, moves to place j.
 //
 // s(j') > j for every j < j': what is written for a token is never the source of a later one,
 // so loads may run ahead of stores as far as they like, and a store has to wait only for the
 // loads of its own round and those before it.  A round is what the blocks of a cluster hold
-// in registers; they meet at one barrier a round, with the next round's loads under way.
+// in shared memory; they meet at one barrier a round, with the next round's loads under way.
 #include <algorithm>
 
 #include "common.cuh"
@@ -17,13 +17,14 @@ namespace lp {
 namespace {
 
 constexpr int kMaxParts = 8;
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMoveThreads = 256;
-constexpr int kAtOnce = 4;       // pieces a thread holds of a round
-constexpr int kRoundTokens = 256;
+constexpr int kRoundBytes = 40 * 1024;  // of a block's round, two at once
+constexpr int kRoundTokens = kMoveThreads;  // a thread looks one up
 constexpr int kMostCluster = 8;
 constexpr int kSms = 152;
-constexpr int kBins = 2048;
+constexpr int kBins = 512;
 constexpr int kHeldTokens = 40 * 1024;  // weights that a block holds in shared memory
 
 struct EvictArgs {
@@ -60,17 +61,26 @@ __device__ __forceinline__ int cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(n));
   return int(n);
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_sync(int blocks) {
+  if (blocks == 1) {
+    __syncthreads();
+    return;
+  }
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A word of another block's shared memory, at the place of `p` in this one's.
-__device__ __forceinline__ int remote(const int* p, int rank) {
-  uint32_t at, v;
+// Words of another block's shared memory, at the place of `p` in this one's.
+__device__ __forceinline__ uint32_t remote_at(const void* p, int rank) {
+  uint32_t at;
   asm("mapa.shared::cluster.u32 %0, %1, %2;"
       : "=r"(at) : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(uint32_t(rank)));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return int(v);
+  return at;
+}
+__device__ __forceinline__ int2 remote2(const void* p, int rank) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y) : "r"(remote_at(p, rank)) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ int64_t place(const EvictArgs& a, int64_t slot, int64_t page_stride,
@@ -112,14 +122,39 @@ __device__ __forceinline__ int scan(int x, int* warps, int* all) {
   return before + incl - x;
 }
 
+// The sums over the warps before this one of each warp's (x, y), and over all: one barrier,
+// and one before it.
+__device__ __forceinline__ int2 warps_before(int2 x, int2* warps, int2* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  if (lane == 0) warps[warp] = x;
+  __syncthreads();
+  int2 v = lane < kWarps ? warps[lane] : make_int2(0, 0);
+  int2 incl = v;
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const int y = __shfl_up_sync(kFullWarp, incl.x, o), z = __shfl_up_sync(kFullWarp, incl.y, o);
+    if (lane >= o) incl.x += y, incl.y += z;
+  }
+  *all = make_int2(__shfl_sync(kFullWarp, incl.x, kWarps - 1),
+                   __shfl_sync(kFullWarp, incl.y, kWarps - 1));
+  return make_int2(__shfl_sync(kFullWarp, incl.x - v.x, warp),
+                   __shfl_sync(kFullWarp, incl.y - v.y, warp));
+}
+
 // Which tokens stay, and where the weights go: a cluster of blocks a sequence and head, each
 // with a slice of the weights in shared memory.
-__global__ void __launch_bounds__(kThreads) evict_slices_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kThreads, 2)
+    evict_slices_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ float held[];
-  __shared__ int bins[3][kBins], warps[2][kThreads / 32], found[2], counts[2];
+  __shared__ alignas(8) int bins[4][kBins];
+  __shared__ int2 warps[kWarps];
+  __shared__ alignas(8) int counts[2];
+  __shared__ int found[2];
   const int blocks = cluster_size(), rank = cluster_rank(), tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
   const int unit = blockIdx.x / blocks, b = unit / a.heads, h = unit - b * a.heads;
+  for (int i = tid; i < 4 * kBins; i += kThreads) bins[0][i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n = min(max(__ldg(a.lengths + b), 0), a.most);
@@ -132,90 +167,111 @@ __global__ void __launch_bounds__(kThreads) evict_slices_kernel(const __grid_con
   int32_t* source = a.source + (int64_t(b) * a.heads + h) * a.keep;
   const int lo = a.first, hi = n - a.recent;
   const int t0 = min(n, rank * a.slice), t1 = min(n, t0 + a.slice);  // this block's
-  for (int i = tid; i < 3 * kBins; i += kThreads) bins[0][i] = 0;
+#pragma unroll 4
   for (int i = tid; i < t1 - t0; i += kThreads) held[i] = w[t0 + i];
   __syncthreads();
   int want = a.keep - a.first - a.recent;  // of [lo, hi)
   const bool none = want == 0;
   uint32_t key = 0;  // of the want-th largest, as far as it is known
 #pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
+  for (int pass = 0; pass < 4; ++pass) {
     if (none) break;
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, digits = pass < 2 ? kBins : 1024;
-    for (int i = tid; i < t1 - t0; i += kThreads) {
-      const int t = t0 + i;
-      if (t < lo || t >= hi) continue;
-      const uint32_t k = weight_key(held[i]);
-      if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == (key >> (pass == 1 ? 21 : 10)))
-        atomicAdd(&bins[pass][(k >> shift) & (digits - 1)], 1);
+    // 9, 8, 8 and 7 bits: the first are sign and exponent
+    constexpr int kShift[4] = {23, 15, 7, 0}, kDigits[4] = {512, 256, 256, 128};
+    const int shift = kShift[pass], digits = kDigits[pass];
+#pragma unroll 4
+    for (int i0 = warp * 32; i0 < t1 - t0; i0 += kThreads) {
+      const int i = i0 + lane, t = t0 + i;
+      const uint32_t k = i < t1 - t0 ? weight_key(held[i]) : 0u;
+      const bool counts_here = i < t1 - t0 && t >= lo && t < hi &&
+                               (pass == 0 || (k >> kShift[max(0, pass - 1)]) ==
+                                                 (key >> kShift[max(0, pass - 1)]));
+      const uint32_t digit = (k >> shift) & (digits - 1);
+      if (pass == 0) {  // many of a warp's share an exponent: one addition for each
+        const uint32_t same = __match_any_sync(kFullWarp, counts_here ? digit : kBins);
+        if (counts_here && lane == __ffs(same) - 1) atomicAdd(&bins[pass][digit], __popc(same));
+      } else if (counts_here) {
+        atomicAdd(&bins[pass][digit], 1);
+      }
     }
-    cluster_sync();
+    cluster_sync(blocks);
     // this thread's two digits, the highest first, over all blocks
-    const int top = digits - 1 - 2 * tid;
-    int c0 = 0, c1 = 0;
-    if (top > 0)
-      for (int r = 0; r < blocks; ++r)
-        c0 += remote(&bins[pass][top], r), c1 += remote(&bins[pass][top - 1], r);
-    int incl = c0 + c1;
+    const int low = digits - 2 * (tid + 1);
+    int2 sum = make_int2(0, 0);
+    if (low >= 0) {
+      if (blocks == 1) {
+        sum = *reinterpret_cast<const int2*>(&bins[pass][low]);
+      } else {
+        int2 v[kMostCluster];
+#pragma unroll
+        for (int r = 0; r < kMostCluster; ++r)
+          v[r] = r < blocks ? remote2(&bins[pass][low], r) : make_int2(0, 0);
+#pragma unroll
+        for (int r = 0; r < kMostCluster; ++r) sum.x += v[r].x, sum.y += v[r].y;
+      }
+    }
+    int incl = sum.x + sum.y;
+    const int own = incl;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(kFullWarp, incl, o);
       if (lane >= o) incl += y;
     }
-    if (lane == 31) warps[0][warp] = incl;
-    __syncthreads();
-    int before = incl - c0 - c1;
-    for (int i = 0; i < warp; ++i) before += warps[0][i];
-    if (top > 0) {
-      if (before < want && want <= before + c0) found[0] = top, found[1] = before;
-      else if (before + c0 < want && want <= before + c0 + c1) found[0] = top - 1, found[1] = before + c0;
+    int2 all;
+    const int before = warps_before(make_int2(__shfl_sync(kFullWarp, incl, 31), 0), warps, &all).x +
+                       incl - own;
+    if (before < want && want <= before + own) {
+      const bool high = want <= before + sum.y;
+      found[0] = high ? low + 1 : low;
+      found[1] = high ? before : before + sum.y;
     }
     __syncthreads();
     key |= uint32_t(found[0]) << shift;
     want -= found[1];
   }
-  // A thread's run of tokens, in order: what stays for sure, and what equals the key
-  const int run = (t1 - t0 + kThreads - 1) / kThreads;
-  const int i0 = min(t1 - t0, tid * run), i1 = min(t1 - t0, i0 + run);
-  int sure = 0, equal = 0;
-  for (int i = i0; i < i1; ++i) {
+  // A warp's run of tokens, in order: what stays for sure, and what equals the key
+  const int run = ((t1 - t0 + kThreads - 1) / kThreads) * 32;
+  const int i0 = min(t1 - t0, warp * run), i1 = min(t1 - t0, i0 + run);
+  const auto kind = [&](int i) {  // 0: goes, 1: equals the key, 2: stays
+    if (i >= i1) return 0;
     const int t = t0 + i;
-    if (t < lo || t >= hi) {
-      ++sure;
-    } else if (!none) {
-      const uint32_t k = weight_key(held[i]);
-      sure += k > key, equal += k == key;
-    }
+    if (t < lo || t >= hi) return 2;
+    if (none) return 0;
+    const uint32_t k = weight_key(held[i]);
+    return k > key ? 2 : int(k == key);
+  };
+  int2 mine = make_int2(0, 0);
+#pragma unroll 4
+  for (int i = i0; i < i1; i += 32) {
+    const int x = kind(i + lane);
+    mine.x += __popc(__ballot_sync(kFullWarp, x == 2));
+    mine.y += __popc(__ballot_sync(kFullWarp, x == 1));
   }
-  int in_sure = sure, in_equal = equal;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFullWarp, in_sure, o), z = __shfl_up_sync(kFullWarp, in_equal, o);
-    if (lane >= o) in_sure += y, in_equal += z;
+  int2 all;
+  int2 at = warps_before(mine, warps, &all);
+  if (tid == 0) counts[0] = all.x, counts[1] = all.y;
+  cluster_sync(blocks);
+  for (int r = 0; r < rank; ++r) {
+    const int2 v = remote2(counts, r);
+    at.x += v.x, at.y += v.y;
   }
-  __syncthreads();
-  if (lane == 31) warps[0][warp] = in_sure, warps[1][warp] = in_equal;
-  __syncthreads();
-  int at_sure = in_sure - sure, at_equal = in_equal - equal;
-  for (int i = 0; i < warp; ++i) at_sure += warps[0][i], at_equal += warps[1][i];
-  if (tid == kThreads - 1) counts[0] = at_sure + sure, counts[1] = at_equal + equal;
-  cluster_sync();
-  for (int r = 0; r < rank; ++r) at_sure += remote(&counts[0], r), at_equal += remote(&counts[1], r);
   // every block has read its weights: they may be written
-  int j = at_sure + min(at_equal, want);
-  for (int i = i0; i < i1; ++i) {
-    const int t = t0 + i;
-    bool stays = t < lo || t >= hi;
-    if (!stays && !none) {
-      const uint32_t k = weight_key(held[i]);
-      stays = k > key || (k == key && at_equal < want);
-      at_equal += k == key;
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int i = i0; i < i1; i += 32) {
+    const int x = kind(i + lane);
+    const uint32_t sure = __ballot_sync(kFullWarp, x == 2), equal = __ballot_sync(kFullWarp, x == 1);
+    const int rank_equal = at.y + __popc(equal & below);
+    if (x == 2 || (x == 1 && rank_equal < want)) {
+      const int j = at.x + __popc(sure & below) + min(rank_equal, want);
+      source[j] = t0 + i + lane;
+      w[j] = held[i + lane];
     }
-    if (stays) source[j] = t, w[j] = held[i], ++j;
+    at.x += __popc(sure), at.y += __popc(equal);
   }
   for (int t = max(t0, left) + tid; t < t1; t += kThreads) w[t] = 0.0f;
   if (h == 0 && rank == 0 && tid == 0) a.new_lengths[b] = left;
-  cluster_sync();  // counts are read by others
+  cluster_sync(blocks);  // counts are read by others
 }
 
 // The same for sequences longer than a cluster's shared memory holds: a block each, going
@@ -279,115 +335,128 @@ struct alignas(16) Piece {
   uint32_t w[4];
 };
 
-__device__ __forceinline__ void load_piece(Piece& p, const char* from, int unit) {
-  if (unit == 16) p = *reinterpret_cast<const Piece*>(from);
-  else if (unit == 8) *reinterpret_cast<uint2*>(&p) = *reinterpret_cast<const uint2*>(from);
-  else if (unit == 4) p.w[0] = *reinterpret_cast<const uint32_t*>(from);
-  else if (unit == 2) p.w[0] = *reinterpret_cast<const uint16_t*>(from);
-  else p.w[0] = *reinterpret_cast<const uint8_t*>(from);
+template <typename T>
+__device__ __forceinline__ void copy_as(void* to, const void* from) {
+  *static_cast<T*>(to) = *static_cast<const T*>(from);
 }
 
-__device__ __forceinline__ void store_piece(const Piece& p, char* to, int unit) {
-  if (unit == 16) *reinterpret_cast<Piece*>(to) = p;
-  else if (unit == 8) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(&p);
-  else if (unit == 4) *reinterpret_cast<uint32_t*>(to) = p.w[0];
-  else if (unit == 2) *reinterpret_cast<uint16_t*>(to) = uint16_t(p.w[0]);
-  else *reinterpret_cast<uint8_t*>(to) = uint8_t(p.w[0]);
+__device__ __forceinline__ void copy_unit(void* to, const void* from, int unit) {
+  if (unit == 16) copy_as<Piece>(to, from);
+  else if (unit == 8) copy_as<uint2>(to, from);
+  else if (unit == 4) copy_as<uint32_t>(to, from);
+  else if (unit == 2) copy_as<uint16_t>(to, from);
+  else copy_as<uint8_t>(to, from);
 }
 
-// Moves codes and params: a cluster of blocks a sequence and head, in rounds.
-__global__ void __launch_bounds__(kMoveThreads, 3)
+// Into shared memory: started, and waited for later, where the unit allows it.
+__device__ __forceinline__ void fetch_unit(char* to, const char* from, int unit) {
+  const uint32_t at = uint32_t(__cvta_generic_to_shared(to));
+  if (unit == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  else if (unit == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
+  else if (unit == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(from) : "memory");
+  else copy_unit(to, from, unit);
+}
+
+// Moves codes and params: a cluster of blocks a sequence and head, in rounds.  A thread has
+// one piece of a token, of every `step`-th token: its strides and bases are worked out once,
+// and what it fetches it stores itself.
+__global__ void __launch_bounds__(kMoveThreads, 2)
     evict_move_kernel(const __grid_constant__ EvictArgs a) {
-  __shared__ int64_t from_slots[2][kRoundTokens], to_slots[2][kRoundTokens];
+  extern __shared__ __align__(16) char staged[];  // [2][round_tokens][pieces][16]
+  __shared__ int64_t from_slots[3][kRoundTokens], to_slots[3][kRoundTokens];
   const int blocks = cluster_size(), rank = cluster_rank();
   const int owner = blockIdx.x / blocks, b = owner / a.heads, h = owner - b * a.heads;
+  const int pieces = int(a.per_token.d), codes = a.code_bytes / a.code_unit;
+  const int per_part = pieces / a.n_parts;
+  const int step = kMoveThreads / pieces, first = int(a.per_token.quot(threadIdx.x));
+  int piece = threadIdx.x - first * pieces;
+  char* stage = staged + piece * 16;
+  const int part = piece / per_part;
+  piece -= part * per_part;
+  const lp_cache_part& p = a.part[part];
+  const bool is_code = piece < codes;
+  const int unit = is_code ? a.code_unit : a.param_unit;
+  const int64_t page_stride = is_code ? p.code_page_stride : p.param_page_stride;
+  const int64_t slot_stride = is_code ? p.code_slot_stride : p.param_slot_stride;
+  char* base = static_cast<char*>(is_code ? p.codes : p.params) +
+               h * (is_code ? p.code_head_stride : p.param_head_stride) +
+               (is_code ? piece : piece - codes) * unit;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n = min(max(__ldg(a.lengths + b), 0), a.most);
   if (n <= a.keep) return;  // for all of the cluster
   const int32_t* source = a.source + (int64_t(b) * a.heads + h) * a.keep;
-  const int codes = a.code_bytes / a.code_unit;
-  const int per_part = codes + a.param_bytes / a.param_unit;
-  const int rounds = (a.keep + a.round_tokens * blocks - 1) / (a.round_tokens * blocks);
+  const int per_round = a.round_tokens * blocks;
+  const int rounds = (a.keep + per_round - 1) / per_round;
 
-  const auto look = [&](int round) {  // the slots of a round's tokens
-    if (threadIdx.x < a.round_tokens && round < rounds) {
-      const int64_t j = (int64_t(round) * blocks + rank) * a.round_tokens + threadIdx.x;
-      int64_t from = -1, to = -1;
-      if (j < a.keep) {
-        const int s = source[j];
-        if (s != j) from = slot_of(a, b, s), to = slot_of(a, b, int(j));
+  // A round's tokens are looked up two rounds ahead, in three steps that wait for one another
+  // only where there is other work between: the source, its block, its slot.
+  const auto place_of = [&](int round) {
+    return (int64_t(round) * blocks + rank) * a.round_tokens + threadIdx.x;
+  };
+  const auto source_of = [&](int round) {
+    const int64_t j = place_of(round);
+    return threadIdx.x < a.round_tokens && round < rounds && j < a.keep ? source[j] : -1;
+  };
+  const auto block_id = [&](int t) {
+    return t < 0 ? -1
+                 : __ldg(a.blocks + int64_t(b) * a.blocks_stride + a.per_block.quot(uint32_t(t)));
+  };
+  const auto slot_in = [&](int id, int t) {
+    const int64_t slot = int64_t(id) * a.block +
+                         (t - int64_t(a.per_block.quot(uint32_t(t))) * a.block);
+    return t >= 0 && slot >= 0 && slot < a.n_slots ? slot : int64_t(-1);
+  };
+  const auto put = [&](int round, int s, int from_id, int to_id) {
+    if (threadIdx.x >= a.round_tokens || round >= rounds) return;
+    const int j = s < 0 || place_of(round) == s ? -1 : int(place_of(round));
+    const int64_t from = slot_in(from_id, j < 0 ? -1 : s), to = slot_in(to_id, j);
+    from_slots[round % 3][threadIdx.x] = to < 0 ? -1 : from;
+    to_slots[round % 3][threadIdx.x] = to;
+  };
+  const auto fetch = [&](int round) {
+    if (round < rounds && first < step)
+#pragma unroll 2
+      for (int i = first; i < a.round_tokens; i += step) {
+        const int64_t from = from_slots[round % 3][i];
+        if (from >= 0)
+          fetch_unit(stage + ((round & 1) * a.round_tokens + i) * pieces * 16,
+                     base + place(a, from, page_stride, slot_stride), unit);
       }
-      if (from < 0 || to < 0) from = to = -1;
-      from_slots[round & 1][threadIdx.x] = from;
-      to_slots[round & 1][threadIdx.x] = to;
-    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  struct Round {
-    Piece held[kAtOnce];
-    char* to[kAtOnce];
-    int unit[kAtOnce];
-  };
-  const auto load = [&](int round, Round& x) {
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      x.to[u] = nullptr;
-      x.unit[u] = 0;
-      if (round >= rounds) continue;
-      const int i = u * kMoveThreads + threadIdx.x;
-      const int token = int(a.per_token.quot(uint32_t(i)));
-      if (token >= a.round_tokens) continue;
-      const int64_t from = from_slots[round & 1][token], to = to_slots[round & 1][token];
-      if (from < 0) continue;
-      int piece = i - token * int(a.per_token.d), part = 0;
-      while (piece >= per_part) piece -= per_part, ++part;
-      const lp_cache_part& p = a.part[part];
-      const bool is_code = piece < codes;
-      const int64_t page_stride = is_code ? p.code_page_stride : p.param_page_stride;
-      const int64_t slot_stride = is_code ? p.code_slot_stride : p.param_slot_stride;
-      char* base = static_cast<char*>(is_code ? p.codes : p.params) +
-                   h * (is_code ? p.code_head_stride : p.param_head_stride) +
-                   (is_code ? piece * a.code_unit : (piece - codes) * a.param_unit);
-      x.unit[u] = is_code ? a.code_unit : a.param_unit;
-      x.to[u] = base + place(a, to, page_stride, slot_stride);
-      load_piece(x.held[u], base + place(a, from, page_stride, slot_stride), x.unit[u]);
-    }
-  };
-  const auto store = [&](const Round& x) {
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u)
-      if (x.to[u] != nullptr) store_piece(x.held[u], x.to[u], x.unit[u]);
-  };
-  const auto landed = [&](Round& x) {  // the loads' values are here
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u)
-      asm volatile("" : "+r"(x.held[u].w[0]), "+r"(x.held[u].w[1]), "+r"(x.held[u].w[2]),
-                        "+r"(x.held[u].w[3]) :: "memory");
+  const auto store = [&](int round) {
+    if (first < step)
+#pragma unroll 2
+      for (int i = first; i < a.round_tokens; i += step)
+        if (from_slots[round % 3][i] >= 0)
+          copy_unit(base + place(a, to_slots[round % 3][i], page_stride, slot_stride),
+                    stage + ((round & 1) * a.round_tokens + i) * pieces * 16, unit);
   };
 
-  Round x, y;
-#pragma unroll
-  for (int u = 0; u < kAtOnce; ++u)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x.held[u].w[e] = y.held[u].w[e] = 0;
-  look(0);
+  for (int round = 0; round < 2; ++round) {
+    const int s = source_of(round);
+    put(round, s, block_id(s), block_id(s < 0 ? -1 : int(place_of(round))));
+  }
   __syncthreads();
-  load(0, x);
-  look(1);
-  for (int round = 0; round < rounds; round += 2) {
-    __syncthreads();
-    load(round + 1, y);
-    landed(x);
-    cluster_sync();
-    look(round + 2);
-    store(x);
-    if (round + 1 >= rounds) break;
-    __syncthreads();
-    load(round + 2, x);
-    landed(y);
-    cluster_sync();
-    look(round + 3);
-    store(y);
+  fetch(0);
+  int ahead = source_of(2);
+  for (int round = 0; round < rounds; ++round) {
+    fetch(round + 1);
+    const int from_id = block_id(ahead), to_id = block_id(ahead < 0 ? -1 : int(place_of(round + 2)));
+    const int after = source_of(round + 3);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if (blocks == 1) {
+      __syncthreads();  // this round's sources are read, by all
+    } else {
+      // nothing was written that the others wait for: the loads are done, and that is all
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    store(round);
+    put(round + 2, ahead, from_id, to_id);
+    ahead = after;
+    __syncthreads();  // the slots of two rounds from here are there
   }
 }
 
@@ -423,11 +492,11 @@ __global__ void __launch_bounds__(kMoveThreads)
                      (is_code ? int64_t(e) * a.code_unit : int64_t(e - codes) * a.param_unit);
         unit = is_code ? a.code_unit : a.param_unit;
         to = base + place(a, to_slot, page_stride, slot_stride);
-        load_piece(held, base + place(a, from_slot, page_stride, slot_stride), unit);
+        copy_unit(&held, base + place(a, from_slot, page_stride, slot_stride), unit);
       }
     }
     __syncthreads();
-    if (to != nullptr) store_piece(held, to, unit);
+    if (to != nullptr) copy_unit(to, &held, unit);
     __syncthreads();
   }
 }
@@ -471,16 +540,18 @@ cudaError_t launch(EvictArgs a, cudaStream_t stream) {
     return e;
   const int64_t pieces = int64_t(a.n_parts) *
                          (a.code_bytes / a.code_unit + a.param_bytes / a.param_unit);
-  if (pieces > kMoveThreads * kAtOnce || units > INT32_MAX / kMostCluster)
+  if (pieces > kMoveThreads || units > INT32_MAX / kMostCluster)
     return launch_kernel(evict_move_wide_kernel, dim3(unsigned(units)), dim3(kMoveThreads), 0,
                          stream, a);
   a.per_token.set(uint32_t(pieces));
-  a.round_tokens = int(std::min<int64_t>(kRoundTokens, kMoveThreads * kAtOnce / pieces));
+  a.round_tokens = int(std::min<int64_t>({kRoundTokens, kRoundBytes / (pieces * 16), a.keep}));
   int blocks = 1;
-  while (blocks < kMostCluster && units * blocks * 2 <= 3 * kSms &&
-         a.keep > a.round_tokens * blocks)
-    blocks *= 2;
-  return launch_cluster(evict_move_kernel, units, blocks, kMoveThreads, 0, stream, a);
+  while (blocks < kMostCluster && units * blocks * 2 <= 2 * kSms && a.keep > 64 * blocks) blocks *= 2;
+  a.round_tokens = std::min(a.round_tokens, (a.keep + blocks - 1) / blocks);
+  const size_t smem = size_t(2) * a.round_tokens * pieces * 16;
+  e = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  return launch_cluster(evict_move_kernel, units, blocks, kMoveThreads, smem, stream, a);
 }
 
 bool fits(int64_t a, int64_t b, int64_t most) { return b == 0 || a <= most / b; }

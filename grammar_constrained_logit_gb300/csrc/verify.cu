@@ -9,9 +9,13 @@
 // each chunk of 2 KB; the second, a cluster of blocks a slot, joins those to (M, S), decides the
 // slot's acceptances, and goes through the one row that says a token.
 //
-// There a token that cannot win is told by its noise word alone: log r + g > best means
-// -log u < r exp(-best), and 1 - u <= -log u, so where 1 - u is not below that (with a margin
-// for its roundings) neither logarithm is taken.
+// log r + g is largest where r / t is, t = -log u > 0.  With m = 1 - u that ratio lies between
+// r / (m / (1 - m)) and r / (m + m^2 / 2): a token whose upper bound is below a lower bound
+// that its block has found is done with, without a logarithm.  Of the others a thread keeps
+// its best, by the upper bound, and the second's bound; the best ones are then scored as
+// defined.  Should a second one still reach the winner (once in some thousand slots), or
+// nothing be left of p - q, the slot's first block goes through the row once more, token by
+// token as defined.
 #include <algorithm>
 
 #include "common.cuh"
@@ -22,9 +26,9 @@ namespace {
 constexpr int kStreamThreads = 256;
 constexpr int kVecs = 4;                    // 16-byte vectors a lane has of a chunk
 constexpr int kChunkVecs = kVecs * 32;
-constexpr int kThreads = 512;               // of a block of the second kernel
+constexpr int kThreads = 256;               // of a block of the second kernel
 constexpr int kWarps = kThreads / 32;
-constexpr int kMostRows = 256;              // of a slot
+constexpr int kMostRows = 256;              // of a slot: a thread has a draft at most
 constexpr int kMostCluster = 8;
 constexpr int kSms = 152;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -94,17 +98,60 @@ struct RowVecs {
     V = a.V;
   }
   __device__ __forceinline__ int64_t count() const {
-    return (int64_t(before) + V + kPer - 1) / kPer;
+    return V == 0 ? 0 : (int64_t(before) + V + kPer - 1) / kPer;
   }
   __device__ __forceinline__ int first_token(int64_t q) const { return int(q * kPer - before); }
   // Bits of the vector's tokens that are candidates, as far as the mask goes.
   __device__ __forceinline__ uint32_t bits(int64_t q) const {
     const int j = first_token(q), lo = max(0, -j), n = min(kPer, V - j);
     uint32_t keep = ((1u << n) - 1u) & ~((1u << lo) - 1u);
-    if (mask != nullptr) keep &= mask_bits(mask, j + lo, kPer - lo, V) << lo;
+    if (mask != nullptr) {
+      // aligned rows: a vector's bits lie within a word
+      if (before == 0) keep &= __ldg(mask + (j >> 5)) >> (j & 31);
+      else keep &= mask_bits(mask, j + lo, kPer - lo, V) << lo;
+    }
     return keep;
   }
 };
+
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  return uint64_t(__float_as_uint(a)) | uint64_t(__float_as_uint(b)) << 32;
+}
+__device__ __forceinline__ float low_of(uint64_t v) { return __uint_as_float(uint32_t(v)); }
+__device__ __forceinline__ float high_of(uint64_t v) { return __uint_as_float(uint32_t(v >> 32)); }
+__device__ __forceinline__ uint64_t add_pairs(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_pairs(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Bytes of x by `sel`'s digits; 8 more than a byte's number is its highest bit, eight times.
+__device__ __forceinline__ uint32_t bytes_by(uint32_t x, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "r"(sel));
+  return r;
+}
+
+// -inf in the places whose bit is clear.  Four bits times 0x10204080 are the highest bits of
+// four bytes, and a byte permutation spreads those over two 16-bit places at a time.
+template <int DT>
+__device__ __forceinline__ uint4 only(const uint4& v, uint32_t keep) {
+  if (DT == LP_F32) return Elt<DT>::blend(v, keep, 0xff800000u);
+  const uint32_t fill = DT == LP_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+  const uint32_t lo = (keep & 15u) * 0x10204080u, hi = (keep >> 4) * 0x10204080u;
+  uint4 r;
+  uint32_t m;
+  m = bytes_by(lo, 0x9988), r.x = (v.x & m) | (fill & ~m);
+  m = bytes_by(lo, 0xbbaa), r.y = (v.y & m) | (fill & ~m);
+  m = bytes_by(hi, 0x9988), r.z = (v.z & m) | (fill & ~m);
+  m = bytes_by(hi, 0xbbaa), r.w = (v.w & m) | (fill & ~m);
+  return r;
+}
 
 // A warp a chunk.
 template <int DT>
@@ -118,6 +165,7 @@ __global__ void __launch_bounds__(kStreamThreads)
        i += int64_t(gridDim.x) * (kStreamThreads / 32)) {
     const int64_t row = i / a.chunks;
     const int chunk = int(i - row * a.chunks);
+    const float rate = rate_of(heat_of(a, int(row / a.per_slot)));
     const RowVecs<DT> x(a, row);
     const int64_t vecs = x.count();
     uint4 raw[kVecs];
@@ -127,28 +175,45 @@ __global__ void __launch_bounds__(kStreamThreads)
       const int64_t q = int64_t(chunk) * kChunkVecs + u * 32 + lane;
       keep[u] = 0;
       raw[u] = make_uint4(0, 0, 0, 0);
-      if (q < vecs) {
-        raw[u] = __ldg(reinterpret_cast<const uint4*>(x.at) + q);
-        keep[u] = x.bits(q);
-      }
+      if (q < vecs) raw[u] = __ldg(reinterpret_cast<const uint4*>(x.at) + q);
     }
-    const float rate = rate_of(heat_of(a, int(row / a.per_slot)));
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int64_t q = int64_t(chunk) * kChunkVecs + u * 32 + lane;
+      if (q < vecs) keep[u] = x.bits(q);
+    }
+    // what is no candidate becomes -inf
     float top = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) top = fmaxf(top, VecMax<DT>::run(raw[u], keep[u]));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullWarp, top, o));
+    for (int u = 0; u < kVecs; ++u) {
+      raw[u] = only<DT>(raw[u], keep[u]);
+      top = fmaxf(top, VecMax<DT>::run(raw[u], (1u << RowVecs<DT>::kPer) - 1u));
+    }
+    top = key_float(__reduce_max_sync(kFullWarp, fkey(top)));
     float sum = 0.0f;
     if (top > -INFINITY) {
+      const uint64_t less = pair_of(-top, -top), by = pair_of(rate, rate);
+      uint64_t sums = 0;
 #pragma unroll
       for (int u = 0; u < kVecs; ++u)
 #pragma unroll
-        for (int e = 0; e < RowVecs<DT>::kPer; ++e) {
-          const float y = Elt<DT>::get(raw[u], e);
-          const float t = (top == INFINITY ? relative(y, top) : y - top) * rate;
-          // NaN is no candidate: a maximum takes the other side
-          sum += ex2((keep[u] >> e) & 1u ? fmaxf(t, -200.0f) : -200.0f);
+        for (int e = 0; e < RowVecs<DT>::kPer; e += 2) {
+          const uint64_t t = mul_pairs(add_pairs(pair_of(Elt<DT>::get(raw[u], e),
+                                                         Elt<DT>::get(raw[u], e + 1)), less), by);
+          sums = add_pairs(sums, pair_of(ex2(low_of(t)), ex2(high_of(t))));
         }
+      sum = low_of(sums) + high_of(sums);
+      if (__any_sync(kFullWarp, !(sum < INFINITY))) {
+        // NaN among the logits, which are no candidates, or a largest of +inf
+        sum = 0.0f;
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u)
+#pragma unroll
+          for (int e = 0; e < RowVecs<DT>::kPer; ++e) {
+            const float y = Elt<DT>::get(raw[u], e);
+            if (y > -INFINITY) sum += ex2(relative(y, top) * rate);
+          }
+      }
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
     }
@@ -172,32 +237,15 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 struct Found {
-  float score;
+  float score;  // as defined; of what r is measured in, less `shift`
   int token;
+  float second;  // the largest upper bound of what was not scored
+  int pad;
 };
 
-// The best of all the cluster's threads, in every thread.
-__device__ __forceinline__ Found cluster_best(Found f, Found* warps, Found* mine) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-    best_of(f.score, f.token, __shfl_xor_sync(kFullWarp, f.score, o),
-            __shfl_xor_sync(kFullWarp, f.token, o));
-  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = f;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kWarps; ++i) best_of(f.score, f.token, warps[i].score, warps[i].token);
-    *mine = f;
-  }
-  cluster_sync();
-  const uint32_t at = uint32_t(__cvta_generic_to_shared(mine));
-  f.score = -INFINITY, f.token = INT32_MAX;
-  for (uint32_t r = 0; r < cluster_size(); ++r) {
-    uint32_t remote, s, t;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(r));
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(s), "=r"(t) : "r"(remote) : "memory");
-    best_of(f.score, f.token, __uint_as_float(s), int(t));
-  }
-  cluster_sync();  // nobody leaves, or writes the next one, before all have read
+__device__ __forceinline__ Found join(Found f, const Found& g) {
+  best_of(f.score, f.token, g.score, g.token);
+  f.second = fmaxf(f.second, g.second);
   return f;
 }
 
@@ -206,27 +254,141 @@ __device__ __forceinline__ float logit_at(const char* x, int v) {
   return Elt<DT>::load1(x + int64_t(v) * Elt<DT>::kBytes);
 }
 
+// The row that says a token.
+struct Row {
+  const char* x;
+  const uint32_t* mask;
+  const float* q;  // what the draft's probabilities are, or NULL
+  int64_t draft;   // NULL: all on this token, if there is one
+  float top, sum, heat, rate, shift;
+  uint2 key;
+  uint32_t row, offset_lo, offset_hi;
+};
+
+// log r + g as defined, or -inf.
+__device__ __forceinline__ float score_of(const Row& w, bool rest, float y, float d, uint32_t word) {
+  if (!(y > -INFINITY)) return -INFINITY;
+  if (!rest) return __fdiv_rn(y, w.heat) + gumbel_from_word(word);
+  const float r = expf(__fdiv_rn(relative(y, w.top), w.heat)) / w.sum - d;
+  return r > 0.0f ? logf(r) + gumbel_from_word(word) : -INFINITY;
+}
+
+template <int N>
+struct Group {  // N tokens
+  float y[N], d[N];
+  uint32_t keep;
+};
+
+// Tokens v0 .. v0 + 7, v0 a multiple of 8.
+template <int DT>
+__device__ __forceinline__ void load_group(Group<8>& g, const Row& w, uint32_t v0, uint32_t V,
+                                           bool whole, bool whole_q) {
+  const uint32_t m = v0 < V ? min(8u, V - v0) : 0u;
+  g.keep = (1u << m) - 1u;
+  if (w.mask != nullptr && m > 0) g.keep &= __ldg(w.mask + (v0 >> 5)) >> (v0 & 31);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) g.y[e] = -INFINITY, g.d[e] = 0.0f;
+  if (g.keep == 0) return;
+  if (whole && m == 8) {
+    uint4 v[2];
+    const uint4* p = reinterpret_cast<const uint4*>(w.x + int64_t(v0) * Elt<DT>::kBytes);
+    v[0] = __ldg(p);
+    if (DT == LP_F32) v[1] = __ldg(p + 1);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      g.y[e] = Elt<DT>::get(v[e / Elt<DT>::kPerVec], e % Elt<DT>::kPerVec);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < int(m)) g.y[e] = logit_at<DT>(w.x, int(v0) + e);
+  }
+  if (w.q == nullptr) return;
+  if (whole_q && m == 8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(w.q + v0) + i);
+      g.d[4 * i] = v.x, g.d[4 * i + 1] = v.y, g.d[4 * i + 2] = v.z, g.d[4 * i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < int(m)) g.d[e] = __ldg(w.q + v0 + e);
+  }
+}
+
+__device__ __forceinline__ uint4 noise(const Row& w, uint32_t v) {
+  return philox4x32_10(make_uint4(v >> 2, w.row, w.offset_lo, w.offset_hi), w.key);
+}
+
+// The best of a block's threads, in every thread; two barriers.
+__device__ __forceinline__ Found block_best(Found f, Found* warps) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    Found g;
+    g.score = __shfl_xor_sync(kFullWarp, f.score, o);
+    g.token = __shfl_xor_sync(kFullWarp, f.token, o);
+    g.second = __shfl_xor_sync(kFullWarp, f.second, o);
+    f = join(f, g);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = f;
+  __syncthreads();
+  f = warps[0];
+#pragma unroll
+  for (int i = 1; i < kWarps; ++i) f = join(f, warps[i]);
+  return f;
+}
+
+// The whole row as defined, by one block.
+template <int DT>
+__device__ __noinline__ Found every_token(Row w, bool rest, int V, Found* warps) {
+  Found f = {-INFINITY, INT32_MAX, 0.0f, 0};
+  for (int64_t v = threadIdx.x; v < V; v += kThreads) {
+    if (!kept(w.mask, int(v))) continue;
+    const float d = !rest ? 0.0f : w.q != nullptr ? w.q[v] : v == w.draft ? 1.0f : 0.0f;
+    const float score = score_of(w, rest, logit_at<DT>(w.x, int(v)), d,
+                                 word_of(noise(w, uint32_t(v)), int(v & 3)));
+    if (score > -INFINITY) best_of(f.score, f.token, score, int(v));
+  }
+  return block_best(f, warps);
+}
+
 // A cluster of blocks a slot.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) verify_say_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) verify_say_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ float tops[kMostRows], sums[kMostRows];
   __shared__ int firsts[kMostRows];  // greedy: the lowest-index largest
   __shared__ Found warps[kWarps];
-  __shared__ alignas(8) Found mine;
+  __shared__ alignas(16) Found founds[kMostCluster];
   __shared__ int count, there;
+  __shared__ uint32_t reached;  // a lower bound of the block's best r / t
   const int blocks = int(cluster_size()), rank = int(cluster_rank());
   const int slot = blockIdx.x / blocks, R = a.per_slot, tid = threadIdx.x, lane = tid & 31;
-  if (tid == 0) count = there = R - 1;
+  if (tid == 0) count = there = R - 1, reached = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const float heat = heat_of(a, slot);
   const bool greedy = !(heat > 0.0f);
   const float rate = rate_of(heat);
   const int64_t* drafts = a.drafts + int64_t(slot) * (R - 1);
+  // a thread's draft, its logit and its probability, under way while the rows are joined
+  int64_t draft = -1;
+  float draft_x = -INFINITY, draft_q = 1.0f, draft_u = 0.0f;
+  if (tid < R - 1) {
+    draft = drafts[tid];
+    if (draft >= 0 && draft < a.V) {
+      const int64_t row = int64_t(slot) * R + tid;
+      if (kept(mask_of(a, row), int(draft)))
+        draft_x = logit_at<DT>(a.logits + row * a.stride, int(draft));
+      if (a.probs != nullptr) draft_q = a.probs[slot * a.probs_slot + tid * a.probs_row + draft];
+      draft_u = a.uniforms[int64_t(slot) * (R - 1) + tid];
+    }
+  }
   for (int i = tid >> 5; i < R; i += kWarps) {
     const int64_t row = int64_t(slot) * R + i;
     const float2* part = a.part + row * a.chunks;
     float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
     for (int c = lane; c < a.chunks; c += 32) {
       const float2 p = part[c];
       const float now = fmaxf(top, p.x);
@@ -234,9 +396,7 @@ __global__ void __launch_bounds__(kThreads) verify_say_kernel(const __grid_const
         sum = sum * ex2(relative(top, now) * rate) + p.y * ex2(relative(p.x, now) * rate);
       top = now;
     }
-    float all = top;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) all = fmaxf(all, __shfl_xor_sync(kFullWarp, all, o));
+    const float all = key_float(__reduce_max_sync(kFullWarp, fkey(top)));
     sum = top > -INFINITY ? sum * ex2(relative(top, all) * rate) : 0.0f;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
@@ -263,109 +423,119 @@ __global__ void __launch_bounds__(kThreads) verify_say_kernel(const __grid_const
     if (lane == 0) tops[i] = all, sums[i] = sum, firsts[i] = first;
   }
   __syncthreads();
-  for (int i = tid; i < R - 1; i += kThreads) {
-    const int64_t v = drafts[i];
+  if (tid < R - 1) {
     bool taken = false;
-    if (v < 0 || v >= a.V) {
-      atomicMin(&there, i);
-    } else {
-      const int64_t row = int64_t(slot) * R + i;
-      double p = 0.0;
-      if (greedy) {
-        p = v == firsts[i] ? 1.0 : 0.0;
-      } else if (kept(mask_of(a, row), int(v))) {
-        const float x = logit_at<DT>(a.logits + row * a.stride, int(v));
-        if (x > -INFINITY) p = exp(double(relative(x, tops[i])) / double(heat)) / double(sums[i]);
-      }
-      const double q = a.probs != nullptr
-                           ? double(a.probs[slot * a.probs_slot + i * a.probs_row + v]) : 1.0;
-      taken = double(a.uniforms[int64_t(slot) * (R - 1) + i]) * q < p;
+    if (draft < 0 || draft >= a.V) {
+      atomicMin(&there, tid);
+    } else if (greedy) {
+      taken = draft == firsts[tid] && draft_u * draft_q < 1.0f;
+    } else if (draft_x > -INFINITY) {
+      // exp(d / T) with the quotient's rounding taken back: an acceptance hangs on p's last
+      // places
+      const float d = relative(draft_x, tops[tid]), quot = __fdiv_rn(d, heat);
+      const float over = d > -INFINITY && quot > -INFINITY ? fmaf(-quot, heat, d) / heat : 0.0f;
+      const float e = expf(quot), p = fmaf(e, over, e);
+      taken = draft_u * draft_q * sums[tid] < p;
     }
-    if (!taken) atomicMin(&count, i);
+    if (!taken) atomicMin(&count, tid);
   }
   __syncthreads();
   const int n = count;
   const int64_t row = int64_t(slot) * R + n;
-  const float top = tops[n], sum = sums[n];
+  const float top = tops[n];
   const bool refused = n < there;
   int token = firsts[n];
   if (!greedy && top > -INFINITY) {
-    const uint32_t* mask = mask_of(a, row);
-    const char* x = a.logits + row * a.stride;
-    const float* q = refused && a.probs != nullptr
-                         ? a.probs + slot * a.probs_slot + n * a.probs_row : nullptr;
-    const int64_t draft = refused ? drafts[n] : -1;
+    Row w;
+    w.x = a.logits + row * a.stride;
+    w.mask = mask_of(a, row);
+    w.q = refused && a.probs != nullptr ? a.probs + slot * a.probs_slot + n * a.probs_row : nullptr;
+    w.draft = refused ? drafts[n] : -1;
+    w.top = top, w.sum = sums[n], w.heat = heat, w.rate = rate;
+    w.shift = refused ? 0.0f : __fdiv_rn(top, heat);
     const uint64_t seed = a.seeds != nullptr ? a.seeds[row] : a.seed;
-    const uint2 key = make_uint2(uint32_t(seed), uint32_t(seed >> 32));
-    const bool whole = (reinterpret_cast<uintptr_t>(x) % (4 * Elt<DT>::kBytes)) == 0;
-    const bool whole_q = q != nullptr && reinterpret_cast<uintptr_t>(q) % 16 == 0;
-    const float inv = 1.0f / sum;
-    const float shift = __fdiv_rn(top, heat);
-    for (int rest = refused; rest >= 0; --rest) {  // the second time where nothing was left
-      Found f = {-INFINITY, INT32_MAX};
-      float bound = 3e38f;  // exp(-best), of what r is measured in
-      const int step = blocks * kThreads * 4;
-      for (int v4 = (rank * kThreads + tid) * 4; v4 < a.V; v4 += step) {
-        const int m = min(4, a.V - v4);
-        uint32_t keep = (1u << m) - 1u;
-        if (mask != nullptr) keep &= __ldg(mask + (v4 >> 5)) >> (v4 & 31);
-        if (keep != 0) {
-          float y[4], d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (whole && m == 4) {
-            if (DT == LP_F32) {
-              const float4 w = __ldg(reinterpret_cast<const float4*>(x) + v4 / 4);
-              y[0] = w.x, y[1] = w.y, y[2] = w.z, y[3] = w.w;
-            } else {
-              const uint2 w = __ldg(reinterpret_cast<const uint2*>(x) + v4 / 4);
-              const uint4 w4 = make_uint4(w.x, w.y, 0, 0);
+    w.key = make_uint2(uint32_t(seed), uint32_t(seed >> 32));
+    w.row = uint32_t(row), w.offset_lo = uint32_t(a.offset), w.offset_hi = uint32_t(a.offset >> 32);
+    const bool whole = reinterpret_cast<uintptr_t>(w.x) % 16 == 0;
+    const bool whole_q = w.q != nullptr && reinterpret_cast<uintptr_t>(w.q) % 16 == 0;
+    const float by = refused ? 1.0f / w.sum : 1.0f;
+    // what rounding in the score as defined may make up for; nothing is passed over where the
+    // scores are so large that it is much, or where the largest is +inf
+    const float slack = fmaxf(0.0f, 0.999f - fabsf(w.shift) * 1e-6f);
+    const float keen = slack > 0.5f ? slack : 0.0f;
+
+    float best = -1.0f, second = -1.0f, best_y = -INFINITY, best_d = 0.0f;
+    uint32_t best_word = 0;
+    int best_v = INT32_MAX;
+    const uint32_t V = uint32_t(a.V), step = uint32_t(blocks) * kThreads * 8;
+    uint32_t v0 = uint32_t(rank * kThreads + tid) * 8;
+    Group<8> g;
+    load_group<DT>(g, w, v0, V, whole, whole_q);
+    while (v0 < V) {
+      Group<8> next;
+      next.keep = 0;
+      load_group<DT>(next, w, v0 + step < V ? v0 + step : V, V, whole, whole_q);
+      const float bound = __uint_as_float(*static_cast<volatile uint32_t*>(&reached)) * keen;
+      float r[8];
+      uint32_t live = 0;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = Elt<DT>::get(w4, e);
-            }
-          } else {
+      for (int e = 0; e < 8; ++e) {
+        if (w.q == nullptr && int64_t(v0) + e == w.draft) g.d[e] = 1.0f;
+        // p is within 1e-5 of itself: r is this, or less
+        r[e] = fmaf(ex2(relative(g.y[e], top) * rate) * by, 1.00002f, -g.d[e]);
+        // (m is 2^-24 at least)
+        live |= uint32_t(r[e] > 0.0f && r[e] >= bound * 5.9e-8f) << e;
+      }
+      live &= g.keep;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = e < m ? logit_at<DT>(x, v4 + e) : -INFINITY;
-          }
-          if (rest && q != nullptr) {
-            if (whole_q && m == 4) {
-              const float4 w = __ldg(reinterpret_cast<const float4*>(q) + v4 / 4);
-              d[0] = w.x, d[1] = w.y, d[2] = w.z, d[3] = w.w;
-            } else {
+      for (int half = 0; half < 2; ++half) {
+        if (((live >> (4 * half)) & 15u) == 0) continue;
+        const uint4 words = noise(w, v0 + 4 * half);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) d[e] = e < m ? __ldg(q + v4 + e) : 0.0f;
-            }
-          } else if (rest) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] = v4 + e == draft ? 1.0f : 0.0f;
-          }
-          const uint4 w = philox4x32_10(make_uint4(uint32_t(v4) >> 2, uint32_t(row),
-                                                   uint32_t(a.offset), uint32_t(a.offset >> 32)), key);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (!((keep >> e) & 1u) || !(y[e] > -INFINITY)) continue;
-            const uint32_t word = word_of(w, e);
-            const float p = ex2(relative(y[e], top) * rate) * (rest ? inv : 1.0f);
-            const float missing = (float(~word >> 9) + 0.5f) * 1.1920928955078125e-07f;  // 1 - u
-            // p is within 1e-5 of itself, whatever is left of p - d
-            if (!(missing < fmaf(p, 1.00002f, -d[e]) * bound * 1.001f)) continue;
-            float score;
-            if (rest) {
-              const float r = expf(__fdiv_rn(relative(y[e], top), heat)) / sum - d[e];
-              if (!(r > 0.0f)) continue;
-              score = logf(r);
-            } else {
-              score = __fdiv_rn(y[e], heat);
-            }
-            best_of(f.score, f.token, score + gumbel_from_word(word), v4 + e);
-            if (fabsf(shift) < 1024.0f) bound = fminf(expf((rest ? 0.0f : shift) - f.score), 3e38f);
+        for (int i = 0; i < 4; ++i) {
+          const int e = 4 * half + i;
+          const uint32_t word = word_of(words, i);
+          const float m = fmaf(float(~word >> 9), 1.1920928955078125e-07f, 5.9604644775390625e-08f);
+          const float least = fmaf(m * 0.5f, m, m);  // t is this, or more
+          if (!((live >> e) & 1u) || r[e] < bound * least) continue;
+          const float s = __fdividef(r[e], least) * 1.00001f;
+          second = fmaxf(second, fminf(s, best));
+          if (s > best) {
+            best = s, best_v = int(v0) + e, best_y = g.y[e], best_d = g.d[e], best_word = word;
+            // t is m / (1 - m) at most, and r no less than p 1e-4 below
+            const float low = fmaf(r[e] + g.d[e], -1e-4f, r[e]) * (1.0f - m) * 0.9999f;
+            if (low > 0.0f && m < 1.0f)
+              atomicMax(&reached, __float_as_uint(fminf(__fdividef(low, m), 1e30f)));
           }
         }
-        // what the warp has found holds for all of its lanes
-        bound = __uint_as_float(__reduce_min_sync(__activemask(), __float_as_uint(bound)));
       }
-      f = cluster_best(f, warps, &mine);
-      token = f.token;
-      if (token != INT32_MAX) break;
+      g = next;
+      v0 += step;
     }
+    Found f = {-INFINITY, INT32_MAX, second, 0};
+    if (best_v != INT32_MAX) {
+      f.score = score_of(w, refused, best_y, best_d, best_word);
+      if (f.score > -INFINITY) f.token = best_v;
+    }
+    f = block_best(f, warps);
+    if (tid == 0) {
+      uint32_t at;
+      asm("mapa.shared::cluster.u32 %0, %1, 0;"
+          : "=r"(at) : "r"(uint32_t(__cvta_generic_to_shared(founds + rank))));
+      asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                   "r"(__float_as_uint(f.score)), "r"(f.token), "r"(__float_as_uint(f.second)), "r"(0)
+                   : "memory");
+    }
+    cluster_sync();
+    if (rank != 0) return;
+    f = founds[0];
+    for (int i = 1; i < blocks; ++i) f = join(f, founds[i]);
+    // whether something that was not scored reaches the best
+    if (f.token != INT32_MAX && !(f.second < expf(f.score - w.shift) * keen))
+      f = every_token<DT>(w, refused, a.V, warps);
+    if (f.token == INT32_MAX) f = every_token<DT>(w, refused, a.V, warps);
+    if (f.token == INT32_MAX) f = every_token<DT>(w, false, a.V, warps);
+    token = f.token;
   }
   if (rank != 0) return;
   if (token == INT32_MAX) token = -1;
@@ -391,7 +561,8 @@ cudaError_t launch(VerifyArgs a, cudaStream_t stream) {
   const int64_t slots = a.rows / a.per_slot;
   // blocks to a slot: as many as have a round of tokens, and as all slots have room for
   int blocks = kMostCluster;
-  while (blocks > 1 && (slots * blocks > kSms * 4 || blocks * kThreads * 4 >= 2 * a.V)) blocks /= 2;
+  while (blocks > 1 && (slots * blocks > kSms * 4 || blocks * kThreads * 8 >= 2 * a.V))
+    blocks /= 2;
   attrs[1].id = cudaLaunchAttributeClusterDimension;
   attrs[1].val.clusterDim.x = unsigned(blocks);
   attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
