@@ -28,9 +28,9 @@ struct AttendArgs {
   float* weights;
   int64_t weights_batch, weights_head;
   float* lse;      // [batch, rows, q_heads]: log2 of a row's sum; only with weights
-  // of the tensor-core kernels: the work is cut into tiles of tokens, in the order
-  // (sequence, group of `team` heads, tile of rows, tile of tokens), and each of `workers`
-  // teams of warps, a warp a head, takes a range of them
+  // of the tensor-core kernels: the work is cut into tiles of tokens, in the order (sequence,
+  // tile of rows, tile of tokens).  `workers` workers take a range of them each: one team of
+  // warps for every `team` heads, a warp a head
   int team, head_groups, row_tiles, workers, min_tiles;
   bool wide_params;   // 16-byte copies of params
   // a slot's place is slot * stride in both parts, and counted in copied units (codes) and

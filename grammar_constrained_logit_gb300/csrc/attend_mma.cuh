@@ -187,10 +187,9 @@ __device__ __forceinline__ Division divide(const AttendArgs& a, int b, int64_t* 
     all += __shfl_xor_sync(kFullWarp, all, o);
     head += __shfl_xor_sync(kFullWarp, head, o);
   }
-  const int64_t units = int64_t(a.head_groups) * a.row_tiles;
-  *before = head * units;
+  *before = head * a.row_tiles;
   Division d;
-  d.total = all * units;
+  d.total = all * a.row_tiles;
   d.workers = int(min(int64_t(a.workers), max(int64_t(1), (d.total + a.min_tiles - 1) / a.min_tiles)));
   return d;
 }
@@ -241,14 +240,15 @@ struct Queries {
       const int up = most > 0.0f && most <= 3.4028235e38f
                          ? 14 - (int(__float_as_uint(most) >> 23) - 127) : 0;
       const float f1 = power_of_two(up / 2), f2 = power_of_two(up - up / 2);
-      const float mine = a.scale / f1 / f2;
+      // (4-bit codes stand for 2^24 of what they are as fp16; so do the lows' sums then)
+      const float mine = a.scale / f1 / f2 * (T::kBits == 4 ? 16777216.0f : 1.0f);
       float sums[kLowSums] = {};
 #pragma unroll
       for (int t = 0; t < T::kDim / 16; ++t) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x[t][e] = x[t][e] * f1 * f2;
-          if (T::kBits == 4) sums[t / T::kSteps] += x[t][e];
+          if (T::kBits == 4) sums[t / T::kSteps] += x[t][e] * 5.9604644775390625e-08f;
         }
         // codes whose bits lie four higher are 16 times what they are
         if (T::kBits == 4) x[t][2] *= 0.0625f, x[t][3] *= 0.0625f;
@@ -406,6 +406,33 @@ struct Loader {
 
 // ------------------------------------------------------------------ scores
 
+// A token's params, of each block of elements.
+template <class T>
+struct BlockParams {
+  uint32_t w[T::kBlocks];
+};
+
+template <class T>
+__device__ __forceinline__ BlockParams<T> block_params(const char* at, int gstep) {
+  BlockParams<T> r;
+  if (T::kBlocks % 4 == 0 && gstep == 1) {
+#pragma unroll
+    for (int k = 0; k < T::kBlocks; k += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(at + 4 * k);
+      r.w[k] = v.x, r.w[(k + 1) % T::kBlocks] = v.y;
+      r.w[(k + 2) % T::kBlocks] = v.z, r.w[(k + 3) % T::kBlocks] = v.w;
+    }
+  } else {
+    int group = 0, in = 0;
+#pragma unroll
+    for (int k = 0; k < T::kBlocks; ++k) {
+      r.w[k] = *reinterpret_cast<const uint32_t*>(at + 4 * group);
+      if (++in == gstep) in = 0, ++group;
+    }
+  }
+  return r;
+}
+
 // S^T of a tile: tokens lane / 4 (and that + 8) of each sixteen, rows 2 (lane % 4) and the
 // next of each eight.
 template <class T>
@@ -416,8 +443,9 @@ __device__ __forceinline__ void scores(float (&s)[T::kM][T::kNR][4], const Queri
 #pragma unroll
   for (int m = 0; m < T::kM; ++m) {
     const char* row = stage + (m * 16 + g) * T::kRow;
-    const uint32_t* held = reinterpret_cast<const uint32_t*>(stage + 2 * T::kCodes) +
-                           (m * 16 + g) * T::kBlocks;
+    const char* held = stage + 2 * T::kCodes + (m * 16 + g) * T::kBlocks * 4;
+    const auto p0 = block_params<T>(held, gstep);
+    const auto p1 = block_params<T>(held + 8 * T::kBlocks * 4, gstep);
 #pragma unroll
     for (int k = 0; k < T::kBlocks; ++k) {
       const int at = k * (T::kBlock * T::kBits / 8) + c * T::kKeyBytes;
@@ -445,8 +473,7 @@ __device__ __forceinline__ void scores(float (&s)[T::kM][T::kNR][4], const Queri
 #pragma unroll
           for (int p = T::kPieces - 1; p >= 0; --p) mma(acc[n], op, q.q[k * T::kSteps + i][n][p]);
       }
-      const int group = T::kBlocks == 1 ? 0 : k / gstep;
-      const uint32_t h0 = held[group], h1 = held[8 * T::kBlocks + group];
+      const uint32_t h0 = p0.w[k], h1 = p1.w[k];
 #pragma unroll
       for (int n = 0; n < T::kNR; ++n)
 #pragma unroll
@@ -457,7 +484,7 @@ __device__ __forceinline__ void scores(float (&s)[T::kM][T::kNR][4], const Queri
             s[m][n][e] = fmaf(acc[n][e], __uint_as_float(h), before);
           } else {
             const float lows = fmaf(__uint_as_float(h & 0xffff0000u), q.low[n][e & 1][k], before);
-            s[m][n][e] = fmaf(acc[n][e] * 16777216.0f, __uint_as_float(h << 16), lows);
+            s[m][n][e] = fmaf(acc[n][e], __uint_as_float(h << 16), lows);
           }
         }
     }
@@ -504,18 +531,18 @@ struct Sums {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     float s[T::kM][T::kNR][4];
     scores<T>(s, q, stage, gstep);
-    // largest scale of each of this lane's tokens, as an exponent
-    const uint32_t* held_at = reinterpret_cast<const uint32_t*>(stage + 2 * T::kCodes + T::kParams);
+    // params of this lane's tokens, and the largest scale of each as an exponent
+    const char* held_at = stage + 2 * T::kCodes + T::kParams;
     float large[T::kM][2];
 #pragma unroll
     for (int m = 0; m < T::kM; ++m)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t* p = held_at + (m * 16 + 8 * u + g) * T::kBlocks;
-        uint32_t most = T::kBits == 8 ? p[0] : p[0] << 16;
+        const auto p = block_params<T>(held_at + (m * 16 + 8 * u + g) * T::kBlocks * 4, gstep);
+        uint32_t most = T::kBits == 8 ? p.w[0] : p.w[0] << 16;
 #pragma unroll
         for (int k = 1; k < T::kBlocks; ++k)
-          if (k * gstep < T::kBlocks) most = max(most, T::kBits == 8 ? p[k] : p[k] << 16);
+          most = max(most, T::kBits == 8 ? p.w[k] : p.w[k] << 16);
         large[m][u] = float(max(int((most >> 23) & 255u) - 127, kLeastScale));
       }
     float now[T::kNR][2];
@@ -571,13 +598,18 @@ struct Sums {
             for (int e = 0; e < 4; ++e) o[k][v][n][e] *= e & 1 ? f1 : f0;
       }
     }
+    float lifted[T::kNR][2];
+#pragma unroll
+    for (int n = 0; n < T::kNR; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) lifted[n][e] = from[n][e] - kLift;
 #pragma unroll
     for (int m = 0; m < T::kM; ++m)
 #pragma unroll
       for (int n = 0; n < T::kNR; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[m][n][e] = ex2(s[m][n][e] - from[n][e & 1] + kLift);
+          s[m][n][e] = ex2(s[m][n][e] - lifted[n][e & 1]);
           mass[n][e & 1] += s[m][n][e];
         }
     char* values = stage + T::kCodes;
@@ -593,12 +625,12 @@ struct Sums {
 #pragma unroll
     for (int m = 0; m < T::kM; ++m) {
       const char* row = values + (m * 16 + 2 * c) * T::kRow;
+      const auto p0 = block_params<T>(held_at + (m * 16 + g) * T::kBlocks * 4, gstep);
+      const auto p1 = block_params<T>(held_at + (m * 16 + 8 + g) * T::kBlocks * 4, gstep);
 #pragma unroll
       for (int k = 0; k < T::kBlocks; ++k) {
         // P s_g, rounded, as the B operand
-        const int group = T::kBlocks == 1 ? 0 : k / gstep;
-        const uint32_t h0 = held_at[(m * 16 + g) * T::kBlocks + group];
-        const uint32_t h1 = held_at[(m * 16 + 8 + g) * T::kBlocks + group];
+        const uint32_t h0 = p0.w[k], h1 = p1.w[k];
         const float s0 = __uint_as_float(T::kBits == 8 ? h0 : h0 << 16);
         const float s1 = __uint_as_float(T::kBits == 8 ? h1 : h1 << 16);
         uint32_t p[T::kNR][T::kPieces][2];
@@ -724,7 +756,9 @@ __global__ void __launch_bounds__(kMostTeamWarps * 32, T::kResident)
   extern __shared__ __align__(128) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int in_team = warp % a.team;
-  const int worker = blockIdx.x * (blockDim.x / 32 / a.team) + warp / a.team;
+  // neighbours have the same tokens' next heads: what lies together is read together
+  const int index = blockIdx.x * (blockDim.x / 32 / a.team) + warp / a.team;
+  const int worker = index / a.head_groups, group = index - worker * a.head_groups;
   // the calls before may still read what this one writes
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -732,7 +766,7 @@ __global__ void __launch_bounds__(kMostTeamWarps * 32, T::kResident)
   const Division d = divide<T::kTile>(a, 0, &at);
   if (d.total == 0 || worker >= d.workers) return;
   const int64_t begin = d.start(worker), stop = d.start(worker + 1);
-  const int units = a.head_groups * a.row_tiles;
+  const int units = a.row_tiles;
   int64_t base = 0;  // tiles before sequence b
   int b = 0;
   {  // the sequence that tile `begin` is of
@@ -767,7 +801,7 @@ __global__ void __launch_bounds__(kMostTeamWarps * 32, T::kResident)
     const int unit = int((at - base) / tiles.count);
     const int tile = int(at - base - int64_t(unit) * tiles.count);
     const int count = int(min(int64_t(tiles.count - tile), stop - at));
-    const int rt = unit % a.row_tiles, h = unit / a.row_tiles * a.team + in_team;
+    const int rt = unit, h = group * a.team + in_team;
     // tiles that a row of this tile of rows sees
     const int r0 = rt * T::kRows / a.shared;
     const int r1 = min(rt * T::kRows + T::kRows - 1, a.rows * a.shared - 1) / a.shared;
@@ -810,7 +844,7 @@ __global__ void __launch_bounds__(kMostTeamWarps * 32, T::kResident)
     sums.join();
     const bool whole = count == tiles.count;
     const int part = at == begin ? 0 : 1;
-    const int64_t slot = (int64_t(worker) * 2 + part) * a.team + in_team;
+    const int64_t slot = ((int64_t(worker) * a.head_groups + group) * 2 + part) * a.team + in_team;
 #pragma unroll
     for (int n = 0; n < T::kNR; ++n)
 #pragma unroll
@@ -875,7 +909,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
              j * a.out.head_stride;
   float* lse = a.lse != nullptr ? a.lse + (int64_t(b) * a.rows + r) * (a.heads * a.shared) + j
                                 : nullptr;
-  const int64_t begin = base + (int64_t(h / a.team) * a.row_tiles + rt) * tiles;
+  const int64_t begin = base + int64_t(rt) * tiles;
   const int w0 = tiles > 0 ? d.owner(begin) : 0, w1 = tiles > 0 ? d.owner(begin + tiles - 1) : 0;
   // a worker's first unit is its part 0, its last one part 1
   const bool inside = tiles > 0 && d.start(w0) != begin;
@@ -889,7 +923,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   if (w0 == w1) return;  // written whole
   const int n = w1 - w0 + 1;
   const auto slot = [&](int i) {
-    return ((int64_t(w0 + i) * 2 + (i == 0 && inside)) * a.team + h % a.team) * ROWS + row % ROWS;
+    return (((int64_t(w0 + i) * a.head_groups + h / a.team) * 2 + (i == 0 && inside)) * a.team +
+            h % a.team) * ROWS + row % ROWS;
   };
   float top = -INFINITY;
   for (int i = threadIdx.x; i < n; i += blockDim.x) top = fmaxf(top, a.tops[slot(i)].x);
@@ -1077,7 +1112,9 @@ cudaError_t attend_with(AttendArgs a, cudaStream_t stream) {
   int blocks = 0;
   cudaError_t e = prepare_kernel<T>(attend_kernel<T>, warps, &blocks);
   if (e != cudaSuccess) return e;
-  a.workers = blocks * teams;
+  // every head group has the same number of workers
+  if (blocks * teams < a.head_groups) blocks = (a.head_groups + teams - 1) / teams;
+  a.workers = blocks * teams / a.head_groups;
   e = launch_after(attend_kernel<T>, dim3(blocks), dim3(warps * 32),
                    size_t(warps) * T::kStages * T::kStage, stream, a);
   if (e != cudaSuccess) return e;

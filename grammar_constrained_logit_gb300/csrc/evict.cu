@@ -20,7 +20,8 @@ constexpr int kMaxParts = 8;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMoveThreads = 256;
-constexpr int kRoundBytes = 40 * 1024;  // of a block's round, two at once
+constexpr int kRoundBytes = 20 * 1024;  // of a block's round, two at once
+constexpr int kCodeThreads = 224;        // of a block: the last warp moves params
 constexpr int kRoundTokens = kMoveThreads;  // a thread looks one up
 constexpr int kMostCluster = 8;
 constexpr int kSms = 152;
@@ -48,7 +49,6 @@ struct EvictArgs {
   int32_t* source;  // [batch, heads, keep]: s(j)
   int slice;        // tokens of a sequence to a block of the selection
   int round_tokens;
-  Div per_token;    // pieces
 };
 
 __device__ __forceinline__ int cluster_size() {
@@ -360,27 +360,29 @@ __device__ __forceinline__ void fetch_unit(char* to, const char* from, int unit)
 // Moves codes and params: a cluster of blocks a sequence and head, in rounds.  A thread has
 // one piece of a token, of every `step`-th token: its strides and bases are worked out once,
 // and what it fetches it stores itself.
-__global__ void __launch_bounds__(kMoveThreads, 2)
+__global__ void __launch_bounds__(kMoveThreads, 4)
     evict_move_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ __align__(16) char staged[];  // [2][round_tokens][pieces][16]
   __shared__ int64_t from_slots[3][kRoundTokens], to_slots[3][kRoundTokens];
   const int blocks = cluster_size(), rank = cluster_rank();
   const int owner = blockIdx.x / blocks, b = owner / a.heads, h = owner - b * a.heads;
-  const int pieces = int(a.per_token.d), codes = a.code_bytes / a.code_unit;
-  const int per_part = pieces / a.n_parts;
-  const int step = kMoveThreads / pieces, first = int(a.per_token.quot(threadIdx.x));
-  int piece = threadIdx.x - first * pieces;
-  char* stage = staged + piece * 16;
+  const int code_pieces = a.code_bytes / a.code_unit, param_pieces = a.param_bytes / a.param_unit;
+  const int staged_bytes = a.n_parts * (code_pieces + param_pieces) * 16;  // of a token
+  const bool is_code = threadIdx.x < kCodeThreads;
+  const int unit = is_code ? a.code_unit : a.param_unit;
+  const int per_part = is_code ? code_pieces : param_pieces, pieces = a.n_parts * per_part;
+  const int at = is_code ? threadIdx.x : threadIdx.x - kCodeThreads;
+  const int step = (is_code ? kCodeThreads : kMoveThreads - kCodeThreads) / pieces;
+  const int first = at / pieces;
+  int piece = at - first * pieces;
+  char* stage = staged + (is_code ? piece : a.n_parts * code_pieces + piece) * 16;
   const int part = piece / per_part;
   piece -= part * per_part;
   const lp_cache_part& p = a.part[part];
-  const bool is_code = piece < codes;
-  const int unit = is_code ? a.code_unit : a.param_unit;
   const int64_t page_stride = is_code ? p.code_page_stride : p.param_page_stride;
   const int64_t slot_stride = is_code ? p.code_slot_stride : p.param_slot_stride;
   char* base = static_cast<char*>(is_code ? p.codes : p.params) +
-               h * (is_code ? p.code_head_stride : p.param_head_stride) +
-               (is_code ? piece : piece - codes) * unit;
+               h * (is_code ? p.code_head_stride : p.param_head_stride) + piece * unit;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n = min(max(__ldg(a.lengths + b), 0), a.most);
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2)
       for (int i = first; i < a.round_tokens; i += step) {
         const int64_t from = from_slots[round % 3][i];
         if (from >= 0)
-          fetch_unit(stage + ((round & 1) * a.round_tokens + i) * pieces * 16,
+          fetch_unit(stage + ((round & 1) * a.round_tokens + i) * staged_bytes,
                      base + place(a, from, page_stride, slot_stride), unit);
       }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2)
       for (int i = first; i < a.round_tokens; i += step)
         if (from_slots[round % 3][i] >= 0)
           copy_unit(base + place(a, to_slots[round % 3][i], page_stride, slot_stride),
-                    stage + ((round & 1) * a.round_tokens + i) * pieces * 16, unit);
+                    stage + ((round & 1) * a.round_tokens + i) * staged_bytes, unit);
   };
 
   for (int round = 0; round < 2; ++round) {
@@ -538,15 +540,16 @@ cudaError_t launch(EvictArgs a, cudaStream_t stream) {
   }
   if (e != cudaSuccess || a.n_parts == 0 || a.weights == nullptr || a.n_slots == 0 || a.keep == 0)
     return e;
-  const int64_t pieces = int64_t(a.n_parts) *
-                         (a.code_bytes / a.code_unit + a.param_bytes / a.param_unit);
-  if (pieces > kMoveThreads || units > INT32_MAX / kMostCluster)
+  const int64_t codes = int64_t(a.n_parts) * (a.code_bytes / a.code_unit);
+  const int64_t params = int64_t(a.n_parts) * (a.param_bytes / a.param_unit);
+  if (codes > kCodeThreads || params > kMoveThreads - kCodeThreads ||
+      units > INT32_MAX / kMostCluster)
     return launch_kernel(evict_move_wide_kernel, dim3(unsigned(units)), dim3(kMoveThreads), 0,
                          stream, a);
-  a.per_token.set(uint32_t(pieces));
+  const int64_t pieces = codes + params;
   a.round_tokens = int(std::min<int64_t>({kRoundTokens, kRoundBytes / (pieces * 16), a.keep}));
   int blocks = 1;
-  while (blocks < kMostCluster && units * blocks * 2 <= 2 * kSms && a.keep > 64 * blocks) blocks *= 2;
+  while (blocks < kMostCluster && units * blocks * 2 <= 8 * kSms && a.keep > 64 * blocks) blocks *= 2;
   a.round_tokens = std::min(a.round_tokens, (a.keep + blocks - 1) / blocks);
   const size_t smem = size_t(2) * a.round_tokens * pieces * 16;
   e = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -625,6 +628,12 @@ extern "C" lp_status lp_cache_evict(const lp_cache_part* parts, int64_t n_parts,
   a.n_parts = dim > 0 ? int(n_parts) : 0;
   a.n_slots = n_slots;
   a.page = page_size;
+  // pages that follow one another are one
+  bool linear = true;
+  for (int i = 0; i < a.n_parts; ++i)
+    linear = linear && a.part[i].code_page_stride == a.part[i].code_slot_stride * page_size &&
+             a.part[i].param_page_stride == a.part[i].param_slot_stride * page_size;
+  if (linear) a.page = std::max(page_size, n_slots);
   if (page_size < n_slots && n_slots <= INT32_MAX) a.per_page.set(uint32_t(page_size));
   a.heads = std::max(1, int(heads));
   a.code_unit = unit_of(code_bits), a.param_unit = unit_of(param_bits);

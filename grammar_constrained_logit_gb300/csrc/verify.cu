@@ -26,6 +26,7 @@ namespace {
 constexpr int kStreamThreads = 256;
 constexpr int kVecs = 4;                    // 16-byte vectors a lane has of a chunk
 constexpr int kChunkVecs = kVecs * 32;
+constexpr int kRun = 4;                     // chunks that a warp takes one after another, at most
 constexpr int kThreads = 256;               // of a block of the second kernel
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostRows = 256;              // of a slot: a thread has a draft at most
@@ -53,6 +54,8 @@ struct VerifyArgs {
   int32_t* out_accepted;
   float2* part;  // [rows, chunks]
   int chunks;
+  int run;       // chunks that a warp takes one after another
+  Div per_row;   // runs of a row
 };
 
 __device__ __forceinline__ float heat_of(const VerifyArgs& a, int slot) {
@@ -97,12 +100,14 @@ struct RowVecs {
     mask = mask_of(a, row);
     V = a.V;
   }
-  __device__ __forceinline__ int64_t count() const {
-    return V == 0 ? 0 : (int64_t(before) + V + kPer - 1) / kPer;
+  __device__ __forceinline__ int count() const {
+    return V == 0 ? 0 : int((uint32_t(before) + uint32_t(V) + kPer - 1) / kPer);
   }
-  __device__ __forceinline__ int first_token(int64_t q) const { return int(q * kPer - before); }
+  __device__ __forceinline__ int first_token(int q) const {
+    return int(uint32_t(q) * kPer - uint32_t(before));
+  }
   // Bits of the vector's tokens that are candidates, as far as the mask goes.
-  __device__ __forceinline__ uint32_t bits(int64_t q) const {
+  __device__ __forceinline__ uint32_t bits(int q) const {
     const int j = first_token(q), lo = max(0, -j), n = min(kPer, V - j);
     uint32_t keep = ((1u << n) - 1u) & ~((1u << lo) - 1u);
     if (mask != nullptr) {
@@ -160,28 +165,36 @@ __global__ void __launch_bounds__(kStreamThreads)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t total = int64_t(a.rows) * a.chunks;
-  for (int64_t i = int64_t(blockIdx.x) * (kStreamThreads / 32) + (threadIdx.x >> 5); i < total;
-       i += int64_t(gridDim.x) * (kStreamThreads / 32)) {
-    const int64_t row = i / a.chunks;
-    const int chunk = int(i - row * a.chunks);
-    const float rate = rate_of(heat_of(a, int(row / a.per_slot)));
-    const RowVecs<DT> x(a, row);
-    const int64_t vecs = x.count();
+  const uint32_t run = blockIdx.x * (kStreamThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t row = a.per_row.quot(run);
+  if (row >= uint32_t(a.rows)) return;
+  const int first = int(run - row * a.per_row.d) * a.run;
+  const int last = min(first + a.run, a.chunks);
+  const float rate = rate_of(heat_of(a, int(row) / a.per_slot));
+  const RowVecs<DT> x(a, row);
+  const int vecs = x.count();
+  uint4 next[kVecs];
+  uint32_t next_keep[kVecs];
+  const auto fetch = [&](int chunk) {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int q = chunk * kChunkVecs + u * 32 + lane;
+      next[u] = make_uint4(0, 0, 0, 0);
+      if (q < vecs) next[u] = __ldg(reinterpret_cast<const uint4*>(x.at) + q);
+    }
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int q = chunk * kChunkVecs + u * 32 + lane;
+      next_keep[u] = q < vecs ? x.bits(q) : 0u;
+    }
+  };
+  fetch(first);
+  for (int chunk = first; chunk < last; ++chunk) {
     uint4 raw[kVecs];
     uint32_t keep[kVecs];
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int64_t q = int64_t(chunk) * kChunkVecs + u * 32 + lane;
-      keep[u] = 0;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (q < vecs) raw[u] = __ldg(reinterpret_cast<const uint4*>(x.at) + q);
-    }
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int64_t q = int64_t(chunk) * kChunkVecs + u * 32 + lane;
-      if (q < vecs) keep[u] = x.bits(q);
-    }
+    for (int u = 0; u < kVecs; ++u) raw[u] = next[u], keep[u] = next_keep[u];
+    if (chunk + 1 < last) fetch(chunk + 1);
     // what is no candidate becomes -inf
     float top = -INFINITY;
 #pragma unroll
@@ -217,7 +230,7 @@ __global__ void __launch_bounds__(kStreamThreads)
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
     }
-    if (lane == 0) a.part[i] = make_float2(top, sum);
+    if (lane == 0) a.part[int64_t(row) * a.chunks + chunk] = make_float2(top, sum);
   }
 }
 
@@ -407,9 +420,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_say_kernel(const __grid_co
         if (chunk == INT32_MAX && part[c].x == all) chunk = c;
       chunk = __reduce_min_sync(kFullWarp, chunk);
       const RowVecs<DT> x(a, row);
-      const int64_t vecs = x.count();
+      const int vecs = x.count();
       for (int u = 0; u < kVecs; ++u) {
-        const int64_t q = int64_t(chunk) * kChunkVecs + u * 32 + lane;
+        const int q = chunk * kChunkVecs + u * 32 + lane;
         if (q >= vecs) continue;
         const uint4 raw = __ldg(reinterpret_cast<const uint4*>(x.at) + q);
         const uint32_t keep = x.bits(q);
@@ -554,8 +567,12 @@ cudaError_t launch(VerifyArgs a, cudaStream_t stream) {
   cfg.attrs = attrs;
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(kStreamThreads);
-  const int64_t warps = int64_t(a.rows) * a.chunks;
-  cfg.gridDim = dim3(unsigned(std::min<int64_t>((warps + 7) / 8, kSms * 64)));
+  // a run of chunks to a warp, or one where there are few in all
+  const int64_t few = int64_t(kSms) * 32;
+  a.run = int64_t(a.rows) * a.chunks < few * kRun ? 1 : kRun;
+  a.per_row.set(uint32_t((a.chunks + a.run - 1) / a.run));
+  const int64_t warps = int64_t(a.rows) * a.per_row.d;
+  cfg.gridDim = dim3(unsigned((warps + kStreamThreads / 32 - 1) / (kStreamThreads / 32)));
   const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_stream_kernel<DT>, a);
   if (e != cudaSuccess) return e;
   const int64_t slots = a.rows / a.per_slot;
@@ -634,6 +651,8 @@ extern "C" lp_status lp_verify_drafts(const void* logits, lp_dtype dt, int64_t B
        reinterpret_cast<uintptr_t>(out_tokens)) % 8 != 0)
     return LP_ERR_INVALID_ARGUMENT;
   const int64_t need = lp_verify_drafts_workspace_bytes(dt, B, V);
+  // (warps are counted in 31 bits)
+  if (B > INT32_MAX / chunks_of(dt, V)) return LP_ERR_TOO_LARGE;
   if (workspace == nullptr || workspace_bytes < need ||
       reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
     return LP_ERR_INVALID_ARGUMENT;

@@ -586,8 +586,8 @@ lp_status lp_cache_evict(const lp_cache_part* parts, int64_t n_parts, int32_t bi
  *                content; calls that share it must be ordered, as lp_beam_select's
  * Invalid: as lp_apply_token_bitmask_rows, rows_per_slot < 1, B not a multiple of it,
  * row_needs_mask without bitmask, logits not aligned to their element, NULL or misaligned
- * pointers with work to do.  rows_per_slot above 256, more than 2^27 rows, or a vocabulary
- * above 2^31 - 65 return LP_ERR_TOO_LARGE.
+ * pointers with work to do.  rows_per_slot above 256, more than 2^27 rows, a vocabulary
+ * above 2^31 - 65, or 2^31 pieces of rows of 2 KB return LP_ERR_TOO_LARGE.
  */
 int64_t lp_verify_drafts_workspace_bytes(lp_dtype dt, int64_t rows, int64_t vocab_size);
 
