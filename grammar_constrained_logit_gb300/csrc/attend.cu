@@ -188,10 +188,11 @@ extern "C" int64_t lp_cache_attend_workspace_bytes(int64_t batch, int64_t rows, 
   if (batch < 0 || rows < 0 || q_heads < 0 || heads < 0 || dim < 0 || dim > kMostDim ||
       !fits(rows, q_heads, 1 << 24) || !fits(batch, rows * q_heads, INT32_MAX))
     return -1;
-  // of each row its sum; and what the workers leave of the units that they share
-  const int64_t left = heads == 0 ? 0 : int64_t(kSms) * kMostWarps * 2 *
-                                            rows_at_once(rows * (q_heads / heads)) * (dim * 4 + 8);
-  return (batch * rows * q_heads * 4 + 15) / 16 * 16 + (left + 15) / 16 * 16;
+  // of each row its sum; who shares a unit; and what the workers leave of the shared ones
+  const int64_t per_head = heads == 0 ? 0 : rows * (q_heads / heads);
+  const int64_t left = int64_t(kSms) * kMostWarps * 2 * rows_at_once(per_head) * (dim * 4 + 8);
+  return (batch * rows * q_heads * 4 + 15) / 16 * 16 + batch * ((per_head + 7) / 8) * 16 +
+         (left + 15) / 16 * 16;
 }
 
 extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, int64_t n_slots,
@@ -282,7 +283,11 @@ extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, i
   a.min_tiles = 2;
   const int at_once = rows_at_once(int64_t(a.rows) * a.shared);
   char* left = static_cast<char*>(workspace) + (batch * rows * q_heads * 4 + 15) / 16 * 16;
+  a.shares = reinterpret_cast<int4*>(left);
+  left += batch * ((rows * (q_heads / heads) + 7) / 8) * 16;
   const int64_t held = int64_t(kSms) * kMostWarps * 2 * at_once;
+  a.wide_q = (reinterpret_cast<uintptr_t>(q->data) | uint64_t(a.q.batch_stride) |
+              uint64_t(a.q.row_stride) | uint64_t(a.q.head_stride)) % 8 == 0;
   a.sums = reinterpret_cast<float*>(left);
   a.tops = reinterpret_cast<float2*>(left + held * a.dim * 4);
   static const Launch launches[2][2][2] = {{{attend_8n1, attend_8n2}, {attend_8w1, attend_8w2}},

@@ -38,6 +38,9 @@ struct AttendArgs {
   uint32_t code_step, param_step;
   float* sums;     // [workers, 2, team, tile's rows, dim]: of what a worker has of a unit
   float2* tops;    // [workers, 2, team, tile's rows]: (largest exponent, mass)
+  int4* shares;    // [batch, row tiles]: a unit's first worker and last, whether the first one
+                   // has it as its part 1
+  bool wide_q;     // queries are loaded 8 bytes at a time
 };
 
 // What a sequence has: its tokens, and the queries that take part.

@@ -172,22 +172,14 @@ struct Division {
   }
 };
 
-// All tiles, and (before) those of the sequences before b: a warp together.
+// All tiles: a warp together.
 template <int TILE>
-__device__ __forceinline__ Division divide(const AttendArgs& a, int b, int64_t* before) {
+__device__ __forceinline__ Division divide(const AttendArgs& a) {
   const int lane = threadIdx.x & 31;
-  int64_t all = 0, head = 0;
-  for (int i = lane; i < a.batch; i += 32) {
-    const int n = tiles_of<TILE>(a, sequence(a, i)).count;
-    all += n;
-    if (i < b) head += n;
-  }
+  int64_t all = 0;
+  for (int i = lane; i < a.batch; i += 32) all += tiles_of<TILE>(a, sequence(a, i)).count;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    all += __shfl_xor_sync(kFullWarp, all, o);
-    head += __shfl_xor_sync(kFullWarp, head, o);
-  }
-  *before = head * a.row_tiles;
+  for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(kFullWarp, all, o);
   Division d;
   d.total = all * a.row_tiles;
   d.workers = int(min(int64_t(a.workers), max(int64_t(1), (d.total + a.min_tiles - 1) / a.min_tiles)));
@@ -227,13 +219,43 @@ struct Queries {
                          r * a.q.row_stride + (h * a.shared + j) * a.q.head_stride;
       float most = 0.0f;
       float x[T::kDim / 16][4];
+      constexpr int kRun = T::kBlock / 4;  // a lane's elements of a block lie together
 #pragma unroll
-      for (int t = 0; t < T::kDim / 16; ++t)
+      for (int k = 0; k < T::kBlocks; ++k) {
+        float run[kRun];
+        const int first = k * T::kBlock + c * kRun;
+        if (!there) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[t][e] = there ? load_as_float(from, element(t, c, e), a.dt) : 0.0f;
-          most = fmaxf(most, fabsf(x[t][e]));
+          for (int e = 0; e < kRun; ++e) run[e] = 0.0f;
+        } else if (!a.wide_q) {
+#pragma unroll
+          for (int e = 0; e < kRun; ++e) run[e] = load_as_float(from, first + e, a.dt);
+        } else if (a.dt == LP_F32) {
+#pragma unroll
+          for (int e = 0; e < kRun; e += 2) {
+            const float2 v = __ldg(reinterpret_cast<const float2*>(from + (first + e) * 4));
+            run[e] = v.x, run[e + 1] = v.y;
+          }
+        } else {
+          uint2 raw[kRun / 4];
+#pragma unroll
+          for (int e = 0; e < kRun / 4; ++e)
+            raw[e] = __ldg(reinterpret_cast<const uint2*>(from + (first + 4 * e) * 2));
+#pragma unroll
+          for (int e = 0; e < kRun; ++e) {
+            const uint32_t w = (e & 2) ? raw[e / 4].y : raw[e / 4].x;
+            const uint32_t u = (e & 1) ? w >> 16 : w & 0xffffu;
+            run[e] = a.dt == LP_BF16 ? __uint_as_float(u << 16) : Elt<LP_F16>::half_bits_to_float(u);
+          }
         }
+#pragma unroll
+        for (int i = 0; i < T::kSteps; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[k * T::kSteps + i][e] = run[element(k * T::kSteps + i, 0, e) - k * T::kBlock];
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) most = fmaxf(most, fabsf(run[e]));
+      }
       most = fmaxf(most, __shfl_xor_sync(kFullWarp, most, 1));
       most = fmaxf(most, __shfl_xor_sync(kFullWarp, most, 2));
       // to [2^14, 2^15); in two steps, a factor can be beyond 2^127
@@ -762,8 +784,7 @@ __global__ void __launch_bounds__(kMostTeamWarps * 32, T::kResident)
   // the calls before may still read what this one writes
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int64_t at;
-  const Division d = divide<T::kTile>(a, 0, &at);
+  const Division d = divide<T::kTile>(a);
   if (d.total == 0 || worker >= d.workers) return;
   const int64_t begin = d.start(worker), stop = d.start(worker + 1);
   const int units = a.row_tiles;
@@ -790,7 +811,7 @@ __global__ void __launch_bounds__(kMostTeamWarps * 32, T::kResident)
       sum += __shfl_sync(kFullWarp, incl, 31);
     }
   }
-  for (at = begin; at < stop;) {
+  for (int64_t at = begin; at < stop;) {
     const Sequence s = sequence(a, b);
     const Tiles tiles = tiles_of<T::kTile>(a, s);
     if (tiles.count == 0 || at >= base + int64_t(tiles.count) * units) {
@@ -844,6 +865,9 @@ __global__ void __launch_bounds__(kMostTeamWarps * 32, T::kResident)
     sums.join();
     const bool whole = count == tiles.count;
     const int part = at == begin ? 0 : 1;
+    if (tile == 0 && in_team == 0 && group == 0 && lane == 0)
+      a.shares[int64_t(b) * a.row_tiles + rt] =
+          make_int4(worker, whole ? worker : d.owner(at + tiles.count - 1), part, 0);
     const int64_t slot = ((int64_t(worker) * a.head_groups + group) * 2 + part) * a.team + in_team;
 #pragma unroll
     for (int n = 0; n < T::kNR; ++n)
@@ -901,29 +925,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int row = blockIdx.x % per_head;
   const int h = blockIdx.x / per_head % a.heads, b = blockIdx.x / per_head / a.heads;
   const int rt = row / ROWS;
-  int64_t base;
-  const Division d = divide<TILE>(a, b, &base);
-  const int tiles = tiles_of<TILE>(a, sequence(a, b)).count;
   const int r = row / a.shared, j = h * a.shared + row - r * a.shared;
   char* to = static_cast<char*>(a.out.data) + b * a.out.batch_stride + r * a.out.row_stride +
              j * a.out.head_stride;
   float* lse = a.lse != nullptr ? a.lse + (int64_t(b) * a.rows + r) * (a.heads * a.shared) + j
                                 : nullptr;
-  const int64_t begin = base + int64_t(rt) * tiles;
-  const int w0 = tiles > 0 ? d.owner(begin) : 0, w1 = tiles > 0 ? d.owner(begin + tiles - 1) : 0;
-  // a worker's first unit is its part 0, its last one part 1
-  const bool inside = tiles > 0 && d.start(w0) != begin;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tiles == 0) {
+  const int4 share = a.shares[int64_t(b) * a.row_tiles + rt];  // of anything, without tiles
+  if (tiles_of<TILE>(a, sequence(a, b)).count == 0) {
     for (int i = threadIdx.x; i < a.dim; i += blockDim.x) store_float(to, i, 0.0f, a.dt);
     if (lse != nullptr && threadIdx.x == 0) *lse = -INFINITY;
     return;
   }
+  const int w0 = share.x, w1 = share.y, inside = share.z;
   if (w0 == w1) return;  // written whole
   const int n = w1 - w0 + 1;
   const auto slot = [&](int i) {
-    return (((int64_t(w0 + i) * a.head_groups + h / a.team) * 2 + (i == 0 && inside)) * a.team +
+    return (((int64_t(w0 + i) * a.head_groups + h / a.team) * 2 + (i == 0 ? inside : 0)) * a.team +
             h % a.team) * ROWS + row % ROWS;
   };
   float top = -INFINITY;

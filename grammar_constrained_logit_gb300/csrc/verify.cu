@@ -106,16 +106,18 @@ struct RowVecs {
   __device__ __forceinline__ int first_token(int q) const {
     return int(uint32_t(q) * kPer - uint32_t(before));
   }
+  // What the mask has of a vector's tokens: asked for early, looked at late.
+  __device__ __forceinline__ uint32_t mask_word(int q) const {
+    if (mask == nullptr) return ~0u;
+    const int j = first_token(q);
+    // aligned rows: a vector's bits lie within a word
+    return before == 0 ? __ldg(mask + (j >> 5)) : mask_bits(mask, max(j, 0), kPer - max(0, -j), V);
+  }
   // Bits of the vector's tokens that are candidates, as far as the mask goes.
-  __device__ __forceinline__ uint32_t bits(int q) const {
+  __device__ __forceinline__ uint32_t bits(int q, uint32_t word) const {
     const int j = first_token(q), lo = max(0, -j), n = min(kPer, V - j);
-    uint32_t keep = ((1u << n) - 1u) & ~((1u << lo) - 1u);
-    if (mask != nullptr) {
-      // aligned rows: a vector's bits lie within a word
-      if (before == 0) keep &= __ldg(mask + (j >> 5)) >> (j & 31);
-      else keep &= mask_bits(mask, j + lo, kPer - lo, V) << lo;
-    }
-    return keep;
+    const uint32_t keep = ((1u << n) - 1u) & ~((1u << lo) - 1u);
+    return keep & (mask == nullptr ? ~0u : before == 0 ? word >> (j & 31) : word << lo);
   }
 };
 
@@ -160,7 +162,7 @@ __device__ __forceinline__ uint4 only(const uint4& v, uint32_t keep) {
 
 // A warp a chunk.
 template <int DT>
-__global__ void __launch_bounds__(kStreamThreads)
+__global__ void __launch_bounds__(kStreamThreads, 4)
     verify_stream_kernel(const __grid_constant__ VerifyArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(kStreamThreads)
   const RowVecs<DT> x(a, row);
   const int vecs = x.count();
   uint4 next[kVecs];
-  uint32_t next_keep[kVecs];
+  uint32_t next_word[kVecs];
   const auto fetch = [&](int chunk) {
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kStreamThreads)
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const int q = chunk * kChunkVecs + u * 32 + lane;
-      next_keep[u] = q < vecs ? x.bits(q) : 0u;
+      next_word[u] = q < vecs ? x.mask_word(q) : 0u;
     }
   };
   fetch(first);
@@ -193,7 +195,11 @@ __global__ void __launch_bounds__(kStreamThreads)
     uint4 raw[kVecs];
     uint32_t keep[kVecs];
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) raw[u] = next[u], keep[u] = next_keep[u];
+    for (int u = 0; u < kVecs; ++u) {
+      const int q = chunk * kChunkVecs + u * 32 + lane;
+      raw[u] = next[u];
+      keep[u] = q < vecs ? x.bits(q, next_word[u]) : 0u;
+    }
     if (chunk + 1 < last) fetch(chunk + 1);
     // what is no candidate becomes -inf
     float top = -INFINITY;
@@ -292,13 +298,17 @@ struct Group {  // N tokens
   uint32_t keep;
 };
 
-// Tokens v0 .. v0 + 7, v0 a multiple of 8.
+// The word of the mask that has tokens v0 .. v0 + 7, v0 a multiple of 8.
+__device__ __forceinline__ uint32_t group_word(const Row& w, uint32_t v0, uint32_t V) {
+  return w.mask != nullptr && v0 < V ? __ldg(w.mask + (v0 >> 5)) : ~0u;
+}
+
+// Tokens v0 .. v0 + 7.
 template <int DT>
-__device__ __forceinline__ void load_group(Group<8>& g, const Row& w, uint32_t v0, uint32_t V,
-                                           bool whole, bool whole_q) {
+__device__ __forceinline__ void load_group(Group<8>& g, const Row& w, uint32_t word, uint32_t v0,
+                                           uint32_t V, bool whole, bool whole_q) {
   const uint32_t m = v0 < V ? min(8u, V - v0) : 0u;
-  g.keep = (1u << m) - 1u;
-  if (w.mask != nullptr && m > 0) g.keep &= __ldg(w.mask + (v0 >> 5)) >> (v0 & 31);
+  g.keep = ((1u << m) - 1u) & (word >> (v0 & 31));
 #pragma unroll
   for (int e = 0; e < 8; ++e) g.y[e] = -INFINITY, g.d[e] = 0.0f;
   if (g.keep == 0) return;
@@ -425,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_say_kernel(const __grid_co
         const int q = chunk * kChunkVecs + u * 32 + lane;
         if (q >= vecs) continue;
         const uint4 raw = __ldg(reinterpret_cast<const uint4*>(x.at) + q);
-        const uint32_t keep = x.bits(q);
+        const uint32_t keep = x.bits(q, x.mask_word(q));
 #pragma unroll
         for (int e = RowVecs<DT>::kPer - 1; e >= 0; --e)
           if (((keep >> e) & 1u) && Elt<DT>::get(raw, e) == all)
@@ -483,11 +493,14 @@ __global__ void __launch_bounds__(kThreads, 4) verify_say_kernel(const __grid_co
     const uint32_t V = uint32_t(a.V), step = uint32_t(blocks) * kThreads * 8;
     uint32_t v0 = uint32_t(rank * kThreads + tid) * 8;
     Group<8> g;
-    load_group<DT>(g, w, v0, V, whole, whole_q);
+    // logits and probabilities come one round ahead, the mask that says which of them two
+    uint32_t word = group_word(w, v0, V), word_after = group_word(w, v0 + step, V);
+    load_group<DT>(g, w, word, v0, V, whole, whole_q);
     while (v0 < V) {
       Group<8> next;
-      next.keep = 0;
-      load_group<DT>(next, w, v0 + step < V ? v0 + step : V, V, whole, whole_q);
+      word = word_after;
+      word_after = group_word(w, v0 + 2 * step, V);
+      load_group<DT>(next, w, word, v0 + step, V, whole, whole_q);
       const float bound = __uint_as_float(*static_cast<volatile uint32_t*>(&reached)) * keen;
       float r[8];
       uint32_t live = 0;
