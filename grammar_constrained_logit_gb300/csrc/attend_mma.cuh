@@ -1111,16 +1111,23 @@ inline cudaError_t launch_after(void (*kernel)(AttendArgs), dim3 grid, dim3 bloc
 }
 
 // Blocks of `warps` warps on all SMs, as registers and shared memory allow, up to kMostWarps
-// warps an SM.  What a launch may take of shared memory is a device's own setting.
+// warps an SM; asked for once a device, with the setting of the shared memory that a launch
+// may take.
 template <class T>
-cudaError_t prepare_kernel(void (*kernel)(AttendArgs), int warps, int* blocks) {
-  const int smem = warps * T::kStages * T::kStage;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t prepare_kernel(void (*kernel)(AttendArgs), int warps, PerDevice<5>& known,
+                           int* blocks) {
+  std::atomic<int>* held = known.at(warps);
+  if (held != nullptr && (*blocks = held->load(std::memory_order_acquire)) > 0) return cudaSuccess;
+  // the largest that any call asks for, so that no order of calls makes it less
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kMostTeamWarps * T::kStages * T::kStage);
   if (e != cudaSuccess) return e;
   int n = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, warps * 32, smem);
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, warps * 32,
+                                                    warps * T::kStages * T::kStage);
   if (e != cudaSuccess) return e;
   *blocks = kSms * max(1, min(n, kMostWarps / warps));
+  if (held != nullptr) held->store(*blocks, std::memory_order_release);
   return cudaSuccess;
 }
 
@@ -1129,7 +1136,8 @@ cudaError_t attend_with(AttendArgs a, cudaStream_t stream) {
   const int teams = a.team >= 3 ? 1 : 4 / a.team, warps = a.team * teams;
   a.row_tiles = (a.rows * a.shared + T::kRows - 1) / T::kRows;
   int blocks = 0;
-  cudaError_t e = prepare_kernel<T>(attend_kernel<T>, warps, &blocks);
+  static PerDevice<5> known, known_weights;
+  cudaError_t e = prepare_kernel<T>(attend_kernel<T>, warps, known, &blocks);
   if (e != cudaSuccess) return e;
   // every head group has the same number of workers
   if (blocks * teams < a.head_groups) blocks = (a.head_groups + teams - 1) / teams;
@@ -1142,7 +1150,7 @@ cudaError_t attend_with(AttendArgs a, cudaStream_t stream) {
                    dim3(kJoinWarps * 32), 0,
                    stream, a);
   if (e != cudaSuccess || a.weights == nullptr) return e;
-  e = prepare_kernel<T>(weights_kernel<T>, warps, &blocks);
+  e = prepare_kernel<T>(weights_kernel<T>, warps, known_weights, &blocks);
   if (e != cudaSuccess) return e;
   a.workers = blocks * teams;
   return launch_after(weights_kernel<T>, dim3(blocks), dim3(warps * 32),

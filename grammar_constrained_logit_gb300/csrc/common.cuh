@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "lp.h"
 
 namespace lp {
@@ -30,6 +32,35 @@ cudaError_t launch_kernel(void (*kernel)(K...), dim3 grid, dim3 block, size_t sm
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// A number for each device and `slot`, 0 until it is set: what is asked of the runtime once.
+template <int N>
+struct PerDevice {
+  std::atomic<int> held[64][N] = {};
+  std::atomic<int>* at(int slot) {
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return nullptr;
+    return &held[device][slot];
+  }
+};
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device.
+template <typename... K>
+cudaError_t allow_shared(void (*kernel)(K...), int bytes, PerDevice<1>& allowed) {
+  std::atomic<int>* a = allowed.at(0);
+  if (a != nullptr && bytes <= a->load(std::memory_order_relaxed)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && a != nullptr) {
+    // (another thread's larger number stays; a smaller setting of its kernel does not)
+    int was = a->load(std::memory_order_relaxed);
+    while (was < bytes && !a->compare_exchange_weak(was, bytes)) {
+    }
+    if (was > bytes)
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, was);
+  }
+  return e;
 }
 
 // ------------------------------------------------------------------ division

@@ -532,7 +532,8 @@ cudaError_t launch(EvictArgs a, cudaStream_t stream) {
       blocks *= 2;
     a.slice = (a.most + blocks - 1) / blocks;
     const int smem = std::max(1, a.slice) * 4;
-    e = cudaFuncSetAttribute(evict_slices_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static PerDevice<1> allowed;
+    e = allow_shared(evict_slices_kernel, smem, allowed);
     if (e == cudaSuccess)
       e = launch_cluster(evict_slices_kernel, units, blocks, kThreads, smem, stream, a);
   } else {
@@ -552,7 +553,8 @@ cudaError_t launch(EvictArgs a, cudaStream_t stream) {
   while (blocks < kMostCluster && units * blocks * 2 <= 8 * kSms && a.keep > 64 * blocks) blocks *= 2;
   a.round_tokens = std::min(a.round_tokens, (a.keep + blocks - 1) / blocks);
   const size_t smem = size_t(2) * a.round_tokens * pieces * 16;
-  e = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  static PerDevice<1> allowed;
+  e = allow_shared(evict_move_kernel, int(smem), allowed);
   if (e != cudaSuccess) return e;
   return launch_cluster(evict_move_kernel, units, blocks, kMoveThreads, smem, stream, a);
 }

@@ -6,7 +6,7 @@
 //   r = p_n else: with Gumbel noise g that is a draw from r / sum r.
 //
 // The first kernel reads every row once and leaves (largest, sum of exp((x - largest) / T)) of
-// each chunk of 2 KB; the second, a cluster of blocks a slot, joins those to (M, S), decides the
+// each of its runs; the second, a cluster of blocks a slot, joins those to (M, S), decides the
 // slot's acceptances, and goes through the one row that says a token.
 //
 // log r + g is largest where r / t is, t = -log u > 0.  With m = 1 - u that ratio lies between
@@ -26,7 +26,6 @@ namespace {
 constexpr int kStreamThreads = 256;
 constexpr int kVecs = 4;                    // 16-byte vectors a lane has of a chunk
 constexpr int kChunkVecs = kVecs * 32;
-constexpr int kRun = 4;                     // chunks that a warp takes one after another, at most
 constexpr int kThreads = 256;               // of a block of the second kernel
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostRows = 256;              // of a slot: a thread has a draft at most
@@ -52,10 +51,9 @@ struct VerifyArgs {
   const uint64_t* seeds;
   int64_t* out_tokens;
   int32_t* out_accepted;
-  float2* part;  // [rows, chunks]
-  int chunks;
-  int run;       // chunks that a warp takes one after another
-  Div per_row;   // runs of a row
+  float2* part;  // [rows, runs]
+  int runs, run; // of a row; vectors of one
+  Div per_row;   // runs
 };
 
 __device__ __forceinline__ float heat_of(const VerifyArgs& a, int slot) {
@@ -77,7 +75,7 @@ __device__ __forceinline__ float relative(float x, float top) { return x == top 
 
 // What a candidate's distance to the largest is multiplied by, as a power of two.
 __device__ __forceinline__ float rate_of(float heat) {
-  return fminf(kLog2e / heat, 3e38f);
+  return heat > 0.0f ? fminf(kLog2e / heat, 3e38f) : 3e38f;
 }
 
 __device__ __forceinline__ void best_of(float& x, int& v, float y, int w) {
@@ -160,84 +158,92 @@ __device__ __forceinline__ uint4 only(const uint4& v, uint32_t keep) {
   return r;
 }
 
-// A warp a chunk.
+// (largest, sum) of vectors [q0, q1) with whatever is among the logits: NaN is no candidate,
+// and candidates at +inf share the mass.
 template <int DT>
-__global__ void __launch_bounds__(kStreamThreads, 4)
+__device__ __noinline__ float2 any_run(const RowVecs<DT> x, int q0, int q1, float rate) {
+  const int lane = threadIdx.x & 31;
+  float top = -INFINITY, sum = 0.0f;
+  for (int q = q0 + lane; q < q1; q += 32) {
+    const uint4 raw = only<DT>(__ldg(reinterpret_cast<const uint4*>(x.at) + q),
+                               x.bits(q, x.mask_word(q)));
+    top = fmaxf(top, VecMax<DT>::run(raw, (1u << RowVecs<DT>::kPer) - 1u));
+  }
+  top = key_float(__reduce_max_sync(kFullWarp, fkey(top)));
+  for (int q = q0 + lane; q < q1; q += 32) {
+    const uint4 raw = only<DT>(__ldg(reinterpret_cast<const uint4*>(x.at) + q),
+                               x.bits(q, x.mask_word(q)));
+#pragma unroll
+    for (int e = 0; e < RowVecs<DT>::kPer; ++e) {
+      const float y = Elt<DT>::get(raw, e);
+      if (y > -INFINITY) sum += ex2(relative(y, top) * rate);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
+  return make_float2(top, sum);
+}
+
+// A warp a run of a row's vectors: each lane its own largest and sum, joined at the end.  A
+// vector's place in registers is loaded again as soon as it is used up.
+template <int DT>
+__global__ void __launch_bounds__(kStreamThreads, 5)
     verify_stream_kernel(const __grid_constant__ VerifyArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr float kLowest = -3.4028234663852886e38f;
   const int lane = threadIdx.x & 31;
-  const uint32_t run = blockIdx.x * (kStreamThreads / 32) + (threadIdx.x >> 5);
-  const uint32_t row = a.per_row.quot(run);
+  const uint32_t warp = blockIdx.x * (kStreamThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t row = a.per_row.quot(warp);
   if (row >= uint32_t(a.rows)) return;
-  const int first = int(run - row * a.per_row.d) * a.run;
-  const int last = min(first + a.run, a.chunks);
+  const int run = int(warp - row * a.per_row.d);
   const float rate = rate_of(heat_of(a, int(row) / a.per_slot));
   const RowVecs<DT> x(a, row);
-  const int vecs = x.count();
-  uint4 next[kVecs];
-  uint32_t next_word[kVecs];
-  const auto fetch = [&](int chunk) {
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int q = chunk * kChunkVecs + u * 32 + lane;
-      next[u] = make_uint4(0, 0, 0, 0);
-      if (q < vecs) next[u] = __ldg(reinterpret_cast<const uint4*>(x.at) + q);
-    }
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int q = chunk * kChunkVecs + u * 32 + lane;
-      next_word[u] = q < vecs ? x.mask_word(q) : 0u;
+  const int q0 = run * a.run, q1 = min(q0 + a.run, x.count());
+  uint4 raw[kVecs];
+  uint32_t word[kVecs];
+  const auto fetch = [&](int u, int q) {
+    raw[u] = make_uint4(0, 0, 0, 0);
+    word[u] = 0;
+    if (q < q1) {
+      raw[u] = __ldg(reinterpret_cast<const uint4*>(x.at) + q);
+      word[u] = x.mask_word(q);
     }
   };
-  fetch(first);
-  for (int chunk = first; chunk < last; ++chunk) {
-    uint4 raw[kVecs];
-    uint32_t keep[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) fetch(u, q0 + u * 32 + lane);
+  float top = kLowest;
+  uint64_t sums = 0;
+  const uint64_t by = pair_of(rate, rate);
+  for (int q = q0 + lane; q - lane < q1; q += kChunkVecs) {
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
-      const int q = chunk * kChunkVecs + u * 32 + lane;
-      raw[u] = next[u];
-      keep[u] = q < vecs ? x.bits(q, next_word[u]) : 0u;
-    }
-    if (chunk + 1 < last) fetch(chunk + 1);
-    // what is no candidate becomes -inf
-    float top = -INFINITY;
+      const int at = q + u * 32;
+      // what is no candidate becomes -inf
+      const uint4 v = only<DT>(raw[u], at < q1 ? x.bits(at, word[u]) : 0u);
+      fetch(u, at + kChunkVecs);
+      const float now = fmaxf(top, VecMax<DT>::run(v, (1u << RowVecs<DT>::kPer) - 1u));
+      const float f = ex2((top - now) * rate);
+      const uint64_t less = pair_of(-now, -now);
+      sums = mul_pairs(sums, pair_of(f, f));
+      top = now;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      raw[u] = only<DT>(raw[u], keep[u]);
-      top = fmaxf(top, VecMax<DT>::run(raw[u], (1u << RowVecs<DT>::kPer) - 1u));
-    }
-    top = key_float(__reduce_max_sync(kFullWarp, fkey(top)));
-    float sum = 0.0f;
-    if (top > -INFINITY) {
-      const uint64_t less = pair_of(-top, -top), by = pair_of(rate, rate);
-      uint64_t sums = 0;
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-        for (int e = 0; e < RowVecs<DT>::kPer; e += 2) {
-          const uint64_t t = mul_pairs(add_pairs(pair_of(Elt<DT>::get(raw[u], e),
-                                                         Elt<DT>::get(raw[u], e + 1)), less), by);
-          sums = add_pairs(sums, pair_of(ex2(low_of(t)), ex2(high_of(t))));
-        }
-      sum = low_of(sums) + high_of(sums);
-      if (__any_sync(kFullWarp, !(sum < INFINITY))) {
-        // NaN among the logits, which are no candidates, or a largest of +inf
-        sum = 0.0f;
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-          for (int e = 0; e < RowVecs<DT>::kPer; ++e) {
-            const float y = Elt<DT>::get(raw[u], e);
-            if (y > -INFINITY) sum += ex2(relative(y, top) * rate);
-          }
+      for (int e = 0; e < RowVecs<DT>::kPer; e += 2) {
+        const uint64_t t = mul_pairs(add_pairs(pair_of(Elt<DT>::get(v, e),
+                                                       Elt<DT>::get(v, e + 1)), less), by);
+        sums = add_pairs(sums, pair_of(ex2(low_of(t)), ex2(high_of(t))));
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
     }
-    if (lane == 0) a.part[int64_t(row) * a.chunks + chunk] = make_float2(top, sum);
   }
+  float sum = low_of(sums) + high_of(sums);
+  const float all = key_float(__reduce_max_sync(kFullWarp, fkey(top)));
+  sum *= ex2((top - all) * rate);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
+  // the largest itself counts 1, so without a candidate there is 0
+  float2 found = make_float2(sum == 0.0f ? -INFINITY : all, sum);
+  if (!(sum < INFINITY)) found = any_run<DT>(x, q0, q1, rate);
+  if (lane == 0) a.part[int64_t(row) * a.runs + run] = found;
 }
 
 __device__ __forceinline__ uint32_t cluster_size() {
@@ -409,10 +415,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_say_kernel(const __grid_co
   }
   for (int i = tid >> 5; i < R; i += kWarps) {
     const int64_t row = int64_t(slot) * R + i;
-    const float2* part = a.part + row * a.chunks;
+    const float2* part = a.part + row * a.runs;
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll 4
-    for (int c = lane; c < a.chunks; c += 32) {
+    for (int c = lane; c < a.runs; c += 32) {
       const float2 p = part[c];
       const float now = fmaxf(top, p.x);
       if (now > -INFINITY)
@@ -424,16 +430,14 @@ __global__ void __launch_bounds__(kThreads, 4) verify_say_kernel(const __grid_co
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFullWarp, sum, o);
     int first = INT32_MAX;
-    if (greedy && all > -INFINITY) {  // in the first chunk that has it
+    if (greedy && all > -INFINITY) {  // in the first run that has it
       int chunk = INT32_MAX;
-      for (int c = lane; c < a.chunks; c += 32)
+      for (int c = lane; c < a.runs; c += 32)
         if (chunk == INT32_MAX && part[c].x == all) chunk = c;
       chunk = __reduce_min_sync(kFullWarp, chunk);
       const RowVecs<DT> x(a, row);
-      const int vecs = x.count();
-      for (int u = 0; u < kVecs; ++u) {
-        const int q = chunk * kChunkVecs + u * 32 + lane;
-        if (q >= vecs) continue;
+      const int q0 = chunk * a.run, q1 = min(q0 + a.run, x.count());
+      for (int q = q0 + lane; q < q1; q += 32) {
         const uint4 raw = __ldg(reinterpret_cast<const uint4*>(x.at) + q);
         const uint32_t keep = x.bits(q, x.mask_word(q));
 #pragma unroll
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_say_kernel(const __grid_co
     w.row = uint32_t(row), w.offset_lo = uint32_t(a.offset), w.offset_hi = uint32_t(a.offset >> 32);
     const bool whole = reinterpret_cast<uintptr_t>(w.x) % 16 == 0;
     const bool whole_q = w.q != nullptr && reinterpret_cast<uintptr_t>(w.q) % 16 == 0;
-    const float by = refused ? 1.0f / w.sum : 1.0f;
+    const float by = (refused ? -log2f(w.sum) : 0.0f) + 2.9e-5f;  // and 1.00002 times that
     // what rounding in the score as defined may make up for; nothing is passed over where the
     // scores are so large that it is much, or where the largest is +inf
     const float slack = fmaxf(0.0f, 0.999f - fabsf(w.shift) * 1e-6f);
@@ -508,7 +512,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_say_kernel(const __grid_co
       for (int e = 0; e < 8; ++e) {
         if (w.q == nullptr && int64_t(v0) + e == w.draft) g.d[e] = 1.0f;
         // p is within 1e-5 of itself: r is this, or less
-        r[e] = fmaf(ex2(relative(g.y[e], top) * rate) * by, 1.00002f, -g.d[e]);
+        const float d = top < INFINITY ? g.y[e] - top : relative(g.y[e], top);
+        r[e] = ex2(fmaf(d, rate, by)) - g.d[e];
         // (m is 2^-24 at least)
         live |= uint32_t(r[e] > 0.0f && r[e] >= bound * 5.9e-8f) << e;
       }
@@ -580,11 +585,15 @@ cudaError_t launch(VerifyArgs a, cudaStream_t stream) {
   cfg.attrs = attrs;
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(kStreamThreads);
-  // a run of chunks to a warp, or one where there are few in all
-  const int64_t few = int64_t(kSms) * 32;
-  a.run = int64_t(a.rows) * a.chunks < few * kRun ? 1 : kRun;
-  a.per_row.set(uint32_t((a.chunks + a.run - 1) / a.run));
-  const int64_t warps = int64_t(a.rows) * a.per_row.d;
+  // as many runs as there are warps on all SMs, of a chunk each at least
+  const int64_t resident = int64_t(kSms) * 5 * (kStreamThreads / 32);
+  const int64_t vecs = std::max<int64_t>(1, a.V / Elt<DT>::kPerVec + 2);
+  const int64_t most = (vecs + kChunkVecs - 1) / kChunkVecs;
+  const int64_t runs = std::max<int64_t>(1, std::min(most, resident / a.rows));
+  a.run = int((vecs + runs - 1) / runs + 31) / 32 * 32;
+  a.runs = int((vecs + a.run - 1) / a.run);
+  a.per_row.set(uint32_t(a.runs));
+  const int64_t warps = int64_t(a.rows) * a.runs;
   cfg.gridDim = dim3(unsigned((warps + kStreamThreads / 32 - 1) / (kStreamThreads / 32)));
   const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_stream_kernel<DT>, a);
   if (e != cudaSuccess) return e;
@@ -602,10 +611,10 @@ cudaError_t launch(VerifyArgs a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, verify_say_kernel<DT>, a);
 }
 
-// Chunks of a row, wherever it starts.
+// Runs of a row, at most: a chunk of vectors each.
 int64_t chunks_of(lp_dtype dt, int64_t V) {
   const int64_t per = dt == LP_F32 ? 4 : 8;
-  return std::max<int64_t>(1, (V + per - 1 + per * kChunkVecs - 1) / (per * kChunkVecs));
+  return (std::max<int64_t>(1, V / per + 2) + kChunkVecs - 1) / kChunkVecs;
 }
 
 }  // namespace
@@ -688,7 +697,6 @@ extern "C" lp_status lp_verify_drafts(const void* logits, lp_dtype dt, int64_t B
   a.out_tokens = out_tokens;
   a.out_accepted = out_accepted;
   a.part = static_cast<float2*>(workspace);
-  a.chunks = int(chunks_of(dt, V));
   const cudaError_t e = dt == LP_F32   ? launch<LP_F32>(a, stream)
                         : dt == LP_F16 ? launch<LP_F16>(a, stream)
                                        : launch<LP_BF16>(a, stream);
