@@ -10,9 +10,12 @@
 #include <cmath>
 
 #include "attend.cuh"
+#include "attend_row.cuh"
 
 namespace lp {
 
+bool chunk_fits(const AttendArgs& a);
+cudaError_t attend_chunk(const AttendArgs& a, cudaStream_t stream);
 cudaError_t attend_8n1(const AttendArgs& a, int block, cudaStream_t stream);
 cudaError_t attend_8n2(const AttendArgs& a, int block, cudaStream_t stream);
 cudaError_t attend_8w1(const AttendArgs& a, int block, cudaStream_t stream);
@@ -27,45 +30,9 @@ namespace {
 constexpr int kWarps = 4;       // of a block of the general kernels
 constexpr int kMostDim = 1024;
 
-// The value of element d of a head's codes.
-__device__ __forceinline__ float value_at(const AttendArgs& a, const uint8_t* codes,
-                                          const char* params, int d) {
-  const uint32_t held = *reinterpret_cast<const uint32_t*>(params + int64_t(d / a.group) * 4);
-  if (a.bits == 8) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(codes[d])));
-    return __fmul_rn(Elt<LP_F16>::half_bits_to_float(h & 0xffffu), __uint_as_float(held));
-  }
-  const uint32_t code = (codes[d >> 1] >> (4 * (d & 1))) & 15u;
-  return __fmaf_rn(float(code), __uint_as_float(held << 16), __uint_as_float(held & 0xffff0000u));
-}
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kFullWarp, x, o);
-  return x;
-}
-
-struct Head {  // of one part, at one slot
-  const uint8_t* codes;
-  const char* params;
-};
-
-__device__ __forceinline__ Head head_at(const AttendArgs& a, int part, int64_t slot, int h) {
-  const lp_cache_part& p = a.part[part];
-  Head r;
-  r.codes = static_cast<const uint8_t*>(p.codes) +
-            slot_place(a, slot, p.code_page_stride, p.code_slot_stride) + h * p.code_head_stride;
-  r.params = static_cast<const char*>(p.params) +
-             slot_place(a, slot, p.param_page_stride, p.param_slot_stride) +
-             h * p.param_head_stride;
-  return r;
-}
-
 // Any width, group, stride and alignment: a warp a query, its lanes across the head.
 __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ float shared_floats[];
-  const int lane = threadIdx.x & 31;
   float* q = shared_floats + (threadIdx.x >> 5) * 2 * a.dim;
   float* sum = q + a.dim;
   const int q_heads = a.heads * a.shared;
@@ -73,36 +40,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(const __grid_co
   for (int64_t i = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < total;
        i += int64_t(gridDim.x) * kWarps) {
     const int j = int(i % q_heads), r = int(i / q_heads % a.rows), b = int(i / q_heads / a.rows);
-    const int h = j / a.shared;
-    const Sequence s = sequence(a, b);
-    const Seen v = seen(a, s, r);
-    const char* from = static_cast<const char*>(a.q.data) + b * a.q.batch_stride +
-                       r * a.q.row_stride + j * a.q.head_stride;
-    char* to = static_cast<char*>(a.out.data) + b * a.out.batch_stride + r * a.out.row_stride +
-               j * a.out.head_stride;
-    for (int d = lane; d < a.dim; d += 32) q[d] = load_as_float(from, d, a.dt), sum[d] = 0.0f;
-    float top = -INFINITY, mass = 0.0f;
-    for (int t = v.lo; t < v.end; ++t) {
-      const int64_t slot = slot_of(a, b, t);
-      if (slot < 0) continue;
-      const Head key = head_at(a, 0, slot, h);
-      float x = 0.0f;
-      for (int d = lane; d < a.dim; d += 32) x += q[d] * value_at(a, key.codes, key.params, d);
-      x = warp_sum(x) * a.scale;
-      const float now = fmaxf(top, x);
-      const float ref = now == -INFINITY ? 0.0f : now;
-      const float keep = exp2f(top - ref), e = exp2f(x - ref);
-      top = now;
-      mass = mass * keep + e;
-      const Head value = head_at(a, 1, slot, h);
-      for (int d = lane; d < a.dim; d += 32)
-        sum[d] = sum[d] * keep + e * value_at(a, value.codes, value.params, d);
-    }
-    const float inv = mass == 0.0f ? 0.0f : 1.0f / mass;
-    for (int d = lane; d < a.dim; d += 32)
-      store_float(to, d, mass == 0.0f ? 0.0f : sum[d] * inv, a.dt);
-    if (a.lse != nullptr && lane == 0)
-      a.lse[i] = mass == 0.0f ? -INFINITY : top + log2f(mass);
+    attend_row(a, b, r, j, q, sum);
   }
 }
 
@@ -292,5 +230,12 @@ extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, i
   a.tops = reinterpret_cast<float2*>(left + held * a.dim * 4);
   static const Launch launches[2][2][2] = {{{attend_8n1, attend_8n2}, {attend_8w1, attend_8w2}},
                                            {{attend_4n1, attend_4n2}, {attend_4w1, attend_4w2}}};
+  a.wide_out = (reinterpret_cast<uintptr_t>(out->data) | uint64_t(a.out.batch_stride) |
+                uint64_t(a.out.row_stride) | uint64_t(a.out.head_stride)) % 8 == 0;
+  if (chunk_fits(a)) {
+    const cudaError_t e = attend_chunk(a, stream);
+    if (e != cudaSuccess || weights == nullptr) return status_of(e);
+    a.weights_only = true;
+  }
   return status_of(launches[bits == 4][dt != LP_BF16][at_once == 16](a, block, stream));
 }

@@ -1,0 +1,624 @@
+// attend_chunk.cu -- attention of many queries at once over a cache of 8 bits with one scale
+// a head: a prompt's chunk over what the cache holds of it, on the 5th-generation tensor cores.
+//
+// A block has 2 x 128 queries of one head of the cache (its query heads side by side) and goes
+// through the tokens in tiles of 128.  Codes become fp16 of the same value on their way to
+// shared memory; the scales stay outside, as in attend_mma.cuh:
+//   S = Q K^T   from shared memory, 128 x 128 in tensor memory
+//   P = 2^(s_k S unit - R) s_v, fp16, over S's place in tensor memory (two pieces, for fp16)
+//   O += P V    P from tensor memory, V from shared memory
+// R, which exponents are taken against, is the largest of x + floor(log2 s_v) some time ago: O
+// is scaled only when that grew by more than 2^kSlack, so P stays below 2^(kLift + kSlack + 1) = 2^15.
+//
+// Four roles, by warps: the two 128s of queries take turns, so that one's products run while
+// the other's exponentials do.
+//   0-3, 4-7   a thread a query: exponents, P, the sums
+//   8-11       codes to fp16, two tiles ahead
+//   12         issues the products
+// Every wait is bounded; where one runs out all roles stop and the block's queries become NaN.
+#include <algorithm>
+
+#include "attend.cuh"
+#include "attend_row.cuh"
+
+namespace lp {
+namespace {
+
+constexpr int kTile = 128;     // tokens
+constexpr int kThreads = 13 * 32;
+constexpr float kLift = 8.0f;
+constexpr float kSlack = 6.0f;
+constexpr int kLeastScale = -60;
+constexpr uint64_t kPatience = 2000000000;  // nanoseconds that a wait may take
+
+struct alignas(1024) Shared {
+  // each half of 64 elements: rows of 128 bytes, their 16-byte pieces permuted by row % 8
+  char q[2][2 * kTile * 128];
+  char k[2][2 * kTile * 128];
+  char v[2][2 * kTile * 128];
+  float key_scale[4][kTile], value_scale[4][kTile], value_log[4][kTile];
+  uint32_t held[4][4];  // bits of the tile's tokens that are there
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], drained;
+  const char* rows[2][2][kTile];  // of codes: [buffer][keys, values][token]
+  uint32_t tmem;
+  int failed, nan_hidden;
+};
+
+__device__ __forceinline__ uint32_t at(const void* p) {
+  return uint32_t(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void bar_init(uint64_t* b, int n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(at(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(at(b)) : "memory");
+}
+// False where the wait runs out, or another's did.
+__device__ __forceinline__ bool bar_wait(Shared& s, uint64_t* b, uint32_t phase) {
+  uint64_t began = 0, now;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done) : "r"(at(b)), "r"(phase) : "memory");
+    if (done) return true;
+    if ((i & 255u) != 255u) continue;
+    if (*static_cast<volatile int*>(&s.failed) != 0) return false;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+    if (began == 0) began = now;
+    if (now - began > kPatience) break;
+  }
+  *static_cast<volatile int*>(&s.failed) = 1;
+  return false;
+}
+
+// Whether it holds for all of the 128 threads that meet here.
+__device__ __forceinline__ bool all_of_128(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.and.pred q, 1, 128, p; "
+      "selp.u32 %0, 1, 0, q; }" : "=r"(r) : "r"(uint32_t(x)) : "memory");
+  return r != 0;
+}
+
+// Shared-memory operands: 128-byte swizzle; `leading` and `stride` in bytes.
+__device__ __forceinline__ uint64_t operand(const void* p, uint32_t leading, uint32_t stride) {
+  return uint64_t((at(p) & 0x3ffffu) >> 4) | uint64_t(leading >> 4) << 16 |
+         uint64_t(stride >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+// fp16 products into fp32; `turned`: B's contraction runs across its rows.
+__host__ __device__ constexpr uint32_t instruction(int m, int n, bool turned) {
+  return (1u << 4) | (turned ? 1u << 16 : 0u) | uint32_t(n / 8) << 17 | uint32_t(m / 16) << 24;
+}
+__device__ __forceinline__ void mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t what,
+                                           bool add) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b),
+      "r"(what), "r"(uint32_t(add))
+      : "memory");
+}
+__device__ __forceinline__ void mma_tensor(uint32_t d, uint32_t a, uint64_t b, uint32_t what,
+                                           bool add) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a), "l"(b),
+      "r"(what), "r"(uint32_t(add))
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(at(b))
+               : "memory");
+}
+
+#define LP_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), \
+                    "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define LP_W8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), \
+                    "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+
+// 32 columns of this thread's row.
+__device__ __forceinline__ void tensor_load(uint32_t (&x)[32], uint32_t from) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : LP_R8(x, 0), LP_R8(x, 8), LP_R8(x, 16), LP_R8(x, 24) : "r"(from));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tensor_store(uint32_t to, const uint32_t (&x)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::LP_W8(x, 0),
+      LP_W8(x, 8), LP_W8(x, 16), LP_W8(x, 24), "r"(to)
+      : "memory");
+}
+__device__ __forceinline__ void tensor_store16(uint32_t to, const uint32_t (&x)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15};" ::LP_W8(x, 0), LP_W8(x, 8), "r"(to)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return uint64_t(__float_as_uint(a)) | uint64_t(__float_as_uint(b)) << 32;
+}
+__device__ __forceinline__ float lower(uint64_t v) { return __uint_as_float(uint32_t(v)); }
+__device__ __forceinline__ float upper(uint64_t v) { return __uint_as_float(uint32_t(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t halves(float low, float high) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(high), "f"(low));
+  return r;
+}
+
+// 16 codes as fp16, two pieces of a row.
+__device__ __forceinline__ void put_codes(char* half, int row, int piece, const uint4& c) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * i]) : "h"(uint16_t(w[i])));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * i + 1]) : "h"(uint16_t(w[i] >> 16)));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    *reinterpret_cast<uint4*>(half + row * 128 + (((piece * 2 + i) ^ (row & 7)) << 4)) =
+        make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+}
+
+__device__ __forceinline__ bool has_nan(const uint4& c) {
+  const auto one = [](uint32_t w) { return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0; };
+  return one(c.x) || one(c.y) || one(c.z) || one(c.w);
+}
+
+template <int DIM, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_chunk_kernel(const __grid_constant__ AttendArgs a) {
+  extern __shared__ char raw_shared[];
+  Shared& s = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw_shared) + 1023) &
+                                         ~uintptr_t(1023));
+  constexpr int kPieces = DIM / 16;      // 16 codes each
+  constexpr uint32_t kHalf = kTile * 128;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per_head = a.rows * a.shared;
+  const int pairs = (per_head + 2 * kTile - 1) / (2 * kTile);
+  // the last rows see most: they begin first
+  const int pr = pairs - 1 - int(blockIdx.x % pairs);
+  const int h = blockIdx.x / pairs % a.heads, b = blockIdx.x / pairs / a.heads;
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(at(&s.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&s.k_full[i], 128), bar_init(&s.v_full[i], 128);
+      bar_init(&s.k_empty[i], 1), bar_init(&s.v_empty[i], 1);
+      bar_init(&s.s_full[i], 1), bar_init(&s.p_full[i], 128), bar_init(&s.o_done[i], 1);
+    }
+    bar_init(&s.drained, 1);
+    s.failed = s.nan_hidden = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Sequence seq = sequence(a, b);
+  const int i0 = pr * 2 * kTile;  // of the rows and query heads of this head
+  const int r0 = i0 / a.shared;
+  const int r1 = min(min(i0 + 2 * kTile, per_head) - 1, max(0, seq.rows * a.shared - 1)) / a.shared;
+  const bool any = r0 < seq.rows;
+  const Seen low = seen(a, seq, any ? r0 : 0), high = seen(a, seq, any ? r1 : 0);
+  // tiles that any row sees; tokens that all of them see
+  const int first = any ? low.lo / kTile : 0;
+  const int last = any ? max(first, (high.end + kTile - 1) / kTile) : 0;
+  const int tiles = last - first;
+  const int all_from = high.lo, all_until = low.end;
+
+  // queries, scaled to 2^14 by a power of two a row
+  float unit = 0.0f;
+  int row = 0, r = 0, j = 0;
+  bool there = false;
+  if (warp < 8) {
+    row = i0 + tid;
+    r = row / a.shared, j = h * a.shared + row - r * a.shared;
+    there = row < per_head && r < seq.rows;
+    const char* from = static_cast<const char*>(a.q.data) + b * a.q.batch_stride +
+                       r * a.q.row_stride + j * a.q.head_stride;
+    char* to = s.q[warp >> 2];
+    const int in = tid & 127;
+    uint2 held[DIM / 4];  // four elements each, of 16 bits
+#pragma unroll
+    for (int c = 0; c < DIM / 4; ++c) {
+      held[c] = make_uint2(0, 0);
+      if (there && a.wide_q) {
+        held[c] = __ldg(reinterpret_cast<const uint2*>(from) + c);
+      } else if (there) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint16_t*>(from + (c * 4 + e) * 2);
+        held[c] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      }
+    }
+    const auto value = [&](int d) {
+      const uint32_t w = (d & 2) ? held[d / 4].y : held[d / 4].x;
+      const uint32_t bits = (d & 1) ? w >> 16 : w & 0xffffu;
+      return WIDE ? Elt<LP_F16>::half_bits_to_float(bits) : __uint_as_float(bits << 16);
+    };
+    float most = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DIM; ++d) most = fmaxf(most, fabsf(value(d)));
+    const int up = most > 0.0f && most <= 3.4028235e38f
+                       ? 14 - (int(__float_as_uint(most) >> 23) - 127) : 0;
+    const float f1 = __uint_as_float(uint32_t(up / 2 + 127) << 23);
+    const float f2 = __uint_as_float(uint32_t(up - up / 2 + 127) << 23);
+    unit = a.scale / f1 / f2;
+#pragma unroll
+    for (int c = 0; c < DIM / 8; ++c) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = halves(value(c * 8 + 2 * e) * f1 * f2, value(c * 8 + 2 * e + 1) * f1 * f2);
+      *reinterpret_cast<uint4*>(to + (c >> 3) * kHalf + in * 128 + (((c & 7) ^ (in & 7)) << 4)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = s.tmem;
+  // columns: S (and P) of the two 128s, then O
+  const uint32_t o_at = tmem + 256;
+
+  float mass = 0.0f, ref = -INFINITY;
+  if (warp < 8) {
+    // ---------------------------------------------------------------- a thread a query
+    const int half = warp >> 2;
+    const uint32_t lanes = uint32_t(warp & 3) << 21;  // 32 lanes, at bit 16
+    const uint32_t s_mine = tmem + half * 128 + lanes, o_mine = o_at + half * DIM + lanes;
+    const Seen v = there ? seen(a, seq, r) : Seen{0, 0};
+    const uint64_t unit2 = pair(unit, unit);
+    for (int t = 0; t < tiles; ++t) {
+      if (!__all_sync(kFullWarp, bar_wait(s, &s.s_full[half], t & 1))) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const int t0 = (first + t) * kTile, slot = t & 3;
+      const float* ks = s.key_scale[slot];
+      const float* vs = s.value_scale[slot];
+      const float* vl = s.value_log[slot];
+      const bool all = t0 >= all_from && t0 + kTile <= all_until &&
+                       (s.held[slot][0] & s.held[slot][1] & s.held[slot][2] & s.held[slot][3]) == ~0u;
+      float now = ref;
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) {
+        uint32_t x[32];
+        tensor_load(x, s_mine + c);
+        // bits of the columns that this row sees
+        uint32_t bits = ~0u;
+        if (!all) {
+          const int lo = min(max(v.lo - t0 - c, 0), 32), hi = min(max(v.end - t0 - c, 0), 32);
+          bits = lo >= hi ? 0u : (hi == 32 ? ~0u : (1u << hi) - 1u) & ~((1u << lo) - 1u);
+          bits &= s.held[slot][c >> 5];
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(ks + c + e);
+          const ulonglong2 l2 = *reinterpret_cast<const ulonglong2*>(vl + c + e);
+          const uint64_t y0 = fma2(mul2(uint64_t(x[e]) | uint64_t(x[e + 1]) << 32, k2.x), unit2, l2.x);
+          const uint64_t y1 = fma2(mul2(uint64_t(x[e + 2]) | uint64_t(x[e + 3]) << 32, k2.y), unit2, l2.y);
+          if (all) {
+            now = fmaxf(now, fmaxf(fmaxf(lower(y0), upper(y0)), fmaxf(lower(y1), upper(y1))));
+          } else {
+            now = fmaxf(now, bits & (1u << e) ? lower(y0) : -INFINITY);
+            now = fmaxf(now, bits & (2u << e) ? upper(y0) : -INFINITY);
+            now = fmaxf(now, bits & (4u << e) ? lower(y1) : -INFINITY);
+            now = fmaxf(now, bits & (8u << e) ? upper(y1) : -INFINITY);
+          }
+        }
+      }
+      // the reference moves where something has outgrown it (the first time, always)
+      const bool grow = now > ref + kSlack || (ref == -INFINITY && now > -INFINITY);
+      if (__any_sync(kFullWarp, grow)) {
+        const float f = grow ? (ref == -INFINITY ? 0.0f : ex2(ref - now)) : 1.0f;
+        if (grow) ref = now, mass *= f;
+        if (t > 0) {
+#pragma unroll 1
+          for (int c = 0; c < DIM; c += 32) {
+            uint32_t x[32];
+            tensor_load(x, o_mine + c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              x[e] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(x[e]) * f);
+            tensor_store(o_mine + c, x);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+      }
+      const float base = (ref == -INFINITY ? 0.0f : -ref) + kLift;
+      const uint64_t base2 = pair(base, base);
+      uint64_t sum2 = 0;
+      uint32_t rest[WIDE ? 64 : 1];
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) {
+        uint32_t x[32];
+        tensor_load(x, s_mine + c);
+        uint32_t bits = ~0u;
+        if (!all) {
+          const int lo = min(max(v.lo - t0 - c, 0), 32), hi = min(max(v.end - t0 - c, 0), 32);
+          bits = lo >= hi ? 0u : (hi == 32 ? ~0u : (1u << hi) - 1u) & ~((1u << lo) - 1u);
+          bits &= s.held[slot][c >> 5];
+        }
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(ks + c + e);
+          const ulonglong2 v2 = *reinterpret_cast<const ulonglong2*>(vs + c + e);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int i = e + 2 * u;
+            const uint64_t y = fma2(mul2(uint64_t(x[i]) | uint64_t(x[i + 1]) << 32, u ? k2.y : k2.x),
+                                    unit2, base2);
+            float e0 = ex2(lower(y)), e1 = ex2(upper(y));
+            if (!all) {
+              e0 = bits & (1u << i) ? e0 : 0.0f;
+              e1 = bits & (2u << i) ? e1 : 0.0f;
+            }
+            const uint64_t ee = pair(e0, e1);
+            sum2 = add2(sum2, ee);
+            const uint64_t w = mul2(ee, u ? v2.y : v2.x);
+            p[i / 2] = halves(lower(w), upper(w));
+            if (WIDE)
+              rest[c / 2 + i / 2] = halves(
+                  lower(w) - Elt<LP_F16>::half_bits_to_float(p[i / 2] & 0xffffu),
+                  upper(w) - Elt<LP_F16>::half_bits_to_float(p[i / 2] >> 16));
+          }
+        }
+        tensor_store16(s_mine + c / 2, p);  // over what was read of S
+      }
+      if (WIDE) {  // over the rest of S, once all of it is read
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = rest[c + e];
+          tensor_store(s_mine + 64 + c, x);
+        }
+      }
+      mass += lower(sum2) + upper(sum2);
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      bar_arrive(&s.p_full[half]);
+    }
+    if (tiles > 0) bar_wait(s, &s.o_done[half], 0);
+    __syncwarp();
+  } else if (warp < 12) {
+    // ------------------------------------------------------- codes on their way to the products
+    const int in = tid - 256;  // its token, for what is done once a token
+    const lp_cache_part &kp = a.part[0], &vp = a.part[1];
+    const int piece = in % kPieces, line = in / kPieces;   // its 16 codes, of every kLines-th token
+    constexpr int kLines = 128 / kPieces, kMine = kTile / kLines;
+    float scale[2];
+    const auto look = [&](int t) {  // a tile's tokens: where they lie, and their scales
+      const int token = (first + t) * kTile + in;
+      const int64_t slot = t < tiles && token < high.end ? slot_of(a, b, token) : -1;
+      const uint32_t held = __ballot_sync(kFullWarp, slot >= 0);
+      if (t >= tiles) return;
+      if (lane == 0) s.held[t & 3][in >> 5] = held;
+      scale[0] = scale[1] = 0.0f;
+      s.rows[t & 1][0][in] = s.rows[t & 1][1][in] = nullptr;
+      if (slot >= 0) {
+        s.rows[t & 1][0][in] = static_cast<const char*>(kp.codes) + h * kp.code_head_stride +
+                               slot_place(a, slot, kp.code_page_stride, kp.code_slot_stride);
+        s.rows[t & 1][1][in] = static_cast<const char*>(vp.codes) + h * vp.code_head_stride +
+                               slot_place(a, slot, vp.code_page_stride, vp.code_slot_stride);
+        scale[0] = *reinterpret_cast<const float*>(
+            static_cast<const char*>(kp.params) + h * kp.param_head_stride +
+            slot_place(a, slot, kp.param_page_stride, kp.param_slot_stride));
+        scale[1] = *reinterpret_cast<const float*>(
+            static_cast<const char*>(vp.params) + h * vp.param_head_stride +
+            slot_place(a, slot, vp.param_page_stride, vp.param_slot_stride));
+      }
+    };
+    const auto put_scales = [&](int t) {
+      s.key_scale[t & 3][in] = scale[0];
+      s.value_scale[t & 3][in] = scale[1];
+      s.value_log[t & 3][in] =
+          float(max(int((__float_as_uint(scale[1]) >> 23) & 255u) - 127, kLeastScale));
+    };
+    uint4 codes[2][kMine];
+    const auto fetch = [&](int t, int part) {
+      if (t >= tiles) return;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const char* p = s.rows[t & 1][part][line + i * kLines];
+        codes[part][i] = p != nullptr ? __ldg(reinterpret_cast<const uint4*>(p) + piece)
+                                      : make_uint4(0, 0, 0, 0);
+      }
+    };
+    look(0);
+    all_of_128(true);
+    fetch(0, 0);
+    fetch(0, 1);
+    for (int t = 0; t < tiles; ++t) {
+      const int stage = t & 1;
+      const uint32_t turn = ((t >> 1) & 1) ^ 1;  // the first turn of each stage does not wait
+      // (a tile's scales are read until its P is there: four tiles have them apart)
+      if (!all_of_128(bar_wait(s, &s.k_empty[stage], turn))) break;
+      put_scales(t);
+      char* k = s.k[stage];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        put_codes(k + (piece >> 2) * kHalf, line + i * kLines, piece & 3, codes[0][i]);
+      look(t + 1);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      bar_arrive(&s.k_full[stage]);
+      // (the next tile's places are there, too)
+      if (!all_of_128(bar_wait(s, &s.v_empty[stage], turn))) break;
+      fetch(t + 1, 0);
+      char* v = s.v[stage];
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        put_codes(v + (piece >> 2) * kHalf, line + i * kLines, piece & 3, codes[1][i]);
+        bad = bad || has_nan(codes[1][i]);
+      }
+      // NaN values in tokens that some rows do not see would reach those by 0 * NaN
+      const int t0 = (first + t) * kTile;
+      if (bad && !(t0 >= all_from && t0 + kTile <= all_until))
+        *static_cast<volatile int*>(&s.nan_hidden) = 1;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      bar_arrive(&s.v_full[stage]);
+      fetch(t + 1, 1);
+    }
+  } else if (lane == 0 && tiles > 0) {
+    // ------------------------------------------------------------------- the products' issue
+    constexpr uint32_t kScore = instruction(kTile, kTile, false);
+    constexpr uint32_t kValue = instruction(kTile, DIM, true);
+    const auto score = [&](int t, int half) {
+#pragma unroll
+      for (int i = 0; i < DIM / 16; ++i) {
+        const uint32_t off = (i >> 2) * kHalf + (i & 3) * 32;
+        mma_shared(tmem + half * 128, operand(s.q[half] + off, 16, 1024),
+                   operand(s.k[t & 1] + off, 16, 1024), kScore, i > 0);
+      }
+      commit(&s.s_full[half]);
+    };
+    bool ok = bar_wait(s, &s.k_full[0], 0);
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (ok) score(0, 0), score(0, 1), commit(&s.k_empty[0]);
+    for (int t = 0; ok && t < tiles; ++t) {
+      for (int half = 0; ok && half < 2; ++half) {
+        ok = bar_wait(s, &s.p_full[half], t & 1) &&
+             (half == 1 || bar_wait(s, &s.v_full[t & 1], (t >> 1) & 1)) &&
+             (half == 1 || t + 1 == tiles || bar_wait(s, &s.k_full[(t + 1) & 1], ((t + 1) >> 1) & 1));
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+        for (int piece = WIDE ? 1 : 0; piece >= 0; --piece)
+#pragma unroll
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_tensor(o_at + half * DIM, tmem + half * 128 + piece * 64 + i * 8,
+                       operand(s.v[t & 1] + i * 2048, kHalf, 1024), kValue,
+                       t > 0 || i > 0 || piece != (WIDE ? 1 : 0));
+        if (t + 1 == tiles) commit(&s.o_done[half]);
+        if (half == 1) commit(&s.v_empty[t & 1]);
+        // S of the next tile goes where this one's P was: products run in their order
+        if (t + 1 < tiles) score(t + 1, half);
+        if (half == 1 && t + 1 < tiles) commit(&s.k_empty[(t + 1) & 1]);
+      }
+    }
+    if (!ok) {  // tensor memory is given back only when nothing writes it any more
+      commit(&s.drained);
+      *static_cast<volatile int*>(&s.failed) = 0;
+      bar_wait(s, &s.drained, 0);
+      *static_cast<volatile int*>(&s.failed) = 1;
+    }
+  }
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const bool failed = *static_cast<volatile int*>(&s.failed) != 0;
+  const bool again = *static_cast<volatile int*>(&s.nan_hidden) != 0 && !failed;
+  if (warp < 8 && !again) {
+    // ------------------------------------------------------------------------------- results
+    char* to = static_cast<char*>(a.out.data) + b * a.out.batch_stride + r * a.out.row_stride +
+               j * a.out.head_stride;
+    const uint32_t o_mine = o_at + (warp >> 2) * DIM + (uint32_t(warp & 3) << 21);
+    const bool none = mass == 0.0f || tiles == 0 || !there;
+    const float inv = failed ? __uint_as_float(0x7fc00000u) : 1.0f / mass;
+    if (a.lse != nullptr && row < per_head)
+      a.lse[(int64_t(b) * a.rows + r) * (a.heads * a.shared) + j] =
+          none ? -INFINITY : ref - kLift + log2f(mass);
+#pragma unroll 1
+    for (int c = 0; c < DIM; c += 32) {
+      uint32_t x[32];
+      __syncwarp();
+      if (tiles > 0) {
+        tensor_load(x, o_mine + c);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = 0;
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        x[e] = none ? 0u : __float_as_uint(__uint_as_float(x[e]) * inv);
+      if (row >= per_head) continue;
+      if (a.wide_out) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          uint32_t w[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float y = __uint_as_float(x[e + 2 * u]), z = __uint_as_float(x[e + 2 * u + 1]);
+            if (WIDE) w[u] = halves(y, z);
+            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[u]) : "f"(z), "f"(y));
+          }
+          *reinterpret_cast<uint2*>(to + (c + e) * 2) = make_uint2(w[0], w[1]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) store_float(to, c + e, __uint_as_float(x[e]), a.dt);
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (again) {  // row by row, as defined: a warp each, its scratch where the queries were
+    float* mine = reinterpret_cast<float*>(s.k[0]) + warp * 2 * DIM;
+    for (int i = warp; i < 2 * kTile; i += kThreads / 32)
+      if (i0 + i < per_head) {
+        const int rr = (i0 + i) / a.shared;
+        attend_row(a, b, rr, h * a.shared + i0 + i - rr * a.shared, mine, mine + DIM);
+      }
+  }
+}
+
+template <int DIM, bool WIDE>
+cudaError_t launch_chunk(const AttendArgs& a, cudaStream_t stream) {
+  static PerDevice<1> allowed;
+  const int smem = int(sizeof(Shared)) + 1024;
+  const cudaError_t e = allow_shared(attend_chunk_kernel<DIM, WIDE>, smem, allowed);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = (int64_t(a.rows) * a.shared + 2 * kTile - 1) / (2 * kTile);
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(pairs * a.heads * a.batch));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_chunk_kernel<DIM, WIDE>, a);
+}
+
+}  // namespace
+
+bool chunk_fits(const AttendArgs& a) {
+  const int64_t rows = int64_t(a.rows) * a.shared;
+  const int64_t blocks = (rows + 2 * kTile - 1) / (2 * kTile) * a.heads * a.batch;
+  return a.bits == 8 && a.group == a.dim && (a.dim == 64 || a.dim == 128) && a.dt != LP_F32 &&
+         rows >= kTile && blocks >= kSms / 4 && blocks <= INT32_MAX;
+}
+
+cudaError_t attend_chunk(const AttendArgs& a, cudaStream_t stream) {
+  if (a.dim == 128)
+    return a.dt == LP_BF16 ? launch_chunk<128, false>(a, stream) : launch_chunk<128, true>(a, stream);
+  return a.dt == LP_BF16 ? launch_chunk<64, false>(a, stream) : launch_chunk<64, true>(a, stream);
+}
+
+}  // namespace lp

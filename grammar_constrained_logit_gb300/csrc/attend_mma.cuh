@@ -1133,28 +1133,29 @@ cudaError_t prepare_kernel(void (*kernel)(AttendArgs), int warps, PerDevice<5>& 
 
 template <class T>
 cudaError_t attend_with(AttendArgs a, cudaStream_t stream) {
+  static PerDevice<5> known, known_weights;
   const int teams = a.team >= 3 ? 1 : 4 / a.team, warps = a.team * teams;
+  const size_t smem = size_t(warps) * T::kStages * T::kStage;
   a.row_tiles = (a.rows * a.shared + T::kRows - 1) / T::kRows;
   int blocks = 0;
-  static PerDevice<5> known, known_weights;
-  cudaError_t e = prepare_kernel<T>(attend_kernel<T>, warps, known, &blocks);
-  if (e != cudaSuccess) return e;
-  // every head group has the same number of workers
-  if (blocks * teams < a.head_groups) blocks = (a.head_groups + teams - 1) / teams;
-  a.workers = blocks * teams / a.head_groups;
-  e = launch_after(attend_kernel<T>, dim3(blocks), dim3(warps * 32),
-                   size_t(warps) * T::kStages * T::kStage, stream, a);
-  if (e != cudaSuccess) return e;
-  const int64_t rows = int64_t(a.batch) * a.heads * a.rows * a.shared;
-  e = launch_after(attend_join_kernel<T::kTile, T::kRows>, dim3(unsigned(rows)),
-                   dim3(kJoinWarps * 32), 0,
-                   stream, a);
+  cudaError_t e = cudaSuccess;
+  if (!a.weights_only) {
+    e = prepare_kernel<T>(attend_kernel<T>, warps, known, &blocks);
+    if (e != cudaSuccess) return e;
+    // every head group has the same number of workers
+    if (blocks * teams < a.head_groups) blocks = (a.head_groups + teams - 1) / teams;
+    a.workers = blocks * teams / a.head_groups;
+    e = launch_after(attend_kernel<T>, dim3(blocks), dim3(warps * 32), smem, stream, a);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = int64_t(a.batch) * a.heads * a.rows * a.shared;
+    e = launch_after(attend_join_kernel<T::kTile, T::kRows>, dim3(unsigned(rows)),
+                     dim3(kJoinWarps * 32), 0, stream, a);
+  }
   if (e != cudaSuccess || a.weights == nullptr) return e;
   e = prepare_kernel<T>(weights_kernel<T>, warps, known_weights, &blocks);
   if (e != cudaSuccess) return e;
   a.workers = blocks * teams;
-  return launch_after(weights_kernel<T>, dim3(blocks), dim3(warps * 32),
-                      size_t(warps) * T::kStages * T::kStage, stream, a);
+  return launch_after(weights_kernel<T>, dim3(blocks), dim3(warps * 32), smem, stream, a);
 }
 
 // The largest block of elements that a group holds whole, of those that there are kernels for.

@@ -487,14 +487,15 @@ lp_status lp_cache_read(const lp_cache_part* parts, const lp_heads* out, int64_t
  *            query heads of h
  * Codes are taken as the whole numbers or e4m3 values that they are, and scaled in 32 bits.
  * Queries of 16 bits are taken as they are, those of 32 bits rounded to 22 bits or more.
- * A weight p_t is rounded to 11 bits for bf16 and to 22 for the other types (1.5 * 2^-39 of
- * the row's largest product of weight and value's scale where it is small).  Sums are 32-bit.
+ * A weight p_t is rounded to 11 bits for bf16 and to 22 for the other types, and to 2^-33 of
+ * the row's largest product of weight and value's scale (2^-39 for 32-bit queries; a scale
+ * below 2^-60 counts as that) where it is smaller.  Sums are 32-bit.
  *   q, out       [batch, rows, q_heads, dim] of type dt, dim contiguous, strides in elements
  *   blocks       device int32 [batch, max_blocks], blocks_stride elements from row to row
  *   lengths      device int32 [batch];  n_rows: device int32 [batch], or NULL: all
  *   workspace    device scratch of lp_cache_attend_workspace_bytes, 16-byte aligned, of any
- *                content.  A call is two kernels, or three with weights, that hand on sums in
- *                it: calls that share it must be ordered, as lp_beam_select's
+ *                content.  A call is one to three kernels that hand on sums in it: calls that
+ *                share it must be ordered, as lp_beam_select's
  * Equal calls give equal results to the last bit.  Invalid: what lp_cache_write refuses of a
  * cache; q_heads not a multiple of heads; a negative size; block_size < 1; blocks_stride <
  * max_blocks; NULL or misaligned pointers with work to do; a scale that is not finite.  dim

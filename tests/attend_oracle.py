@@ -61,7 +61,9 @@ def attended(kv, q, blocks, lengths, size, *, n_rows=None, scale=None, window=No
     products in 32 bits, of which tensor cores cut off bits (2^-23 a step, at most), a product
     with the scale and one with its group's params; an exponential is off by 2^-21.  A
     weight that is small beside the row's largest product of weight and scale is rounded to
-    1.5 * 2^-39 of that, times codes up to 448."""
+    1.5 * 2^-39 of that (2^-32 for 16-bit queries, whose largest product is held at 2^8 to
+    2^15), times codes up to 448; a scale below 2^-60, as of a value of zeros, counts as
+    2^-60 there."""
     batch, rows, q_heads, dim = q.shape
     slots, heads = kv.shape[1], kv.shape[2]
     shared = q_heads // heads
@@ -92,7 +94,8 @@ def attended(kv, q, blocks, lengths, size, *, n_rows=None, scale=None, window=No
                 out[b, r, j] = p @ v
                 mass = p @ np.abs(v)
                 far = mass if reach is None else p @ reach[at[t], h]
-                small = t.size * 448 * 2.0 ** -38 * np.nanmax(p[:, None] * np.abs(v))
+                small = t.size * 448 * (2.0 ** -38 if dtype == "f32" else 2.0 ** -32) * \
+                    max(np.nanmax(p[:, None] * np.abs(v)), p.max() * 2.0 ** -60)
                 rel = 2 * d + (t.size + 64) * 2.0 ** -24
                 off[b, r, j] = rel * (mass + far) + WEIGHT[dtype] * far + small + \
                     HALF_STEP[dtype] * np.abs(out[b, r, j])

@@ -272,6 +272,72 @@ def test_prompt_chunk(bits, group, rows, dtype):
           n_rows=[rows, rows - 7, rows])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [128, 64])
+@pytest.mark.parametrize("window", [None, 100])
+def test_many_rows(dtype, dim, window):
+    """As many queries to a head as the tensor-memory kernels take: odd numbers of them, rows
+    that see nothing or are not there, lengths below a tile and at its end."""
+    rng = np.random.default_rng(20)
+    rows, heads, shared = 97, 8, 3
+    lengths = [97, 600, 128, 256, 5, 0, 301]
+    n_rows = [97, 97, 60, 97, 97, 97, 0]
+    total = (sum(-(-n // 16) for n in lengths) + 1) * 16
+    cache = filled(total, heads, dim, 8, dim, page=16)
+    blocks = table(rng, lengths, 16, total)
+    blocks[1, 20] = -1  # 16 tokens that are not there
+    q = rng.standard_normal((7, rows, heads * shared, dim)).astype(np.float32)
+    kw = {} if window is None else {"window": window}
+    check(cache, q, blocks, lengths, 16, dtype, weights=True, n_rows=n_rows, **kw)
+
+
+def test_many_rows_peaked_and_far():
+    """Scores of hundreds, and values of sizes far apart: what a row's weights are taken against
+    moves often."""
+    rng = np.random.default_rng(21)
+    cache = filled(1024, 8, 128, 8, 128, spread=3.0)
+    g = torch.Generator("cuda").manual_seed(9)
+    x = torch.randn(1024, 8, 128, device="cuda", generator=g)
+    mag = torch.exp(torch.randn(1024, 1, 1, device="cuda", generator=g) * 4)
+    mag[::5] = 0.0
+    ops.cache_write(cache, (x * 2, x.flip(0) * mag), torch.arange(1024, device="cuda"))
+    blocks = np.arange(64, dtype=np.int32)[None].repeat(5, 0)
+    for scale in (None, 2.0, -1.0, 0.0):
+        q = rng.standard_normal((5, 40, 32, 128)).astype(np.float32)
+        check(cache, q, blocks, [1000, 900, 777, 512, 300], 16, "bf16", scale=scale, weights=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_many_rows_nan(dtype):
+    """NaN values where some rows do not look, and where all of them do."""
+    rng = np.random.default_rng(22)
+    cache = filled(512, 8, 128, 8, 128)
+    blocks = np.arange(32, dtype=np.int32)[None].repeat(5, 0)
+    q = rng.standard_normal((5, 130, 16, 128)).astype(np.float32)
+    bad = torch.full((1, 8, 128), 0.5, device="cuda")
+    bad[..., 7] = float("nan")
+    fine = torch.full((1, 8, 128), 0.5, device="cuda")
+    lengths = [400] * 5
+    qd = torch.from_numpy(q).cuda().to(TYPES[dtype])
+    args = (torch.from_numpy(blocks).cuda(),
+            torch.tensor(lengths, dtype=torch.int32, device="cuda"))
+    # token 390 is hidden from rows below 120; tokens behind the end are nobody's
+    for t in (390, 400, 511):
+        ops.cache_write(cache, (fine, bad), torch.tensor([t], device="cuda"))
+    got = ops.cache_attend(cache, qd, *args, block_size=16).double().cpu().numpy()
+    assert np.isnan(got[:, 120:, :, 7]).all()
+    got[:, 120:, :, 7] = 0.0
+    assert np.isfinite(got).all()
+    want, off, _, _ = attended(np.nan_to_num(held(cache)), qd[:1].double().cpu().numpy(),
+                               blocks[:1], lengths[:1], 16, dtype=dtype)
+    want[:, 120:, :, 7] = 0.0
+    assert (np.abs(got[:1] - want) <= off).all()
+    # seen by all
+    ops.cache_write(cache, (fine, bad), torch.tensor([3], device="cuda"))
+    got = ops.cache_attend(cache, qd, *args, block_size=16)
+    assert got[..., 7].isnan().all() and got[..., :7].isfinite().all()
+
+
 def test_block_larger_than_a_page_and_smaller():
     rng = np.random.default_rng(13)
     cache = filled(512, 2, 64, 8, 64, page=32)
