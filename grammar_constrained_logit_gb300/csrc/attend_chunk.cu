@@ -131,13 +131,6 @@ __device__ __forceinline__ void tensor_store(uint32_t to, const uint32_t (&x)[32
       LP_W8(x, 8), LP_W8(x, 16), LP_W8(x, 24), "r"(to)
       : "memory");
 }
-__device__ __forceinline__ void tensor_store16(uint32_t to, const uint32_t (&x)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15};" ::LP_W8(x, 0), LP_W8(x, 8), "r"(to)
-      : "memory");
-}
-
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   return uint64_t(__float_as_uint(a)) | uint64_t(__float_as_uint(b)) << 32;
 }
@@ -182,6 +175,134 @@ __device__ __forceinline__ void put_codes(char* half, int row, int piece, const 
 __device__ __forceinline__ bool has_nan(const uint4& c) {
   const auto one = [](uint32_t w) { return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0; };
   return one(c.x) || one(c.y) || one(c.z) || one(c.w);
+}
+
+// 16 columns, under way while the ones before are worked on.
+__device__ __forceinline__ void tensor_load16(uint32_t (&x)[16], uint32_t from) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : LP_R8(x, 0), LP_R8(x, 8) : "r"(from));
+}
+// What was loaded is there; ties its registers to this place.
+__device__ __forceinline__ void tensor_landed(uint32_t (&x)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int e = 0; e < 16; e += 8)
+    asm volatile("" : "+r"(x[e]), "+r"(x[e + 1]), "+r"(x[e + 2]), "+r"(x[e + 3]), "+r"(x[e + 4]),
+                      "+r"(x[e + 5]), "+r"(x[e + 6]), "+r"(x[e + 7]));
+}
+
+// One query's view of a tile.
+struct Look {
+  uint32_t s_mine;          // its row of S
+  const float *ks, *vs, *vl;
+  const uint32_t* held;
+  uint64_t unit2;
+  int lo, end;              // tokens that it sees, from the tile's first
+
+  // bits of 16 columns from c
+  __device__ __forceinline__ uint32_t bits(int c) const {
+    const int a = min(max(lo - c, 0), 16), b = min(max(end - c, 0), 16);
+    return (a >= b ? 0u : ((1u << b) - 1u) & ~((1u << a) - 1u)) & (held[c >> 5] >> (c & 31));
+  }
+};
+
+// The largest of x + floor(log2 s_v), and of `now`.  ALL: the query sees every token.
+template <bool ALL>
+__device__ __forceinline__ float row_largest(const Look& w, float now) {
+  uint32_t x[2][16];
+  tensor_load16(x[0], w.s_mine);
+#pragma unroll
+  for (int c = 0; c < kTile; c += 16) {
+    uint32_t(&y)[16] = x[(c >> 4) & 1];
+    tensor_landed(y);
+    if (c + 16 < kTile) tensor_load16(x[((c >> 4) + 1) & 1], w.s_mine + c + 16);
+    const uint32_t bits = ALL ? 0u : w.bits(c);
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(w.ks + c + e);
+      const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(w.vl + c + e);
+      const uint64_t a = fma2(mul2(uint64_t(y[e]) | uint64_t(y[e + 1]) << 32, k.x), w.unit2, l.x);
+      const uint64_t b = fma2(mul2(uint64_t(y[e + 2]) | uint64_t(y[e + 3]) << 32, k.y), w.unit2, l.y);
+      if (ALL) {
+        now = fmaxf(now, fmaxf(fmaxf(lower(a), upper(a)), fmaxf(lower(b), upper(b))));
+      } else {
+        now = fmaxf(now, bits & (1u << e) ? lower(a) : -INFINITY);
+        now = fmaxf(now, bits & (2u << e) ? upper(a) : -INFINITY);
+        now = fmaxf(now, bits & (4u << e) ? lower(b) : -INFINITY);
+        now = fmaxf(now, bits & (8u << e) ? upper(b) : -INFINITY);
+      }
+    }
+  }
+  return now;
+}
+
+// P of 16 columns from c, whose S is y: eight words.
+template <bool ALL, typename F>
+__device__ __forceinline__ void weights16(const Look& w, int c, const uint32_t (&y)[16],
+                                          uint64_t base2, F&& each) {
+  const uint32_t bits = ALL ? 0u : w.bits(c);
+#pragma unroll
+  for (int e = 0; e < 16; e += 4) {
+    const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(w.ks + c + e);
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(w.vs + c + e);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = e + 2 * u;
+      const uint64_t z = fma2(mul2(uint64_t(y[i]) | uint64_t(y[i + 1]) << 32, u ? k.y : k.x),
+                              w.unit2, base2);
+      float e0 = ex2(lower(z)), e1 = ex2(upper(z));
+      if (!ALL) {
+        e0 = bits & (1u << i) ? e0 : 0.0f;
+        e1 = bits & (2u << i) ? e1 : 0.0f;
+      }
+      const uint64_t ee = pair(e0, e1);
+      each(i / 2, ee, mul2(ee, u ? v.y : v.x));
+    }
+  }
+}
+
+// P and its sum; *most: the largest of its even and odd columns, as fp16.
+template <bool ALL>
+__device__ __forceinline__ void row_weights(const Look& w, uint64_t base2, uint32_t (&p)[64],
+                                            uint64_t* sum, uint32_t* most) {
+  uint32_t x[2][16];
+  uint64_t sums[2] = {0, 0};
+  uint32_t top[2] = {0, 0};
+  tensor_load16(x[0], w.s_mine);
+#pragma unroll
+  for (int c = 0; c < kTile; c += 16) {
+    uint32_t(&y)[16] = x[(c >> 4) & 1];
+    tensor_landed(y);
+    if (c + 16 < kTile) tensor_load16(x[((c >> 4) + 1) & 1], w.s_mine + c + 16);
+    weights16<ALL>(w, c, y, base2, [&](int i, uint64_t ee, uint64_t z) {
+      sums[i & 1] = add2(sums[i & 1], ee);
+      p[c / 2 + i] = halves(lower(z), upper(z));
+      asm("max.f16x2 %0, %0, %1;" : "+r"(top[i & 1]) : "r"(p[c / 2 + i]));
+    });
+  }
+  *sum = add2(sums[0], sums[1]);
+  asm("max.f16x2 %0, %1, %2;" : "=r"(*most) : "r"(top[0]), "r"(top[1]));
+}
+
+// What fp16 left of P, over S from its end: a second piece.
+template <bool ALL>
+__device__ __forceinline__ void row_rest(const Look& w, uint64_t base2, const uint32_t (&p)[64]) {
+#pragma unroll
+  for (int c = kTile - 16; c >= 0; c -= 16) {
+    uint32_t y[16], rest[8];
+    tensor_load16(y, w.s_mine + c);
+    tensor_landed(y);
+    weights16<ALL>(w, c, y, base2, [&](int i, uint64_t, uint64_t z) {
+      const uint32_t h = p[c / 2 + i];
+      rest[i] = halves(lower(z) - Elt<LP_F16>::half_bits_to_float(h & 0xffffu),
+                       upper(z) - Elt<LP_F16>::half_bits_to_float(h >> 16));
+    });
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::LP_W8(rest, 0),
+        "r"(w.s_mine + 64 + c / 2) : "memory");
+  }
 }
 
 template <int DIM, bool WIDE>
@@ -290,113 +411,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // 32 lanes, at bit 16
     const uint32_t s_mine = tmem + half * 128 + lanes, o_mine = o_at + half * DIM + lanes;
     const Seen v = there ? seen(a, seq, r) : Seen{0, 0};
-    const uint64_t unit2 = pair(unit, unit);
+    Look w;
+    w.s_mine = s_mine;
+    w.unit2 = pair(unit, unit);
     for (int t = 0; t < tiles; ++t) {
       if (!__all_sync(kFullWarp, bar_wait(s, &s.s_full[half], t & 1))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int t0 = (first + t) * kTile, slot = t & 3;
-      const float* ks = s.key_scale[slot];
-      const float* vs = s.value_scale[slot];
-      const float* vl = s.value_log[slot];
+      w.ks = s.key_scale[slot], w.vs = s.value_scale[slot], w.vl = s.value_log[slot];
+      w.held = s.held[slot];
+      w.lo = v.lo - t0, w.end = v.end - t0;
       const bool all = t0 >= all_from && t0 + kTile <= all_until &&
-                       (s.held[slot][0] & s.held[slot][1] & s.held[slot][2] & s.held[slot][3]) == ~0u;
-      float now = ref;
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) {
-        uint32_t x[32];
-        tensor_load(x, s_mine + c);
-        // bits of the columns that this row sees
-        uint32_t bits = ~0u;
-        if (!all) {
-          const int lo = min(max(v.lo - t0 - c, 0), 32), hi = min(max(v.end - t0 - c, 0), 32);
-          bits = lo >= hi ? 0u : (hi == 32 ? ~0u : (1u << hi) - 1u) & ~((1u << lo) - 1u);
-          bits &= s.held[slot][c >> 5];
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(ks + c + e);
-          const ulonglong2 l2 = *reinterpret_cast<const ulonglong2*>(vl + c + e);
-          const uint64_t y0 = fma2(mul2(uint64_t(x[e]) | uint64_t(x[e + 1]) << 32, k2.x), unit2, l2.x);
-          const uint64_t y1 = fma2(mul2(uint64_t(x[e + 2]) | uint64_t(x[e + 3]) << 32, k2.y), unit2, l2.y);
-          if (all) {
-            now = fmaxf(now, fmaxf(fmaxf(lower(y0), upper(y0)), fmaxf(lower(y1), upper(y1))));
-          } else {
-            now = fmaxf(now, bits & (1u << e) ? lower(y0) : -INFINITY);
-            now = fmaxf(now, bits & (2u << e) ? upper(y0) : -INFINITY);
-            now = fmaxf(now, bits & (4u << e) ? lower(y1) : -INFINITY);
-            now = fmaxf(now, bits & (8u << e) ? upper(y1) : -INFINITY);
-          }
-        }
-      }
-      // the reference moves where something has outgrown it (the first time, always)
-      const bool grow = now > ref + kSlack || (ref == -INFINITY && now > -INFINITY);
-      if (__any_sync(kFullWarp, grow)) {
-        const float f = grow ? (ref == -INFINITY ? 0.0f : ex2(ref - now)) : 1.0f;
-        if (grow) ref = now, mass *= f;
-        if (t > 0) {
+                       (w.held[0] & w.held[1] & w.held[2] & w.held[3]) == ~0u;
+      // P is taken against the reference that there is; only where something has outgrown it
+      // (the first time, always) is the largest looked for, and the reference moved
+      uint32_t p[64], most;
+      uint64_t sum2, base2;
+      bool look = __any_sync(kFullWarp, ref == -INFINITY);
+      for (;;) {
+        if (look) {
+          const float now = all ? row_largest<true>(w, ref) : row_largest<false>(w, ref);
+          const bool grow = now > ref + kSlack || (ref == -INFINITY && now > -INFINITY);
+          const float f = grow ? (ref == -INFINITY ? 0.0f : ex2(ref - now)) : 1.0f;
+          if (grow) ref = now, mass *= f;
+          if (t > 0 && __any_sync(kFullWarp, grow)) {
 #pragma unroll 1
-          for (int c = 0; c < DIM; c += 32) {
-            uint32_t x[32];
-            tensor_load(x, o_mine + c);
+            for (int c = 0; c < DIM; c += 32) {
+              uint32_t x[32];
+              tensor_load(x, o_mine + c);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              x[e] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(x[e]) * f);
-            tensor_store(o_mine + c, x);
-          }
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        }
-      }
-      const float base = (ref == -INFINITY ? 0.0f : -ref) + kLift;
-      const uint64_t base2 = pair(base, base);
-      uint64_t sum2 = 0;
-      uint32_t rest[WIDE ? 64 : 1];
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) {
-        uint32_t x[32];
-        tensor_load(x, s_mine + c);
-        uint32_t bits = ~0u;
-        if (!all) {
-          const int lo = min(max(v.lo - t0 - c, 0), 32), hi = min(max(v.end - t0 - c, 0), 32);
-          bits = lo >= hi ? 0u : (hi == 32 ? ~0u : (1u << hi) - 1u) & ~((1u << lo) - 1u);
-          bits &= s.held[slot][c >> 5];
-        }
-        uint32_t p[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(ks + c + e);
-          const ulonglong2 v2 = *reinterpret_cast<const ulonglong2*>(vs + c + e);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int i = e + 2 * u;
-            const uint64_t y = fma2(mul2(uint64_t(x[i]) | uint64_t(x[i + 1]) << 32, u ? k2.y : k2.x),
-                                    unit2, base2);
-            float e0 = ex2(lower(y)), e1 = ex2(upper(y));
-            if (!all) {
-              e0 = bits & (1u << i) ? e0 : 0.0f;
-              e1 = bits & (2u << i) ? e1 : 0.0f;
+              for (int e = 0; e < 32; ++e)
+                x[e] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(x[e]) * f);
+              tensor_store(o_mine + c, x);
             }
-            const uint64_t ee = pair(e0, e1);
-            sum2 = add2(sum2, ee);
-            const uint64_t w = mul2(ee, u ? v2.y : v2.x);
-            p[i / 2] = halves(lower(w), upper(w));
-            if (WIDE)
-              rest[c / 2 + i / 2] = halves(
-                  lower(w) - Elt<LP_F16>::half_bits_to_float(p[i / 2] & 0xffffu),
-                  upper(w) - Elt<LP_F16>::half_bits_to_float(p[i / 2] >> 16));
           }
         }
-        tensor_store16(s_mine + c / 2, p);  // over what was read of S
-      }
-      if (WIDE) {  // over the rest of S, once all of it is read
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t x[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = rest[c + e];
-          tensor_store(s_mine + 64 + c, x);
-        }
+        const float base = (ref == -INFINITY ? 0.0f : -ref) + kLift;
+        base2 = pair(base, base);
+        if (all) row_weights<true>(w, base2, p, &sum2, &most);
+        else row_weights<false>(w, base2, p, &sum2, &most);
+        // 2^15 and above
+        const bool over = (most & 0xffffu) >= 0x7800u || (most >> 16) >= 0x7800u;
+        if (look || !__any_sync(kFullWarp, over)) break;
+        look = true;
       }
       mass += lower(sum2) + upper(sum2);
+      if (WIDE) {
+        if (all) row_rest<true>(w, base2, p);
+        else row_rest<false>(w, base2, p);
+      }
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t x[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = p[c + e];
+        tensor_store(s_mine + c, x);
+      }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       bar_arrive(&s.p_full[half]);
