@@ -36,7 +36,7 @@ struct alignas(1024) Shared {
   char q[2][2 * kTile * 128];
   char k[2][2 * kTile * 128];
   char v[2][2 * kTile * 128];
-  float key_scale[4][kTile], value_scale[4][kTile], value_log[4][kTile];
+  float scales[4][3][kTile];  // keys', values', and the values' as exponents
   uint32_t held[4][4];  // bits of the tile's tokens that are there
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], drained;
   const char* rows[2][2][kTile];  // of codes: [buffer][keys, values][token]
@@ -196,7 +196,7 @@ __device__ __forceinline__ void tensor_landed(uint32_t (&x)[16]) {
 // One query's view of a tile.
 struct Look {
   uint32_t s_mine;          // its row of S
-  const float *ks, *vs, *vl;
+  const float* scales;
   const uint32_t* held;
   uint64_t unit2;
   int lo, end;              // tokens that it sees, from the tile's first
@@ -221,8 +221,8 @@ __device__ __forceinline__ float row_largest(const Look& w, float now) {
     const uint32_t bits = ALL ? 0u : w.bits(c);
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
-      const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(w.ks + c + e);
-      const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(w.vl + c + e);
+      const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(w.scales + c + e);
+      const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(w.scales + 2 * kTile + c + e);
       const uint64_t a = fma2(mul2(uint64_t(y[e]) | uint64_t(y[e + 1]) << 32, k.x), w.unit2, l.x);
       const uint64_t b = fma2(mul2(uint64_t(y[e + 2]) | uint64_t(y[e + 3]) << 32, k.y), w.unit2, l.y);
       if (ALL) {
@@ -245,8 +245,8 @@ __device__ __forceinline__ void weights16(const Look& w, int c, const uint32_t (
   const uint32_t bits = ALL ? 0u : w.bits(c);
 #pragma unroll
   for (int e = 0; e < 16; e += 4) {
-    const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(w.ks + c + e);
-    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(w.vs + c + e);
+    const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(w.scales + c + e);
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(w.scales + kTile + c + e);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int i = e + 2 * u;
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(kFullWarp, bar_wait(s, &s.s_full[half], t & 1))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int t0 = (first + t) * kTile, slot = t & 3;
-      w.ks = s.key_scale[slot], w.vs = s.value_scale[slot], w.vl = s.value_log[slot];
+      w.scales = s.scales[slot][0];
       w.held = s.held[slot];
       w.lo = v.lo - t0, w.end = v.end - t0;
       const bool all = t0 >= all_from && t0 + kTile <= all_until &&
@@ -502,9 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     const auto put_scales = [&](int t) {
-      s.key_scale[t & 3][in] = scale[0];
-      s.value_scale[t & 3][in] = scale[1];
-      s.value_log[t & 3][in] =
+      s.scales[t & 3][0][in] = scale[0];
+      s.scales[t & 3][1][in] = scale[1];
+      s.scales[t & 3][2][in] =
           float(max(int((__float_as_uint(scale[1]) >> 23) & 255u) - 127, kLeastScale));
     };
     uint4 codes[2][kMine];
@@ -556,12 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------- the products' issue
     constexpr uint32_t kScore = instruction(kTile, kTile, false);
     constexpr uint32_t kValue = instruction(kTile, DIM, true);
+    // (places in an operand are added to its address, which counts 16 bytes)
+    const uint64_t q_op[2] = {operand(s.q[0], 16, 1024), operand(s.q[1], 16, 1024)};
+    const uint64_t k_op[2] = {operand(s.k[0], 16, 1024), operand(s.k[1], 16, 1024)};
+    const uint64_t v_op[2] = {operand(s.v[0], kHalf, 1024), operand(s.v[1], kHalf, 1024)};
     const auto score = [&](int t, int half) {
+      const uint64_t qo = half ? q_op[1] : q_op[0], ko = t & 1 ? k_op[1] : k_op[0];
 #pragma unroll
       for (int i = 0; i < DIM / 16; ++i) {
-        const uint32_t off = (i >> 2) * kHalf + (i & 3) * 32;
-        mma_shared(tmem + half * 128, operand(s.q[half] + off, 16, 1024),
-                   operand(s.k[t & 1] + off, 16, 1024), kScore, i > 0);
+        const uint32_t off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
+        mma_shared(tmem + half * 128, qo + off, ko + off, kScore, i > 0);
       }
       commit(&s.s_full[half]);
     };
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kTile / 16; ++i)
             mma_tensor(o_at + half * DIM, tmem + half * 128 + piece * 64 + i * 8,
-                       operand(s.v[t & 1] + i * 2048, kHalf, 1024), kValue,
+                       (t & 1 ? v_op[1] : v_op[0]) + i * (2048 >> 4), kValue,
                        t > 0 || i > 0 || piece != (WIDE ? 1 : 0));
         if (t + 1 == tiles) commit(&s.o_done[half]);
         if (half == 1) commit(&s.v_empty[t & 1]);

@@ -20,7 +20,6 @@ constexpr int kMaxParts = 8;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMoveThreads = 256;
-constexpr int kRoundBytes = 20 * 1024;  // of a block's round, two at once
 constexpr int kCodeThreads = 224;        // of a block: the last warp moves params
 constexpr int kRoundTokens = kMoveThreads;  // a thread looks one up
 constexpr int kMostCluster = 8;
@@ -548,9 +547,11 @@ cudaError_t launch(EvictArgs a, cudaStream_t stream) {
     return launch_kernel(evict_move_wide_kernel, dim3(unsigned(units)), dim3(kMoveThreads), 0,
                          stream, a);
   const int64_t pieces = codes + params;
-  a.round_tokens = int(std::min<int64_t>({kRoundTokens, kRoundBytes / (pieces * 16), a.keep}));
   int blocks = 1;
   while (blocks < kMostCluster && units * blocks * 2 <= 8 * kSms && a.keep > 64 * blocks) blocks *= 2;
+  // of a block's round, two at once: as much as leaves room for all blocks, four an SM
+  const int64_t bytes = units * blocks <= 2 * kSms ? 48 * 1024 : 20 * 1024;
+  a.round_tokens = int(std::min<int64_t>({kRoundTokens, bytes / (pieces * 16), a.keep}));
   a.round_tokens = std::min(a.round_tokens, (a.keep + blocks - 1) / blocks);
   const size_t smem = size_t(2) * a.round_tokens * pieces * 16;
   static PerDevice<1> allowed;

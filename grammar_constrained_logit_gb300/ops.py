@@ -826,7 +826,7 @@ def _per_sequence(t: torch.Tensor, name: str, batch: int, device) -> int:
         raise TypeError(f"{name} must be int32")
     if t.device != device:
         raise ValueError(f"{name} must be on the cache's device")
-    if t.shape != (batch,) or (batch > 1 and t.stride(0) != 1):
+    if t.dim() != 1 or t.size(0) != batch or (batch > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be contiguous [{batch}], got {list(t.shape)}")
     return t.data_ptr()
 
@@ -856,7 +856,8 @@ def _weights(weights: torch.Tensor, batch: int, heads: int, tokens: int, device)
             weights.size(2) < tokens:
         raise ValueError(f"weights must be [{batch}, {heads}, {tokens} or more], "
                          f"got {list(weights.shape)}")
-    if (weights.size(2) > 1 and weights.stride(2) != 1) or _expanded(weights):
+    if not weights.is_contiguous() and (
+            (weights.size(2) > 1 and weights.stride(2) != 1) or _expanded(weights)):
         raise ValueError("a head's weights must be contiguous, and weights not expanded")
     return weights.data_ptr(), weights.stride(0), weights.stride(1)
 
@@ -912,7 +913,8 @@ def cache_attend(cache: QuantCache, q: torch.Tensor, blocks: torch.Tensor, lengt
         raise ValueError(f"q must be [batch, rows, q_heads, {dim}], got {list(q.shape)}")
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=device)
-    elif out.dtype != q.dtype or out.shape != q.shape or out.device != device or _expanded(out):
+    elif out.dtype != q.dtype or out.shape != q.shape or out.device != device or \
+            (not out.is_contiguous() and _expanded(out)):
         raise ValueError("out must be like q, and not expanded")
     q4, out4 = (q, out) if q.dim() == 4 else (q.unsqueeze(1), out.unsqueeze(1))
     batch, rows, q_heads, _ = q4.shape
@@ -1033,11 +1035,13 @@ def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, uniforms: torch.Te
         raise ValueError(f"drafts must be [slots, rows - 1], got {tuple(drafts.shape)}")
     if drafts.dtype != torch.int64:
         raise TypeError("drafts must be int64")
-    slots, per_slot = drafts.size(0), drafts.size(1) + 1
+    shape = drafts.shape
+    slots, per_slot = shape[0], shape[1] + 1
     if logits.dim() == 3:
         if logits.size(0) != slots or logits.size(1) != per_slot:
             raise ValueError("logits [slots, rows, V] must match drafts [slots, rows - 1]")
-        logits = logits.flatten(0, 1)
+        logits = logits.view(-1, logits.size(2)) if logits.is_contiguous() else \
+            logits.flatten(0, 1)
     lg = _matrix(logits, "logits")
     dtype = lg.dtype
     rows, cols = lg.shape
@@ -1047,7 +1051,7 @@ def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, uniforms: torch.Te
     dt = _DT[dtype] if dtype in _DT else _dtype_code(lg)
     if uniforms.dtype != torch.float32:
         raise TypeError("uniforms must be float32")
-    if uniforms.shape != drafts.shape:
+    if uniforms.shape != shape:
         raise ValueError("uniforms must be like drafts")
     if drafts.device != device or uniforms.device != device:
         raise ValueError("drafts and uniforms must be on the same device as logits")
@@ -1065,7 +1069,7 @@ def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, uniforms: torch.Te
         if draft_probs.device != device:
             raise ValueError("draft_probs must be on the same device as logits")
         used = vocab if vocab >= 0 else cols if bm is None else min(cols, bm.size(1) * 32)
-        if draft_probs.dim() != 3 or draft_probs.shape[:2] != drafts.shape or \
+        if draft_probs.dim() != 3 or draft_probs.shape[:2] != shape or \
                 draft_probs.size(2) < used:
             raise ValueError(f"draft_probs must be [{slots}, {per_slot - 1}, {used} or more], "
                              f"got {list(draft_probs.shape)}")
@@ -1077,14 +1081,19 @@ def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, uniforms: torch.Te
     if seeds is not None:
         if seeds.dtype != torch.int64 or seeds.device != device or seeds.numel() != rows:
             raise ValueError(f"seeds must be {rows} int64 values on the logits' device")
-        sd = seeds.contiguous()
+        sd = seeds if seeds.is_contiguous() else seeds.contiguous()
     heat = 0.0
-    if isinstance(temperature, torch.Tensor) and temperature.numel() != 1:
-        if temperature.numel() != slots:
-            raise ValueError(f"temperature must have {slots} values, got {temperature.numel()}")
-        temperature = temperature.to(device=device, dtype=torch.float32).contiguous()
-    elif isinstance(temperature, torch.Tensor) and temperature.is_cuda:
-        temperature = temperature.to(device=device, dtype=torch.float32).expand(slots).contiguous()
+    if isinstance(temperature, torch.Tensor) and (temperature.is_cuda or
+                                                  temperature.numel() != 1):
+        n = temperature.numel()
+        if n != slots and n != 1:
+            raise ValueError(f"temperature must have {slots} values, got {n}")
+        if temperature.dtype != torch.float32 or temperature.device != device:
+            temperature = temperature.to(device=device, dtype=torch.float32)
+        if n != slots:  # one for all, without asking the device for it
+            temperature = temperature.reshape(1).expand(slots)
+        if not temperature.is_contiguous():
+            temperature = temperature.contiguous()
     else:
         heat, temperature = float(temperature), None
     if out is None:
@@ -1096,7 +1105,8 @@ def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, uniforms: torch.Te
             if t.dtype != d or t.shape != shape or not t.is_contiguous() or t.device != device:
                 raise ValueError("out must be contiguous int64 [slots, rows] and int32 [slots] "
                                  "tensors on the logits' device")
-    dr, un = drafts.contiguous(), uniforms.contiguous()
+    dr = drafts if drafts.is_contiguous() else drafts.contiguous()
+    un = uniforms if uniforms.is_contiguous() else uniforms.contiguous()
     stream = _raw_stream(device.index)
     if workspace is None:
         workspace = _scratch(_verify_scratch, device, stream,
