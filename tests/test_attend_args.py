@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 
 from attend_oracle import attended, evicted, row_probs, verified  # noqa: E402
 from grammar_constrained_logit_gb300 import _lib, build, ops  # noqa: E402
-from test_beam_calls import OnGpu  # noqa: E402
+from test_beam_calls import OnGpu, recorded  # noqa: E402, F401
 
 FAKE = 0x10000  # never dereferenced: every call below is refused or has nothing to do
 
@@ -272,3 +272,30 @@ def test_definitions_by_hand():
     assert got[1] == 1
     got = verified(x, ok, [1], None, [0.8], 1.0, none)
     assert got[0].tolist() == [0, -1]                      # p without the draft
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_launches_are_on_the_tensors_device(recorded, monkeypatch, index):
+    """With another device current, a call is made with the tensors' device current, and that
+    one is current again after it."""
+    def gpu(*shape, dtype=torch.float32):
+        return OnGpu(torch.zeros(*shape, dtype=dtype), index)
+
+    for name in ("cache_attend", "cache_evict", "verify_drafts"):
+        monkeypatch.setattr(ops, f"{name}_workspace_bytes", lambda *a: 8)
+    cache = ops.QuantCache(gpu(2, 32, 2, 64, dtype=torch.uint8), gpu(2, 32, 2, 1), dim=64)
+    ws = gpu(8, dtype=torch.uint8)
+    table, lens = gpu(2, 2, dtype=INT), gpu(2, dtype=INT)
+    weights = gpu(2, 2, 32)
+    weights.__dict__["is_contiguous"] = lambda: True
+    q = gpu(2, 1, 4, 64)
+    ops.cache_attend(cache, q, table, lens, block_size=16, out=gpu(2, 1, 4, 64), workspace=ws,
+                     weights=weights)
+    ops.cache_evict(cache, weights, table, lens, 8, block_size=16, out=gpu(2, dtype=INT),
+                    workspace=ws)
+    ops.verify_drafts(gpu(8, 40), gpu(2, 3, dtype=torch.int64), gpu(2, 3), workspace=ws,
+                      out=(gpu(2, 4, dtype=torch.int64), gpu(2, dtype=INT)))
+    assert [name for name, _ in recorded.calls] == ["lp_cache_attend", "lp_cache_evict",
+                                                    "lp_verify_drafts"]
+    assert {device for _, device in recorded.calls} == {index}
+    assert recorded.current == [0]
