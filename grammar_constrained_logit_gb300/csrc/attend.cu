@@ -157,7 +157,7 @@ extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, i
   if (batch == 0 || rows == 0 || q_heads == 0 || dim == 0) return LP_OK;
   const int eb = dt == LP_F32 ? 4 : 2;
   if (parts == nullptr || q == nullptr || out == nullptr || q->data == nullptr ||
-      out->data == nullptr || lengths == nullptr || (max_blocks > 0 && blocks == nullptr) ||
+      out->data == nullptr || out->data == q->data || lengths == nullptr || (max_blocks > 0 && blocks == nullptr) ||
       (reinterpret_cast<uintptr_t>(q->data) | reinterpret_cast<uintptr_t>(out->data)) % eb != 0 ||
       (reinterpret_cast<uintptr_t>(blocks) | reinterpret_cast<uintptr_t>(lengths) |
        reinterpret_cast<uintptr_t>(n_rows) | reinterpret_cast<uintptr_t>(weights)) % 4 != 0)

@@ -393,6 +393,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_say_kernel(const __grid_co
   __shared__ uint32_t reached;  // a lower bound of the block's best r / t
   const int blocks = int(cluster_size()), rank = int(cluster_rank());
   const int slot = blockIdx.x / blocks, R = a.per_slot, tid = threadIdx.x, lane = tid & 31;
+  // (a block may write to another's shared memory once that one has begun: told here, waited
+  // for below)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if (tid == 0) count = there = R - 1, reached = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -450,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_say_kernel(const __grid_co
     if (lane == 0) tops[i] = all, sums[i] = sum, firsts[i] = first;
   }
   __syncthreads();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (tid < R - 1) {
     bool taken = false;
     if (draft < 0 || draft >= a.V) {

@@ -897,7 +897,7 @@ def cache_attend(cache: QuantCache, q: torch.Tensor, blocks: torch.Tensor, lengt
 
     ``weights`` float32 [batch, heads, at least n * block_size] takes up, added, each token's
     attention weight over the rows and the query heads of its head: what ``cache_evict`` goes
-    by.  Returns what ``q`` is like, or ``out``.  ``workspace`` (uint8,
+    by.  Returns what ``q`` is like, or ``out``, which must not overlap it.  ``workspace`` (uint8,
     ``cache_attend_workspace_bytes``, any content) is scratch to use instead of what is kept
     for the thread and stream, or in a capture a part of the graph's memory; two threads, or
     graphs that replay side by side, must not share one."""

@@ -490,7 +490,8 @@ lp_status lp_cache_read(const lp_cache_part* parts, const lp_heads* out, int64_t
  * A weight p_t is rounded to 11 bits for bf16 and to 22 for the other types, and to 2^-33 of
  * the row's largest product of weight and value's scale (2^-39 for 32-bit queries; a scale
  * below 2^-60 counts as that) where it is smaller.  Sums are 32-bit.
- *   q, out       [batch, rows, q_heads, dim] of type dt, dim contiguous, strides in elements
+ *   q, out       [batch, rows, q_heads, dim] of type dt, dim contiguous, strides in elements;
+ *                out must not overlap q (the same pointer is refused) nor itself
  *   blocks       device int32 [batch, max_blocks], blocks_stride elements from row to row
  *   lengths      device int32 [batch];  n_rows: device int32 [batch], or NULL: all
  *   workspace    device scratch of lp_cache_attend_workspace_bytes, 16-byte aligned, of any

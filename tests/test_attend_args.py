@@ -29,9 +29,8 @@ def _parts(n=2, **kw):
 
 
 def _attend(lib, **kw):
-    rows = ctypes.byref(_lib.Rows(FAKE, 4096, 4096, 128))
-    a = dict(parts=_parts(), bits=8, n_slots=64, page=16, heads=8, dim=128, group=128, q=rows,
-             out=rows, dt=2, batch=2, rows=1, q_heads=32, blocks=FAKE, blocks_stride=4,
+    a = dict(parts=_parts(), bits=8, n_slots=64, page=16, heads=8, dim=128, group=128,
+             q=_at(FAKE), out=_at(2 * FAKE), dt=2, batch=2, rows=1, q_heads=32, blocks=FAKE, blocks_stride=4,
              max_blocks=4, block=16, lengths=FAKE, n_rows=None, scale=0.1, window=0,
              weights=None, wb=0, wh=0, ws=FAKE, ws_bytes=1 << 40, stream=None)
     assert set(kw) <= set(a)
@@ -51,7 +50,7 @@ def _at(p):
     (dict(heads=0), 1), (dict(max_blocks=-1), 1), (dict(block=0), 1), (dict(blocks_stride=3), 1),
     (dict(window=-1), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
     (dict(parts=None), 1), (dict(q=None), 1), (dict(out=None), 1), (dict(q=_at(None)), 1),
-    (dict(out=_at(None)), 1), (dict(q=_at(FAKE + 1)), 1), (dict(out=_at(FAKE + 1)), 1),
+    (dict(out=_at(None)), 1), (dict(out=_at(FAKE)), 1), (dict(q=_at(FAKE + 1)), 1), (dict(out=_at(FAKE + 1)), 1),
     (dict(dt=0, q=_at(FAKE + 2)), 1), (dict(blocks=None), 1), (dict(lengths=None), 1),
     (dict(blocks=FAKE + 2), 1), (dict(lengths=FAKE + 1), 1), (dict(n_rows=FAKE + 2), 1),
     (dict(weights=FAKE + 2), 1), (dict(ws=None), 1), (dict(ws=FAKE + 8), 1), (dict(ws_bytes=0), 1),

@@ -239,6 +239,30 @@ def test_strides(bits, group, dtype):
     assert (np.abs(one.double().cpu().numpy() - want[:, 2]) <= off[:, 2]).all()
 
 
+@pytest.mark.parametrize("rows", [2, 70])
+@pytest.mark.parametrize("bits, dim, group", [(8, 128, 128), (4, 128, 32), (4, 80, 16),
+                                              (8, 96, 32)])
+def test_pages_among_others(bits, dim, group, rows):
+    """A page holds several layers' slots, and codes and params start where they like: a
+    layer's pages are apart, its addresses of any alignment."""
+    rng = np.random.default_rng(30)
+    heads, pages, page, layers = 4, 14, 16, 3
+    tail, ptype = ((), torch.float32) if bits == 8 else ((2,), torch.bfloat16)
+    for shift in (0, 8, 1):  # bytes; params stay on their words
+        n = 2 * pages * layers * page * heads * (dim * bits // 8)
+        codes = torch.zeros(n + 16, dtype=torch.uint8, device="cuda")[shift:shift + n]
+        codes = codes.view(2, pages, layers, page, heads, -1)[:, :, 1]
+        params = torch.zeros(2, pages, layers, page, heads, dim // group, *tail, dtype=ptype,
+                             device="cuda")[:, :, 1]
+        cache = ops.QuantCache(codes, params, dim=dim, bits=bits)
+        x = [torch.randn(cache.slots, heads, dim, device="cuda") for _ in range(2)]
+        ops.cache_write(cache, x, torch.arange(cache.slots, device="cuda"))
+        lengths = [100, 75]
+        q = rng.standard_normal((2, rows, heads * 3, dim)).astype(np.float32)
+        check(cache, q, table(rng, lengths, page, cache.slots), lengths, page, "bf16",
+              weights=True)
+
+
 @pytest.mark.parametrize("bits, group, dtype", [(8, 128, "bf16"), (4, 32, "f16")])
 def test_long_and_ragged(bits, group, dtype):
     rng = np.random.default_rng(10)

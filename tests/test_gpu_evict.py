@@ -149,6 +149,26 @@ def test_layouts():
         check(cache, w, blocks, [100, 90, 10], 100, 40, 2, 3)
 
 
+@pytest.mark.parametrize("shift", [0, 4, 1])
+def test_pages_among_others(shift):
+    """A page holds several layers' slots; codes start at any byte."""
+    rng = np.random.default_rng(6)
+    heads, pages, page, dim = 3, 14, 16, 64
+    n = 2 * pages * 3 * page * heads * dim
+    every = torch.from_numpy(rng.integers(0, 256, n + 16, dtype=np.uint8)).cuda()
+    was = every.clone()
+    codes = every[shift:shift + n].view(2, pages, 3, page, heads, dim)[:, :, 1]
+    params = torch.rand(2, pages, 3, page, heads, 1, device="cuda")[:, :, 1]
+    cache = ops.QuantCache(codes, params, dim=dim, bits=8)
+    blocks = table(rng, [100, 90], page, pages * page)
+    w = some_weights(rng, 2, heads, blocks.shape[1] * page, "spread")
+    check(cache, w, blocks, [100, 90], page, 40, 2, 5)
+    for layer in (0, 2):  # the others' bytes stay
+        a, b = (t[shift:shift + n].view(2, pages, 3, page, heads, dim)[:, :, layer]
+                for t in (every, was))
+        assert torch.equal(a, b)
+
+
 def test_slots_outside_and_long_lengths():
     rng = np.random.default_rng(4)
     cache = random_cache(rng, 320, 2, 64, 4, 32)
