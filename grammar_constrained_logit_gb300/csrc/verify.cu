@@ -187,7 +187,7 @@ __device__ __noinline__ float2 any_run(const RowVecs<DT> x, int q0, int q1, floa
 // A warp a run of a row's vectors: each lane its own largest and sum, joined at the end.  A
 // vector's place in registers is loaded again as soon as it is used up.
 template <int DT>
-__global__ void __launch_bounds__(kStreamThreads, 5)
+__global__ void __launch_bounds__(kStreamThreads, 4)
     verify_stream_kernel(const __grid_constant__ VerifyArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -590,7 +590,7 @@ cudaError_t launch(VerifyArgs a, cudaStream_t stream) {
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(kStreamThreads);
   // as many runs as there are warps on all SMs, of a chunk each at least
-  const int64_t resident = int64_t(kSms) * 5 * (kStreamThreads / 32);
+  const int64_t resident = int64_t(kSms) * 4 * (kStreamThreads / 32);
   const int64_t vecs = std::max<int64_t>(1, a.V / Elt<DT>::kPerVec + 2);
   const int64_t most = (vecs + kChunkVecs - 1) / kChunkVecs;
   const int64_t runs = std::max<int64_t>(1, std::min(most, resident / a.rows));
