@@ -199,3 +199,28 @@ def test_weights_with_gaps():
             assert np.array_equal(w[b, h, n:].cpu().numpy(), was[b, h, n:])
     w.fill_(9.0)
     assert (room == 9.0).all()
+
+
+@pytest.mark.parametrize("kind, keep", [("spread", 1000), ("ties", 300000), ("equal", 7)])
+def test_longer_than_shared_memory(kind, keep):
+    """More weights than a cluster's shared memory holds: one block reads them a digit a time."""
+    rng = np.random.default_rng(keep)
+    n, size = 330001, 512
+    total = -(-n // size) * size + 3 * size
+    cache = random_cache(rng, total, 1, 16, 8, 16)
+    blocks = table(rng, [n, 900], size, total)
+    w = some_weights(rng, 2, 1, blocks.shape[1] * size, kind)
+    check(cache, w, blocks, [n, 900], size, keep, first=3, recent=4)
+
+
+@pytest.mark.parametrize("bits, heads, dim, group", [
+    (8, 2, 4096, 4096), (8, 3, 301, 301), (8, 2, 256, 1), (4, 1, 8192, 32)])
+def test_wide_heads(bits, heads, dim, group):
+    """More pieces to a token than a block has threads for."""
+    rng = np.random.default_rng(dim)
+    lengths = [90, 300, 12, 0]
+    total = 40 * 16
+    cache = random_cache(rng, total, heads, dim, bits, group, page=16)
+    blocks = table(rng, lengths, 16, total)
+    w = some_weights(rng, len(lengths), heads, blocks.shape[1] * 16, "ties")
+    check(cache, w, blocks, lengths, 16, 50, first=2, recent=6)
