@@ -29,90 +29,165 @@ namespace {
 
 constexpr int kWarps = 4;       // of a block of weights_any_kernel
 constexpr int kMostAnyWarps = 16;
-constexpr int kGroup = 4;       // tokens that a warp of attend_any_kernel has at a time
+constexpr int kQueries = 4;     // of a block of attend_any_kernel
+constexpr int kGroup = 2;       // tokens that a warp of it has at a time
 constexpr int kMostDim = 1024;
 
-// Any width, group, stride and alignment: a block a query, its warps with kGroup
-// tokens in turn, whose trips to memory run side by side, their lanes
-// across the head; the warps' sums are joined at the end.
-//   What a lane loads is one byte, so it is the trips that bound it: 8 x 32 queries of 72
-// elements over 4096 tokens took 7893 us with a warp a query and a token at a time.
+// Elements d0 .. d0 + 127 of kGroup heads, four to a lane; 0 behind the last (whose
+// place loads the last again: no load waits for a choice).
+template <int BITS>
+__device__ __forceinline__ void unpack(const AttendArgs& a, const Head (&from)[kGroup], int d0,
+                                       float (&to)[4][kGroup]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int d = d0 + 32 * e + lane;
+#pragma unroll
+    for (int u = 0; u < kGroup; ++u) {
+      const float x = value_at<BITS>(a, from[u].codes, from[u].params, min(d, a.dim - 1));
+      to[e][u] = d < a.dim ? x : 0.0f;
+    }
+  }
+}
+
+// Any width, group, stride and alignment: a block has up to kQueries queries of one head of the
+// cache, its warps kGroup tokens in turn, their lanes across the head: what a lane has unpacked
+// meets all queries.  The warps' sums are joined at the end.
+//   Bound by instructions: a lane has one element at a time, whatever the alignment.  8 x 32
+// queries of 72 elements, four to a head, over 4096 tokens of 8 bits: 7893 us with a warp a
+// query, 830 with a block a query, 416 so (the heads' codes read once: 6).
+template <int BITS>
 __global__ void __launch_bounds__(kMostAnyWarps * 32)
-    attend_any_kernel(const __grid_constant__ AttendArgs a) {
+    attend_any_kernel(const __grid_constant__ AttendArgs a, const int tiles) {
   extern __shared__ float shared_floats[];
-  __shared__ float tops[kMostAnyWarps], masses[kMostAnyWarps];
+  __shared__ float tops[kMostAnyWarps][kQueries], masses[kMostAnyWarps][kQueries];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* q = shared_floats;
-  float* sums = shared_floats + a.dim;
-  float* sum = sums + warp * a.dim;
-  const int q_heads = a.heads * a.shared;
-  const int64_t total = int64_t(a.batch) * a.rows * q_heads;
-  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
-    const int j = int(i % q_heads), r = int(i / q_heads % a.rows), b = int(i / q_heads / a.rows);
-    const int h = j / a.shared;
-    const Seen v = seen(a, sequence(a, b), r);
-    const char* from = static_cast<const char*>(a.q.data) + b * a.q.batch_stride +
-                       r * a.q.row_stride + j * a.q.head_stride;
-    for (int d = threadIdx.x; d < a.dim; d += blockDim.x) q[d] = load_as_float(from, d, a.dt);
-    for (int d = lane; d < a.dim; d += 32) sum[d] = 0.0f;
+  const int q_heads = a.heads * a.shared, per_head = a.rows * a.shared;
+  float* q = shared_floats;                     // [kQueries][dim]
+  float* sums = shared_floats + kQueries * a.dim;  // [warps][kQueries][dim]
+  float* sum = sums + warp * kQueries * a.dim;
+  const int64_t total = int64_t(a.batch) * a.heads * tiles;
+  for (int64_t unit = blockIdx.x; unit < total; unit += gridDim.x) {
+    const int tile = int(unit % tiles), h = int(unit / tiles % a.heads),
+              b = int(unit / tiles / a.heads);
+    const Sequence s = sequence(a, b);
+    Seen v[kQueries];
+    int lo = INT32_MAX, end = 0;
+#pragma unroll
+    for (int i = 0; i < kQueries; ++i) {
+      const int row = tile * kQueries + i;
+      v[i] = seen(a, s, row < per_head ? row / a.shared : a.rows);
+      if (v[i].lo < v[i].end && a.n_slots > 0) lo = min(lo, v[i].lo), end = max(end, v[i].end);
+    }
+#pragma unroll
+    for (int i = 0; i < kQueries; ++i) {
+      const int row = tile * kQueries + i, r = row / a.shared;
+      const char* from = static_cast<const char*>(a.q.data) + b * a.q.batch_stride +
+                         r * a.q.row_stride + (h * a.shared + row - r * a.shared) * a.q.head_stride;
+      for (int d = threadIdx.x; d < a.dim; d += blockDim.x)
+        q[i * a.dim + d] = row < per_head ? load_as_float(from, d, a.dt) : 0.0f;
+      for (int d = lane; d < a.dim; d += 32) sum[i * a.dim + d] = 0.0f;
+    }
     __syncthreads();
-    float top = -INFINITY, mass = 0.0f;
-    for (int t = v.lo + warp * kGroup; t < v.end; t += warps * kGroup) {
+    float top[kQueries], mass[kQueries];
+#pragma unroll
+    for (int i = 0; i < kQueries; ++i) top[i] = -INFINITY, mass[i] = 0.0f;
+    for (int64_t t64 = int64_t(lo) + warp * kGroup; t64 < end; t64 += warps * kGroup) {
+      const int t = int(t64);
       Head key[kGroup], value[kGroup];
       bool there[kGroup];
-      float x[kGroup];
+      float x[kQueries][kGroup];
 #pragma unroll
       for (int u = 0; u < kGroup; ++u) {
-        const int64_t slot = t + u < v.end ? slot_of(a, b, t + u) : -1;
+        const int64_t slot = t + u < end ? slot_of(a, b, t + u) : -1;
         there[u] = slot >= 0;
-        x[u] = 0.0f;
-        if (there[u]) key[u] = head_at(a, 0, slot, h), value[u] = head_at(a, 1, slot, h);
-      }
-      for (int d = lane; d < a.dim; d += 32) {
-        const float qd = q[d];
+        // (where there is none any other is loaded, so that loads do not wait for a choice)
+        key[u] = head_at(a, 0, there[u] ? slot : 0, h);
+        value[u] = head_at(a, 1, there[u] ? slot : 0, h);
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
-          if (there[u]) x[u] += qd * value_at(a, key[u].codes, key[u].params, d);
+        for (int i = 0; i < kQueries; ++i) x[i][u] = 0.0f;
       }
-      float now = top;
+      // 128 elements at once; keys' and values' first ones are under way together
+      float k[4][kGroup], y[4][kGroup];
+      unpack<BITS>(a, value, 0, y);
+      for (int d0 = 0; d0 < a.dim; d0 += 128) {
+        unpack<BITS>(a, key, d0, k);
 #pragma unroll
-      for (int u = 0; u < kGroup; ++u) {
-        x[u] = warp_sum(x[u]) * a.scale;
-        if (there[u]) now = fmaxf(now, x[u]);
+        for (int e = 0; e < 4; ++e) {
+          const int d = d0 + 32 * e + lane;
+#pragma unroll
+          for (int i = 0; i < kQueries; ++i) {
+            const float qd = d < a.dim ? q[i * a.dim + d] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) x[i][u] += qd * k[e][u];
+          }
+        }
       }
-      const float ref = now == -INFINITY ? 0.0f : now;
-      const float keep = exp2f(top - ref);
-      top = now;
-      mass *= keep;
+      float keep[kQueries];
+      uint32_t live = 0;  // who sees what of the kGroup tokens
 #pragma unroll
-      for (int u = 0; u < kGroup; ++u) {
-        x[u] = there[u] ? exp2f(x[u] - ref) : 0.0f;
-        mass += x[u];
+      for (int i = 0; i < kQueries; ++i) {
+        float now = top[i];
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+          x[i][u] = warp_sum(x[i][u]) * a.scale;
+          if (there[u] && t + u >= v[i].lo && t + u < v[i].end) {
+            live |= 1u << (i * kGroup + u);
+            now = fmaxf(now, x[i][u]);
+          }
+        }
+        const float ref = now == -INFINITY ? 0.0f : now;
+        keep[i] = exp2f(top[i] - ref);
+        top[i] = now;
+        mass[i] *= keep[i];
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+          x[i][u] = (live >> (i * kGroup + u)) & 1u ? exp2f(x[i][u] - ref) : 0.0f;
+          mass[i] += x[i][u];
+        }
       }
-      for (int d = lane; d < a.dim; d += 32) {
-        float y = sum[d] * keep;
+      for (int d0 = 0; d0 < a.dim; d0 += 128) {
+        if (d0 > 0) unpack<BITS>(a, value, d0, y);
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
-          if (there[u]) y += x[u] * value_at(a, value[u].codes, value[u].params, d);
-        sum[d] = y;
+        for (int e = 0; e < 4; ++e) {
+          const int d = d0 + 32 * e + lane;
+          if (d >= a.dim) continue;
+#pragma unroll
+          for (int i = 0; i < kQueries; ++i) {
+            float z = sum[i * a.dim + d] * keep[i];
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u)  // (what is not seen may be no number)
+              if ((live >> (i * kGroup + u)) & 1u) z += x[i][u] * y[e][u];
+            sum[i * a.dim + d] = z;
+          }
+        }
       }
     }
-    if (lane == 0) tops[warp] = top, masses[warp] = mass;
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < kQueries; ++i) tops[warp][i] = top[i], masses[warp][i] = mass[i];
     __syncthreads();
-    float most = -INFINITY, all = 0.0f;
-    for (int w = 0; w < warps; ++w) most = fmaxf(most, tops[w]);
-    const float ref = most == -INFINITY ? 0.0f : most;
-    for (int w = 0; w < warps; ++w) all += masses[w] * exp2f(tops[w] - ref);
-    const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-    char* to = static_cast<char*>(a.out.data) + b * a.out.batch_stride + r * a.out.row_stride +
-               j * a.out.head_stride;
-    for (int d = threadIdx.x; d < a.dim; d += blockDim.x) {
-      float y = 0.0f;
-      for (int w = 0; w < warps; ++w) y += sums[w * a.dim + d] * exp2f(tops[w] - ref);
-      store_float(to, d, all == 0.0f ? 0.0f : y * inv, a.dt);
+#pragma unroll 1
+    for (int i = 0; i < kQueries; ++i) {
+      const int row = tile * kQueries + i, r = row / a.shared, j = h * a.shared + row - r * a.shared;
+      if (row >= per_head) break;
+      float most = -INFINITY, all = 0.0f;
+      for (int w = 0; w < warps; ++w) most = fmaxf(most, tops[w][i]);
+      const float ref = most == -INFINITY ? 0.0f : most;
+      for (int w = 0; w < warps; ++w) all += masses[w][i] * exp2f(tops[w][i] - ref);
+      const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+      char* to = static_cast<char*>(a.out.data) + b * a.out.batch_stride + r * a.out.row_stride +
+                 j * a.out.head_stride;
+      for (int d = threadIdx.x; d < a.dim; d += blockDim.x) {
+        float y = 0.0f;
+        for (int w = 0; w < warps; ++w)
+          y += sums[(w * kQueries + i) * a.dim + d] * exp2f(tops[w][i] - ref);
+        store_float(to, d, all == 0.0f ? 0.0f : y * inv, a.dt);
+      }
+      if (a.lse != nullptr && threadIdx.x == 0)
+        a.lse[(int64_t(b) * a.rows + r) * q_heads + j] =
+            all == 0.0f ? -INFINITY : ref + log2f(all);
     }
-    if (a.lse != nullptr && threadIdx.x == 0)
-      a.lse[(int64_t(b) * a.rows + r) * q_heads + j] = all == 0.0f ? -INFINITY : ref + log2f(all);
     __syncthreads();  // the sums are read
   }
 }
@@ -154,11 +229,18 @@ __global__ void __launch_bounds__(kWarps * 32) weights_any_kernel(const __grid_c
 }
 
 cudaError_t attend_any(const AttendArgs& a, cudaStream_t stream) {
-  const int64_t queries = int64_t(a.batch) * a.rows * a.heads * a.shared;
-  const int warps = a.dim <= 512 ? kMostAnyWarps : kMostAnyWarps / 2;  // 48 KB hold their sums
-  cudaError_t e = launch_kernel(attend_any_kernel,
-                                dim3(unsigned(std::min<int64_t>(queries, kSms * 64))),
-                                dim3(warps * 32), size_t(warps + 1) * a.dim * 4, stream, a);
+  const int tiles = (a.rows * a.shared + kQueries - 1) / kQueries;
+  const int64_t units = int64_t(a.batch) * a.heads * tiles;
+  // as many warps as 96 KB hold the sums of
+  const int warps = std::min(kMostAnyWarps, 96 * 1024 / 4 / a.dim / kQueries - 1);
+  const int smem = (warps + 1) * kQueries * a.dim * 4;
+  static PerDevice<1> allowed[2];
+  void (*kernel)(AttendArgs, int) = a.bits == 8 ? attend_any_kernel<8> : attend_any_kernel<4>;
+  cudaError_t e = allow_shared(kernel, smem, allowed[a.bits == 8]);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(kernel,
+                                dim3(unsigned(std::min<int64_t>(units, kSms * 64))),
+                                dim3(warps * 32), size_t(smem), stream, a, tiles);
   if (e != cudaSuccess || a.weights == nullptr || a.most == 0) return e;
   const int64_t tokens = int64_t(a.batch) * a.heads * a.most;
   const dim3 all(unsigned(std::min<int64_t>((tokens + kWarps - 1) / kWarps, kSms * 64)));
@@ -264,6 +346,7 @@ extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, i
   a.per_block.set(uint32_t(std::min<int64_t>(block_size, INT32_MAX)));
   a.lengths = lengths;
   a.n_rows = n_rows;
+  a.per_group.set(uint32_t(group));
   a.scale = float(double(scale) * 1.4426950408889634);
   a.window = window;
   a.weights = weights;

@@ -21,6 +21,7 @@ struct AttendArgs {
   int64_t blocks_stride, block;
   int most;        // tokens of a sequence, at most
   Div per_block;
+  Div per_group;
   const int32_t* lengths;
   const int32_t* n_rows;
   float scale;     // times log2(e): scores are exponents of two

@@ -7,16 +7,22 @@
 namespace lp {
 
 // The value of element d of a head's codes.
+template <int BITS>
 __device__ __forceinline__ float value_at(const AttendArgs& a, const uint8_t* codes,
                                           const char* params, int d) {
-  const uint32_t held = *reinterpret_cast<const uint32_t*>(params + int64_t(d / a.group) * 4);
-  if (a.bits == 8) {
+  const uint32_t held = *reinterpret_cast<const uint32_t*>(params + a.per_group.quot(uint32_t(d)) * 4);
+  if (BITS == 8) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(codes[d])));
     return __fmul_rn(Elt<LP_F16>::half_bits_to_float(h & 0xffffu), __uint_as_float(held));
   }
   const uint32_t code = (codes[d >> 1] >> (4 * (d & 1))) & 15u;
   return __fmaf_rn(float(code), __uint_as_float(held << 16), __uint_as_float(held & 0xffff0000u));
+}
+
+__device__ __forceinline__ float value_at(const AttendArgs& a, const uint8_t* codes,
+                                          const char* params, int d) {
+  return a.bits == 8 ? value_at<8>(a, codes, params, d) : value_at<4>(a, codes, params, d);
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
