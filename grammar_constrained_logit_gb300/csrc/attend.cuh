@@ -32,7 +32,7 @@ struct AttendArgs {
   // of the tensor-core kernels: the work is cut into tiles of tokens, in the order (sequence,
   // tile of rows, tile of tokens).  `workers` workers take a range of them each: one team of
   // warps for every `team` heads, a warp a head
-  int team, head_groups, row_tiles, workers, min_tiles;
+  int team, head_groups, row_tiles, workers;
   bool wide_params;   // 16-byte copies of params
   // a slot's place is slot * stride in both parts, and counted in copied units (codes) and
   // words (params) it is below 2^32: then these are the strides

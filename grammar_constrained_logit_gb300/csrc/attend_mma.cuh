@@ -16,6 +16,14 @@
 //
 // The order of the contraction's elements is free as long as both sides have the same one:
 // a lane's share of a row is contiguous, read from shared memory as it lies.
+//
+// Measured, in a graph: 32 sequences of up to 8192 tokens, 8 heads of 128 with 4 queries each,
+// 8 bits: 55.7 us for 251 MB; all of 8192: 96.7 us for 554 MB, 84% of the copy rate, with the
+// join some 5 us of it.  Memory bounds it.  4 sequences of up to 65536 with 8 queries, 4 bits in
+// groups of 32: 89 us for 273 MB: 48 M warp instructions, 55% of the issue slots, and waits
+// for one another's results.  A warp a query, on the other units: 20197 and
+// 147804 us.  A worker may have a single tile: with two at least one token's attention takes
+// 10.1 us for 9.7, with eight 15.7.
 #pragma once
 
 #include "attend.cuh"
@@ -46,6 +54,7 @@ struct Shape {
   static constexpr int kStages = 2;
   static constexpr int kRows = 8 * NR;
   // blocks of four warps on an SM: 168 registers a thread where that holds the sums, else 255
+  // (a fourth block leaves 128, and the sums of 8 rows by 128 elements are spilled)
   static constexpr int kResident = NR == 1 && DIM <= 128 ? 3 : 2;
 };
 
@@ -182,7 +191,7 @@ __device__ __forceinline__ Division divide(const AttendArgs& a) {
   for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(kFullWarp, all, o);
   Division d;
   d.total = all * a.row_tiles;
-  d.workers = int(min(int64_t(a.workers), max(int64_t(1), (d.total + a.min_tiles - 1) / a.min_tiles)));
+  d.workers = int(min(int64_t(a.workers), max(int64_t(1), d.total)));
   return d;
 }
 

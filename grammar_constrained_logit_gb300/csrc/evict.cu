@@ -9,6 +9,12 @@
 // so loads may run ahead of stores as far as they like, and a store has to wait only for the
 // loads of its own round and those before it.  A round is what the blocks of a cluster hold
 // in shared memory; they meet at one barrier a round, with the next round's loads under way.
+//
+// Measured, in a graph, 8 heads of 128: 32 sequences of up to 4096 tokens to 2048 in 8 bits 68 us
+// (17 the selection, 50 the moves; 113 MB), 4 of 65536 to 16384 in 4 bits 102 us (37 and 64), one
+// of 640 to 512 11.5 us.  Selection: chains of barriers over a cluster.  Moves: instructions,
+// 53% of the issue slots, for pieces of 16 bytes, and the rounds' barriers; with a thread's
+// place worked out for each piece instead of once they took twice as long.
 #include <algorithm>
 
 #include "common.cuh"

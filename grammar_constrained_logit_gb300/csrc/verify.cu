@@ -16,6 +16,13 @@
 // defined.  Should a second one still reach the winner (once in some thousand slots), or
 // nothing be left of p - q, the slot's first block goes through the row once more, token by
 // token as defined.
+//
+// Measured, in a graph: 64 x 8 rows of 128256 bf16 with a tenth kept 66 us for 144 MB, 48 x 5 of
+// 65519 fp16 27.6, 1 x 4 of 32000 f32 9.8.  The first kernel (33 us cold) is bound by instructions,
+// 11.7 for each of a lane's tokens, 71% of the issue slots: four blocks an SM, that leave a lane
+// 64 registers for what is under way (five: 71 us for the whole, six: 81).  The second (39 us
+// cold) by the noise of the tokens that the bounds leave, four words for each four of which one
+// is left (three blocks an SM: 80 us for the whole).
 #include <algorithm>
 
 #include "common.cuh"
