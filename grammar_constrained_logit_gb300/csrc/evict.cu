@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
     const int after = source_of(round + 3);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     if (blocks == 1) {
-      __syncthreads();  // this round's sources are read, by all
+      __syncthreads();  // the sources are read, by all
     } else {
       // nothing was written that the others wait for: the loads are done, and that is all
       asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");

@@ -315,9 +315,10 @@ def test_many_rows(dtype, dim, window):
     check(cache, q, blocks, lengths, 16, dtype, weights=True, n_rows=n_rows, **kw)
 
 
-def test_many_rows_peaked_and_far():
+@pytest.mark.parametrize("batch", [5, 9])
+def test_many_rows_peaked_and_far(batch):
     """Scores of hundreds, and values of sizes far apart: what a row's weights are taken against
-    moves often."""
+    moves often.  With few queries in all, and with as many as the tensor-memory kernels take."""
     rng = np.random.default_rng(21)
     cache = filled(1024, 8, 128, 8, 128, spread=3.0)
     g = torch.Generator("cuda").manual_seed(9)
@@ -325,23 +326,25 @@ def test_many_rows_peaked_and_far():
     mag = torch.exp(torch.randn(1024, 1, 1, device="cuda", generator=g) * 4)
     mag[::5] = 0.0
     ops.cache_write(cache, (x * 2, x.flip(0) * mag), torch.arange(1024, device="cuda"))
-    blocks = np.arange(64, dtype=np.int32)[None].repeat(5, 0)
+    blocks = np.arange(64, dtype=np.int32)[None].repeat(batch, 0)
+    lengths = [1000, 900, 777, 512, 300, 41, 128, 129, 1024][:batch]
     for scale in (None, 2.0, -1.0, 0.0):
-        q = rng.standard_normal((5, 40, 32, 128)).astype(np.float32)
-        check(cache, q, blocks, [1000, 900, 777, 512, 300], 16, "bf16", scale=scale, weights=True)
+        q = rng.standard_normal((batch, 40, 32, 128)).astype(np.float32)
+        check(cache, q, blocks, lengths, 16, "bf16", scale=scale, weights=True)
 
 
+@pytest.mark.parametrize("batch", [5, 6])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_many_rows_nan(dtype):
+def test_many_rows_nan(dtype, batch):
     """NaN values where some rows do not look, and where all of them do."""
     rng = np.random.default_rng(22)
     cache = filled(512, 8, 128, 8, 128)
-    blocks = np.arange(32, dtype=np.int32)[None].repeat(5, 0)
-    q = rng.standard_normal((5, 130, 16, 128)).astype(np.float32)
+    blocks = np.arange(32, dtype=np.int32)[None].repeat(batch, 0)
+    q = rng.standard_normal((batch, 130, 16, 128)).astype(np.float32)
     bad = torch.full((1, 8, 128), 0.5, device="cuda")
     bad[..., 7] = float("nan")
     fine = torch.full((1, 8, 128), 0.5, device="cuda")
-    lengths = [400] * 5
+    lengths = [400] * batch
     qd = torch.from_numpy(q).cuda().to(TYPES[dtype])
     args = (torch.from_numpy(blocks).cuda(),
             torch.tensor(lengths, dtype=torch.int32, device="cuda"))
