@@ -413,3 +413,32 @@ def test_offsets_past_32_bits():
     a = ops.cache_attend(cache, q, ids + base // size, lens, block_size=size)
     b = ops.cache_attend(small, q, ids, lens, block_size=size)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bits, dim, group", [(8, 40, 40), (4, 112, 16), (8, 160, 10), (4, 300, 30),
+                                              (8, 1024, 128), (4, 514, 514), (8, 1, 1)])
+def test_widths_without_tensor_cores(bits, dim, group, dtype):
+    """Queries of several rows in a block's four, more tokens than its warps take at once."""
+    rng = np.random.default_rng(dim)
+    rows, heads, shared = 3, 2, 3
+    lengths, n_rows = [400, 0, 1, 33, 290], [3, 3, 3, 2, 0]
+    total = (sum(-(-n // 16) for n in lengths) + 1) * 16
+    cache = filled(total, heads, dim, bits, group, page=16)
+    blocks = table(rng, lengths, 16, total)
+    blocks[0, 4] = -1
+    q = rng.standard_normal((5, rows, heads * shared, dim)).astype(np.float32)
+    for window in (None, 37):
+        kw = {} if window is None else {"window": window}
+        check(cache, q, blocks, lengths, 16, dtype, weights=True, n_rows=n_rows, **kw)
+
+
+@pytest.mark.parametrize("dim", [128, 72])
+def test_empty_cache(dim):
+    cache = ops.QuantCache.allocate(0, 2, dim)
+    q = torch.randn(2, 3, 4, dim, device="cuda")
+    blocks = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([20, 0], dtype=torch.int32, device="cuda")
+    weights = torch.ones(2, 2, 32, device="cuda")
+    out = ops.cache_attend(cache, q, blocks, lengths, block_size=16, weights=weights)
+    assert (out == 0).all() and (weights == 1).all()
