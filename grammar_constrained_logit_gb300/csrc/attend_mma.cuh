@@ -5,11 +5,15 @@
 // columns are the queries that share a head: one decoded token's four or eight queries leave
 // no columns empty that cost anything.
 //
-// Codes go into the products as they are, exactly: e4m3 as the fp16 of the same value, a
-// 4-bit code c as the subnormal fp16 c * 2^-24 (or 16 c * 2^-24: its bits where they lie).
-// A group's scale s and low l come in 32 bits outside: for keys
-//   S = sum over groups of s_g (q_g . c_g) + l_g (sum of q_g),
-// for values P_g = P s_g meets the codes, and sum_t P_t l_tg is kept beside.  Queries are
+// Codes go into the products exactly, as normal fp16: e4m3 as the fp16 of the same value, a
+// 4-bit code c as c - 8 (or 16 (c - 8): its bits stay where they lie).  A product's sum is cut
+// at a place that goes by its operands' exponents, and a subnormal's is -14 whatever its value:
+// c * 2^-24, which needs no subtraction, leaves the sum six to ten bits less.  Less 8, codes are
+// even about zero, and what is added up is no larger than the values are.  (8000 tokens in groups
+// of 32, f32: 6.6e-7 off in norm; as subnormals 5.6e-5, in 121 us for 140 at the size below.)
+// A group's scale s and middle m = l + 8 s come in 32 bits outside: for keys
+//   S = sum over groups of s_g (q_g . c_g) + m_g (sum of q_g),
+// for values P_g = P s_g meets the codes, and sum_t P_t m_tg is kept beside.  Queries are
 // scaled to 2^14 by a power of two a row and taken in one piece of 11 bits (bf16) or two.
 // P s_g is held at most 2^15: M, which exponents are taken against, is the largest of
 // x + floor(log2 s), so what is rounded off is small beside the largest product.
@@ -20,8 +24,7 @@
 // Measured, in a graph: 32 sequences of up to 8192 tokens, 8 heads of 128 with 4 queries each,
 // 8 bits: 55.7 us for 251 MB; all of 8192: 96.7 us for 554 MB, 84% of the copy rate, with the
 // join some 5 us of it.  Memory bounds it.  4 sequences of up to 65536 with 8 queries, 4 bits in
-// groups of 32: 89 us for 273 MB: 48 M warp instructions, 55% of the issue slots, and waits
-// for one another's results.  A warp a query, on the other units: 20197 and
+// groups of 32: 99.5 us for 273 MB: instructions, and waits for one another's results.  A warp a query, on the other units: 20197 and
 // 147804 us.  A worker may have a single tile: with two at least one token's attention takes
 // 10.1 us for 9.7, with eight 15.7.
 #pragma once
@@ -114,6 +117,25 @@ __device__ __forceinline__ uint32_t f16_two(float low, float high) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(high), "f"(low));
   return r;
+}
+
+// Two 4-bit codes less 8, as fp16: c (bits 0 to 3 of each half) in the last places of 1024, or
+// 16 c (bits 4 to 7), less 1024 and 8 or 128.
+__device__ __forceinline__ uint32_t codes_low(uint32_t x) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"((x & 0x000f000fu) | 0x64006400u), "r"(0x64086408u));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes_high(uint32_t x) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"((x & 0x00f000f0u) | 0x64006400u), "r"(0x64806480u));
+  return r;
+}
+
+// Of 4-bit params: a group's scale, and the value in its middle.
+__device__ __forceinline__ float scale_of(uint32_t held) { return __uint_as_float(held << 16); }
+__device__ __forceinline__ float middle_of(uint32_t held) {
+  return fmaf(8.0f, scale_of(held), __uint_as_float(held & 0xffff0000u));
 }
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -271,15 +293,14 @@ struct Queries {
       const int up = most > 0.0f && most <= 3.4028235e38f
                          ? 14 - (int(__float_as_uint(most) >> 23) - 127) : 0;
       const float f1 = power_of_two(up / 2), f2 = power_of_two(up - up / 2);
-      // (4-bit codes stand for 2^24 of what they are as fp16; so do the lows' sums then)
-      const float mine = a.scale / f1 / f2 * (T::kBits == 4 ? 16777216.0f : 1.0f);
+      const float mine = a.scale / f1 / f2;
       float sums[kLowSums] = {};
 #pragma unroll
       for (int t = 0; t < T::kDim / 16; ++t) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x[t][e] = x[t][e] * f1 * f2;
-          if (T::kBits == 4) sums[t / T::kSteps] += x[t][e] * 5.9604644775390625e-08f;
+          if (T::kBits == 4) sums[t / T::kSteps] += x[t][e];
         }
         // codes whose bits lie four higher are 16 times what they are
         if (T::kBits == 4) x[t][2] *= 0.0625f, x[t][3] *= 0.0625f;
@@ -491,13 +512,13 @@ __device__ __forceinline__ void scores(float (&s)[T::kM][T::kNR][4], const Queri
           op[2] = e4m3_two(x.w[i] >> 16), op[3] = e4m3_two(y.w[i] >> 16);
         } else if (T::kBlock == 16) {
           const uint32_t u = __byte_perm(x.w[0], 0, 0x4140), v = __byte_perm(y.w[0], 0, 0x4140);
-          op[0] = u & 0x000f000fu, op[1] = v & 0x000f000fu;
-          op[2] = u & 0x00f000f0u, op[3] = v & 0x00f000f0u;
+          op[0] = codes_low(u), op[1] = codes_low(v);
+          op[2] = codes_high(u), op[3] = codes_high(v);
         } else {
           const uint32_t u = i & 1 ? x.w[i / 2] >> 8 : x.w[i / 2];
           const uint32_t v = i & 1 ? y.w[i / 2] >> 8 : y.w[i / 2];
-          op[0] = u & 0x000f000fu, op[1] = v & 0x000f000fu;
-          op[2] = u & 0x00f000f0u, op[3] = v & 0x00f000f0u;
+          op[0] = codes_low(u), op[1] = codes_low(v);
+          op[2] = codes_high(u), op[3] = codes_high(v);
         }
 #pragma unroll
         for (int n = 0; n < T::kNR; ++n)
@@ -514,8 +535,8 @@ __device__ __forceinline__ void scores(float (&s)[T::kM][T::kNR][4], const Queri
           if (T::kBits == 8) {
             s[m][n][e] = fmaf(acc[n][e], __uint_as_float(h), before);
           } else {
-            const float lows = fmaf(__uint_as_float(h & 0xffff0000u), q.low[n][e & 1][k], before);
-            s[m][n][e] = fmaf(acc[n][e], __uint_as_float(h << 16), lows);
+            const float lows = fmaf(middle_of(h), q.low[n][e & 1][k], before);
+            s[m][n][e] = fmaf(acc[n][e], scale_of(h), lows);
           }
         }
     }
@@ -662,8 +683,8 @@ struct Sums {
       for (int k = 0; k < T::kBlocks; ++k) {
         // P s_g, rounded, as the B operand
         const uint32_t h0 = p0.w[k], h1 = p1.w[k];
-        const float s0 = __uint_as_float(T::kBits == 8 ? h0 : h0 << 16);
-        const float s1 = __uint_as_float(T::kBits == 8 ? h1 : h1 << 16);
+        const float s0 = T::kBits == 8 ? __uint_as_float(h0) : scale_of(h0);
+        const float s1 = T::kBits == 8 ? __uint_as_float(h1) : scale_of(h1);
         uint32_t p[T::kNR][T::kPieces][2];
 #pragma unroll
         for (int n = 0; n < T::kNR; ++n) {
@@ -680,8 +701,7 @@ struct Sums {
                                    w3 - Elt<LP_F16>::half_bits_to_float(b >> 16)));
           }
           if (T::kBits == 4) {
-            const float l0 = __uint_as_float(h0 & 0xffff0000u);
-            const float l1 = __uint_as_float(h1 & 0xffff0000u);
+            const float l0 = middle_of(h0), l1 = middle_of(h1);
             low[k % kLows][n][0] = fmaf(e[0], l0, fmaf(e[2], l1, low[k % kLows][n][0]));
             low[k % kLows][n][1] = fmaf(e[1], l0, fmaf(e[3], l1, low[k % kLows][n][1]));
           }
@@ -704,8 +724,8 @@ struct Sums {
             const int i = v & 3, sel = i | (4 + i) << 8;
             const uint32_t x = __byte_perm(va.w[v / 4], vb.w[v / 4], sel);
             const uint32_t y = __byte_perm(vc.w[v / 4], vd.w[v / 4], sel);
-            op[0] = x & 0x000f000fu, op[1] = x & 0x00f000f0u;
-            op[2] = y & 0x000f000fu, op[3] = y & 0x00f000f0u;
+            op[0] = codes_low(x), op[1] = codes_high(x);
+            op[2] = codes_low(y), op[3] = codes_high(y);
           }
 #pragma unroll
           for (int n = 0; n < T::kNR; ++n)
@@ -741,7 +761,7 @@ struct Sums {
           for (int n = 0; n < T::kNR; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              o[k][v][n][e] = fmaf(o[k][v][n][e], e < 2 ? 16777216.0f : 1048576.0f,
+              o[k][v][n][e] = fmaf(o[k][v][n][e], e < 2 ? 1.0f : 0.0625f,
                                    low[k % kLows][n][e & 1]);
     }
   }
