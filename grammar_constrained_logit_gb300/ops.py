@@ -832,7 +832,8 @@ def _per_sequence(t: torch.Tensor, name: str, batch: int, device) -> int:
 
 
 def _blocks(blocks: torch.Tensor, block_size, cache: QuantCache) -> tuple:
-    """(pointer, stride, blocks a sequence, their size) of a block table."""
+    """(stride, blocks a sequence, their size) of a block table; a stride below the blocks a
+    sequence where rows overlap."""
     if blocks.dtype != torch.int32:
         raise TypeError("blocks must be int32")
     if blocks.device != cache.device:
@@ -843,7 +844,7 @@ def _blocks(blocks: torch.Tensor, block_size, cache: QuantCache) -> tuple:
     if size < 1:
         raise ValueError("block_size must be at least 1")
     n = blocks.size(1)
-    return blocks.data_ptr(), max(blocks.stride(0), n), n, size
+    return blocks.stride(0) if blocks.size(0) > 1 else max(blocks.stride(0), n), n, size
 
 
 def _weights(weights: torch.Tensor, batch: int, heads: int, tokens: int, device) -> tuple:
@@ -889,7 +890,9 @@ def cache_attend(cache: QuantCache, q: torch.Tensor, blocks: torch.Tensor, lengt
 
     Sequence b has ``lengths[b]`` tokens (int32); token t lies in slot ``blocks[b, t //
     block_size] * block_size + t % block_size`` (``blocks`` int32 [batch, n]; ``block_size``:
-    the cache's page size when None), and takes no part where that is outside the cache.  Its
+    the cache's page size when None), and takes no part where that is outside the cache.
+    Sequences may share blocks, and one table's rows their memory (``table.expand(batch, n)``:
+    it is copied then).  Its
     queries are its last tokens: row r of n sees tokens below lengths[b] - (n - 1 - r), of
     those the last ``window`` where one is given.  n is the number of rows, or ``n_rows[b]``
     (int32); rows behind it, and rows that see nothing, give zeros.  ``scale``: dim ** -0.5
@@ -928,7 +931,10 @@ def cache_attend(cache: QuantCache, q: torch.Tensor, blocks: torch.Tensor, lengt
     if window is not None and window < 1:
         raise ValueError("window must be at least 1")
     held = (None, 0, 0) if weights is None else \
-        _weights(weights, batch, heads, table[2] * table[3], device)
+        _weights(weights, batch, heads, table[1] * table[2], device)
+    if table[0] < table[1]:  # the library takes rows apart alone
+        blocks = blocks.contiguous()
+        table = (table[1], *table[1:])
     stream = _raw_stream(device.index)
     if workspace is None:
         workspace = _scratch(_attend_scratch, device, stream,
@@ -938,7 +944,8 @@ def cache_attend(cache: QuantCache, q: torch.Tensor, blocks: torch.Tensor, lengt
         _given_workspace(workspace, device, "cache's")
     _call("lp_cache_attend", device, (
         cache._parts, cache.bits, *cache._sizes, ctypes.byref(_lib.Rows(*_rows(q4, dim))),
-        ctypes.byref(_lib.Rows(*_rows(out4, dim))), dt, batch, rows, q_heads, *table, lens, taken,
+        ctypes.byref(_lib.Rows(*_rows(out4, dim))), dt, batch, rows, q_heads, blocks.data_ptr(),
+        *table, lens, taken,
         dim ** -0.5 if scale is None else float(scale), 0 if window is None else int(window),
         *held, workspace.data_ptr(), workspace.numel(), stream))
     return out
@@ -967,9 +974,9 @@ def cache_evict(cache: QuantCache, weights: torch.Tensor, blocks: torch.Tensor,
     its order, weights too; the weights of the places behind become 0.
 
     ``blocks``, ``block_size`` and ``lengths`` as ``cache_attend``'s; sequences must not share
-    blocks.  Returns the new lengths, int32 [batch] (or ``out``, apart from ``lengths``); their
-    next token goes to place new_length.  ``workspace``: as ``cache_attend``'s, of
-    ``cache_evict_workspace_bytes``."""
+    blocks (rows of ``blocks`` that share their memory are refused).  Returns the new lengths,
+    int32 [batch] (or ``out``, apart from ``lengths``); their next token goes to place
+    new_length.  ``workspace``: as ``cache_attend``'s, of ``cache_evict_workspace_bytes``."""
     device, heads = cache.device, cache.heads
     keep, first, recent = int(keep), int(first), int(recent)
     if min(keep, first, recent) < 0 or first + recent > keep:
@@ -977,12 +984,14 @@ def cache_evict(cache: QuantCache, weights: torch.Tensor, blocks: torch.Tensor,
     table = _blocks(blocks, block_size, cache)
     batch = blocks.size(0)
     lens = _per_sequence(lengths, "lengths", batch, device)
-    held = _weights(weights, batch, heads, table[2] * table[3], device)
+    if table[0] < table[1]:
+        raise ValueError("rows of blocks must not overlap: sequences would share blocks")
+    held = _weights(weights, batch, heads, table[1] * table[2], device)
     if out is None:
         out = torch.empty(batch, dtype=torch.int32, device=device)
     else:
         _per_sequence(out, "out", batch, device)
-    keep = min(keep, max(table[2] * table[3], first + recent))  # no sequence is longer
+    keep = min(keep, max(table[1] * table[2], first + recent))  # no sequence is longer
     stream = _raw_stream(device.index)
     if workspace is None:
         workspace = _scratch(_evict_scratch, device, stream,
@@ -990,8 +999,9 @@ def cache_evict(cache: QuantCache, weights: torch.Tensor, blocks: torch.Tensor,
     else:
         _given_workspace(workspace, device, "cache's")
     _call("lp_cache_evict", device, (
-        cache._parts, cache.parts, cache.bits, *cache._sizes, *held, batch, *table, lens, keep,
-        first, recent, out.data_ptr(), workspace.data_ptr(), workspace.numel(), stream))
+        cache._parts, cache.parts, cache.bits, *cache._sizes, *held, batch, blocks.data_ptr(),
+        *table, lens, keep, first, recent, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        stream))
     return out
 
 
