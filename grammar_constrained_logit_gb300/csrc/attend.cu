@@ -10,7 +10,6 @@
 #include <cmath>
 
 #include "attend.cuh"
-#include "attend_row.cuh"
 
 namespace lp {
 
@@ -32,6 +31,47 @@ constexpr int kMostAnyWarps = 16;
 constexpr int kQueries = 4;     // of a block of attend_any_kernel
 constexpr int kGroup = 2;       // tokens that a warp of it has at a time
 constexpr int kMostDim = 1024;
+
+// The value of element d of a head's codes.
+template <int BITS>
+__device__ __forceinline__ float value_at(const AttendArgs& a, const uint8_t* codes,
+                                          const char* params, int d) {
+  const uint32_t held = *reinterpret_cast<const uint32_t*>(params + a.per_group.quot(uint32_t(d)) * 4);
+  if (BITS == 8) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(codes[d])));
+    return __fmul_rn(Elt<LP_F16>::half_bits_to_float(h & 0xffffu), __uint_as_float(held));
+  }
+  const uint32_t code = (codes[d >> 1] >> (4 * (d & 1))) & 15u;
+  return __fmaf_rn(float(code), __uint_as_float(held << 16), __uint_as_float(held & 0xffff0000u));
+}
+
+__device__ __forceinline__ float value_at(const AttendArgs& a, const uint8_t* codes,
+                                          const char* params, int d) {
+  return a.bits == 8 ? value_at<8>(a, codes, params, d) : value_at<4>(a, codes, params, d);
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kFullWarp, x, o);
+  return x;
+}
+
+struct Head {  // of one part, at one slot
+  const uint8_t* codes;
+  const char* params;
+};
+
+__device__ __forceinline__ Head head_at(const AttendArgs& a, int part, int64_t slot, int h) {
+  const lp_cache_part& p = a.part[part];
+  Head r;
+  r.codes = static_cast<const uint8_t*>(p.codes) +
+            slot_place(a, slot, p.code_page_stride, p.code_slot_stride) + h * p.code_head_stride;
+  r.params = static_cast<const char*>(p.params) +
+             slot_place(a, slot, p.param_page_stride, p.param_slot_stride) +
+             h * p.param_head_stride;
+  return r;
+}
 
 // Elements d0 .. d0 + 127 of kGroup heads, four to a lane; 0 behind the last (whose
 // place loads the last again: no load waits for a choice).

@@ -15,18 +15,17 @@
 //   0-3, 4-7   a thread a query: exponents, P, the sums
 //   8-11       codes to fp16, two tiles ahead
 //   12         issues the products
-// Measured: 1024 queries of 32 heads over 16384 tokens, in a graph: 521 us, 512 TFLOP/s, 26% of
+// Measured: 1024 queries of 32 heads over 16384 tokens, in a graph: 510 us, 522 TFLOP/s, 27% of
 // the tensor pipe; by m16n8k16 1447.  What bounds it is the softmax's way out of tensor memory
 // and back: 6.0 thousand cycles of the 7.5 thousand that a tile takes (a pair's two loads, 128
 // exponents, the stores); the products are 2.  One block an SM, of 13 warps with 128 registers;
 // with the softmax over 16 warps 567 to 695 us, with registers moved to it 803, with 12 warps of
-// 168 registers 584 to 642.  fp16 takes P in two pieces, 771 us; heads of 64 take 440.
+// 168 registers 584 to 642.  fp16 takes P in two pieces, 810 us; heads of 64 take 431.
 //
 // Every wait is bounded; where one runs out all roles stop and the block's queries become NaN.
 #include <algorithm>
 
 #include "attend.cuh"
-#include "attend_row.cuh"
 
 namespace lp {
 namespace {
@@ -47,6 +46,9 @@ struct alignas(1024) Shared {
   uint32_t held[4][4];  // bits of the tile's tokens that are there
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], drained;
   const char* rows[2][2][kTile];  // of codes: [buffer][keys, values][token]
+  // what is no number in tokens that some queries do not see is taken out of the products, and
+  // noted at the end for those that do: a bit a query, of each element and of all
+  uint32_t nan[kTile][8], nan_all[8];
   uint32_t tmem;
   int failed, nan_hidden;
 };
@@ -182,6 +184,59 @@ __device__ __forceinline__ void put_codes(char* half, int row, int piece, const 
 __device__ __forceinline__ bool has_nan(const uint4& c) {
   const auto one = [](uint32_t w) { return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0; };
   return one(c.x) || one(c.y) || one(c.z) || one(c.w);
+}
+
+// The block's queries [lo, hi) that see a token, in bits.
+struct Seers {
+  int lo, hi;
+  __device__ __forceinline__ void note(uint32_t* bits) const {
+    for (int i = 0; i < 8; ++i) {
+      const int a = min(max(lo - 32 * i, 0), 32), b = min(max(hi - 32 * i, 0), 32);
+      if (a < b) atomicOr(bits + i, uint32_t(((uint64_t(1) << b) - 1) ^ ((uint64_t(1) << a) - 1)));
+    }
+  }
+};
+
+__device__ __forceinline__ Seers seers_of(const AttendArgs& a, const Sequence& seq, int i0, int t) {
+  // row r's end is the tokens less (rows - 1 - r), and its first the end less the window
+  const int64_t first = int64_t(t) - seq.tokens + seq.rows;
+  const int64_t rows = seq.rows;
+  const int64_t last = (a.window > 0 ? min(rows, first + min(a.window, int64_t(1) << 31)) : rows) - 1;
+  Seers s;
+  s.lo = int(min(max(max(first, int64_t(0)) * a.shared - i0, int64_t(0)), int64_t(2 * kTile)));
+  s.hi = int(min(max((last + 1) * a.shared - i0, int64_t(0)), int64_t(2 * kTile)));
+  return s;
+}
+
+// 16 codes without NaN.
+__device__ __forceinline__ uint4 without_nan(const uint4& c) {
+  const auto one = [](uint32_t w) {
+    return w & ~(((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu);
+  };
+  return make_uint4(one(c.x), one(c.y), one(c.z), one(c.w));
+}
+
+// Notes what a tile's tokens, of which some queries see not all, have of values that are no
+// numbers: threads `index` of `count`.
+__device__ __noinline__ void note_hidden(Shared& s, const AttendArgs& a, int b, int h, int i0,
+                                         int tile, int end, int index, int count) {
+  const Sequence seq = sequence(a, b);
+  const lp_cache_part& p = a.part[1];
+  const int pieces = a.dim / 16;
+  for (int i = index; i < kTile * pieces; i += count) {
+    const int t = tile * kTile + i / pieces, d = i % pieces * 16;
+    const int64_t slot = t < end ? slot_of(a, b, t) : -1;
+    if (slot < 0) continue;
+    const Seers seers = seers_of(a, seq, i0, t);
+    const float scale = *reinterpret_cast<const float*>(
+        static_cast<const char*>(p.params) + h * p.param_head_stride +
+        slot_place(a, slot, p.param_page_stride, p.param_slot_stride));
+    if (d == 0 && !(fabsf(scale) < INFINITY)) seers.note(s.nan_all);
+    const uint8_t* codes = static_cast<const uint8_t*>(p.codes) + h * p.code_head_stride +
+                           slot_place(a, slot, p.code_page_stride, p.code_slot_stride) + d;
+    for (int e = 0; e < 16; ++e)
+      if ((codes[e] & 0x7f) == 0x7f) seers.note(s.nan[d + e]);
+  }
 }
 
 // 16 columns, under way while the ones before are worked on.
@@ -508,7 +563,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             slot_place(a, slot, vp.param_page_stride, vp.param_slot_stride));
       }
     };
+    // (rows that do not see a token have 0 * what it holds)
+    const auto hides = [&](int t) {
+      const int t0 = (first + t) * kTile;
+      return !(t0 >= all_from && t0 + kTile <= all_until);
+    };
     const auto put_scales = [&](int t) {
+      if (!(fabsf(scale[1]) < INFINITY) && hides(t)) {
+        *static_cast<volatile int*>(&s.nan_hidden) = 1;
+        scale[1] = 0.0f;
+      }
       s.scales[t & 3][0][in] = scale[0];
       s.scales[t & 3][1][in] = scale[1];
       s.scales[t & 3][2][in] =
@@ -551,10 +615,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         put_codes(v + (piece >> 2) * kHalf, line + i * kLines, piece & 3, codes[1][i]);
         bad = bad || has_nan(codes[1][i]);
       }
-      // NaN values in tokens that some rows do not see would reach those by 0 * NaN
-      const int t0 = (first + t) * kTile;
-      if (bad && !(t0 >= all_from && t0 + kTile <= all_until))
+      if (bad && hides(t)) {
         *static_cast<volatile int*>(&s.nan_hidden) = 1;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+          put_codes(v + (piece >> 2) * kHalf, line + i * kLines, piece & 3,
+                    without_nan(codes[1][i]));
+      }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       bar_arrive(&s.v_full[stage]);
       fetch(t + 1, 1);
@@ -610,8 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const bool failed = *static_cast<volatile int*>(&s.failed) != 0;
-  const bool again = *static_cast<volatile int*>(&s.nan_hidden) != 0 && !failed;
-  if (warp < 8 && !again) {
+  const bool hidden = *static_cast<volatile int*>(&s.nan_hidden) != 0;
+  if (warp < 8) {
     // ------------------------------------------------------------------------------- results
     char* to = static_cast<char*>(a.out.data) + b * a.out.batch_stride + r * a.out.row_stride +
                j * a.out.head_stride;
@@ -657,13 +724,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 12)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-  if (again) {  // row by row, as defined: a warp each, its scratch where the queries were
-    float* mine = reinterpret_cast<float*>(s.k[0]) + warp * 2 * DIM;
-    for (int i = warp; i < 2 * kTile; i += kThreads / 32)
-      if (i0 + i < per_head) {
-        const int rr = (i0 + i) / a.shared;
-        attend_row(a, b, rr, h * a.shared + i0 + i - rr * a.shared, mine, mine + DIM);
-      }
+  if (hidden) {  // for all of the block: rows that see what was taken out have it
+    for (int i = tid; i < DIM * 8; i += kThreads) s.nan[i >> 3][i & 7] = 0;
+    if (tid < 8) s.nan_all[tid] = 0;
+    __syncthreads();
+    for (int t = first; t < last; ++t)
+      if (t * kTile < all_from || t * kTile + kTile > all_until)
+        note_hidden(s, a, b, h, i0, t, high.end, tid, kThreads);
+    __syncthreads();
+    if (warp < 8 && there) {
+      char* to = static_cast<char*>(a.out.data) + b * a.out.batch_stride + r * a.out.row_stride +
+                 j * a.out.head_stride;
+      for (int d = 0; d < DIM; ++d)
+        if (((s.nan[d][warp] | s.nan_all[warp]) >> lane) & 1u)
+          store_float(to, d, __uint_as_float(0x7fc00000u), a.dt);
+    }
   }
 }
 

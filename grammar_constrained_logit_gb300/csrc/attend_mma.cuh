@@ -138,6 +138,12 @@ __device__ __forceinline__ float middle_of(uint32_t held) {
   return fmaf(8.0f, scale_of(held), __uint_as_float(held & 0xffff0000u));
 }
 
+// Whether what is held for a group stands for numbers.
+template <int BITS>
+__device__ __forceinline__ bool numbers(uint32_t held) {
+  return fabsf(BITS == 8 ? __uint_as_float(held) : middle_of(held)) < INFINITY;
+}
+
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -577,6 +583,9 @@ struct Sums {
   // NaN codes of values of tokens that some rows do not see: those that see them get NaN,
   // and the codes become 0, which adds nothing to the others.
   __device__ __forceinline__ void split_nan(const Queries<T>& q, char* values, int t0, uint32_t held);
+  // The same for groups whose params are no numbers.
+  __device__ __forceinline__ void split_params(const Queries<T>& q, char* params, int t0,
+                                               uint32_t held, int gstep);
 
   __device__ __forceinline__ void add(const Queries<T>& q, char* stage, int t0, uint32_t held,
                                       int gstep, bool all_seen) {
@@ -584,19 +593,33 @@ struct Sums {
     float s[T::kM][T::kNR][4];
     scores<T>(s, q, stage, gstep);
     // params of this lane's tokens, and the largest scale of each as an exponent
-    const char* held_at = stage + 2 * T::kCodes + T::kParams;
+    char* held_at = stage + 2 * T::kCodes + T::kParams;
     float large[T::kM][2];
+    const auto look = [&] {
+      uint32_t all = 0;
 #pragma unroll
-    for (int m = 0; m < T::kM; ++m)
+      for (int m = 0; m < T::kM; ++m)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const auto p = block_params<T>(held_at + (m * 16 + 8 * u + g) * T::kBlocks * 4, gstep);
-        uint32_t most = T::kBits == 8 ? p.w[0] : p.w[0] << 16;
+        for (int u = 0; u < 2; ++u) {
+          const auto p = block_params<T>(held_at + (m * 16 + 8 * u + g) * T::kBlocks * 4, gstep);
+          uint32_t most = T::kBits == 8 ? p.w[0] : p.w[0] << 16;
 #pragma unroll
-        for (int k = 1; k < T::kBlocks; ++k)
-          most = max(most, T::kBits == 8 ? p.w[k] : p.w[k] << 16);
-        large[m][u] = float(max(int((most >> 23) & 255u) - 127, kLeastScale));
-      }
+          for (int k = 1; k < T::kBlocks; ++k)
+            most = max(most, T::kBits == 8 ? p.w[k] : p.w[k] << 16);
+          large[m][u] = float(max(int((most >> 23) & 255u) - 127, kLeastScale));
+          all = max(all, most);
+        }
+      return all < 0x7f800000u;
+    };
+    bool fine = look();
+    if (T::kBits == 4 && !all_seen)
+      for (int i = lane; i < T::kTile * T::kBlocks; i += 32)
+        fine = fine && numbers<T::kBits>(reinterpret_cast<const uint32_t*>(held_at)[i]);
+    // a weight of 0 does not take away an infinity; and an infinite scale is nobody's largest
+    if (!__all_sync(kFullWarp, fine)) {
+      split_params(q, held_at, t0, held, gstep);
+      look();
+    }
     float now[T::kNR][2];
 #pragma unroll
     for (int n = 0; n < T::kNR; ++n)
@@ -793,6 +816,35 @@ __device__ __forceinline__ void Sums<T>::split_nan(const Queries<T>& q, char* va
   __syncwarp();
   for (int i = lane; i < T::kCodes; i += 32)
     if ((values[i] & 0x7f) == 0x7f) values[i] = 0;
+  __syncwarp();
+}
+
+template <class T>
+__device__ __forceinline__ void Sums<T>::split_params(const Queries<T>& q, char* params, int t0,
+                                                      uint32_t held, int gstep) {
+  const int lane = threadIdx.x & 31;
+  for (int i = 0; i < T::kTile; ++i) {
+    const auto p = block_params<T>(params + i * T::kBlocks * 4, gstep);
+#pragma unroll
+    for (int k = 0; k < T::kBlocks; ++k) {
+      if (numbers<T::kBits>(p.w[k])) continue;
+#pragma unroll
+      for (int n = 0; n < T::kNR; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const Seen& v = q.see[n][e];
+          if (t0 + i < v.lo || t0 + i >= v.end || !((held >> i) & 1u)) continue;
+#pragma unroll
+          for (int j = 0; j < T::kValues / 2; ++j)
+            o[k][j][n][e] = o[k][j][n][2 + e] = __uint_as_float(0x7fc00000u);
+        }
+    }
+  }
+  __syncwarp();
+  for (int i = lane; i < T::kTile * T::kBlocks; i += 32) {
+    uint32_t& w = reinterpret_cast<uint32_t*>(params)[i];  // (some are nobody's)
+    if (!numbers<T::kBits>(w)) w = 0;
+  }
   __syncwarp();
 }
 

@@ -481,7 +481,8 @@ lp_status lp_cache_read(const lp_cache_part* parts, const lp_heads* out, int64_t
  *   t < end_r = lengths[b] - (n - 1 - r), and t >= end_r - window where window > 0:
  *   out[b, r, j] = sum_t p_t value_t,  p = softmax over those t of (scale * q[b, r, j] . key_t).
  * Rows from n on, and rows that see nothing, are zeros.  What a row does not see does not
- * count, whatever it holds.
+ * count, whatever it holds.  Of a value that a row sees, a code of NaN is NaN in its element,
+ * and params that are not finite leave no number in their group's elements.
  *   weights  device float32 [batch, heads, max_blocks * block_size], or NULL; a head's
  *            tokens are contiguous.  weights[b, h, t] += the sum of p_t over the rows and the
  *            query heads of h

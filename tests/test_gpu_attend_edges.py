@@ -47,3 +47,82 @@ def test_one_table_for_all(bits, dim, group, rows):
     out.zero_()
     graph.replay()
     assert torch.equal(out, ops.cache_attend(cache, q, table.contiguous(), lengths))
+
+
+def spoil(cache, t, bad, part=1):
+    """Puts what is no number into a token's params, in each of its groups in turn."""
+    params = cache.params.flatten(1, 2) if cache.codes.dim() == 5 else cache.params
+    for i in range(params.size(3)):
+        if cache.bits == 8:
+            params[part, t, :, i] = bad
+        else:
+            params[part, t, :, i, i % 2] = bad
+
+
+SPOILT = [float("nan"), float("inf"), -float("inf")]
+
+
+@pytest.mark.parametrize("bad", SPOILT)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("bits, dim, group, rows, shared", [
+    (8, 128, 128, 3, 2), (8, 128, 32, 3, 2), (8, 64, 64, 5, 4), (8, 72, 72, 3, 2),
+    (4, 128, 32, 3, 2), (4, 128, 128, 2, 8), (4, 80, 16, 6, 3), (4, 192, 64, 3, 2),
+    (4, 112, 16, 3, 2), (8, 128, 128, 130, 2), (8, 64, 64, 130, 2)])
+def test_params_that_are_no_numbers(bits, dim, group, rows, shared, dtype, bad):
+    """Scales and lows of tokens that a row does not see, before its window and behind it, do
+    not count, whatever they are, keys' as values'; rows that see them have no number."""
+    n, window, batch = 400, 150, 6
+    g = torch.Generator("cuda").manual_seed(dim)
+    q = torch.randn(batch, rows, 8 * shared, dim, device="cuda", generator=g).to(dtype)
+    blocks = torch.arange(32, dtype=torch.int32, device="cuda").expand(batch, 32).contiguous()
+    lengths = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    cache = filled(512, 8, dim, bits, group, page=16)
+    want = ops.cache_attend(cache, q, blocks, lengths, window=window)
+    weights = torch.zeros(batch, 8, 512, device="cuda")
+    ops.cache_attend(cache, q, blocks, lengths, window=window, weights=weights)
+    last = n - rows  # what the first row sees last
+    # nobody sees these, though they share a tile with tokens that somebody sees
+    for t in (last - window, last - window - 1, n, n + 1):
+        for part in range(2):
+            spoil(cache, t, bad, part)
+    again = torch.zeros_like(weights)
+    got = ops.cache_attend(cache, q, blocks, lengths, window=window, weights=again)
+    assert torch.equal(got, want) and torch.equal(again, weights)
+    # the last row alone sees the last token
+    spoil(cache, n - 1, bad)
+    got = ops.cache_attend(cache, q, blocks, lengths, window=window)
+    assert torch.equal(got[:, :-1], want[:, :-1]) and not got[:, -1].isfinite().any()
+    # the first row alone sees what its window begins with
+    spoil(cache, last - window + 1, bad)
+    got = ops.cache_attend(cache, q, blocks, lengths, window=window)
+    assert torch.equal(got[:, 1:-1], want[:, 1:-1])
+    assert not got[:, 0].isfinite().any() and not got[:, -1].isfinite().any()
+
+
+@pytest.mark.parametrize("bad", SPOILT)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("bits, dim, group", [(8, 128, 32), (4, 128, 32), (4, 80, 16), (8, 72, 24)])
+def test_a_group_that_is_no_number(bits, dim, group, dtype, bad):
+    """A value's group that is no number leaves the head's other elements as they are, whether
+    all rows see the token or some."""
+    g = torch.Generator("cuda").manual_seed(dim)
+    q = torch.randn(2, 4, 4, dim, device="cuda", generator=g).to(dtype)
+    blocks = torch.arange(20, dtype=torch.int32, device="cuda").expand(2, 20).contiguous()
+    lengths = torch.full((2,), 300, dtype=torch.int32, device="cuda")
+    for t, first in ((40, 0), (299, 3)):  # and the first row that sees it
+        cache = filled(320, 2, dim, bits, group)
+        for bits_of_it in range(1 if bits == 8 else 2):
+            was = cache.params[1, t].clone()
+            zeroed = cache.params[1, t, :, 1].clone()
+            cache.params[1, t, :, 1] = 0.0
+            want = ops.cache_attend(cache, q, blocks, lengths, block_size=16)
+            cache.params[1, t, :, 1] = zeroed
+            (cache.params[1, t, :, 1] if bits == 8 else
+             cache.params[1, t, :, 1, bits_of_it]).fill_(bad)
+            got = ops.cache_attend(cache, q, blocks, lengths, block_size=16)
+            cache.params[1, t] = was
+            mine = slice(group, 2 * group)
+            assert not got[:, first:, :, mine].isfinite().any()
+            got[..., mine] = want[..., mine] = 0.0
+            assert (got.double() - want.double()).abs().max() < 2.0 ** -7 * want.abs().max()
+            # (the token's largest scale may have been that group's: weights are rounded anew)
