@@ -71,12 +71,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
-def build_variant(name: str, defines: dict, sources=("sample.cu",), force: bool = False) -> str:
+def build_variant(name: str, defines: dict, sources=("sample.cu",), force: bool = False,
+                  rest: bool = False) -> str:
     """A test build: the given csrc sources compiled with extra preprocessor
-    definitions and linked as ``_build/<name>/liblp.so``.  Test builds exercise
+    definitions and linked as ``_build/<name>/liblp.so``, with the product's
+    objects of all others where ``rest`` is true.  Test builds exercise
     paths that the product build cannot reach on demand (a bounded wait made to
     run out); the product library ``liblp.so`` is never one of them."""
     nvcc = _nvcc()
+    others = []
+    if rest:
+        build()
+        others = sorted(os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
+                        for src in glob.glob(os.path.join(CSRC, "*.cu"))
+                        if os.path.basename(src) not in sources)
     out_dir = os.path.join(BUILD, name)
     os.makedirs(out_dir, exist_ok=True)
     srcs = [os.path.join(CSRC, x) for x in sources]
@@ -85,8 +93,8 @@ def build_variant(name: str, defines: dict, sources=("sample.cu",), force: bool 
     defs = [f"-D{k}={v}" for k, v in sorted(defines.items())]
     stamp = os.path.join(out_dir, "defines.txt")
     same = os.path.exists(stamp) and open(stamp).read() == " ".join(defs)
-    if force or not same or _stale(lib, srcs + headers):
-        objs = []
+    if force or not same or _stale(lib, srcs + headers + others):
+        objs = list(others)
         for src in srcs:
             obj = os.path.join(out_dir, os.path.basename(src)[:-3] + ".o")
             subprocess.check_call([nvcc, *ARCH, *FLAGS, *defs, "-c", src, "-o", obj])

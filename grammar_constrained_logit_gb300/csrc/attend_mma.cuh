@@ -32,6 +32,7 @@
 #include "attend.cuh"
 
 namespace lp {
+namespace {  // what a launch asks the runtime once belongs to its own library
 
 constexpr float kLift = 14.0f;    // the largest weight is near 2^14
 constexpr int kLeastScale = -60;  // scales below 2^-60 count as 2^-60 in M
@@ -1254,4 +1255,5 @@ cudaError_t attend_mma(const AttendArgs& a, int block, cudaStream_t stream) {
   return cudaErrorInvalidValue;
 }
 
+}  // namespace
 }  // namespace lp

@@ -498,8 +498,10 @@ lp_status lp_cache_read(const lp_cache_part* parts, const lp_heads* out, int64_t
  *   workspace    device scratch of lp_cache_attend_workspace_bytes, 16-byte aligned, of any
  *                content.  A call is one to three kernels that hand on sums in it: calls that
  *                share it must be ordered, as lp_beam_select's
- * Equal calls give equal results to the last bit.  Invalid: what lp_cache_write refuses of a
- * cache; q_heads not a multiple of heads; a negative size; block_size < 1; blocks_stride <
+ * Equal calls give equal results to the last bit.  Should a wait inside the kernel of many rows
+ * run out (3 s for what takes microseconds; no such case is known), the call still returns
+ * normally, and 256 queries of a head are NaN, and so are the weights of the tokens that they
+ * see.  Invalid: what lp_cache_write refuses of a cache; q_heads not a multiple of heads; a negative size; block_size < 1; blocks_stride <
  * max_blocks; NULL or misaligned pointers with work to do; a scale that is not finite.  dim
  * above 1024, more than 2^30 tokens (max_blocks * block_size), rows * q_heads above 2^24, or
  * more than 2^31 - 1 rows of heads in all return LP_ERR_TOO_LARGE.
