@@ -80,9 +80,10 @@ __device__ __forceinline__ bool kept(const uint32_t* mask, int v) {
 // x / T of a candidate relative to the row's largest; candidates at +inf share the mass.
 __device__ __forceinline__ float relative(float x, float top) { return x == top ? 0.0f : x - top; }
 
-// What a candidate's distance to the largest is multiplied by, as a power of two.
+// What a candidate's distance to the largest is multiplied by, as a power of two.  Not 0, with an
+// infinite temperature: a candidate's distance stays finite and what is none keeps -inf.
 __device__ __forceinline__ float rate_of(float heat) {
-  return heat > 0.0f ? fminf(kLog2e / heat, 3e38f) : 3e38f;
+  return heat > 0.0f ? fmaxf(fminf(kLog2e / heat, 3e38f), 1.4012984643248171e-45f) : 3e38f;
 }
 
 __device__ __forceinline__ void best_of(float& x, int& v, float y, int w) {
@@ -471,7 +472,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_say_kernel(const __grid_co
       // exp(d / T) with the quotient's rounding taken back: an acceptance hangs on p's last
       // places
       const float d = relative(draft_x, tops[tid]), quot = __fdiv_rn(d, heat);
-      const float over = d > -INFINITY && quot > -INFINITY ? fmaf(-quot, heat, d) / heat : 0.0f;
+      const float over = d > -INFINITY && quot > -INFINITY && heat < INFINITY
+                             ? fmaf(-quot, heat, d) / heat : 0.0f;
       const float e = expf(quot), p = fmaf(e, over, e);
       taken = draft_u * draft_q * sums[tid] < p;
     }
