@@ -31,6 +31,7 @@ constexpr int kMostAnyWarps = 16;
 constexpr int kQueries = 4;     // of a block of attend_any_kernel
 constexpr int kGroup = 2;       // tokens that a warp of it has at a time
 constexpr int kMostDim = 1024;
+constexpr int kAnyBytes = 96 * 1024;  // of shared memory of a block of attend_any_kernel
 
 // The value of element d of a head's codes.
 template <int BITS>
@@ -271,12 +272,12 @@ __global__ void __launch_bounds__(kWarps * 32) weights_any_kernel(const __grid_c
 cudaError_t attend_any(const AttendArgs& a, cudaStream_t stream) {
   const int tiles = (a.rows * a.shared + kQueries - 1) / kQueries;
   const int64_t units = int64_t(a.batch) * a.heads * tiles;
-  // as many warps as 96 KB hold the sums of
-  const int warps = std::min(kMostAnyWarps, 96 * 1024 / 4 / a.dim / kQueries - 1);
+  // as many warps as it holds the sums of
+  const int warps = std::min(kMostAnyWarps, kAnyBytes / 4 / a.dim / kQueries - 1);
   const int smem = (warps + 1) * kQueries * a.dim * 4;
   static PerDevice<1> allowed[2];
   void (*kernel)(AttendArgs, int) = a.bits == 8 ? attend_any_kernel<8> : attend_any_kernel<4>;
-  cudaError_t e = allow_shared(kernel, smem, allowed[a.bits == 8]);
+  cudaError_t e = allow_shared(kernel, kAnyBytes, allowed[a.bits == 8]);
   if (e != cudaSuccess) return e;
   e = launch_kernel(kernel,
                                 dim3(unsigned(std::min<int64_t>(units, kSms * 64))),

@@ -45,21 +45,15 @@ struct PerDevice {
   }
 };
 
-// Lets a kernel have `bytes` of dynamic shared memory on the current device.
+// Lets a kernel have up to `most` bytes of dynamic shared memory on the current device: the most
+// that any call asks for, so that no call, in no order of threads, takes it from another's launch.
 template <typename... K>
-cudaError_t allow_shared(void (*kernel)(K...), int bytes, PerDevice<1>& allowed) {
+cudaError_t allow_shared(void (*kernel)(K...), int most, PerDevice<1>& allowed) {
   std::atomic<int>* a = allowed.at(0);
-  if (a != nullptr && bytes <= a->load(std::memory_order_relaxed)) return cudaSuccess;
+  if (a != nullptr && a->load(std::memory_order_acquire) != 0) return cudaSuccess;
   const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && a != nullptr) {
-    // (another thread's larger number stays; a smaller setting of its kernel does not)
-    int was = a->load(std::memory_order_relaxed);
-    while (was < bytes && !a->compare_exchange_weak(was, bytes)) {
-    }
-    if (was > bytes)
-      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, was);
-  }
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess && a != nullptr) a->store(1, std::memory_order_release);
   return e;
 }
 

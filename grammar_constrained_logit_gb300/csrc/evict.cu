@@ -32,6 +32,7 @@ constexpr int kMostCluster = 8;
 constexpr int kSms = 152;
 constexpr int kBins = 512;
 constexpr int kHeldTokens = 40 * 1024;  // weights that a block holds in shared memory
+constexpr int kRoundBytes = 48 * 1024;  // of a round's tokens, at most; a block holds two
 
 struct EvictArgs {
   lp_cache_part part[kMaxParts];
@@ -538,7 +539,7 @@ cudaError_t launch(EvictArgs a, cudaStream_t stream) {
     a.slice = (a.most + blocks - 1) / blocks;
     const int smem = std::max(1, a.slice) * 4;
     static PerDevice<1> allowed;
-    e = allow_shared(evict_slices_kernel, smem, allowed);
+    e = allow_shared(evict_slices_kernel, kHeldTokens * 4, allowed);
     if (e == cudaSuccess)
       e = launch_cluster(evict_slices_kernel, units, blocks, kThreads, smem, stream, a);
   } else {
@@ -556,12 +557,12 @@ cudaError_t launch(EvictArgs a, cudaStream_t stream) {
   int blocks = 1;
   while (blocks < kMostCluster && units * blocks * 2 <= 8 * kSms && a.keep > 64 * blocks) blocks *= 2;
   // of a block's round, two at once: as much as leaves room for all blocks, four an SM
-  const int64_t bytes = units * blocks <= 2 * kSms ? 48 * 1024 : 20 * 1024;
+  const int64_t bytes = units * blocks <= 2 * kSms ? kRoundBytes : 20 * 1024;
   a.round_tokens = int(std::min<int64_t>({kRoundTokens, bytes / (pieces * 16), a.keep}));
   a.round_tokens = std::min(a.round_tokens, (a.keep + blocks - 1) / blocks);
   const size_t smem = size_t(2) * a.round_tokens * pieces * 16;
   static PerDevice<1> allowed;
-  e = allow_shared(evict_move_kernel, int(smem), allowed);
+  e = allow_shared(evict_move_kernel, 2 * kRoundBytes, allowed);
   if (e != cudaSuccess) return e;
   return launch_cluster(evict_move_kernel, units, blocks, kMoveThreads, smem, stream, a);
 }
