@@ -546,6 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int piece = in % kPieces, line = in / kPieces;   // its 16 codes, of every kLines-th token
     constexpr int kLines = 128 / kPieces, kMine = kTile / kLines;
     float scale[2];
+    // (rows that do not see a token have 0 * what it holds)
+    const auto hides = [&](int t) {
+      const int t0 = (first + t) * kTile;
+      return !(t0 >= all_from && t0 + kTile <= all_until);
+    };
     const auto look = [&](int t) {  // a tile's tokens: where they lie, and their scales
       const int token = (first + t) * kTile + in;
       const int64_t slot = t < tiles && token < high.end ? slot_of(a, b, token) : -1;
@@ -565,18 +570,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         scale[1] = *reinterpret_cast<const float*>(
             static_cast<const char*>(vp.params) + h * vp.param_head_stride +
             slot_place(a, slot, vp.param_page_stride, vp.param_slot_stride));
+        if (!(fabsf(scale[1]) < INFINITY) && hides(t)) {
+          *static_cast<volatile int*>(&s.nan_hidden) = 1;
+          scale[1] = 0.0f;
+        }
       }
-    };
-    // (rows that do not see a token have 0 * what it holds)
-    const auto hides = [&](int t) {
-      const int t0 = (first + t) * kTile;
-      return !(t0 >= all_from && t0 + kTile <= all_until);
     };
     const auto put_scales = [&](int t) {
-      if (!(fabsf(scale[1]) < INFINITY) && hides(t)) {
-        *static_cast<volatile int*>(&s.nan_hidden) = 1;
-        scale[1] = 0.0f;
-      }
       s.scales[t & 3][0][in] = scale[0];
       s.scales[t & 3][1][in] = scale[1];
       s.scales[t & 3][2][in] =
