@@ -121,15 +121,18 @@ __device__ __forceinline__ uint32_t f16_two(float low, float high) {
 }
 
 // Two 4-bit codes less 8, as fp16: c (bits 0 to 3 of each half) in the last places of 1024, or
-// 16 c (bits 4 to 7), less 1024 and 8 or 128.
+// 16 c (bits 4 to 7), less 1024 and 8 or 128.  Mask and places are one instruction where they are
+// written as one (as two: 99.7 us for 90.4 at the long size below).
 __device__ __forceinline__ uint32_t codes_low(uint32_t x) {
   uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"((x & 0x000f000fu) | 0x64006400u), "r"(0x64086408u));
+  asm("{ .reg .b32 t; lop3.b32 t, %1, 0x000f000f, 0x64006400, 0xea; add.rn.f16x2 %0, t, %2; }"
+      : "=r"(r) : "r"(x), "r"(0xe408e408u));
   return r;
 }
 __device__ __forceinline__ uint32_t codes_high(uint32_t x) {
   uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"((x & 0x00f000f0u) | 0x64006400u), "r"(0x64806480u));
+  asm("{ .reg .b32 t; lop3.b32 t, %1, 0x00f000f0, 0x64006400, 0xea; add.rn.f16x2 %0, t, %2; }"
+      : "=r"(r) : "r"(x), "r"(0xe480e480u));
   return r;
 }
 
