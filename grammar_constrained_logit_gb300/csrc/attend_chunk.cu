@@ -15,12 +15,14 @@
 //   0-3, 4-7   a thread a query: exponents, P, the sums
 //   8-11       codes to fp16, two tiles ahead
 //   12         issues the products
-// Measured: 1024 queries of 32 heads over 16384 tokens, in a graph: 510 us, 522 TFLOP/s, 27% of
+// Measured: 1024 queries of 32 heads over 16384 tokens, in a graph: 504 us, 528 TFLOP/s, 27% of
 // the tensor pipe; by m16n8k16 1447.  What bounds it is the softmax's way out of tensor memory
 // and back: 6.0 thousand cycles of the 7.5 thousand that a tile takes (a pair's two loads, 128
 // exponents, the stores); the products are 2.  One block an SM, of 13 warps with 128 registers;
 // with the softmax over 16 warps 567 to 695 us, with registers moved to it 803, with 12 warps of
-// 168 registers 584 to 642.  fp16 takes P in two pieces, 810 us; heads of 64 take 431.
+// 168 registers 584 to 642.  fp16 takes P in two pieces, 809 us; heads of 64 take 433.
+// (One piece rounds P to 11 bits, an eighth of a bf16 result's step, which is 1.65e-3 off in norm
+// by its own rounding alone and 1.66e-3 so.)
 //
 // Every wait is bounded, by tries and not by a clock, which goes on while the kernel is off the
 // GPU.  Where one runs out all roles stop, the products that were begun end, and the block's

@@ -10,7 +10,7 @@
 // at a place that goes by its operands' exponents, and a subnormal's is -14 whatever its value:
 // c * 2^-24, which needs no subtraction, leaves the sum six to ten bits less.  Less 8, codes are
 // even about zero, and what is added up is no larger than the values are.  (8000 tokens in groups
-// of 32, f32: 6.6e-7 off in norm; as subnormals 5.6e-5, in 121 us for 140 at the size below.)
+// of 32, f32: 6.6e-7 off in norm; as subnormals 5.6e-5, and 4 to 12% less time.)
 // A group's scale s and middle m = l + 8 s come in 32 bits outside: for keys
 //   S = sum over groups of s_g (q_g . c_g) + m_g (sum of q_g),
 // for values P_g = P s_g meets the codes, and sum_t P_t m_tg is kept beside.  Queries are
@@ -22,11 +22,12 @@
 // a lane's share of a row is contiguous, read from shared memory as it lies.
 //
 // Measured, in a graph: 32 sequences of up to 8192 tokens, 8 heads of 128 with 4 queries each,
-// 8 bits: 55.7 us for 251 MB; all of 8192: 96.7 us for 554 MB, 84% of the copy rate, with the
+// 8 bits: 54.6 us for 251 MB; all of 8192: 98.7 us for 554 MB, 83% of the copy rate, with the
 // join some 5 us of it.  Memory bounds it.  4 sequences of up to 65536 with 8 queries, 4 bits in
-// groups of 32: 99.5 us for 273 MB: instructions, and waits for one another's results.  A warp a query, on the other units: 20197 and
-// 147804 us.  A worker may have a single tile: with two at least one token's attention takes
-// 10.1 us for 9.7, with eight 15.7.
+// groups of 32: 90 to 95 us for 273 MB: 56.6 M warp instructions, 61% of the issue slots, and
+// waits for one another's results.  A warp a query, on the other units: 20197 and 147804 us.  A
+// worker may have a single tile: with two at least one token's attention takes 10.1 us for 9.7,
+// with eight 15.7.
 #pragma once
 
 #include "attend.cuh"
@@ -47,6 +48,9 @@ struct Shape {
   static constexpr int kKeyBytes = BS / 4 * BITS / 8;    // a lane's, of a block of a key
   static constexpr int kValues = BS / 8;             // a lane's elements, of a block of a value
   static constexpr int kValueBytes = kValues * BITS / 8;
+  // of queries and of P s_g.  A piece has 11 bits, and bf16 queries no more than 8; one piece of
+  // P rounds by an eighth of the step of a bf16 result: 1.68e-3 off in norm, where the result's
+  // own rounding leaves 1.67e-3.  Two cost 1% of a step in 8 bits, some 20% in 4.
   static constexpr int kPieces = WIDE ? 2 : 1;
   static constexpr int kTile = kRow <= 128 ? 32 : 16;    // tokens
   static constexpr int kM = kTile / 16;

@@ -1,8 +1,9 @@
 // evict.cu -- a cache's sequences cut to their tokens of most attention weight, in place.
 //
 // Of a head's n > keep tokens stay the first ones, the last ones and the K = keep - first -
-// recent heaviest of those between.  The K-th largest weight is found digit by digit, eight
-// bits of an order-preserving key at a time; what is above it stays, and of what equals it
+// recent heaviest of those between.  The K-th largest weight is found digit by digit of
+// an order-preserving key, of 9, 8, 8 and 7 bits (four of 8 past a cluster's shared memory); what
+// is above it stays, and of what equals it
 // the lowest ones.  The j-th kept token, at s(j) >= j, moves to place j.
 //
 // s(j') > j for every j < j': what is written for a token is never the source of a later one,

@@ -490,7 +490,8 @@ lp_status lp_cache_read(const lp_cache_part* parts, const lp_heads* out, int64_t
  * Queries of 16 bits are taken as they are, those of 32 bits rounded to 22 bits or more.
  * A weight p_t is rounded to 11 bits for bf16 and to 22 for the other types, and to 2^-33 of
  * the row's largest product of weight and value's scale (2^-39 for 32-bit queries; a scale
- * below 2^-60 counts as that) where it is smaller.  Sums are 32-bit.
+ * below 2^-60 counts as that) where it is smaller.  Sums are 32-bit; a score is one of codes and
+ * queries scaled to 2^15, so keys whose scales are 2^96 and above can make it infinite.
  *   q, out       [batch, rows, q_heads, dim] of type dt, dim contiguous, strides in elements;
  *                out must not overlap q (the same pointer is refused) nor itself
  *   blocks       device int32 [batch, max_blocks], blocks_stride elements from row to row
@@ -501,10 +502,11 @@ lp_status lp_cache_read(const lp_cache_part* parts, const lp_heads* out, int64_t
  * Equal calls give equal results to the last bit.  Should a wait inside the kernel of many rows
  * run out (3 s for what takes microseconds; no such case is known), the call still returns
  * normally, and 256 queries of a head are NaN, and so are the weights of the tokens that they
- * see.  Invalid: what lp_cache_write refuses of a cache; q_heads not a multiple of heads; a negative size; block_size < 1; blocks_stride <
- * max_blocks; NULL or misaligned pointers with work to do; a scale that is not finite.  dim
- * above 1024, more than 2^30 tokens (max_blocks * block_size), rows * q_heads above 2^24, or
- * more than 2^31 - 1 rows of heads in all return LP_ERR_TOO_LARGE.
+ * see.  Invalid: what lp_cache_write refuses of a cache; q_heads not a multiple of heads; a
+ * negative size; block_size < 1; blocks_stride < max_blocks; NULL or misaligned pointers with
+ * work to do; a scale that is not finite.  dim above 1024, more than 2^30 tokens (max_blocks *
+ * block_size), rows * q_heads above 2^24, or more than 2^31 - 1 rows of heads in all return
+ * LP_ERR_TOO_LARGE.
  */
 typedef struct {
   void* data;
@@ -574,7 +576,9 @@ lp_status lp_cache_evict(const lp_cache_part* parts, int64_t n_parts, int32_t bi
  *     or r = p_n where that is 0 everywhere (NaN counts as 0, and so does p below 2^-120);
  *   - else argmax over v of logit_v / temperature + g_v, or the largest logit with
  *     temperature <= 0,
- * over the row's candidates, ties to the lowest; -1 if it has none.  g is lp_sample's noise,
+ * over the row's candidates, ties to the lowest; -1 if it has none.  Sums and probabilities are
+ * 32-bit: where the two sides of an acceptance, or the two best of a draw, are within 2e-5 of
+ * each other, either may win.  g is lp_sample's noise,
  * of row b = slot * rows_per_slot + n keyed by (seeds[b], b, offset), or (seed, b, offset)
  * where seeds is NULL.  rows_per_slot = 1 is lp_mask_and_sample_slots without filters.
  *   logits       device, B = slots * rows_per_slot rows of cols elements
