@@ -8,9 +8,12 @@
 // Codes go into the products exactly, as normal fp16: e4m3 as the fp16 of the same value, a
 // 4-bit code c as c - 8 (or 16 (c - 8): its bits stay where they lie).  A product's sum is cut
 // at a place that goes by its operands' exponents, and a subnormal's is -14 whatever its value:
-// c * 2^-24, which needs no subtraction, leaves the sum six to ten bits less.  Less 8, codes are
-// even about zero, and what is added up is no larger than the values are.  (8000 tokens in groups
-// of 32, f32: 6.6e-7 off in norm; as subnormals 5.6e-5, and 4 to 12% less time.)
+// c * 2^-24, which needs no subtraction, leaves the sum six to ten bits less.  Less 8 (values' less
+// 8 and less 7 in turn), codes are even about zero, and what is added up is no larger than the
+// values are.  (8000 tokens in groups of 32, f32: 6.6e-7 off in norm; as subnormals 5.6e-5.)
+// A sum is cut toward zero, so one that goes on through all tokens loses 2^-26 of itself at each
+// product: 500 queries over 40000 tokens of 8 bits were 3.3e-5 off.  Products of 16 tokens are
+// therefore added up outside, where sums are rounded: 8e-7, for 1 to 8% of the time.
 // A group's scale s and middle m = l + 8 s come in 32 bits outside: for keys
 //   S = sum over groups of s_g (q_g . c_g) + m_g (sum of q_g),
 // for values P_g = P s_g meets the codes, and sum_t P_t m_tg is kept beside.  Queries are
@@ -124,26 +127,29 @@ __device__ __forceinline__ uint32_t f16_two(float low, float high) {
   return r;
 }
 
-// Two 4-bit codes less 8, as fp16: c (bits 0 to 3 of each half) in the last places of 1024, or
-// 16 c (bits 4 to 7), less 1024 and 8 or 128.  Mask and places are one instruction where they are
-// written as one (as two: 99.7 us for 90.4 at the long size below).
+// Two 4-bit codes less a middle, as fp16: c (bits 0 to 3 of each half) in the last places of 1024,
+// or 16 c (bits 4 to 7), less 1024 and the middle.  Mask and places are one instruction where they
+// are written as one (as two: 99.7 us for 90.4 at the long size below).
+template <int MIDDLE = 8>
 __device__ __forceinline__ uint32_t codes_low(uint32_t x) {
   uint32_t r;
   asm("{ .reg .b32 t; lop3.b32 t, %1, 0x000f000f, 0x64006400, 0xea; add.rn.f16x2 %0, t, %2; }"
-      : "=r"(r) : "r"(x), "r"(0xe408e408u));
+      : "=r"(r) : "r"(x), "r"(0xe400e400u + 0x00010001u * MIDDLE));
   return r;
 }
+template <int MIDDLE = 8>
 __device__ __forceinline__ uint32_t codes_high(uint32_t x) {
   uint32_t r;
   asm("{ .reg .b32 t; lop3.b32 t, %1, 0x00f000f0, 0x64006400, 0xea; add.rn.f16x2 %0, t, %2; }"
-      : "=r"(r) : "r"(x), "r"(0xe480e480u));
+      : "=r"(r) : "r"(x), "r"(0xe400e400u + 0x00100010u * MIDDLE));
   return r;
 }
 
-// Of 4-bit params: a group's scale, and the value in its middle.
+// Of 4-bit params: a group's scale, and the value of its middle code.
 __device__ __forceinline__ float scale_of(uint32_t held) { return __uint_as_float(held << 16); }
+template <int MIDDLE = 8>
 __device__ __forceinline__ float middle_of(uint32_t held) {
-  return fmaf(8.0f, scale_of(held), __uint_as_float(held & 0xffff0000u));
+  return fmaf(float(MIDDLE), scale_of(held), __uint_as_float(held & 0xffff0000u));
 }
 
 // Whether what is held for a group stands for numbers.
@@ -164,6 +170,15 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// The first product of a sum.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.0f));
 }
 
 __device__ __forceinline__ void copy_async(uint32_t to, const char* from, int unit, int bytes) {
@@ -732,7 +747,9 @@ struct Sums {
                                    w3 - Elt<LP_F16>::half_bits_to_float(b >> 16)));
           }
           if (T::kBits == 4) {
-            const float l0 = middle_of(h0), l1 = middle_of(h1);
+            // (less 8 and less 7, in turn: codes' mean is between, and what all have in common
+            // would grow with the tokens, where their sum does as the root)
+            const float l0 = middle_of<8>(h0), l1 = middle_of<7>(h1);
             low[k % kLows][n][0] = fmaf(e[0], l0, fmaf(e[2], l1, low[k % kLows][n][0]));
             low[k % kLows][n][1] = fmaf(e[1], l0, fmaf(e[3], l1, low[k % kLows][n][1]));
           }
@@ -756,12 +773,16 @@ struct Sums {
             const uint32_t x = __byte_perm(va.w[v / 4], vb.w[v / 4], sel);
             const uint32_t y = __byte_perm(vc.w[v / 4], vd.w[v / 4], sel);
             op[0] = codes_low(x), op[1] = codes_high(x);
-            op[2] = codes_low(y), op[3] = codes_high(y);
+            op[2] = codes_low<7>(y), op[3] = codes_high<7>(y);
           }
 #pragma unroll
-          for (int n = 0; n < T::kNR; ++n)
+          for (int n = 0; n < T::kNR; ++n) {  // (added outside, where a sum is rounded, not cut)
+            float t[4];
+            mma_first(t, op, p[n][T::kPieces - 1]);
+            if (T::kWide) mma(t, op, p[n][0]);
 #pragma unroll
-            for (int i = T::kPieces - 1; i >= 0; --i) mma(o[k][v][n], op, p[n][i]);
+            for (int e = 0; e < 4; ++e) o[k][v][n][e] += t[e];
+          }
         }
       }
     }

@@ -16,9 +16,11 @@ add in squares:
   * sums on tensor cores.  A product of 16 cuts its 17 addends at 2^-24 of the largest, to zero:
     e = sqrt(17 / 3) 2^-24 of it at the root of the mean square.  A score has dim / 16 such steps
     in two pieces, at most 32, and partial sums of up to 4 times its deviation, which is 1 here:
-    sqrt(32) * 4 e = 3.2e-6, which is what a weight is off by, relatively.  700 tokens of values
-    that are even about zero are 88 steps whose parts are the size of their sum, to the next
-    power of two: sqrt(88) * 1.5 e = 2.0e-6.  In squares 3.8e-6; 4e-6 is allowed.
+    sqrt(32) * 4 e = 3.2e-6, which is what a weight is off by, relatively.  What is added up over
+    tokens is cut within 16 of them, sqrt(2) * 1.5 e, and rounded from there on: n / 16 sums, the
+    root of the mean square of whose roundings is 2^-24 / sqrt(3) of them, that grow as the root
+    of what they are made of: sqrt(n / 32) * 2^-24 / sqrt(3), 1.2e-6 for 40000.  In squares
+    3.5e-6; 4e-6 is allowed.
 
 A weight that is added up is rounded to 32 bits, so the last is its bound for all types."""
 import math
@@ -125,3 +127,15 @@ def test_norm_of_many_rows(bits, dim, group, dtype, window):
     g = torch.Generator("cuda").manual_seed(32)
     q = torch.randn(5, 97, 24, dim, device="cuda", generator=g)
     close(cache, q, table(rng, lengths, 16, total), lengths, 16, dtype, window)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("bits, dim, group", [(8, 128, 32), (4, 128, 32), (4, 64, 16)])
+def test_norm_over_many_tokens(bits, dim, group, dtype):
+    """So many rows that a worker goes through hundreds of tiles of tokens."""
+    lengths = [40000]
+    total = 40016
+    cache = even(total, 4, dim, bits, group)
+    g = torch.Generator("cuda").manual_seed(33)
+    q = torch.randn(1, 500, 16, dim, device="cuda", generator=g)
+    close(cache, q, table(np.random.default_rng(34), lengths, 16, total), lengths, 16, dtype)
