@@ -13,6 +13,7 @@
 
 namespace lp {
 
+int64_t chunk_kept(int64_t rows, int64_t heads, int64_t batch, int64_t dim);
 bool chunk_fits(const AttendArgs& a);
 cudaError_t attend_chunk(const AttendArgs& a, cudaStream_t stream);
 cudaError_t attend_8n1(const AttendArgs& a, int block, cudaStream_t stream);
@@ -326,11 +327,12 @@ extern "C" int64_t lp_cache_attend_workspace_bytes(int64_t batch, int64_t rows, 
   if (batch < 0 || rows < 0 || q_heads < 0 || heads < 0 || dim < 0 || dim > kMostDim ||
       !fits(rows, q_heads, 1 << 24) || !fits(batch, rows * q_heads, INT32_MAX))
     return -1;
-  // of each row its sum; who shares a unit; and what the workers leave of the shared ones
+  // of each row its sum; who shares a unit; what the workers leave of the shared ones; and what
+  // blocks of many rows keep
   const int64_t per_head = heads == 0 ? 0 : rows * (q_heads / heads);
   const int64_t left = int64_t(kSms) * kMostWarps * 2 * rows_at_once(per_head) * (dim * 4 + 8);
   return (batch * rows * q_heads * 4 + 15) / 16 * 16 + batch * ((per_head + 7) / 8) * 16 +
-         (left + 15) / 16 * 16;
+         (left + 15) / 16 * 16 + chunk_kept(per_head, heads, batch, dim) * 4;
 }
 
 extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, int64_t n_slots,
@@ -429,6 +431,7 @@ extern "C" lp_status lp_cache_attend(const lp_cache_part* parts, int32_t bits, i
               uint64_t(a.q.row_stride) | uint64_t(a.q.head_stride)) % 8 == 0;
   a.sums = reinterpret_cast<float*>(left);
   a.tops = reinterpret_cast<float2*>(left + held * a.dim * 4);
+  a.kept = reinterpret_cast<float*>(left + held * (a.dim * 4 + 8));  // (a multiple of 16)
   static const Launch launches[2][2][2] = {{{attend_8n1, attend_8n2}, {attend_8w1, attend_8w2}},
                                            {{attend_4n1, attend_4n2}, {attend_4w1, attend_4w2}}};
   a.wide_out = (reinterpret_cast<uintptr_t>(out->data) | uint64_t(a.out.batch_stride) |

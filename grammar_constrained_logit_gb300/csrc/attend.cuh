@@ -41,6 +41,7 @@ struct AttendArgs {
   float2* tops;    // [workers, 2, team, tile's rows]: (largest exponent, mass)
   int4* shares;    // [batch, row tiles]: a unit's first worker and last, whether the first one
                    // has it as its part 1
+  float* kept;     // of the kernel of many rows: [blocks, 2, dim, 128]
   bool wide_q, wide_out;  // queries are loaded, results stored, 8 bytes at a time
   bool weights_only;      // the queries' sums are there
 };

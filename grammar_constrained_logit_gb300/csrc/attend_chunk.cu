@@ -7,6 +7,9 @@
 //   S = Q K^T   from shared memory, 128 x 128 in tensor memory
 //   P = 2^(s_k S unit - R) s_v, fp16, over S's place in tensor memory (two pieces, for fp16)
 //   O += P V    P from tensor memory, V from shared memory
+// A tensor core cuts sums toward zero, 2^-26 of them at each product: 1.3e-4 over 65536 tokens, in
+// two pieces.  Every kRun tiles O is added to what is kept outside (in L2), in 32 bits with
+// rounding, and begins anew: 8e-6, 4 us each.
 // R, which exponents are taken against, is the largest of x + floor(log2 s_v) some time ago: O
 // is scaled only when that grew by more than 2^kSlack, so P stays below 2^(kLift + kSlack + 1) = 2^15.
 //
@@ -39,6 +42,7 @@ constexpr int kThreads = 13 * 32;
 constexpr float kLift = 8.0f;
 constexpr float kSlack = 6.0f;
 constexpr int kLeastScale = -60;
+constexpr int kRun = 64;       // tiles that are added up in tensor memory
 constexpr uint32_t kPatience = 1u << 21;  // tries of a wait, of 1.5 us: 3 s in all
 
 struct alignas(1024) Shared {
@@ -240,6 +244,43 @@ __device__ __noinline__ void note_hidden(Shared& s, const AttendArgs& a, int b, 
     for (int e = 0; e < 16; ++e)
       if ((codes[e] & 0x7f) == 0x7f) seers.note(s.nan[d + e]);
   }
+}
+
+// What is kept of this thread's row, a column every kTile floats.
+template <int DIM>
+__device__ __forceinline__ float* kept_at(const AttendArgs& a) {
+  return a.kept + (int64_t(blockIdx.x) * 2 + (threadIdx.x >> 7)) * DIM * kTile +
+         (threadIdx.x & (kTile - 1));
+}
+
+// Adds what tensor memory has of a row to what is kept of it.
+template <int DIM>
+__device__ __noinline__ void keep(uint32_t o_mine, float* kept, float factor, bool first) {
+#pragma unroll 1
+  for (int c = 0; c < DIM; c += 32) {
+    uint32_t x[32];
+    tensor_load(x, o_mine + c);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      float* at = kept + (c + e) * kTile;
+      *at = first ? __uint_as_float(x[e]) : fmaf(*at, factor, __uint_as_float(x[e]));
+    }
+  }
+}
+
+// And the other way.
+template <int DIM>
+__device__ __noinline__ void add_kept(uint32_t o_mine, const float* kept, float factor) {
+#pragma unroll 1
+  for (int c = 0; c < DIM; c += 32) {
+    uint32_t x[32];
+    tensor_load(x, o_mine + c);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      x[e] = __float_as_uint(fmaf(kept[(c + e) * kTile], factor, __uint_as_float(x[e])));
+    tensor_store(o_mine + c, x);
+  }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // 16 columns, under way while the ones before are worked on.
@@ -472,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // columns: S (and P) of the two 128s, then O
   const uint32_t o_at = tmem + 256;
 
-  float mass = 0.0f, ref = -INFINITY;
+  float mass = 0.0f, ref = -INFINITY, kept_ref = -INFINITY;
   if (warp < 8) {
     // ---------------------------------------------------------------- a thread a query
     const int half = warp >> 2;
@@ -482,63 +523,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     Look w;
     w.s_mine = s_mine;
     w.unit2 = pair(unit, unit);
-    for (int t = 0; t < tiles; ++t) {
-      if (!__all_sync(kFullWarp, bar_wait(s, &s.s_full[half], t & 1))) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const int t0 = (first + t) * kTile, slot = t & 3;
-      w.scales = s.scales[slot][0];
-      w.held = s.held[slot];
-      w.lo = v.lo - t0, w.end = v.end - t0;
-      const bool all = t0 >= all_from && t0 + kTile <= all_until &&
-                       (w.held[0] & w.held[1] & w.held[2] & w.held[3]) == ~0u;
-      // P is taken against the reference that there is; only where something has outgrown it
-      // (the first time, always) is the largest looked for, and the reference moved
-      uint32_t p[64], most;
-      uint64_t sum2, base2;
-      bool look = __any_sync(kFullWarp, ref == -INFINITY);
-      for (;;) {
-        if (look) {
-          const float now = all ? row_largest<true>(w, ref) : row_largest<false>(w, ref);
-          const bool grow = now > ref + kSlack || (ref == -INFINITY && now > -INFINITY);
-          const float f = grow ? (ref == -INFINITY ? 0.0f : ex2(ref - now)) : 1.0f;
-          if (grow) ref = now, mass *= f;
-          if (t > 0 && __any_sync(kFullWarp, grow)) {
+    for (int run = 0; run < tiles; run += kRun) {
+      if (run > 0) {  // O begins anew with the next product
+        if (!__all_sync(kFullWarp, bar_wait(s, &s.s_full[half], run & 1))) goto stopped;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        keep<DIM>(o_mine, kept_at<DIM>(a), kept_ref == -INFINITY ? 0.0f : ex2(kept_ref - ref),
+                  run == kRun);
+        kept_ref = ref;
+      }
+      for (int t = run; t < min(tiles, run + kRun); ++t) {
+        if (!__all_sync(kFullWarp, bar_wait(s, &s.s_full[half], t & 1))) goto stopped;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const int t0 = (first + t) * kTile, slot = t & 3;
+        w.scales = s.scales[slot][0];
+        w.held = s.held[slot];
+        w.lo = v.lo - t0, w.end = v.end - t0;
+        const bool all = t0 >= all_from && t0 + kTile <= all_until &&
+                         (w.held[0] & w.held[1] & w.held[2] & w.held[3]) == ~0u;
+        // P is taken against the reference that there is; only where something has outgrown it
+        // (the first time, always) is the largest looked for, and the reference moved
+        uint32_t p[64], most;
+        uint64_t sum2, base2;
+        bool look = __any_sync(kFullWarp, ref == -INFINITY);
+        for (;;) {
+          if (look) {
+            const float now = all ? row_largest<true>(w, ref) : row_largest<false>(w, ref);
+            const bool grow = now > ref + kSlack || (ref == -INFINITY && now > -INFINITY);
+            const float f = grow ? (ref == -INFINITY ? 0.0f : ex2(ref - now)) : 1.0f;
+            if (grow) ref = now, mass *= f;
+            if (t > 0 && __any_sync(kFullWarp, grow)) {
 #pragma unroll 1
-            for (int c = 0; c < DIM; c += 32) {
-              uint32_t x[32];
-              tensor_load(x, o_mine + c);
+              for (int c = 0; c < DIM; c += 32) {
+                uint32_t x[32];
+                tensor_load(x, o_mine + c);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                x[e] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(x[e]) * f);
-              tensor_store(o_mine + c, x);
+                for (int e = 0; e < 32; ++e)
+                  x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                tensor_store(o_mine + c, x);
+              }
             }
           }
+          const float base = (ref == -INFINITY ? 0.0f : -ref) + kLift;
+          base2 = pair(base, base);
+          if (all) row_weights<true>(w, base2, p, &sum2, &most);
+          else row_weights<false>(w, base2, p, &sum2, &most);
+          // 2^15 and above
+          const bool over = (most & 0xffffu) >= 0x7800u || (most >> 16) >= 0x7800u;
+          if (look || !__any_sync(kFullWarp, over)) break;
+          look = true;
         }
-        const float base = (ref == -INFINITY ? 0.0f : -ref) + kLift;
-        base2 = pair(base, base);
-        if (all) row_weights<true>(w, base2, p, &sum2, &most);
-        else row_weights<false>(w, base2, p, &sum2, &most);
-        // 2^15 and above
-        const bool over = (most & 0xffffu) >= 0x7800u || (most >> 16) >= 0x7800u;
-        if (look || !__any_sync(kFullWarp, over)) break;
-        look = true;
-      }
-      mass += lower(sum2) + upper(sum2);
-      if (WIDE) {
-        if (all) row_rest<true>(w, base2, p);
-        else row_rest<false>(w, base2, p);
-      }
+        mass += lower(sum2) + upper(sum2);
+        if (WIDE) {
+          if (all) row_rest<true>(w, base2, p);
+          else row_rest<false>(w, base2, p);
+        }
 #pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        uint32_t x[32];
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t x[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = p[c + e];
-        tensor_store(s_mine + c, x);
+          for (int e = 0; e < 32; ++e) x[e] = p[c + e];
+          tensor_store(s_mine + c, x);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        bar_arrive(&s.p_full[half]);
       }
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      bar_arrive(&s.p_full[half]);
     }
+  stopped:
     if (tiles > 0) bar_wait(s, &s.o_done[half], 0);
     __syncwarp();
   } else if (warp < 12) {
@@ -671,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kTile / 16; ++i)
             mma_tensor(o_at + half * DIM, tmem + half * 128 + piece * 64 + i * 8,
                        (t & 1 ? v_op[1] : v_op[0]) + i * (2048 >> 4), kValue,
-                       t > 0 || i > 0 || piece != (WIDE ? 1 : 0));
+                       t % kRun != 0 || i > 0 || piece != (WIDE ? 1 : 0));
         if (t + 1 == tiles) commit(&s.o_done[half]);
         if (half == 1) commit(&s.v_empty[t & 1]);
         // S of the next tile goes where this one's P was: products run in their order
@@ -700,6 +751,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a.lse != nullptr && row < per_head)
       a.lse[(int64_t(b) * a.rows + r) * (a.heads * a.shared) + j] =
           none ? -INFINITY : ref - kLift + log2f(mass);
+    if (tiles > kRun)
+      add_kept<DIM>(o_mine, kept_at<DIM>(a),
+                    kept_ref == -INFINITY ? 0.0f : ex2(kept_ref - ref));
 #pragma unroll 1
     for (int c = 0; c < DIM; c += 32) {
       uint32_t x[32];
@@ -776,15 +830,21 @@ cudaError_t launch_chunk(const AttendArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-bool chunk_fits(const AttendArgs& a) {
-  const int64_t rows = int64_t(a.rows) * a.shared;
-  const int64_t blocks = (rows + 2 * kTile - 1) / (2 * kTile) * a.heads * a.batch;
+// Floats that the blocks keep of their rows, `rows` to a head of the cache; 0 where these are
+// too few for the kernel.
+int64_t chunk_kept(int64_t rows, int64_t heads, int64_t batch, int64_t dim) {
   // A block's time is that of its tokens, whoever else runs (507 us for 16384, 285 for 8192),
   // the other kernel's that of all queries: 382 us for 32 x 256 of them over 16384, 477 for 40 x
   // 256; 120 us for 16 x 256 over 8192, in half-filled blocks.  They meet near 43 x 256.
-  const int64_t full = rows * a.heads * a.batch / (2 * kTile);
-  return a.bits == 8 && a.group == a.dim && (a.dim == 64 || a.dim == 128) && a.dt != LP_F32 &&
-         rows >= kTile && full >= 43 && blocks <= INT32_MAX;
+  const int64_t full = rows * heads * batch / (2 * kTile);
+  if ((dim != 64 && dim != 128) || rows < kTile || full < 43) return 0;
+  return (rows + 2 * kTile - 1) / (2 * kTile) * 2 * kTile * heads * batch * dim;
+}
+
+bool chunk_fits(const AttendArgs& a) {
+  const int64_t floats = chunk_kept(int64_t(a.rows) * a.shared, a.heads, a.batch, a.dim);
+  return a.bits == 8 && a.group == a.dim && a.dt != LP_F32 && floats > 0 &&
+         floats / (2 * kTile * a.dim) <= INT32_MAX;
 }
 
 cudaError_t attend_chunk(const AttendArgs& a, cudaStream_t stream) {

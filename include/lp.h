@@ -491,7 +491,9 @@ lp_status lp_cache_read(const lp_cache_part* parts, const lp_heads* out, int64_t
  * A weight p_t is rounded to 11 bits for bf16 and to 22 for the other types, and to 2^-33 of
  * the row's largest product of weight and value's scale (2^-39 for 32-bit queries; a scale
  * below 2^-60 counts as that) where it is smaller.  Sums are 32-bit; a score is one of codes and
- * queries scaled to 2^15, so keys whose scales are 2^96 and above can make it infinite.
+ * queries scaled to 2^15, so keys whose scales are 2^96 and above can make it infinite.  What the
+ * tensor cores cut off sums over tokens, toward zero, is below 1e-6 of them, and below 2.1e-5 for
+ * 16-bit queries, 43 * 256 and more in all, over a cache of 8 bits with one scale a head.
  *   q, out       [batch, rows, q_heads, dim] of type dt, dim contiguous, strides in elements;
  *                out must not overlap q (the same pointer is refused) nor itself
  *   blocks       device int32 [batch, max_blocks], blocks_stride elements from row to row
