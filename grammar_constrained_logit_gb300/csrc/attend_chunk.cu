@@ -18,12 +18,12 @@
 //   0-3, 4-7   a thread a query: exponents, P, the sums
 //   8-11       codes to fp16, two tiles ahead
 //   12         issues the products
-// Measured: 1024 queries of 32 heads over 16384 tokens, in a graph: 504 us, 528 TFLOP/s, 27% of
+// Measured: 1024 queries of 32 heads over 16384 tokens, in a graph: 528 us, 504 TFLOP/s, 26% of
 // the tensor pipe; by m16n8k16 1447.  What bounds it is the softmax's way out of tensor memory
 // and back: 6.0 thousand cycles of the 7.5 thousand that a tile takes (a pair's two loads, 128
 // exponents, the stores); the products are 2.  One block an SM, of 13 warps with 128 registers;
 // with the softmax over 16 warps 567 to 695 us, with registers moved to it 803, with 12 warps of
-// 168 registers 584 to 642.  fp16 takes P in two pieces, 809 us; heads of 64 take 433.
+// 168 registers 584 to 642.  fp16 takes P in two pieces, 828 us; heads of 64 take 445.
 // (One piece rounds P to 11 bits, an eighth of a bf16 result's step, which is 1.65e-3 off in norm
 // by its own rounding alone and 1.66e-3 so.)
 //
@@ -833,9 +833,9 @@ cudaError_t launch_chunk(const AttendArgs& a, cudaStream_t stream) {
 // Floats that the blocks keep of their rows, `rows` to a head of the cache; 0 where these are
 // too few for the kernel.
 int64_t chunk_kept(int64_t rows, int64_t heads, int64_t batch, int64_t dim) {
-  // A block's time is that of its tokens, whoever else runs (507 us for 16384, 285 for 8192),
-  // the other kernel's that of all queries: 382 us for 32 x 256 of them over 16384, 477 for 40 x
-  // 256; 120 us for 16 x 256 over 8192, in half-filled blocks.  They meet near 43 x 256.
+  // A block's time is that of its tokens, whoever else runs (528 us for 16384), the other kernel's
+  // that of all queries: 407 us for 32 x 256 of them over 16384, 503 for 40 x 256; 127 us for
+  // 16 x 256 over 8192, in half-filled blocks.  They meet near 43 x 256.
   const int64_t full = rows * heads * batch / (2 * kTile);
   if ((dim != 64 && dim != 128) || rows < kTile || full < 43) return 0;
   return (rows + 2 * kTile - 1) / (2 * kTile) * 2 * kTile * heads * batch * dim;

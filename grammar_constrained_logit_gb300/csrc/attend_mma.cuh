@@ -25,9 +25,9 @@
 // a lane's share of a row is contiguous, read from shared memory as it lies.
 //
 // Measured, in a graph: 32 sequences of up to 8192 tokens, 8 heads of 128 with 4 queries each,
-// 8 bits: 54.6 us for 251 MB; all of 8192: 98.7 us for 554 MB, 83% of the copy rate, with the
+// 8 bits: 57 us for 251 MB; all of 8192: 100 us for 554 MB, 81% of the copy rate, with the
 // join some 5 us of it.  Memory bounds it.  4 sequences of up to 65536 with 8 queries, 4 bits in
-// groups of 32: 90 to 95 us for 273 MB: 56.6 M warp instructions, 61% of the issue slots, and
+// groups of 32: 94 to 101 us for 273 MB: 60.6 M warp instructions, 62% of the issue slots, and
 // waits for one another's results.  A warp a query, on the other units: 20197 and 147804 us.  A
 // worker may have a single tile: with two at least one token's attention takes 10.1 us for 9.7,
 // with eight 15.7.
@@ -53,7 +53,7 @@ struct Shape {
   static constexpr int kValueBytes = kValues * BITS / 8;
   // of queries and of P s_g.  A piece has 11 bits, and bf16 queries no more than 8; one piece of
   // P rounds by an eighth of the step of a bf16 result: 1.68e-3 off in norm, where the result's
-  // own rounding leaves 1.67e-3.  Two cost 1% of a step in 8 bits, some 20% in 4.
+  // own rounding leaves 1.67e-3.  Two cost 9% of a step in 8 bits, some 20% in 4.
   static constexpr int kPieces = WIDE ? 2 : 1;
   static constexpr int kTile = kRow <= 128 ? 32 : 16;    // tokens
   static constexpr int kM = kTile / 16;
@@ -129,7 +129,7 @@ __device__ __forceinline__ uint32_t f16_two(float low, float high) {
 
 // Two 4-bit codes less a middle, as fp16: c (bits 0 to 3 of each half) in the last places of 1024,
 // or 16 c (bits 4 to 7), less 1024 and the middle.  Mask and places are one instruction where they
-// are written as one (as two: 99.7 us for 90.4 at the long size below).
+// are written as one (as two they take a tenth more at the long size below).
 template <int MIDDLE = 8>
 __device__ __forceinline__ uint32_t codes_low(uint32_t x) {
   uint32_t r;
